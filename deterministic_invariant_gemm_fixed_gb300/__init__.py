@@ -56,6 +56,12 @@ SIGNATURES = {
     "bi_fp8_forward": (_i32, [_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p]),
     "bi_fp8_backward_dx": (_i32, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p]),
     "bi_fp8_backward_dw": (_i32, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p]),
+    "bi_adapter_forward": (_i32, [_p] * 10 + [_i64] * 5 + [_i32, _p, _i32]),
+    "bi_adapter_backward": (_i32, [_p] * 12 + [_i64] * 5 + [_i32, _p, _i32]),
+    "bi_router_forward": (_i32, [_p] * 10 + [_i64] * 3 + [_i32, _i32, _p]),
+    "bi_router_backward": (_i32, [_p] * 10 + [_i64] * 3 + [_i32, _i32, _p]),
+    "bi_grad_norm": (_i32, [_p, _p, _p, _p, _p, _i64, _p]),
+    "bi_grad_clip": (_i32, [_p, _p, _p, _p, _p, _i64, _p, ctypes.c_float, _p]),
     "bi_grouped_forward_noalloc": (_i32, [_p, _p, _p, _p, _i64, _i64, _i64, _i64, _i32, _p]),
 }
 
@@ -226,6 +232,71 @@ def bi_grouped_forward_noalloc(y, x, w, row_experts, m, k, n, e, dtype, stream=N
                                            dtype_code(dtype), _stream(stream))
 
 
+def bi_adapter_forward(engine, y, h, x, w, bias, a, b, scales, row_adapters, m, k, n, r, g, dtype, stream=None,
+                       tensor_cores=1) -> int:
+    return _lib.bi_adapter_forward(engine, _ptr(y), _ptr(h), _ptr(x), _ptr(w), _ptr(bias), _ptr(a), _ptr(b),
+                                   _ptr(scales), _ptr(row_adapters), m, k, n, r, g, dtype_code(dtype),
+                                   _stream(stream), int(tensor_cores))
+
+
+def bi_adapter_backward(engine, dx, da, db, x, h, w, dy, a, b, scales, row_adapters, m, k, n, r, g, dtype,
+                        stream=None, tensor_cores=1) -> int:
+    return _lib.bi_adapter_backward(engine, _ptr(dx), _ptr(da), _ptr(db), _ptr(x), _ptr(h), _ptr(w), _ptr(dy),
+                                    _ptr(a), _ptr(b), _ptr(scales), _ptr(row_adapters), m, k, n, r, g,
+                                    dtype_code(dtype), _stream(stream), int(tensor_cores))
+
+
+def bi_router_forward(engine, ids, weights, counts, rows, mean_prob, loss, lse, logits, valid, t, e, k, normalize,
+                      dtype, stream=None) -> int:
+    return _lib.bi_router_forward(engine, _ptr(ids), _ptr(weights), _ptr(counts), _ptr(rows), _ptr(mean_prob),
+                                  _ptr(loss), _ptr(lse), _ptr(logits), _ptr(valid), t, e, k, int(normalize),
+                                  dtype_code(dtype), _stream(stream))
+
+
+def bi_router_backward(engine, dlogits, logits, lse, ids, weights, counts, rows, dweights, dloss, t, e, k, normalize,
+                       dtype, stream=None) -> int:
+    return _lib.bi_router_backward(engine, _ptr(dlogits), _ptr(logits), _ptr(lse), _ptr(ids), _ptr(weights),
+                                   _ptr(counts), _ptr(rows), _ptr(dweights), _ptr(dloss), t, e, k, int(normalize),
+                                   dtype_code(dtype), _stream(stream))
+
+
+class TensorSet:
+    """A set of tensors as bi_grad_norm and bi_grad_clip take it: the host arrays
+    of device pointers, element counts and dtypes.  Holds its tensors, so the
+    pointers stay valid; a program whose gradient buffers persist makes one set
+    and uses it every step."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        n = self.n = len(self.tensors)
+        # an empty tensor has no storage to point at
+        self.ptrs = (ctypes.c_void_p * n)(*[_ptr(t) if t.numel() else None for t in self.tensors])
+        self.counts = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
+        self.dtypes = (ctypes.c_int * n)(*[dtype_code(t.dtype) for t in self.tensors])
+
+    def __len__(self):
+        return self.n
+
+
+def _set(tensors):
+    return tensors if isinstance(tensors, TensorSet) else TensorSet(tensors)
+
+
+def bi_grad_norm(engine, norm, tensors, stream=None) -> int:
+    """tensors: a TensorSet, or a sequence of tensors."""
+    t = _set(tensors)
+    return _lib.bi_grad_norm(engine, _ptr(norm), t.ptrs, t.counts, t.dtypes, t.n, _stream(stream))
+
+
+def bi_grad_clip(engine, dst, src, norm, max_norm, stream=None) -> int:
+    """dst and src: TensorSets (or sequences) of the same shapes and dtypes; dst
+    may be src."""
+    s, d = _set(src), _set(dst)
+    if d is not s and (d.n != s.n or d.counts[:] != s.counts[:] or d.dtypes[:] != s.dtypes[:]):
+        raise ValueError("bi: dst and src must hold tensors of the same sizes and dtypes")
+    return _lib.bi_grad_clip(engine, d.ptrs, s.ptrs, s.counts, s.dtypes, s.n, _ptr(norm), max_norm, _stream(stream))
+
+
 def bi_dispatch_tier(pass_, dtype, tensor_cores, k, n) -> int:
     return _lib.bi_dispatch_tier(int(pass_), dtype_code(dtype), int(tensor_cores), k, n)
 
@@ -309,6 +380,37 @@ class Engine:
 
     def fp8_backward_dw(self, dw, xq, gq, scale_x, scale_g, m, k, n, out_dtype, stream=None):
         self._ok(bi_fp8_backward_dw(self.handle, dw, xq, gq, scale_x, scale_g, m, k, n, out_dtype, stream))
+
+    def adapter_forward(self, y, h, x, w, bias, a, b, scales, ids, m, k, n, r, g, dtype, stream=None, tensor_cores=1):
+        self._ok(bi_adapter_forward(self.handle, y, h, x, w, bias, a, b, scales, ids, m, k, n, r, g, dtype, stream,
+                                    tensor_cores))
+
+    def adapter_backward(self, dx, da, db, x, h, w, dy, a, b, scales, ids, m, k, n, r, g, dtype, stream=None,
+                         tensor_cores=1):
+        self._ok(bi_adapter_backward(self.handle, dx, da, db, x, h, w, dy, a, b, scales, ids, m, k, n, r, g, dtype,
+                                     stream, tensor_cores))
+
+    def router_forward(self, ids, weights, counts, rows, mean_prob, loss, lse, logits, valid, t, e, k, normalize,
+                       dtype, stream=None):
+        self._ok(bi_router_forward(self.handle, ids, weights, counts, rows, mean_prob, loss, lse, logits, valid,
+                                   t, e, k, normalize, dtype, stream))
+
+    def router_backward(self, dlogits, logits, lse, ids, weights, counts, rows, dweights, dloss, t, e, k, normalize,
+                        dtype, stream=None):
+        self._ok(bi_router_backward(self.handle, dlogits, logits, lse, ids, weights, counts, rows, dweights, dloss,
+                                    t, e, k, normalize, dtype, stream))
+
+    def grad_norm(self, norm, tensors, stream=None):
+        self._ok(bi_grad_norm(self.handle, norm, tensors, stream))
+
+    def grad_clip(self, dst, src, norm, max_norm, stream=None):
+        self._ok(bi_grad_clip(self.handle, dst, src, norm, max_norm, stream))
+
+    def clip_gradients(self, dst, src, norm, max_norm, stream=None):
+        """norm = the set's global norm, then dst = src scaled to at most max_norm."""
+        src = _set(src)
+        self.grad_norm(norm, src, stream)
+        self.grad_clip(dst, src, norm, max_norm, stream)
 
     def check(self, stream=None):
         self._ok(bi_engine_check(self.handle, stream))

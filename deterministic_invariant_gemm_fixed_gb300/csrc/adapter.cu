@@ -1,0 +1,539 @@
+// Low-rank adapters of many requests beside a shared projection: entry points,
+// and the kernels that every tier shares or that run in plain f32 FMAs.  See
+// include/bi.h (bi_adapter_forward, bi_adapter_backward).
+//
+//   h[m,:] = X[m,:] A[g]^T          g = row_adapters[m]
+//   Y[m,:] = round( X[m,:] W + bias + (s_g h[m,:]) B[g] )
+//   u[m,:] = s_g dY[m,:] B[g]^T,    dX[m,:] = round( dY[m,:] W^T + u[m,:] A[g] )
+//   dA[g]  = sum_m u[m,:]^T X[m,:], dB[g]  = sum_m (s_g h[m,:])^T dY[m,:]
+//
+// With A stored [G, R, K] and B stored [G, R, N] the two directions are the same
+// two products: a narrow one that contracts a row of length L against P[g]
+// [R, L] (h and u), and a wide one that adds R terms of Q[g] [R, C] (to Y and
+// dX); dA and dB are one product too, [R, C] summed over an adapter's rows.
+//
+// A row's h, u, Y and dX read only its own operands and its own adapter, in an
+// order fixed by K, N and R: they do not depend on the other rows of the batch,
+// on their number, or on other requests' adapters (an infinity or NaN in one
+// adapter stays in its rows).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "abi_util.h"
+#include "adapter.h"
+
+namespace bi {
+namespace {
+
+template <typename T> __device__ __forceinline__ float up(T v);
+template <> __device__ __forceinline__ float up<float>(float v) { return v; }
+template <> __device__ __forceinline__ float up<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float up<__half>(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T down(float v);
+template <> __device__ __forceinline__ float down<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 down<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half down<__half>(float v) { return __float2half_rn(v); }
+
+// ---------------------------------------------------------------- plan
+
+// One block per 256-row tile, one thread per row.  Rows of a warp with the same
+// adapter are found by a match; the first of them stands for the group and
+// looks for its adapter among the groups of the warps before (then it is no
+// new entry), and gathers the masks of the warps after.
+__global__ void __launch_bounds__(256) adapter_plan_kernel(const uint32_t* ids, int64_t M, uint32_t G, AdapterPlan plan) {
+    __shared__ uint32_t s_id[256], s_mask[256];  // groups of warp w at [32 w, 32 w + s_n[w])
+    __shared__ uint32_t s_n[8], s_new[8];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 256 + tid;
+    const uint32_t id = row < M ? ids[row] : G;
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    const bool lead = id < G && (same & ((1u << lane) - 1)) == 0;
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    if (lead) {
+        const int k = 32 * warp + __popc(leads & ((1u << lane) - 1));
+        s_id[k] = id;
+        s_mask[k] = same;
+    }
+    if (lane == 0) s_n[warp] = __popc(leads);
+    __syncthreads();
+    uint32_t mask[8];
+    bool fresh = lead;
+    if (lead) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            mask[w] = 0;
+            for (uint32_t i = 0; i < s_n[w]; ++i)
+                if (s_id[32 * w + i] == id) {
+                    mask[w] = s_mask[32 * w + i];
+                    break;
+                }
+            if (w < warp && mask[w] != 0) fresh = false;
+        }
+    }
+    const uint32_t fr = __ballot_sync(0xffffffffu, fresh);
+    if (lane == 0) s_new[warp] = __popc(fr);
+    __syncthreads();
+    uint32_t at = __popc(fr & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) at += s_new[w];
+    if (fresh) {
+        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 256 + at;
+        plan.ids[slot] = id;
+        uint4* m = reinterpret_cast<uint4*>(plan.masks + slot * 8);
+        m[0] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+        m[1] = make_uint4(mask[4], mask[5], mask[6], mask[7]);
+    }
+    if (tid == 0) {
+        uint32_t n = 0;
+        for (int w = 0; w < 8; ++w) n += s_new[w];
+        plan.count[blockIdx.x] = n;
+    }
+}
+
+// Chunk tables of the sorted rows (AdapterChunks), one block.
+__global__ void __launch_bounds__(1024) adapter_chunks_kernel(const uint32_t* off, uint32_t G, AdapterChunks ch) {
+    __shared__ uint32_t s_a[32], s_b[32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t base_a = 0, base_b = 0;
+    for (uint32_t g0 = 0; g0 < G; g0 += 1024) {
+        const uint32_t g = g0 + tid;
+        const uint32_t n = g < G ? (off[g + 1] - off[g] + ADAPTER_CHUNK - 1) / ADAPTER_CHUNK : 0;
+        uint32_t a = n, b = n > 1 ? n : 0;
+        const uint32_t own_a = a, own_b = b;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t ya = __shfl_up_sync(0xffffffffu, a, o), yb = __shfl_up_sync(0xffffffffu, b, o);
+            if (lane >= o) { a += ya; b += yb; }
+        }
+        __syncthreads();
+        if (lane == 31) { s_a[warp] = a; s_b[warp] = b; }
+        __syncthreads();
+        uint32_t pa = base_a, pb = base_b;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) { pa += s_a[w]; pb += s_b[w]; }
+            base_a += s_a[w];
+            base_b += s_b[w];
+        }
+        if (g < G) {
+            ch.first[g] = pa + a - own_a;
+            ch.part[g] = pb + b - own_b;
+        }
+    }
+    if (tid == 0) {
+        ch.first[G] = base_a;
+        ch.part[G] = base_b;
+    }
+}
+
+// ---------------------------------------------------------------- narrow product, scalar
+
+// partial[piece][m][r] = sum over the piece's l ascending of X[m,l] P[g][r,l]
+// (one fmaf chain from +0).  A block has 16 rows and 16 ranks, one result per
+// thread; for each adapter among its rows it stages 64 steps of both operands.
+constexpr int NP_STEPS = 64;
+template <typename T>
+__global__ void __launch_bounds__(256)
+    narrow_scalar_kernel(const T* x, const T* p, AdapterPlan plan, float* partial, int64_t M, int64_t L, int R) {
+    __shared__ float s_x[16][NP_STEPS + 1], s_p[16][NP_STEPS + 1];
+    const int tid = threadIdx.x, i = tid >> 4, j = tid & 15;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, tile = m0 / ADAPTER_TILE;
+    const int r0 = blockIdx.y * 16, word = static_cast<int>(m0 % ADAPTER_TILE) / 32;
+    const int shift = static_cast<int>(m0 % 32);
+    const int64_t l0 = static_cast<int64_t>(blockIdx.z) * ADAPTER_PIECE, l1 = lmin(L, l0 + ADAPTER_PIECE);
+    const uint32_t n = plan.count[tile];
+    for (uint32_t e = 0; e < n; ++e) {
+        const uint32_t mask = (plan.masks[(tile * 256 + e) * 8 + word] >> shift) & 0xffffu;
+        if (mask == 0) continue;
+        const T* pg = p + static_cast<int64_t>(plan.ids[tile * 256 + e]) * R * L;
+        const bool mine = (mask >> i) & 1u;
+        float acc = 0.0f;
+        for (int64_t l = l0; l < l1; l += NP_STEPS) {
+            __syncthreads();
+            for (int q = tid; q < 16 * NP_STEPS; q += 256) {
+                const int a = q / NP_STEPS, s = q % NP_STEPS;
+                const bool in = l + s < l1;
+                s_x[a][s] = in && m0 + a < M ? up<T>(x[(m0 + a) * L + l + s]) : 0.0f;
+                s_p[a][s] = in && r0 + a < R ? up<T>(pg[static_cast<int64_t>(r0 + a) * L + l + s]) : 0.0f;
+            }
+            __syncthreads();
+            const int steps = static_cast<int>(lmin(NP_STEPS, l1 - l));
+            for (int s = 0; s < steps; ++s) acc = fmaf(s_x[i][s], s_p[j][s], acc);
+        }
+        if (mine && r0 + j < R) partial[(static_cast<int64_t>(blockIdx.z) * M + m0 + i) * R + r0 + j] = acc;
+    }
+}
+
+// v = the pieces' sums added in order (+0 for a row without adapter); h = v,
+// hs = s_g v (either nullable).
+__global__ void __launch_bounds__(256)
+    narrow_finish_kernel(const float* partial, const uint32_t* ids, const float* scales, float* h, float* hs,
+                         int64_t M, int R, uint32_t G, int pieces) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= M * R) return;
+    const uint32_t g = ids[i / R];
+    float v = 0.0f, s = 0.0f;
+    if (g < G) {
+        v = partial[i];
+        for (int q = 1; q < pieces; ++q) v += partial[static_cast<int64_t>(q) * M * R + i];
+        s = scales != nullptr ? v * scales[g] : v;
+    }
+    if (h != nullptr) h[i] = v;
+    if (hs != nullptr) hs[i] = s;
+}
+
+// hs = s_g h, 0 for a row without adapter.
+__global__ void __launch_bounds__(256) scale_rows_kernel(const float* h, const uint32_t* ids, const float* scales, float* hs, int64_t M,
+                                                         int R, uint32_t G) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= M * R) return;
+    const uint32_t g = ids[i / R];
+    hs[i] = g < G ? (scales != nullptr ? h[i] * scales[g] : h[i]) : 0.0f;
+}
+
+// ---------------------------------------------------------------- wide product, scalar
+
+// out[m,c] = round( base[m,c] + sum over r ascending of hs[m,r] Q[g][r,c] ), base
+// in f32 (for f32 it is out itself).  16 rows by 256 columns per block, a column
+// per thread: an element of Q is read once for all of the block's rows with
+// that adapter.
+template <typename T>
+__global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* base, const float* hs, const T* q,
+                                                          AdapterPlan plan, int64_t M, int64_t C, int R) {
+    extern __shared__ float s_h[];  // [R][16]
+    const int tid = threadIdx.x;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, tile = m0 / ADAPTER_TILE;
+    const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + tid;
+    const int word = static_cast<int>(m0 % ADAPTER_TILE) / 32, shift = static_cast<int>(m0 % 32);
+    for (int i = tid; i < 16 * R; i += 256) {
+        const int row = i / R, r = i % R;
+        s_h[r * 16 + row] = m0 + row < M ? hs[(m0 + row) * R + r] : 0.0f;
+    }
+    __syncthreads();
+    const uint32_t n = plan.count[tile];
+    uint32_t any = 0;
+    for (uint32_t e = 0; e < n; ++e) {
+        const uint32_t mask = (plan.masks[(tile * 256 + e) * 8 + word] >> shift) & 0xffffu;
+        if (mask == 0) continue;
+        any |= mask;
+        if (c >= C) continue;
+        const T* qg = q + static_cast<int64_t>(plan.ids[tile * 256 + e]) * R * C + c;
+        float acc[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+        for (int r = 0; r < R; ++r) {
+            const float v = up<T>(qg[static_cast<int64_t>(r) * C]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i] = fmaf(s_h[r * 16 + i], v, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if ((mask >> i) & 1u) out[(m0 + i) * C + c] = down<T>(base[(m0 + i) * C + c] + acc[i]);
+    }
+    if (c >= C || reinterpret_cast<const void*>(base) == reinterpret_cast<const void*>(out)) return;
+    for (int i = 0; i < 16; ++i)  // rows without adapter
+        if (!((any >> i) & 1u) && m0 + i < M) out[(m0 + i) * C + c] = down<T>(base[(m0 + i) * C + c]);
+}
+
+// ---------------------------------------------------------------- dA, dB, scalar
+
+// One block: one chunk of one adapter's sorted rows, 128 columns, 16 ranks;
+// a column per thread, out[r][c] = the chain over the chunk's rows ascending of
+// hs[m,r] Z[m,c].  Adapters of one chunk write out, others their partial slot.
+constexpr int GR_ROWS = 32;
+template <typename T>
+__global__ void __launch_bounds__(128)
+    grad_scalar_kernel(float* out, float* parts, const float* hs, const T* z, const uint32_t* off, const uint32_t* perm,
+                       AdapterChunks ch, int64_t C, int R, uint32_t G) {
+    __shared__ float s_h[GR_ROWS][16];
+    __shared__ uint32_t s_row[GR_ROWS];
+    const uint32_t chunk = blockIdx.x;
+    if (chunk >= ch.first[G]) return;
+    uint32_t lo = 0, hi = G - 1;  // the last g with first[g] <= chunk
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi + 1) >> 1;
+        if (ch.first[mid] <= chunk) lo = mid; else hi = mid - 1;
+    }
+    const uint32_t j = chunk - ch.first[lo], nchunks = ch.first[lo + 1] - ch.first[lo];
+    const uint32_t s0 = off[lo] + j * static_cast<uint32_t>(ADAPTER_CHUNK);
+    const uint32_t s1 = min(off[lo + 1], s0 + static_cast<uint32_t>(ADAPTER_CHUNK));
+    const int64_t c = static_cast<int64_t>(blockIdx.y) * 128 + threadIdx.x;
+    const int r0 = blockIdx.z * 16;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (uint32_t s = s0; s < s1; s += GR_ROWS) {
+        const int n = static_cast<int>(min(s1 - s, static_cast<uint32_t>(GR_ROWS)));
+        __syncthreads();
+        for (int i = threadIdx.x; i < GR_ROWS * 16; i += 128) {
+            const int a = i >> 4, b = i & 15;
+            s_h[a][b] = a < n && r0 + b < R ? hs[static_cast<int64_t>(perm[s + a]) * R + r0 + b] : 0.0f;
+        }
+        if (threadIdx.x < GR_ROWS) s_row[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? perm[s + threadIdx.x] : 0;
+        __syncthreads();
+        if (c < C) {
+#pragma unroll 4
+            for (int a = 0; a < n; ++a) {
+                const float v = up<T>(z[static_cast<int64_t>(s_row[a]) * C + c]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = fmaf(s_h[a][i], v, acc[i]);
+            }
+        }
+    }
+    if (c >= C) return;
+    float* dst = nchunks > 1 ? parts + static_cast<int64_t>(ch.part[lo] + j) * R * C : out + static_cast<int64_t>(lo) * R * C;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (r0 + i < R) dst[static_cast<int64_t>(r0 + i) * C + c] = acc[i];
+}
+
+// out[g] = the chunks' sums added in order; +0 for an adapter without rows.
+__global__ void __launch_bounds__(256) grad_sum_kernel(float* out, const float* parts, AdapterChunks ch, int64_t RC) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const uint32_t g = blockIdx.x;
+    const uint32_t n = ch.first[g + 1] - ch.first[g];
+    if (n == 1) return;
+    float* o = out + static_cast<int64_t>(g) * RC;
+    const float* p = parts + static_cast<int64_t>(ch.part[g]) * RC;
+    for (int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; i < RC; i += static_cast<int64_t>(gridDim.y) * 256) {
+        float v = 0.0f;
+        if (n > 1) {
+            v = p[i];
+            for (uint32_t j = 1; j < n; ++j) v += p[static_cast<int64_t>(j) * RC + i];
+        }
+        o[i] = v;
+    }
+}
+
+// ---------------------------------------------------------------- launchers
+
+cudaError_t launched(const LaunchCtx& c) {
+    c.count();
+    return cudaGetLastError();
+}
+
+cudaError_t build_plan(const LaunchCtx& c, const uint32_t* ids, int64_t M, int64_t G, const AdapterPlan& plan) {
+    const cudaError_t e = launch_pdl(adapter_plan_kernel, dim3(static_cast<unsigned>(AdapterPlan::tiles(M))), dim3(256), 0,
+                                     c.stream, ids, M, static_cast<uint32_t>(G), plan);
+    if (e == cudaSuccess) c.count();
+    return e;
+}
+
+unsigned grid1(int64_t n) { return static_cast<unsigned>((n + 255) / 256); }
+int pieces_of(int64_t L) { return static_cast<int>((L + ADAPTER_PIECE - 1) / ADAPTER_PIECE); }
+
+template <typename T>
+cudaError_t narrow_scalar(const LaunchCtx& c, const T* x, const T* p, const AdapterPlan& plan, float* partial, int64_t M,
+                          int64_t L, int R) {
+    const dim3 grid(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>((R + 15) / 16), static_cast<unsigned>(pieces_of(L)));
+    narrow_scalar_kernel<T><<<grid, 256, 0, c.stream>>>(x, p, plan, partial, M, L, R);
+    return launched(c);
+}
+
+template <typename T>
+cudaError_t wide_scalar(const LaunchCtx& c, T* out, const float* base, const float* hs, const T* q, const AdapterPlan& plan,
+                        int64_t M, int64_t C, int R) {
+    const dim3 grid(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>((C + 255) / 256));
+    wide_scalar_kernel<T><<<grid, 256, static_cast<size_t>(16 * R * 4), c.stream>>>(out, base, hs, q, plan, M, C, R);
+    return launched(c);
+}
+
+template <typename T>
+cudaError_t grad_scalar(const LaunchCtx& c, float* out, float* parts, const float* hs, const T* z, const uint32_t* seg,
+                        const uint32_t* perm, const AdapterChunks& ch, int64_t M, int64_t C, int R, int64_t G) {
+    const dim3 grid(static_cast<unsigned>(AdapterChunks::max_chunks(M, G)), static_cast<unsigned>((C + 127) / 128),
+                    static_cast<unsigned>((R + 15) / 16));
+    grad_scalar_kernel<T><<<grid, 128, 0, c.stream>>>(out, parts, hs, z, seg, perm, ch, C, R, static_cast<uint32_t>(G));
+    return launched(c);
+}
+
+cudaError_t grad_sum(const LaunchCtx& c, float* out, const float* parts, const AdapterChunks& ch, int64_t RC, int64_t G) {
+    const dim3 grid(static_cast<unsigned>(G), static_cast<unsigned>(lmin((RC + 255) / 256, 1024)));
+    const cudaError_t e = launch_pdl(grad_sum_kernel, grid, dim3(256), 0, c.stream, out, parts, ch, RC);
+    if (e == cudaSuccess) c.count();
+    return e;
+}
+
+// Calls f with a null pointer of dt's element type.
+template <typename F>
+cudaError_t with_type(bi_dtype dt, F&& f) {
+    return dt == BI_F32 ? f(static_cast<float*>(nullptr))
+         : dt == BI_BF16 ? f(static_cast<__nv_bfloat16*>(nullptr)) : f(static_cast<__half*>(nullptr));
+}
+
+bi_status check_adapter(bi_engine eng, bi_dtype dt, int64_t m, int64_t k, int64_t n, int64_t r, int64_t g) {
+    if (!eng) return fail(nullptr, BI_ERR_INVALID_ARG, "engine is NULL");
+    const char* why = "";
+    const bi_status st = check_sizes(dt, m, k, n, -1, &why);
+    if (st != BI_OK) return fail(eng, st, why);
+    if (r <= 0 || g <= 0) return fail(eng, BI_ERR_INVALID_ARG, "r and g must be > 0");
+    if (r > ADAPTER_MAX_RANK) return fail(eng, BI_ERR_UNSUPPORTED, "adapters are limited to rank 256");
+    if (g > 65535) return fail(eng, BI_ERR_UNSUPPORTED, "g is limited to 65535 adapters");
+    return BI_OK;
+}
+
+// Cuts of one scratch allocation.
+struct Cut {
+    int64_t at = 0;
+    int64_t take(int64_t bytes) {
+        const int64_t r = at;
+        at += round256(bytes);
+        return r;
+    }
+};
+
+}  // namespace
+}  // namespace bi
+
+using namespace bi;
+
+extern "C" {
+
+bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, const void* w, const void* bias,
+                             const void* a, const void* b, const float* scales, const uint32_t* row_adapters,
+                             int64_t m, int64_t k, int64_t n, int64_t r, int64_t g, bi_dtype dtype, void* stream,
+                             int tensor_cores) {
+    bi_status st = check_adapter(eng, dtype, m, k, n, r, g);
+    if (st != BI_OK) return st;
+    if (m == 0) return BI_OK;
+    if (!y || !x || !w || !a || !b || !row_adapters)
+        return fail(eng, BI_ERR_INVALID_ARG, "y, x, w, a, b and row_adapters must not be NULL");
+    DeviceGuard guard(eng->device);
+    if (!guard.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const LaunchCtx c = ctx(eng, stream);
+    const int R = static_cast<int>(r), pieces = pieces_of(k);
+    // scratch: plan | pieces of h | s h | the shared product in f32 (16-bit types)
+    Cut cut;
+    const int64_t o_plan = cut.take(AdapterPlan::words(m) * 4), o_part = cut.take(pieces * m * r * 4),
+                  o_hs = cut.take(m * r * 4), o_base = cut.take(dtype == BI_F32 ? 0 : m * n * 4);
+    Scratch sc(eng, s, static_cast<size_t>(cut.at));
+    if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "adapter scratch");
+    uint8_t* p = static_cast<uint8_t*>(sc.ptr);
+    const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
+    float* part = reinterpret_cast<float*>(p + o_part);
+    float* hs = reinterpret_cast<float*>(p + o_hs);
+    float* base = dtype == BI_F32 ? static_cast<float*>(y) : reinterpret_cast<float*>(p + o_base);
+    cudaError_t e = cudaSuccess;
+    // the shared product first: it may need scratch of its own, and a call that
+    // gets none must leave nothing enqueued
+    if (dtype == BI_F32) {
+        st = bi_forward(eng, y, x, w, bias, m, k, n, dtype, stream, tensor_cores);
+        if (st != BI_OK) return st;
+    } else {
+        e = scalar_rows(c, dtype, base, x, w, bias, m, k, n, 0, 1);
+    }
+    if (e == cudaSuccess) e = build_plan(c, row_adapters, m, g, plan);
+    if (e == cudaSuccess)
+        e = with_type(dtype, [&](auto* t) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            return narrow_scalar<T>(c, static_cast<const T*>(x), static_cast<const T*>(a), plan, part, m, k, R);
+        });
+    if (e == cudaSuccess) {
+        narrow_finish_kernel<<<grid1(m * r), 256, 0, s>>>(part, row_adapters, scales, h, hs, m, R, static_cast<uint32_t>(g), pieces);
+        e = launched(c);
+    }
+    if (e == cudaSuccess)
+        e = with_type(dtype, [&](auto* t) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            return wide_scalar<T>(c, static_cast<T*>(y), base, hs, static_cast<const T*>(b), plan, m, n, R);
+        });
+    return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
+}
+
+bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, const void* x, const float* h,
+                              const void* w, const void* dy, const void* a, const void* b, const float* scales,
+                              const uint32_t* row_adapters, int64_t m, int64_t k, int64_t n, int64_t r, int64_t g,
+                              bi_dtype dtype, void* stream, int tensor_cores) {
+    bi_status st = check_adapter(eng, dtype, m, k, n, r, g);
+    if (st != BI_OK) return st;
+    DeviceGuard guard(eng->device);
+    if (!guard.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (m == 0) {  // empty sums
+        cudaError_t e = da ? cudaMemsetAsync(da, 0, static_cast<size_t>(g * r * k * 4), s) : cudaSuccess;
+        if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, static_cast<size_t>(g * r * n * 4), s);
+        return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_backward");
+    }
+    if (!dx && !da && !db) return BI_OK;
+    if (!dy || !row_adapters || ((dx || da) && !b) || (dx && (!w || !a)) || (da && !x) || (db && !h))
+        return fail(eng, BI_ERR_INVALID_ARG, "an operand that a requested gradient needs is NULL");
+    const LaunchCtx c = ctx(eng, stream);
+    const int R = static_cast<int>(r), pieces = pieces_of(n);
+    const bool need_u = dx || da;
+    // scratch: plan | pieces of u | u | s h | sorted rows | chunk tables | chunk
+    // sums (of dA, then of dB) | the shared product in f32 (16-bit types)
+    Cut cut;
+    const int64_t o_plan = cut.take(need_u ? AdapterPlan::words(m) * 4 : 0), o_part = cut.take(need_u ? pieces * m * r * 4 : 0),
+                  o_u = cut.take(need_u ? m * r * 4 : 0), o_hs = cut.take(db ? m * r * 4 : 0);
+    const bool grads = da || db;
+    const int64_t o_seg = cut.take(grads ? seg_table_len(g) * 4 : 0), o_perm = cut.take(grads ? m * 4 : 0),
+                  o_hist = cut.take(grads ? segment_scratch_bytes(m, g) : 0),
+                  o_ch = cut.take(grads ? AdapterChunks::words(g) * 4 : 0),
+                  o_sum = cut.take(grads ? AdapterChunks::max_parts(m) * r * lmax(da ? k : 0, db ? n : 0) * 4 : 0),
+                  o_base = cut.take(dx && dtype != BI_F32 ? m * k * 4 : 0);
+    Scratch sc(eng, s, static_cast<size_t>(cut.at));
+    if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "adapter scratch");
+    uint8_t* p = static_cast<uint8_t*>(sc.ptr);
+    const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
+    float* part = reinterpret_cast<float*>(p + o_part);
+    float* u = reinterpret_cast<float*>(p + o_u);
+    float* hs = reinterpret_cast<float*>(p + o_hs);
+    uint32_t* seg = reinterpret_cast<uint32_t*>(p + o_seg);
+    uint32_t* perm = reinterpret_cast<uint32_t*>(p + o_perm);
+    const AdapterChunks ch = AdapterChunks::at(p + o_ch, g);
+    float* sums = reinterpret_cast<float*>(p + o_sum);
+    float* base = dtype == BI_F32 ? static_cast<float*>(dx) : reinterpret_cast<float*>(p + o_base);
+    const uint32_t G = static_cast<uint32_t>(g);
+    cudaError_t e = cudaSuccess;
+    if (dx && dtype == BI_F32) {  // first, as in the forward
+        st = bi_backward_dx(eng, dx, dy, w, m, k, n, dtype, stream, tensor_cores);
+        if (st != BI_OK) return st;
+    } else if (dx) {
+        e = scalar_rows(c, dtype, base, dy, w, nullptr, m, n, k, 1, 1);
+    }
+    if (e == cudaSuccess && need_u) {
+        e = build_plan(c, row_adapters, m, g, plan);
+        if (e == cudaSuccess)
+            e = with_type(dtype, [&](auto* t) {
+                using T = std::remove_pointer_t<decltype(t)>;
+                return narrow_scalar<T>(c, static_cast<const T*>(dy), static_cast<const T*>(b), plan, part, m, n, R);
+            });
+        if (e == cudaSuccess) {
+            narrow_finish_kernel<<<grid1(m * r), 256, 0, s>>>(part, row_adapters, scales, nullptr, u, m, R, G, pieces);
+            e = launched(c);
+        }
+    }
+    if (e == cudaSuccess && dx) {
+        e = with_type(dtype, [&](auto* t) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            return wide_scalar<T>(c, static_cast<T*>(dx), base, u, static_cast<const T*>(a), plan, m, k, R);
+        });
+    }
+    if (e == cudaSuccess && grads) {
+        e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
+        if (e == cudaSuccess) {
+            e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, G, ch);
+            if (e == cudaSuccess) c.count();
+        }
+        auto one = [&](float* out, const float* f, const void* z, int64_t C) {
+            cudaError_t err = with_type(dtype, [&](auto* t) {
+                using T = std::remove_pointer_t<decltype(t)>;
+                return grad_scalar<T>(c, out, sums, f, static_cast<const T*>(z), seg, perm, ch, m, C, R, g);
+            });
+            if (err == cudaSuccess) err = grad_sum(c, out, sums, ch, r * C, g);
+            return err;
+        };
+        if (e == cudaSuccess && da) e = one(da, u, x, k);
+        if (e == cudaSuccess && db) {
+            scale_rows_kernel<<<grid1(m * r), 256, 0, s>>>(h, row_adapters, scales, hs, m, R, G);
+            e = launched(c);
+            if (e == cudaSuccess) e = one(db, hs, dy, n);
+        }
+    }
+    return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_backward");
+}
+
+}  // extern "C"

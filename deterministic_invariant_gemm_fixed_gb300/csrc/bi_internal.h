@@ -87,8 +87,9 @@ struct LaunchCtx {
 // "rows" kernels: out[r, c] = down( chain_l A[r, l] * B(l, c) (+ bias[c]) ), A
 // contraction-contiguous [R, L]; B is [L, C] (b_contr_contig = 0) or [C, L] (1).
 // Grouped: rows come from expert segments (seg/perm), B advanced by expert.
+// out_f32 = 1 writes the chain (+ bias) in f32, unrounded.
 cudaError_t scalar_rows(const LaunchCtx& c, bi_dtype dt, void* out, const void* a, const void* b,
-                        const void* bias, int64_t R, int64_t L, int64_t C, int b_contr_contig);
+                        const void* bias, int64_t R, int64_t L, int64_t C, int b_contr_contig, int out_f32 = 0);
 cudaError_t scalar_rows_grouped(const LaunchCtx& c, bi_dtype dt, void* out, const void* a,
                                 const void* b, int64_t M, int64_t L, int64_t C, int64_t E,
                                 int b_contr_contig, const uint32_t* seg, const uint32_t* perm);

@@ -5,72 +5,19 @@
 #include <new>
 #include <string>
 
-#include "bi_internal.h"
+#include "abi_util.h"
 
 namespace {
 
 thread_local std::string tl_error;
 
-// Record an error on the engine (or on the calling thread) and return `st`.
-bi_status fail(bi_engine eng, bi_status st, const std::string& msg) {
-    if (eng) {
-        std::lock_guard<std::mutex> g(eng->mu);
-        eng->last_error = msg;
-    } else {
-        tl_error = msg;
-    }
-    return st;
-}
-
-bi_status cuda_fail(bi_engine eng, cudaError_t e, const char* where) {
-    return fail(eng, e == cudaErrorMemoryAllocation ? BI_ERR_OOM : BI_ERR_CUDA,
-                std::string(where) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t dsize(bi_dtype dt) { return dt == BI_F32 ? 4 : 2; }
-
-// Makes the engine's device current for the duration of a call, then restores.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
-// Stream-ordered scratch from the engine's pool, released in stream order.
-struct Scratch {
-    bi_engine eng;
-    cudaStream_t stream;
-    void* ptr = nullptr;
-    cudaError_t err = cudaSuccess;
-    Scratch(bi_engine e, cudaStream_t s, size_t bytes) : eng(e), stream(s) {
-        if (!bytes) return;
-        if (take_injected_failure(e)) {  // bi_engine_fail_allocations: fail as an exhausted pool would
-            err = cudaErrorMemoryAllocation;
-            return;
-        }
-        err = cudaMallocFromPoolAsync(&ptr, bytes, e->pool, s);
-    }
-    static bool take_injected_failure(bi_engine e) {
-        int64_t v = e->failing_allocs.load();
-        while (v != 0) {
-            if (v < 0) return true;
-            if (e->failing_allocs.compare_exchange_weak(v, v - 1)) return true;
-        }
-        return false;
-    }
-    ~Scratch() {
-        if (ptr) cudaFreeAsync(ptr, stream);
-    }
-};
+using bi::aligned16;
+using bi::ctx;
+using bi::cuda_fail;
+using bi::DeviceGuard;
+using bi::dsize;
+using bi::fail;
+using bi::Scratch;
 
 const int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
@@ -79,11 +26,6 @@ bi_status check_common(bi_engine eng, bi_dtype dt, int64_t m, int64_t k, int64_t
     const char* why = "";
     const bi_status st = bi::check_sizes(dt, m, k, n, -1, &why);
     return st == BI_OK ? BI_OK : fail(eng, st, why);
-}
-
-bi::LaunchCtx ctx(bi_engine eng, void* stream) {
-    return bi::LaunchCtx{eng, static_cast<cudaStream_t>(stream), eng->sm_count, eng->d_status,
-                         eng->wait_limit_ns};
 }
 
 // f32 operands on the tensor cores (3xTF32).  Each operand is a row-major
@@ -121,6 +63,21 @@ bi_status tf32x3(bi_engine eng, const bi::LaunchCtx& c, const Tf32Operand& a, co
 }  // namespace
 
 namespace bi {
+bi_status fail(bi_engine eng, bi_status st, const std::string& msg) {
+    if (eng) {
+        std::lock_guard<std::mutex> g(eng->mu);
+        eng->last_error = msg;
+    } else {
+        tl_error = msg;
+    }
+    return st;
+}
+
+bi_status cuda_fail(bi_engine eng, cudaError_t e, const char* where) {
+    return fail(eng, e == cudaErrorMemoryAllocation ? BI_ERR_OOM : BI_ERR_CUDA,
+                std::string(where) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
+}
+
 bi_status set_thread_error(bi_status st, const std::string& msg) { return fail(nullptr, st, msg); }
 
 bi_status check_sizes(bi_dtype dt, int64_t m, int64_t k, int64_t n, int64_t e, const char** why) {
@@ -466,7 +423,7 @@ cudaError_t build_grouping(const bi::LaunchCtx& c, const Grouping& src, int64_t 
     return bi::segment_from_offsets(c, src.offsets, m, e, seg, perm);
 }
 
-int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+using bi::round256;
 
 bi_status grouped_forward_impl(bi_engine eng, void* y, const void* x, const void* w, const Grouping& src,
                                int64_t m, int64_t k, int64_t n, int64_t e, bi_dtype dtype,

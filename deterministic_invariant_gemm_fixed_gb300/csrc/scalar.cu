@@ -232,7 +232,15 @@ struct RowsArgs {
     int64_t E;
     const uint32_t* seg;
     const uint32_t* perm;
+    int out_f32 = 0;    // dense: write the f32 result (bias added) unrounded
 };
+
+// Store one finished value: rounded to T, or in f32 (RowsArgs::out_f32).
+template <typename T>
+__device__ __forceinline__ void store_rows(const RowsArgs& p, int64_t i, float v) {
+    if (p.out_f32) static_cast<float*>(p.out)[i] = v;
+    else static_cast<T*>(p.out)[i] = Elem<T>::down(v);
+}
 
 // out[r, c] = down( chain_l a[r, l] * b(l, c) (+ bias[c]) )
 // TMV = tile height (128 or 64); 2*TMV threads, each owning 8 x 8 outputs.
@@ -445,7 +453,6 @@ __global__ void __launch_bounds__(2 * TMV, TMV == 128 ? 1 : (VEC ? 4 : 3)) scala
     }
 
     // epilogue: (+ bias), one rounding, store
-    T* out = static_cast<T*>(p.out);
     const T* bias = static_cast<const T*>(p.bias);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -458,7 +465,7 @@ __global__ void __launch_bounds__(2 * TMV, TMV == 128 ? 1 : (VEC ? 4 : 3)) scala
             if (c >= C) continue;
             float v = acc_lane(acc, i, j);
             if (bias) v = v + Elem<T>::up(bias[c]);
-            out[orow * C + c] = Elem<T>::down(v);
+            store_rows<T>(p, orow * C + c, v);
         }
     }
 }
@@ -677,7 +684,6 @@ __global__ void __launch_bounds__(NW_THREADS) scalar_rows_narrow_kernel(const Ro
     }
     const int64_t r = r0 + lane;
     if (!active || r >= R) return;
-    T* out = static_cast<T*>(p.out);
     const T* bias = static_cast<const T*>(p.bias);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(NW_THREADS) scalar_rows_narrow_kernel(const Ro
         if (c >= C) break;
         float v = __uint_as_float(static_cast<uint32_t>((j & 1) ? (acc[j >> 1] >> 32) : acc[j >> 1]));
         if (bias) v = v + Elem<T>::up(bias[c]);
-        out[r * C + c] = Elem<T>::down(v);
+        store_rows<T>(p, r * C + c, v);
     }
 }
 
@@ -1071,13 +1077,12 @@ __global__ void __launch_bounds__(32) scalar_rows_gemv_kernel(const RowsArgs p) 
     cp_async_wait<0>();
     const int64_t c = c0 + lane;
     if (c >= C) return;
-    T* out = static_cast<T*>(p.out);
     const T* bias = static_cast<const T*>(p.bias);
     const float bc = bias != nullptr ? Elem<T>::up(bias[c]) : 0.0f;
 #pragma unroll
     for (int r = 0; r < RR; ++r) {
         if (r >= R) break;
-        out[r * C + c] = Elem<T>::down(bias != nullptr ? __fadd_rn(acc[r], bc) : acc[r]);
+        store_rows<T>(p, r * C + c, bias != nullptr ? __fadd_rn(acc[r], bc) : acc[r]);
     }
 }
 
@@ -1445,8 +1450,8 @@ cudaError_t dw_narrow_t(const LaunchCtx& c, const DwArgs& a, int64_t chunks) {
 }
 
 cudaError_t scalar_rows(const LaunchCtx& c, bi_dtype dt, void* out, const void* a, const void* b,
-                        const void* bias, int64_t R, int64_t L, int64_t C, int b_contr_contig) {
-    RowsArgs args{out, a, b, bias, R, L, C, 0, nullptr, nullptr};
+                        const void* bias, int64_t R, int64_t L, int64_t C, int b_contr_contig, int out_f32) {
+    RowsArgs args{out, a, b, bias, R, L, C, 0, nullptr, nullptr, out_f32};
     if (C > NARROW_COLS && R <= SK_R) {  // a few rows: one lane per output column (the kernel changes no chain)
         switch (dt) {
             case BI_F32: if (gemv_ok<float>(args)) return rows_gemv_t<float>(c, args, b_contr_contig); break;

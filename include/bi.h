@@ -277,6 +277,99 @@ bi_status bi_grouped_forward_noalloc(void* y, const void* x, const void* w,
                                      const uint32_t* row_experts, int64_t m, int64_t k, int64_t n,
                                      int64_t e, bi_dtype dtype, void* stream);
 
+/* ---- Low-rank adapters of many requests beside a shared projection ------
+ *
+ *   h[m,:]  = X[m,:] * A[g]^T                       g = row_adapters[m], h [M,R] f32
+ *   Y[m,:]  = round( X[m,:] * W + bias + (s_g h[m,:]) * B[g] )
+ *   u[m,:]  = s_g dY[m,:] * B[g]^T
+ *   dX[m,:] = round( dY[m,:] * W^T + u[m,:] * A[g] )
+ *   dA[g]   = sum over rows m of g, of u[m,:]^T X[m,:]            [G,R,K] f32
+ *   dB[g]   = sum over rows m of g, of (s_g h[m,:])^T dY[m,:]     [G,R,N] f32
+ *
+ * X [M,K], W [K,N] and bias [N] (nullable) as in bi_forward; A [G,R,K] and
+ * B [G,R,N] have the operands' type; scales [G] f32 (nullable: all 1);
+ * row_adapters [M] u32, a row with an id >= G has no adapter (its h is +0 and
+ * its Y and dX are the shared projection's).  Rows need not be sorted, and an
+ * adapter may have none (its dA and dB are +0).  R <= 256, G <= 65535.
+ *
+ * h and u contract in pieces of 512 elements counted from 0, added in order in
+ * f32; the R terms are added to the row's f32 sum before its one rounding.  A
+ * row's h, Y and dX depend on that row, W, bias and its own adapter alone:
+ * they are bit-identical for any M and any other rows beside it, and an
+ * infinity or NaN in another adapter does not reach them.  dA and dB add an
+ * adapter's rows in ascending order in chunks of 1024, the chunks in order;
+ * run-to-run identical.  The tiers and their conditions are those of bi_forward
+ * (forward) and bi_backward_dx (backward).  On the tensor-core tier with 16-bit
+ * operands h and u enter the second product as two 16-bit parts (high part and
+ * remainder); with f16 a magnitude of s_g h or u beyond 65504 is not
+ * representable there and gives an infinity. */
+
+/* h (nullable) receives X A^T unscaled, which the backward's dB needs. */
+bi_status bi_adapter_forward(bi_engine engine, void* y, float* h, const void* x, const void* w, const void* bias,
+                             const void* a, const void* b, const float* scales, const uint32_t* row_adapters,
+                             int64_t m, int64_t k, int64_t n, int64_t r, int64_t g, bi_dtype dtype, void* stream,
+                             int tensor_cores);
+
+/* Any of dx, da, db may be NULL (not computed); only the operands of the
+ * gradients asked for are read: dX needs w, dy, a, b; dA needs x, dy, b; dB
+ * needs h, dy.  The shared W and bias have their own gradients in
+ * bi_backward_dw and bi_bias_grad.  m = 0 zeroes dA and dB. */
+bi_status bi_adapter_backward(bi_engine engine, void* dx, float* da, float* db, const void* x, const float* h,
+                              const void* w, const void* dy, const void* a, const void* b, const float* scales,
+                              const uint32_t* row_adapters, int64_t m, int64_t k, int64_t n, int64_t r, int64_t g,
+                              bi_dtype dtype, void* stream, int tensor_cores);
+
+/* ---- Router: expert choice, counts, balance loss ------------------------
+ *
+ *   p = softmax(logits[t,:]);  ids[t,:] = the k largest logits, largest first
+ *   (ties to the lowest index);  weights[t,j] = p[ids[t,j]], or with normalize
+ *   divided by their sum over the k choices
+ *   counts[e] = choices of expert e;  V = rows counted;  mean_prob[e] = mean of
+ *   p[:,e] over them;  loss = E * sum_e counts[e] / (k V) * mean_prob[e]
+ *
+ * logits [T,E] of dtype, E <= 1024, k <= min(E, 64); valid [T] u8 (nullable:
+ * all rows), a row with valid 0 is left out and its logits are not read.  A
+ * logit of -inf or NaN is never chosen.  A choice that a row cannot make (fewer
+ * than k such logits) has id E and weight 0, and so have all choices of a row
+ * left out; id E is a padding row for the grouped calls, which take ids as
+ * [T*k].  A row of -inf alone is left out too; a row with a NaN or +inf counts
+ * and its probabilities are NaN.  lse [T] f32 = log-sum-exp of the row (+inf
+ * for a row left out), for the backward.  counts [E] and rows [1] (= V) are
+ * u32, mean_prob [E], loss [1] and weights [T,k] f32.  V = 0 gives a loss of 0.
+ * Sums over rows are f32 in a fixed order (a function of T and E):
+ * bit-identical run to run. */
+bi_status bi_router_forward(bi_engine engine, uint32_t* ids, float* weights, uint32_t* counts, uint32_t* rows,
+                            float* mean_prob, float* loss, float* lse, const void* logits, const uint8_t* valid,
+                            int64_t t, int64_t e, int64_t k, int normalize, bi_dtype dtype, void* stream);
+
+/* dlogits [T,E] (dtype) from dweights [T,k] f32 (nullable: zero) and dloss [1]
+ * f32 (nullable: zero), with the forward's lse, ids, weights, counts and rows;
+ * counts carry no gradient.  A row left out gets +0. */
+bi_status bi_router_backward(bi_engine engine, void* dlogits, const void* logits, const float* lse,
+                             const uint32_t* ids, const float* weights, const uint32_t* counts, const uint32_t* rows,
+                             const float* dweights, const float* dloss, int64_t t, int64_t e, int64_t k,
+                             int normalize, bi_dtype dtype, void* stream);
+
+/* ---- Gradient norm and clipping over a set of tensors --------------------
+ *
+ * A set is n tensors: host arrays of n device pointers, element counts and
+ * dtypes (bi_dtype values; they may differ).  The arrays are read during the
+ * call only.  Tensors need the alignment of their element type; tensors that
+ * are 16-byte aligned are faster. */
+
+/* *norm = sqrt(sum of all squares), norm [1] f32 on the device.  Chunks of 32768
+ * elements are summed in f32 (again in f64 where f32's range does not hold
+ * their squares), the chunks in f64, all in a fixed order: bit-identical run
+ * to run.  An empty set has norm 0. */
+bi_status bi_grad_norm(bi_engine engine, float* norm, const void* const* tensors, const int64_t* counts,
+                       const int* dtypes, int64_t n, void* stream);
+
+/* dst[i] = round( src[i] * c ), c = *norm > max_norm ? max_norm / *norm : 1 (NaN
+ * for a NaN norm; 0 for an infinite one).  c = 1 copies the bits.  dst[i] may be
+ * src[i] itself (in place); otherwise no dst may overlap any src.  max_norm >= 0. */
+bi_status bi_grad_clip(bi_engine engine, void* const* dst, const void* const* src, const int64_t* counts,
+                       const int* dtypes, int64_t n, const float* norm, float max_norm, void* stream);
+
 /* ---- introspection ---------------------------------------------------- */
 
 /* The dispatcher's choice for a call: 0 = scalar tier, 1 = tensor-core tier.

@@ -1,0 +1,326 @@
+"""Low-rank adapters beside a shared projection, against a 64-bit implementation.
+
+Bounds, per element, with u = 2^-24 (f32's rounding), S the sum of the magnitudes
+of all products that enter the element (the inner products' magnitudes included),
+L the longest chain of additions behind it:
+
+* scalar tier and f32 inputs: any order of f32 additions is within L u S of the
+  exact value (first order); 4 more for the scale, the bias and the piece sums.
+* tensor-core tier: the framework's published 2e-6 S for an f32 accumulation,
+  taken twice where an inner product feeds an outer one; the inner product
+  enters the outer one as two 16-bit parts, which adds 2^-16 of its own terms
+  (bf16: two roundings to 8 bits; f16: 2^-22 of the value plus 2^-24 absolute).
+  3xTF32 (f32 inputs with tensor cores): the same 2e-6 S for the shared product.
+* a 16-bit result adds its own rounding, half an ulp.
+"""
+import numpy as np
+import pytest
+import torch
+
+import deterministic_invariant_gemm_fixed_gb300 as bi
+from helpers import ulp_of
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+TD = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def eng():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    e = bi.Engine(0)
+    yield e
+    e.close()
+
+
+def inputs(m, k, n, r, g, dtype, seed=0, order="runs", none=0.1, scales=True, bias=True):
+    rng = np.random.default_rng(seed)
+    def t(*shape, std=1.0):
+        return torch.from_numpy(rng.standard_normal(shape) * std).to(TD[dtype]).cuda()
+    ids = rng.integers(0, g, size=m)
+    if order == "runs":
+        ids = np.sort(ids)
+        ids = np.roll(ids, m // 3)
+    drop = rng.random(m) < none
+    ids[drop] = rng.choice([g, g + 5, 0x7FFFFFFF], size=int(drop.sum()))
+    return dict(x=t(m, k), w=t(k, n, std=k ** -0.5), bias=t(n) if bias else None, a=t(g, r, k, std=k ** -0.5), b=t(g, r, n, std=0.3),
+                dy=t(m, n), ids=torch.from_numpy(ids.astype(np.int32)).cuda(),
+                scales=torch.from_numpy((rng.integers(1, 9, size=g) / 4.0).astype(np.float32)).cuda() if scales else None,
+                m=m, k=k, n=n, r=r, g=g, dtype=dtype)
+
+
+def sizes(d):
+    return [d[v] for v in "mknrg"] + [d["dtype"]]
+
+
+def forward(eng, d, tc, stream=None):
+    y = torch.full((d["m"], d["n"]), float("nan"), dtype=TD[d["dtype"]], device="cuda")
+    h = torch.full((d["m"], d["r"]), float("nan"), dtype=torch.float32, device="cuda")
+    eng.adapter_forward(y, h, d["x"], d["w"], d["bias"], d["a"], d["b"], d["scales"], d["ids"], *sizes(d), stream, tc)
+    return y, h
+
+
+def backward(eng, d, h, tc, which=("dx", "da", "db")):
+    dx = torch.full((d["m"], d["k"]), float("nan"), dtype=TD[d["dtype"]], device="cuda") if "dx" in which else None
+    da = torch.full((d["g"], d["r"], d["k"]), float("nan"), dtype=torch.float32, device="cuda") if "da" in which else None
+    db = torch.full((d["g"], d["r"], d["n"]), float("nan"), dtype=torch.float32, device="cuda") if "db" in which else None
+    eng.adapter_backward(dx, da, db, d["x"], h, d["w"], d["dy"], d["a"], d["b"], d["scales"], d["ids"], *sizes(d),
+                         None, tc)
+    return dx, da, db
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def exact(d, h_in=None):
+    """All results and their magnitude sums in 64 bits."""
+    x, w, a, b, dy = (f64(d[v]) for v in ("x", "w", "a", "b", "dy"))
+    ids, g = d["ids"].cpu().numpy().view(np.uint32), d["g"]
+    s = f64(d["scales"]) if d["scales"] is not None else np.ones(g)
+    bias = f64(d["bias"]) if d["bias"] is not None else np.zeros(d["n"])
+    m, r = d["m"], d["r"]
+    o = {"h": np.zeros((m, r)), "h_s": np.zeros((m, r)), "y": x @ w + bias, "y_s": abs(x) @ abs(w) + abs(bias),
+         "dx": dy @ w.T, "dx_s": abs(dy) @ abs(w).T, "u": np.zeros((m, r)),
+         "da": np.zeros(a.shape), "da_s": np.zeros(a.shape), "db": np.zeros(b.shape), "db_s": np.zeros(b.shape),
+         "y_in": np.zeros((m, d["n"])), "dx_in": np.zeros((m, d["k"])), "most": 0}
+    for j in range(g):
+        q = np.flatnonzero(ids == j)
+        o["most"] = max(o["most"], len(q))
+        if not len(q):
+            continue
+        h, hs = x[q] @ a[j].T, abs(x[q]) @ abs(a[j]).T
+        o["h"][q], o["h_s"][q] = h, hs
+        o["y"][q] += s[j] * (h @ b[j])
+        o["y_s"][q] += s[j] * (hs @ abs(b[j]))
+        o["y_in"][q] = (s[j] * abs(h)) @ abs(b[j])
+        u, us = s[j] * (dy[q] @ b[j].T), s[j] * (abs(dy[q]) @ abs(b[j]).T)
+        o["dx"][q] += u @ a[j]
+        o["dx_s"][q] += us @ abs(a[j])
+        o["dx_in"][q] = abs(u) @ abs(a[j])
+        o["da"][j], o["da_s"][j] = u.T @ x[q], us.T @ abs(x[q])
+        hh = h if h_in is None else f64(h_in)[q]
+        o["db"][j], o["db_s"][j] = (s[j] * hh).T @ dy[q], (s[j] * abs(hh)).T @ abs(dy[q])
+    return o
+
+
+def close(got, want, scale, dtype, chain, tc, inner=None, floor=0.0):
+    got = f64(got)
+    tol = (4e-6 if tc else (chain + 4) * U) * scale + floor
+    if tc and inner is not None and dtype != "f32":
+        tol = tol + 2.0 ** -16 * inner
+        if dtype == "f16":
+            tol = tol + 2.0 ** -24 * 64
+    if dtype != "f32":
+        tol = tol + 0.5 * ulp_of(np.maximum(abs(got), abs(want)), dtype)
+    bad = ~(abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.size, float((abs(got - want) / np.maximum(tol, 1e-300)).max()))
+
+
+SHAPES = [  # m, k, n, r, g, order
+    (1, 64, 64, 1, 1, "runs"),
+    (1, 7, 5, 3, 2, "runs"),              # nothing aligned
+    (5, 72, 136, 4, 3, "random"),
+    (33, 1000, 200, 20, 40, "random"),    # more adapters than rows of some
+    (130, 520, 264, 16, 7, "runs"),       # the narrow product's second piece is 8 long
+    (300, 513, 129, 5, 6, "random"),      # odd rows: scalar tier whatever is asked
+    (257, 1024, 512, 64, 2, "runs"),
+    (515, 256, 320, 100, 300, "random"),  # more adapters than a tile's rows, rank over 64
+    (2100, 192, 128, 8, 2, "runs"),       # more than one chunk of rows per adapter
+    (1300, 64, 64, 33, 1, "random"),
+    (70, 128, 96, 256, 3, "runs"),        # the largest rank
+]
+
+
+@pytest.mark.parametrize("tc", [0, 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,k,n,r,g,order", SHAPES)
+def test_against_64_bits(eng, m, k, n, r, g, order, dtype, tc):
+    d = inputs(m, k, n, r, g, dtype, seed=m + k, order=order)
+    y, h = forward(eng, d, tc)
+    e = exact(d, h)
+    dx, da, db = backward(eng, d, h, tc)
+    eng.check()
+    chain = k + n + r + 16
+    close(h, e["h"], e["h_s"], "f32", k, tc)
+    close(y, e["y"], e["y_s"], dtype, chain, tc, e["y_in"])
+    close(dx, e["dx"], e["dx_s"], dtype, chain, tc, e["dx_in"])
+    rows = min(e["most"], 1024) + e["most"] // 1024
+    close(da, e["da"], e["da_s"], "f32", n + rows, tc)
+    close(db, e["db"], e["db_s"], "f32", rows, tc)
+
+
+@pytest.mark.parametrize("dtype,tc", [("f32", 0), ("f32", 1), ("bf16", 0), ("bf16", 1), ("f16", 1)])
+def test_rows_do_not_depend_on_the_batch(eng, dtype, tc):
+    """Every prefix, and a shuffled copy, gives each row the same bits; so does a second run."""
+    d = inputs(700, 1032, 328, 24, 9, dtype, seed=3, order="random")
+    y, h = forward(eng, d, tc)
+    dx, da, db = backward(eng, d, h, tc)
+    y2, h2 = forward(eng, d, tc)
+    dx2, da2, db2 = backward(eng, d, h, tc)
+    for p, q in ((y, y2), (h, h2), (dx, dx2), (da, da2), (db, db2)):
+        assert torch.equal(p, q)
+    for m in (1, 2, 17, 64, 65, 128, 129, 256, 300, 513):
+        e = dict(d, m=m, x=d["x"][:m].contiguous(), dy=d["dy"][:m].contiguous(), ids=d["ids"][:m].contiguous())
+        ye, he = forward(eng, e, tc)
+        dxe = backward(eng, e, he, tc, ("dx",))[0]
+        assert torch.equal(ye, y[:m]) and torch.equal(he, h[:m]) and torch.equal(dxe, dx[:m]), m
+    perm = torch.randperm(700, generator=torch.Generator().manual_seed(1)).cuda()
+    e = dict(d, x=d["x"][perm].contiguous(), dy=d["dy"][perm].contiguous(), ids=d["ids"][perm].contiguous())
+    ye, he = forward(eng, e, tc)
+    dxe = backward(eng, e, he, tc, ("dx",))[0]
+    assert torch.equal(ye, y[perm]) and torch.equal(he, h[perm]) and torch.equal(dxe, dx[perm])
+
+
+@pytest.mark.parametrize("dtype,tc", [("f32", 0), ("bf16", 0), ("bf16", 1), ("f16", 1)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_one_request_cannot_reach_another(eng, dtype, tc, bad):
+    """Infinities and NaN in one adapter, its rows and their gradients stay there, and in rows without adapter they stay there too."""
+    d = inputs(400, 264, 328, 16, 5, dtype, seed=5, order="random", none=0.2)
+    y, h = forward(eng, d, tc)
+    dx, da, db = backward(eng, d, h, tc)
+    ids = d["ids"].cpu().numpy().view(np.uint32)
+    hit = torch.from_numpy((ids == 2) | (ids >= 5)).cuda()
+    e = dict(d, x=d["x"].clone(), dy=d["dy"].clone(), a=d["a"].clone(), b=d["b"].clone())
+    e["x"][hit] = bad
+    e["dy"][hit] = bad
+    e["a"][2] = bad
+    e["b"][2] = bad
+    ye, he = forward(eng, e, tc)
+    dxe, dae, dbe = backward(eng, e, he, tc)
+    for p, q in ((y, ye), (h, he), (dx, dxe)):
+        assert torch.equal(p[~hit], q[~hit])
+    keep = torch.tensor([0, 1, 3, 4], device="cuda")
+    assert torch.equal(da[keep], dae[keep]) and torch.equal(db[keep], dbe[keep])
+    assert not torch.isfinite(ye[hit]).any()
+
+
+def test_rows_without_adapter_are_the_shared_projection(eng):
+    """No id in range: y and dx are the plain layer's, bit for bit, h, dA and dB are 0."""
+    for dtype, tc in (("f32", 0), ("f32", 1), ("bf16", 0)):
+        d = inputs(200, 136, 264, 8, 4, dtype, seed=6)
+        d["ids"].fill_(4)
+        y, h = forward(eng, d, tc)
+        dx, da, db = backward(eng, d, h, tc)
+        y0, dx0 = torch.empty_like(y), torch.empty_like(dx)
+        eng.forward(y0, d["x"], d["w"], d["bias"], d["m"], d["k"], d["n"], dtype, None, tc)
+        eng.backward_dx(dx0, d["dy"], d["w"], d["m"], d["k"], d["n"], dtype, None, tc)
+        assert torch.equal(y, y0) and torch.equal(dx, dx0)
+        assert not h.any() and not da.any() and not db.any()
+
+
+@pytest.mark.parametrize("dtype,tc", [("f32", 0), ("bf16", 1)])
+def test_gradients_against_differences(eng, dtype, tc):
+    """sum(Y * dY) is linear in A and in B each, so a central difference of any step is its derivative up to rounding."""
+    d = inputs(96, 128, 192, 8, 3, dtype, seed=7, order="random")
+    y, h = forward(eng, d, tc)
+    e = exact(d)
+    dx, da, db = backward(eng, d, h, tc)
+    dy = f64(d["dy"])
+    ulp = ulp_of(np.abs(e["y"]) + 2 * e["y_in"], dtype) if dtype != "f32" else 0.0
+    for name, got in (("a", da), ("b", db)):
+        for idx in ((0, 0, 0), (1, 3, 77), (2, 7, 127)):
+            up_, dn = d[name].clone(), d[name].clone()
+            up_[idx] += 1
+            dn[idx] -= 1
+            step = float(up_[idx].double() - dn[idx].double())
+            hi, lo = f64(forward(eng, dict(d, **{name: up_}), tc)[0]), f64(forward(eng, dict(d, **{name: dn}), tc)[0])
+            diff = float(((hi - lo) * dy).sum()) / step
+            rows = (d["ids"] == idx[0]).cpu().numpy()
+            # each of hi, lo is off by a bound of y's at that row; S grows by the perturbed term
+            grow = e["y_s"] + 4 * (abs(f64(d["x"])).max() * abs(f64(d["b"])).max() + e["h_s"].max())
+            tol = float((np.abs(dy) * (8e-6 * grow + 2.0 ** -15 * grow * (tc == 1) + ulp))[rows].sum()) * 2 / step
+            assert abs(diff - float(got[idx])) <= tol, (name, idx, diff, float(got[idx]), tol)
+
+
+def test_parts_are_optional(eng):
+    for dtype, tc in (("f32", 1), ("bf16", 1), ("bf16", 0)):
+        d = inputs(150, 136, 264, 8, 4, dtype, seed=8, scales=False, bias=False)
+        y, h = forward(eng, d, tc)
+        y2 = torch.empty_like(y)
+        eng.adapter_forward(y2, None, d["x"], d["w"], None, d["a"], d["b"], None, d["ids"], *sizes(d), None, tc)
+        assert torch.equal(y, y2)
+        ones = dict(d, scales=torch.ones(4, device="cuda"))
+        assert torch.equal(forward(eng, ones, tc)[0], y)
+        full = backward(eng, d, h, tc)
+        for i, name in enumerate(("dx", "da", "db")):
+            got = backward(eng, d, h, tc, (name,))
+            assert torch.equal(got[i], full[i]) and all(v is None for j, v in enumerate(got) if j != i)
+
+
+def test_empty_batch_and_refusals(eng):
+    d = inputs(4, 64, 64, 4, 2, "bf16")
+    y, h = forward(eng, d, 1)
+    none = dict(d, m=0)
+    _, da, db = backward(eng, none, h, 1)
+    assert not da.any() and not db.any()
+    eng.adapter_forward(y, h, d["x"], d["w"], None, d["a"], d["b"], None, d["ids"], *sizes(none))
+    def status(**change):
+        q = dict(d, **change)
+        return bi.bi_adapter_forward(eng.handle, y, h, q["x"], q["w"], None, q["a"], q["b"], None, q["ids"], *sizes(q))
+    assert status() == bi.BI_OK
+    for change in (dict(r=0), dict(g=0), dict(k=0), dict(n=0), dict(m=-1), dict(dtype=7), dict(x=None), dict(w=None),
+                   dict(a=None), dict(b=None), dict(ids=None)):
+        assert status(**change) == bi.BI_ERR_INVALID_ARG, change
+    assert status(r=257) == bi.BI_ERR_UNSUPPORTED and status(g=65536) == bi.BI_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):
+        status(a=d["a"].transpose(1, 2))
+    with pytest.raises(bi.BiError):
+        eng.adapter_backward(y, None, None, None, None, d["w"], None, d["a"], d["b"], None, d["ids"], *sizes(d))
+    assert bi.bi_adapter_forward(None, *[16] * 9, 1, 1, 1, 1, 1, "bf16", 0) == bi.BI_ERR_INVALID_ARG
+
+
+def test_no_scratch_leaves_outputs_alone(eng):
+    for dtype, tc in (("f32", 1), ("bf16", 1), ("bf16", 0)):
+        d = inputs(64, 64, 64, 4, 2, dtype)
+        want, h0 = forward(eng, d, tc)
+        y, h = torch.zeros_like(want), torch.zeros_like(h0)
+        args = (y, h, d["x"], d["w"], d["bias"], d["a"], d["b"], d["scales"], d["ids"], *sizes(d), None, tc)
+        for nth in (1, -1):
+            bi.bi_engine_fail_allocations(eng.handle, nth)
+            assert bi.bi_adapter_forward(eng.handle, *args) == bi.BI_ERR_OOM
+            bi.bi_engine_fail_allocations(eng.handle, 0)
+            assert not y.any() and not h.any()
+        eng.adapter_forward(*args)
+        assert torch.equal(y, want)
+
+
+def test_side_stream_and_graph(eng):
+    d = inputs(40, 256, 320, 16, 6, "bf16", seed=9, order="random")
+    y, h = forward(eng, d, 1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        y2, h2 = forward(eng, d, 1)
+    s.synchronize()
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    y3, h3 = torch.zeros_like(y), torch.zeros_like(h)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        eng.adapter_forward(y3, h3, d["x"], d["w"], d["bias"], d["a"], d["b"], d["scales"], d["ids"], *sizes(d))
+    for _ in range(2):
+        y3.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y3, y)
+
+
+@pytest.mark.parametrize("dtype,tc", [("f32", 0), ("bf16", 0), ("bf16", 1), ("f16", 1)])
+def test_nothing_is_written_outside_the_outputs(eng, dtype, tc):
+    """Poisoned bands around every output of ragged shapes stay as they were."""
+    d = inputs(133, 136, 200, 12, 5, dtype, seed=10, order="random")
+    pad = 64
+    outs = {}
+    for name, shape, t in (("y", (133, 200), TD[dtype]), ("h", (133, 12), torch.float32), ("dx", (133, 136), TD[dtype]),
+                           ("da", (5, 12, 136), torch.float32), ("db", (5, 12, 200), torch.float32)):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 2 * pad,), 7.0, dtype=t, device="cuda")
+        outs[name] = (buf, buf[pad:pad + n].view(shape))
+    eng.adapter_forward(outs["y"][1], outs["h"][1], d["x"], d["w"], d["bias"], d["a"], d["b"], d["scales"], d["ids"],
+                        *sizes(d), None, tc)
+    eng.adapter_backward(outs["dx"][1], outs["da"][1], outs["db"][1], d["x"], outs["h"][1], d["w"], d["dy"], d["a"], d["b"],
+                         d["scales"], d["ids"], *sizes(d), None, tc)
+    torch.cuda.synchronize()
+    for buf, _ in outs.values():
+        assert bool((buf[:pad] == 7).all() and (buf[-pad:] == 7).all())
