@@ -19,6 +19,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "abi_util.h"
 #include "adapter.h"
 
@@ -181,6 +183,71 @@ __global__ void __launch_bounds__(256)
     }
     if (h != nullptr) h[i] = v;
     if (hs != nullptr) hs[i] = s;
+}
+
+// The same for the tensor cores: v = the pieces' sums (row stride rp), or h_in;
+// h = v; then s_g v in two parts (hh, for the wide product) and in four (v4, for
+// dA and dB), any of them nullable.  A part that would be an infinity's
+// remainder is 0, so an infinity stays one.  One thread per row and rank up to
+// `width`, which covers both formats' padding (zeros).
+template <typename T>
+__device__ __forceinline__ float part_rest(float v, T hi, float scale) {
+    const float h = up<T>(hi) * scale;
+    return isinf(h) ? 0.0f : v - h;
+}
+template <typename T>
+__global__ void __launch_bounds__(256)
+    narrow_finish_tc_kernel(const float* partial, const float* h_in, const uint32_t* ids, const float* scales, float* h,
+                            T* hh, T* v4, int64_t M, int R, int rp, uint32_t G, int pieces, int width) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= M * width) return;
+    const int64_t m = i / width;
+    const int r = static_cast<int>(i - m * width);
+    const uint32_t g = ids[m];
+    float v = 0.0f, s = 0.0f;
+    if (g < G && r < R) {
+        if (partial != nullptr) {
+            const float* p = partial + m * rp + r;
+            v = *p;
+#pragma unroll 8
+            for (int q = 1; q < pieces; ++q) v += p[static_cast<int64_t>(q) * M * rp];
+        } else {
+            v = h_in[m * R + r];
+        }
+        s = scales != nullptr ? v * scales[g] : v;
+    }
+    if (h != nullptr && r < R) h[m * R + r] = v;
+    if (hh != nullptr && r < (R + 31) / 32 * 32) {
+        const T hi = down<T>(s);
+        T* o = hh + m * ((R + 31) / 32 * 64) + (r / 32) * 64 + r % 32;
+        o[0] = hi;
+        o[32] = down<T>(part_rest<T>(s, hi, 1.0f));
+    }
+    const int run = adapter_rank_run(R);
+    if (v4 != nullptr && r < (R + 63) / 64 * run) {
+        T part[4];
+        part[0] = down<T>(0.0f);
+        if (std::is_same<T, __half>::value) {  // see adapter.h
+            float rest = s, scale = 0x1p11f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i, scale *= 0x1p-11f) {
+                const float x = rest * (1.0f / scale);
+                const bool none = i == 0 ? !(fabsf(s) > 65504.0f) : (i < 3 && fabsf(x) < 0x1p-14f);
+                part[i] = down<T>(none ? 0.0f : x);
+                rest = none ? rest : part_rest<T>(rest, part[i], scale);
+            }
+        } else {
+            part[1] = down<T>(s);
+            const float r1 = part_rest<T>(s, part[1], 1.0f);
+            part[2] = down<T>(r1);
+            part[3] = down<T>(part_rest<T>(r1, part[2], 1.0f));
+        }
+        T* o = v4 + m * adapter_grad_cols(R) + (r / 64) * 256 + r % 64;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i * run] = part[i];
+    }
 }
 
 // hs = s_g h, 0 for a row without adapter.
@@ -356,6 +423,22 @@ cudaError_t grad_sum(const LaunchCtx& c, float* out, const float* parts, const A
     return e;
 }
 
+cudaError_t narrow_finish_tc(const LaunchCtx& c, bi_dtype dt, const float* partial, const float* h_in, const uint32_t* ids,
+                             const float* scales, float* h, void* hh, void* v4, int64_t M, int R, int64_t G, int pieces) {
+    const int rp = (R + 15) / 16 * 16;
+    const int width = static_cast<int>(lmax(hh ? (R + 31) / 32 * 32 : R, v4 ? (R + 63) / 64 * adapter_rank_run(R) : R));
+    const dim3 grid(static_cast<unsigned>((M * width + 255) / 256));
+    const cudaError_t e =
+        dt == BI_BF16 ? launch_pdl(narrow_finish_tc_kernel<__nv_bfloat16>, grid, dim3(256), 0, c.stream, partial, h_in, ids, scales,
+                                   h, static_cast<__nv_bfloat16*>(hh), static_cast<__nv_bfloat16*>(v4), M, R, rp,
+                                   static_cast<uint32_t>(G), pieces, width)
+                      : launch_pdl(narrow_finish_tc_kernel<__half>, grid, dim3(256), 0, c.stream, partial, h_in, ids, scales, h,
+                                   static_cast<__half*>(hh), static_cast<__half*>(v4), M, R, rp, static_cast<uint32_t>(G), pieces,
+                                   width);
+    if (e == cudaSuccess) c.count();
+    return e;
+}
+
 // Calls f with a null pointer of dt's element type.
 template <typename F>
 cudaError_t with_type(bi_dtype dt, F&& f) {
@@ -400,11 +483,32 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
     if (m == 0) return BI_OK;
     if (!y || !x || !w || !a || !b || !row_adapters)
         return fail(eng, BI_ERR_INVALID_ARG, "y, x, w, a, b and row_adapters must not be NULL");
+    // (f32 takes its tier in the shared product; the adapters' terms are f32 FMAs)
+    const int tier = dtype != BI_F32 && bi_dispatch_tier(BI_PASS_FORWARD, dtype, tensor_cores, k, n);
+    if (tier && (!aligned16(y) || !aligned16(x) || !aligned16(w) || !aligned16(a) || !aligned16(b)))
+        return fail(eng, BI_ERR_MISALIGNED, "tensor-core tier needs 16-byte aligned y, x, w, a, b");
     DeviceGuard guard(eng->device);
     if (!guard.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const LaunchCtx c = ctx(eng, stream);
     const int R = static_cast<int>(r), pieces = pieces_of(k);
+    if (tier) {
+        // scratch: plan | pieces of h | s h in two parts
+        Cut cut;
+        const int64_t o_plan = cut.take(AdapterPlan::words(m) * 4), o_part = cut.take(pieces * m * ((r + 15) / 16 * 16) * 4),
+                      o_hh = cut.take(m * adapter_part_cols(r) * 2);
+        Scratch sc(eng, s, static_cast<size_t>(cut.at));
+        if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "adapter scratch");
+        uint8_t* p = static_cast<uint8_t*>(sc.ptr);
+        const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
+        float* part = reinterpret_cast<float*>(p + o_part);
+        cudaError_t e = build_plan(c, row_adapters, m, g, plan);
+        if (e == cudaSuccess) e = tc_adapter_narrow(c, dtype, part, x, a, plan, m, k, R, g);
+        if (e == cudaSuccess)
+            e = narrow_finish_tc(c, dtype, part, nullptr, row_adapters, scales, h, p + o_hh, nullptr, m, R, g, pieces);
+        if (e == cudaSuccess) e = tc_adapter_rows(c, dtype, 0, y, x, w, bias, p + o_hh, b, plan, m, k, n, R, g);
+        return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
+    }
     // scratch: plan | pieces of h | s h | the shared product in f32 (16-bit types)
     Cut cut;
     const int64_t o_plan = cut.take(AdapterPlan::words(m) * 4), o_part = cut.take(pieces * m * r * 4),
@@ -463,6 +567,59 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     const LaunchCtx c = ctx(eng, stream);
     const int R = static_cast<int>(r), pieces = pieces_of(n);
     const bool need_u = dx || da;
+    const int tier = dtype != BI_F32 && bi_dispatch_tier(BI_PASS_DX, dtype, tensor_cores, k, n);
+    if (tier) {
+        if (!aligned16(dy) || (need_u && !aligned16(b)) || (da && !aligned16(x)) ||
+            (dx && (!aligned16(dx) || !aligned16(w) || !aligned16(a))))
+            return fail(eng, BI_ERR_MISALIGNED, "tensor-core tier needs 16-byte aligned dx, x, w, dy, a, b");
+        // scratch: plan | pieces of u | u in two parts | u, s h in four parts |
+        // sorted rows | chunk tables | chunk sums (of dA, then of dB)
+        const bool grads = da || db;
+        Cut cut;
+        const int64_t o_plan = cut.take(need_u ? AdapterPlan::words(m) * 4 : 0),
+                      o_part = cut.take(need_u ? pieces * m * ((r + 15) / 16 * 16) * 4 : 0),
+                      o_uu = cut.take(dx ? m * adapter_part_cols(r) * 2 : 0),
+                      o_u3 = cut.take(da ? m * adapter_grad_cols(R) * 2 : 0), o_h3 = cut.take(db ? m * adapter_grad_cols(R) * 2 : 0),
+                      o_seg = cut.take(grads ? seg_table_len(g) * 4 : 0), o_perm = cut.take(grads ? m * 4 : 0),
+                      o_hist = cut.take(grads ? segment_scratch_bytes(m, g) : 0),
+                      o_ch = cut.take(grads ? AdapterChunks::words(g) * 4 : 0),
+                      o_sum = cut.take(grads ? AdapterChunks::max_parts(m) * r * lmax(da ? k : 0, db ? n : 0) * 4 : 0);
+        Scratch sc(eng, s, static_cast<size_t>(cut.at));
+        if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "adapter scratch");
+        uint8_t* p = static_cast<uint8_t*>(sc.ptr);
+        const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
+        float* part = reinterpret_cast<float*>(p + o_part);
+        uint32_t* seg = reinterpret_cast<uint32_t*>(p + o_seg);
+        uint32_t* perm = reinterpret_cast<uint32_t*>(p + o_perm);
+        const AdapterChunks ch = AdapterChunks::at(p + o_ch, g);
+        float* sums = reinterpret_cast<float*>(p + o_sum);
+        cudaError_t e = cudaSuccess;
+        if (need_u) {
+            e = build_plan(c, row_adapters, m, g, plan);
+            if (e == cudaSuccess) e = tc_adapter_narrow(c, dtype, part, dy, b, plan, m, n, R, g);
+            if (e == cudaSuccess)
+                e = narrow_finish_tc(c, dtype, part, nullptr, row_adapters, scales, nullptr, dx ? p + o_uu : nullptr,
+                                     da ? p + o_u3 : nullptr, m, R, g, pieces);
+        }
+        if (e == cudaSuccess && dx) e = tc_adapter_rows(c, dtype, 1, dx, dy, w, nullptr, p + o_uu, a, plan, m, k, n, R, g);
+        if (e == cudaSuccess && grads) {
+            e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
+            if (e == cudaSuccess) {
+                e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, static_cast<uint32_t>(g), ch);
+                if (e == cudaSuccess) c.count();
+            }
+        }
+        if (e == cudaSuccess && da) {
+            e = tc_adapter_grad(c, dtype, da, sums, p + o_u3, x, seg, perm, ch, m, k, R, g);
+            if (e == cudaSuccess) e = grad_sum(c, da, sums, ch, r * k, g);
+        }
+        if (e == cudaSuccess && db) {
+            e = narrow_finish_tc(c, dtype, nullptr, h, row_adapters, scales, nullptr, nullptr, p + o_h3, m, R, g, 0);
+            if (e == cudaSuccess) e = tc_adapter_grad(c, dtype, db, sums, p + o_h3, dy, seg, perm, ch, m, n, R, g);
+            if (e == cudaSuccess) e = grad_sum(c, db, sums, ch, r * n, g);
+        }
+        return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_backward");
+    }
     // scratch: plan | pieces of u | u | s h | sorted rows | chunk tables | chunk
     // sums (of dA, then of dB) | the shared product in f32 (16-bit types)
     Cut cut;

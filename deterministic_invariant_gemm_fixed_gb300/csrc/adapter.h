@@ -52,4 +52,34 @@ struct AdapterChunks {
     static int64_t max_parts(int64_t M) { return 2 * (M / ADAPTER_CHUNK); }
 };
 
+// Tensor-core formats of an inner product v (h or u, scaled), 16-bit.
+// Two parts, for the wide product: row m holds per 32 ranks 32 high parts and 32
+// remainders, v ~ hi + lo (bf16: to 2^-17 of v, f16: to 2^-22 or 2^-25).
+inline int64_t adapter_part_cols(int64_t R) { return (R + 31) / 32 * 64; }
+// Four parts, for dA and dB: row m holds per 64 ranks four runs of rank_run
+// columns whose products are summed apart.  bf16: v = p1 + p2 + p3, together f32's
+// 24 bits (p0 = 0).  f16, whose exponent is narrow: v = 2^11 p0 + p1 + 2^-11 p2 +
+// 2^-22 p3, p0 for magnitudes beyond 65504 only (up to 2^27); a part that would be
+// subnormal is 0 and its value left to the next one, because the tensor core
+// aligns a sum's products by exponents that a subnormal factor overstates (a
+// part of 2^-24 took the sum's last bits with it: 2^-17 of the result).
+__host__ __device__ inline int adapter_rank_run(int R) { return R > 64 ? 64 : (R + 15) / 16 * 16; }
+__host__ __device__ inline int64_t adapter_grad_cols(int R) { return (R + 63) / 64 * 4 * adapter_rank_run(R); }
+
+// The wide product on the tensor cores: forward (dx = 0) or dX with the shared
+// product, its bias and the adapters' terms in one pass (tc.cu).
+cudaError_t tc_adapter_rows(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
+                            const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
+                            int64_t K, int64_t N, int R, int64_t G);
+// The narrow product on the tensor cores (adapter_tc.cu): partial[piece][m][rp] =
+// the piece's sum of z[m,l] p[g][r,l], rp = R rounded up to 16 the row stride.
+cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, const void* z, const void* p,
+                              const AdapterPlan& plan, int64_t M, int64_t L, int R, int64_t G);
+// dA and dB on the tensor cores: out[g][r,c] (or its chunks' partial slots) =
+// sum over the adapter's sorted rows of v[m,r] z[m,c], v in four parts [M,
+// adapter_grad_cols(R)].
+cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, float* out, float* parts, const void* v4, const void* z,
+                            const uint32_t* off, const uint32_t* perm, const AdapterChunks& ch, int64_t M, int64_t C,
+                            int R, int64_t G);
+
 }  // namespace bi

@@ -1,0 +1,503 @@
+// Low-rank adapters on the tensor cores: the narrow product (h and u) and the
+// adapters' gradients.  The wide product runs inside the projection's own kernel
+// (tc.cu, mode ADAPTER).
+#include "adapter.h"
+#include "tc_common.cuh"
+
+namespace bi {
+namespace {
+
+constexpr int BK = 64;  // contraction block: one 128-byte swizzle row of 16-bit data
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(COLS) : "memory");
+}
+// kind::f16, f32 accumulation, M = 128; format 0 f16, 1 bf16.
+__device__ __forceinline__ uint32_t instr_desc(int fmt, bool a_mn, bool b_mn, int n) {
+    const uint32_t f = static_cast<uint32_t>(fmt);
+    return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// A producer that gives up waits (a bounded number of tries) for the copies it
+// has issued before its CTA's shared memory goes away: the last min(issued,
+// stages) fills, fill f on stage f % stages in phase f / stages.
+template <typename Bar>
+__device__ __forceinline__ void drain_copies(Bar&& full_bar, int issued, int stages) {
+    for (int f = max(0, issued - stages); f < issued; ++f)
+        for (int i = 0; i < (1 << 20) && !mbar_try_wait(full_bar(f % stages), (f / stages) & 1); ++i) {}
+}
+
+// ---------------------------------------------------------------- narrow product
+//
+// A CTA takes 128 rows and one 512-element piece of the contraction, and for
+// these the adapters among its rows, four groups of 16 ranks (64 accumulator
+// columns) at a time: D [128 rows x 64] += X [128 x 64] P^T, P the groups' rows
+// stacked.  Every row is multiplied with every adapter of the tile, and reads
+// back its own adapter's columns; the other products are thrown away.  They are
+// free: the pass is bound by reading X once (8192 rows of 4096: 67 MB, 10 us at
+// the copy rate) and the tensor cores idle beside it, while sorting the rows
+// first would read and write X once more.  128 rows x 512 elements is a unit
+// small enough that a batch of 8192 rows gives 512 of them, and one of 64 rows
+// with an own adapter each 128.
+//
+// Roles: warp 0 TMA, warp 1 MMA, warps 2-5 epilogue; two CTAs per SM, so one
+// CTA's set-up and drain run beside the other's loads.
+constexpr int NP_THREADS = 192, NP_STAGES = 4;
+constexpr int NP_A = 128 * 128, NP_B = 64 * 128, NP_STAGE = NP_A + NP_B;
+constexpr int NP_BARS = 2 * NP_STAGES + 5;
+constexpr int NP_SMEM = 1024 + NP_STAGES * NP_STAGE + NP_BARS * 8 + 16 + 128 * 8 + 256;
+constexpr int NP_KB = static_cast<int>(ADAPTER_PIECE / BK);
+
+struct NarrowParams {
+    AdapterPlan plan;
+    float* partial;
+    int64_t M;
+    int R, rp, num_kb, fmt;
+    int* status;
+    unsigned long long wait_limit;
+};
+
+__global__ void __launch_bounds__(NP_THREADS, 2)
+    narrow_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmP, const NarrowParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NP_STAGES * NP_STAGE);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (NP_STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * NP_STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * NP_STAGES + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * NP_STAGES + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NP_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint32_t* s_count = tmem_slot + 2;
+    uint32_t* s_ent = tmem_slot + 4;  // the tile's entries with a row in this half: plan slot
+    uint32_t* s_id = s_ent + 128;     // ... and adapter
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t tile = blockIdx.x >> 1;
+    const int half = blockIdx.x & 1;
+    const int row0 = static_cast<int>(blockIdx.x) * 128;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NP_STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), 4);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<128>(smem_u32(tmem_slot));
+    tc_fence_before();
+    __syncthreads();  // this CTA has its TMEM before a dependent kernel may start and ask for some
+    tc_fence_after();
+    grid_dep_wait();
+    grid_dep_launch();
+    if (warp == 2) {
+        const uint32_t n = p.plan.count[tile];
+        uint32_t total = 0;
+        for (uint32_t i0 = 0; i0 < n; i0 += 32) {
+            const uint32_t i = i0 + lane;
+            bool has = false;
+            if (i < n) {
+                const uint4 m = *reinterpret_cast<const uint4*>(p.plan.masks + (tile * ADAPTER_TILE + i) * 8 + 4 * half);
+                has = (m.x | m.y | m.z | m.w) != 0;
+            }
+            const uint32_t b = __ballot_sync(0xffffffffu, has);
+            if (has) {
+                const uint32_t at = total + __popc(b & ((1u << lane) - 1));
+                s_ent[at] = i;
+                s_id[at] = p.plan.ids[tile * ADAPTER_TILE + i];
+            }
+            total += __popc(b);
+        }
+        if (lane == 0) *s_count = total;
+    }
+    __syncthreads();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const int rg = p.rp / 16;                                    // groups of 16 ranks per adapter
+    const int groups = static_cast<int>(*s_count) * rg;          // of this tile
+    const int batches = (groups + 3) / 4;                        // four groups at a time
+    const int kb0 = blockIdx.y * NP_KB, nkb = min(NP_KB, p.num_kb - kb0);
+
+    if (warp == 0 && lane == 0) {
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        for (int q = blockIdx.z; q < batches; q += gridDim.z) {
+            const int n = min(4, groups - 4 * q);
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) {
+                    drain_copies(full_bar, issued, NP_STAGES);
+                    goto done_p;
+                }
+                ++issued;
+                mbar_expect_tx(full_bar(s), NP_A + n * 2048);
+                const uint32_t a = sbase + s * NP_STAGE;
+                tma_load_2d(a, &tmX, (kb0 + kb) * BK, row0, full_bar(s));
+                for (int i = 0; i < n; ++i) {
+                    const int gi = 4 * q + i;
+                    tma_load_3d(a + NP_A + i * 2048, &tmP, (kb0 + kb) * BK, (gi % rg) * 16, static_cast<int>(s_id[gi / rg]),
+                                full_bar(s));
+                }
+                if (++s == NP_STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+    done_p:;
+    } else if (warp == 1 && lane == 0) {
+        int s = 0, ab = 0;
+        uint32_t ph = 0, aph = 0;
+        for (int q = blockIdx.z; q < batches; q += gridDim.z) {
+            const uint32_t idesc = instr_desc(p.fmt, false, false, 16 * min(4, groups - 4 * q));
+            if (!mbar_wait(tempty_bar(ab), aph ^ 1u, abort_flag, p, DEV_TIMEOUT_MMA)) goto done_m;
+            tc_fence_after();
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA)) goto done_m;
+                tc_fence_after();
+                const uint32_t a = sbase + s * NP_STAGE, b = a + NP_A;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_one(tmem_base + ab * 64, smem_desc(a + kk * 32, 16, 1024), smem_desc(b + kk * 32, 16, 1024), idesc,
+                            (kb | kk) != 0 ? 1u : 0u);
+                mma_commit(empty_bar(s));
+                if (++s == NP_STAGES) { s = 0; ph ^= 1u; }
+            }
+            mma_commit(tfull_bar(ab));
+            if (++ab == 2) { ab = 0; aph ^= 1u; }
+        }
+    done_m:
+        // the MMAs issued above have finished before the CTA leaves, and with
+        // them the copies they waited for
+        mma_commit(drain_bar);
+        mbar_wait(drain_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+    } else if (warp >= 2) {
+        const int w = warp & 3;  // the TMEM lanes a warp may read
+        const int64_t row = row0 + 32 * w + lane;
+        int ab = 0;
+        uint32_t aph = 0;
+        for (int q = blockIdx.z; q < batches; q += gridDim.z) {
+            const int n = min(4, groups - 4 * q);
+            bool ok = mbar_wait(tfull_bar(ab), aph, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            for (int i = 0; i < n; ++i) {
+                const int gi = 4 * q + i;
+                const uint32_t mask = p.plan.masks[(tile * ADAPTER_TILE + s_ent[gi / rg]) * 8 + 4 * half + w];
+                if (mask == 0) continue;  // the same for the whole warp
+                __syncwarp();
+                uint32_t v[16];
+                tmem_ld16(tmem_base + (static_cast<uint32_t>(32 * w) << 16) + ab * 64 + 16 * i, v);
+                if ((mask >> lane) & 1u) {
+                    float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<int64_t>(blockIdx.y) * p.M + row) * p.rp +
+                                                            (gi % rg) * 16);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(ab));
+            if (++ab == 2) { ab = 0; aph ^= 1u; }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<128>(tmem_base);
+    }
+}
+
+// ---------------------------------------------------------------- gradients
+//
+// A CTA takes one chunk (at most 1024) of one adapter's sorted rows, 128 columns
+// of z and up to 64 ranks: D [128 columns x 4 rank_run] += z^T v, both operands
+// with the output index contiguous, 64 rows per block.  The rows lie anywhere in
+// z: four warps copy them 16 bytes at a time (cp.async) into the swizzled tiles,
+// rows past the chunk's end as zeros, so rows of other adapters are never read.
+// v comes in four 16-bit parts whose products stand in columns of their own and
+// are added at the end, so dA and dB keep f32's precision.  z is read once per 64
+// ranks, which bounds the pass (8192 rows of 4096: 67 MB, 10 us at the copy
+// rate); two CTAs per SM keep about 190 KB in flight.
+constexpr int GT_THREADS = 160, GT_ROWS = 64;
+constexpr int GT_A = 2 * 8192;  // 64 rows x 128 columns, two 64-column atoms
+__host__ __device__ constexpr int gt_atoms(int run) { return 4 * run / 64; }
+__host__ __device__ constexpr int gt_stage(int run) { return GT_A + gt_atoms(run) * 8192; }
+__host__ __device__ constexpr int gt_stages(int run) { return 98304 / gt_stage(run); }
+__host__ __device__ constexpr int gt_smem(int run) { return 1024 + gt_stages(run) * gt_stage(run) + 256; }
+static_assert(gt_stages(16) == 4 && gt_stages(32) == 3 && gt_stages(64) == 2, "ring depths");
+
+struct GradParams {
+    float* out;
+    float* parts;
+    const uint16_t* v4;  // [M, vcols]
+    const uint16_t* z;   // [M, C]
+    const uint32_t* off;
+    const uint32_t* perm;
+    AdapterChunks ch;
+    int64_t C, vcols;
+    uint32_t chunk0, strips;  // block x: strip x % strips of chunk chunk0 + x / strips
+    int R, G, fmt;
+    int* status;
+    unsigned long long wait_limit;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+    const int n = in ? 16 : 0;  // 0: the 16 bytes are filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+template <int RUN>
+__global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams p) {
+    constexpr int ATOMS = gt_atoms(RUN), STAGE = gt_stage(RUN), STAGES = gt_stages(RUN), LAG = STAGES - 1;
+    constexpr int COLS = 4 * RUN <= 128 ? 4 * RUN : 256;  // TMEM columns, a power of two
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * STAGES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dep_wait();
+    const uint32_t chunk = p.chunk0 + blockIdx.x / p.strips;
+    if (chunk >= p.ch.first[p.G]) return;
+    int g = 0;  // the last adapter whose first chunk is <= chunk
+    for (int hi = p.G - 1; g < hi;) {
+        const int mid = (g + hi + 1) >> 1;
+        if (p.ch.first[mid] <= chunk) g = mid; else hi = mid - 1;
+    }
+    const uint32_t j = chunk - p.ch.first[g], nchunks = p.ch.first[g + 1] - p.ch.first[g];
+    const uint32_t s0 = p.off[g] + j * static_cast<uint32_t>(ADAPTER_CHUNK);
+    const uint32_t s1 = min(p.off[g + 1], s0 + static_cast<uint32_t>(ADAPTER_CHUNK));
+    const int blocks = static_cast<int>((s1 - s0 + GT_ROWS - 1) / GT_ROWS);
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x % p.strips) * 128;
+    const int r0 = blockIdx.y * 64;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 128);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4) tmem_alloc<COLS>(smem_u32(tmem_slot));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    grid_dep_launch();  // after the CTA has its TMEM: a dependent kernel may ask for some
+
+    if (warp < 4) {
+        // thread t copies 16-byte piece t % 8 of each 128-byte atom row, rows t / 8 + 16 i
+        const int piece = tid & 7, rr = tid >> 3;
+        const uint32_t sw = static_cast<uint32_t>((piece ^ (rr & 7)) * 16);  // rr + 16 i has the same low bits
+        const bool in0 = c0 + piece * 8 < p.C, in1 = c0 + 64 + piece * 8 < p.C;
+        const uint16_t* zc = p.z + c0 + piece * 8;
+        const uint16_t* vc = p.v4 + static_cast<int64_t>(blockIdx.y) * (4 * RUN) + piece * 8;
+        uint32_t row[4];
+        auto rows_of = [&](int b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t s = s0 + b * GT_ROWS + rr + 16 * i;
+                row[i] = b < blocks && s < s1 ? p.perm[s] : 0xffffffffu;
+            }
+        };
+        rows_of(0);
+        bool ok = true;
+        int st = 0, st_done = 0;
+        uint32_t ph = 0;
+        for (int b = 0; b < blocks + LAG; ++b) {
+            if (b < blocks) {
+                ok = ok && mbar_wait(empty_bar(st), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+                if (ok) {
+                    const uint32_t a = sbase + st * STAGE;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = row[i] != 0xffffffffu;
+                        const int64_t m = in ? row[i] : 0;
+                        const uint32_t dst = a + (rr + 16 * i) * 128 + sw;
+                        copy16(dst, in && in0 ? zc + m * p.C : p.z, in && in0);
+                        copy16(dst + 8192, in && in1 ? zc + m * p.C + 64 : p.z, in && in1);
+#pragma unroll
+                        for (int q = 0; q < ATOMS; ++q) copy16(dst + GT_A + q * 8192, vc + m * p.vcols + q * 64, in);
+                    }
+                }
+                rows_of(b + 1);
+                if (++st == STAGES) { st = 0; ph ^= 1u; }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (b >= LAG) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
+                fence_proxy_async_smem();
+                mbar_arrive(full_bar(st_done));
+                if (++st_done == STAGES) st_done = 0;
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        // epilogue: this thread's column, ranks ascending, the parts added from the smallest
+        ok = mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tc_fence_after();
+            const int64_t col = c0 + 32 * warp + lane;
+            float* dst = nchunks > 1 ? p.parts + static_cast<int64_t>(p.ch.part[g] + j) * p.R * p.C
+                                     : p.out + static_cast<int64_t>(g) * p.R * p.C;
+            const uint32_t t = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
+            for (int q = 0; q < RUN && r0 + q < p.R; q += 16) {
+                uint32_t v0[16], v1[16], v2[16], v3[16];
+                tmem_ld16(t + q, v0);
+                tmem_ld16(t + RUN + q, v1);
+                tmem_ld16(t + 2 * RUN + q, v2);
+                tmem_ld16(t + 3 * RUN + q, v3);
+                if (col < p.C) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = __uint_as_float(v0[i]), m = __uint_as_float(v1[i]), l = __uint_as_float(v2[i]);
+                        const float t = __uint_as_float(v3[i]);
+                        const float s = p.fmt ? m + (l + t)
+                                              : fmaf(a, 0x1p11f, fmaf(fmaf(t, 0x1p-11f, l), 0x1p-11f, m));
+                        if (r0 + q + i < p.R) dst[static_cast<int64_t>(r0 + q + i) * p.C + col] = s;
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (lane == 0) {
+        const uint32_t idesc = instr_desc(p.fmt, true, true, 4 * RUN);
+        int s = 0;
+        uint32_t ph = 0;
+        for (int b = 0; b < blocks; ++b) {
+            if (!mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA)) break;
+            tc_fence_after();
+            const uint32_t a = sbase + s * STAGE, v = a + GT_A;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_one(tmem_base, smem_desc(a + kk * 2048, 8192, 1024), smem_desc(v + kk * 2048, 8192, 1024), idesc,
+                        (b | kk) != 0 ? 1u : 0u);
+            mma_commit(empty_bar(s));
+            if (++s == STAGES) { s = 0; ph ^= 1u; }
+        }
+        mma_commit(done_bar);
+        mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_free<COLS>(tmem_base);
+    }
+}
+
+template <int RUN>
+cudaError_t grad_run(const LaunchCtx& c, const GradParams& p, dim3 grid) {
+    static PerDeviceOnce setup;
+    const cudaError_t e = setup.run(c.eng->device, [](int&) {
+        return cudaFuncSetAttribute(grad_tc_kernel<RUN>, cudaFuncAttributeMaxDynamicSharedMemorySize, gt_smem(RUN));
+    });
+    if (e != cudaSuccess) return e;
+    const cudaError_t r = launch_pdl(grad_tc_kernel<RUN>, grid, dim3(GT_THREADS), gt_smem(RUN), c.stream, p);
+    if (r == cudaSuccess) c.count();
+    return r;
+}
+
+}  // namespace
+
+cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, const void* z, const void* pw,
+                              const AdapterPlan& plan, int64_t M, int64_t L, int R, int64_t G) {
+    static PerDeviceOnce setup;
+    cudaError_t e = setup.run(c.eng->device, [](int&) {
+        return cudaFuncSetAttribute(narrow_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NP_SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    CUtensorMap x, w;
+    if ((e = make_map(&x, dt, z, L, M, 1, 128)) != cudaSuccess) return e;
+    if ((e = make_map(&w, dt, pw, L, R, G, 16, true)) != cudaSuccess) return e;
+    NarrowParams p{};
+    p.plan = plan; p.partial = partial; p.M = M; p.R = R; p.rp = (R + 15) / 16 * 16;
+    p.num_kb = static_cast<int>((L + BK - 1) / BK);
+    p.fmt = dt == BI_BF16 ? 1 : 0;
+    p.status = c.status; p.wait_limit = c.wait_limit_ns;
+    const int64_t tiles = (M + 127) / 128, pieces = (L + ADAPTER_PIECE - 1) / ADAPTER_PIECE;
+    // batches of four 16-rank groups: at most one adapter per row; a CTA takes
+    // several where the tiles and pieces alone fill the GPU
+    const int64_t most = (lmin(lmin(G, M), 128) * (p.rp / 16) + 3) / 4;
+    const int64_t want = (4 * int64_t(c.sm_count) + tiles * pieces - 1) / (tiles * pieces);
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(pieces), static_cast<unsigned>(lmin(most, want)));
+    e = launch_pdl(narrow_tc_kernel, grid, dim3(NP_THREADS), NP_SMEM, c.stream, x, w, p);
+    if (e == cudaSuccess) c.count();
+    return e;
+}
+
+cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, float* out, float* parts, const void* v4, const void* z,
+                            const uint32_t* off, const uint32_t* perm, const AdapterChunks& ch, int64_t M, int64_t C,
+                            int R, int64_t G) {
+    GradParams p{};
+    p.out = out; p.parts = parts; p.v4 = static_cast<const uint16_t*>(v4); p.z = static_cast<const uint16_t*>(z);
+    p.off = off; p.perm = perm; p.ch = ch; p.C = C; p.vcols = adapter_grad_cols(R); p.R = R; p.G = static_cast<int>(G);
+    p.fmt = dt == BI_BF16 ? 1 : 0;
+    p.status = c.status; p.wait_limit = c.wait_limit_ns;
+    const int64_t strips = (C + 127) / 128, chunks = AdapterChunks::max_chunks(M, G);
+    p.strips = static_cast<uint32_t>(strips);
+    const int64_t slice = ((int64_t(1) << 31) - 1) / strips;  // chunks per launch
+    for (int64_t q = 0; q < chunks; q += slice) {
+        p.chunk0 = static_cast<uint32_t>(q);
+        const dim3 grid(static_cast<unsigned>(lmin(slice, chunks - q) * strips), static_cast<unsigned>((R + 63) / 64));
+        const int run = adapter_rank_run(R);
+        const cudaError_t e = run == 16 ? grad_run<16>(c, p, grid) : run == 32 ? grad_run<32>(c, p, grid)
+                            : run == 48 ? grad_run<48>(c, p, grid) : grad_run<64>(c, p, grid);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace bi

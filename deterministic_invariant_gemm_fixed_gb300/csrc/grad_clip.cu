@@ -185,7 +185,7 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t e0, int len
         const int nv = len / PER;
         const uint4* v = reinterpret_cast<const uint4*>(src);
         uint4* o = reinterpret_cast<uint4*>(dst);
-        constexpr int U = 8;
+        constexpr int U = 4;
         for (int b = threadIdx.x; b < nv; b += U * GC_THREADS) {
             uint4 raw[U];
 #pragma unroll

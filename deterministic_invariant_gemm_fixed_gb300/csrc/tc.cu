@@ -26,13 +26,10 @@
 // one tile overlaps the main loop of the next.  Every mbarrier wait is bounded
 // by a %globaltimer limit; on expiry the kernel records a status code, stops all
 // roles, drains its own copies and MMAs, frees TMEM and returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "bi_internal.h"
+#include "adapter.h"
+#include "tc_common.cuh"
 
 namespace bi {
 namespace {
@@ -46,7 +43,7 @@ constexpr int GROUP_M = 16;    // raster: 16 row-tiles share the column sweep (L
 static_assert(GROUPED_TILE_ROWS == 256 && GROUPED_TAIL_ROWS == BK,
               "the grouping's tile and tail sizes are the pair kernel's");
 
-enum Mode { DENSE = 0, GROUPED_ROWS = 1, GROUPED_DW = 2 };
+enum Mode { DENSE = 0, GROUPED_ROWS = 1, GROUPED_DW = 2, ADAPTER = 3 };
 
 struct Params {
     void* out;
@@ -62,126 +59,10 @@ struct Params {
     int accum_out;           // f32 out, a contraction piece after the first: out += result
     int split_from, split_s; // dense: tiles from split_from on run their contraction as split_s chunks
     float* partials;         // ... whose f32 results go here, 256 x BN per (tile, chunk)
+    AdapterPlan plan;        // adapter passes: the adapters of each 256-row tile
+    int rank;
     int* status;
     unsigned long long wait_limit;
-};
-
-// ---------------------------------------------------------------- PTX helpers
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ unsigned long long globaltimer() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait.  Returns false if this CTA is aborting or the limit ran out
-// (then the status word is written and the CTA-wide abort flag raised).
-__device__ __noinline__ bool mbar_wait_impl(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                            int* status, unsigned long long limit, int code) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15u) == 0) {
-            if (*abort_flag) return false;
-            if (globaltimer() - t0 > limit) {
-                *abort_flag = 1;
-                if (status) *reinterpret_cast<volatile int*>(status) = code;
-                return false;
-            }
-        }
-    }
-}
-#define mbar_wait(bar, parity, abort_flag, p, code) \
-    mbar_wait_impl((bar), (parity), (abort_flag), (p).status, (p).wait_limit, (code))
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// Shared-memory matrix descriptor (tcgen05 format): start address, leading and
-// stride byte offsets (>> 4), version 1 at bit 46, 128-byte swizzle (2) at bit 61.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-    d |= 1ull << 46;
-    d |= 2ull << 61;
-    return d;
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
-        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// ---------------------------------------------------------------- output types
-
-template <int FMT> struct OutT;
-template <> struct OutT<0> {
-    using T = __half;
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&h);
-    }
-    static __device__ __forceinline__ float load(const void* p, int64_t i) {
-        return __half2float(reinterpret_cast<const __half*>(p)[i]);
-    }
-    static __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-        reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
-    }
-};
-template <> struct OutT<1> {
-    using T = __nv_bfloat16;
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&h);
-    }
-    static __device__ __forceinline__ float load(const void* p, int64_t i) {
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-    }
-    static __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-        reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    }
 };
 
 // ---------------------------------------------------------------- CTA-pair kernel
@@ -205,7 +86,20 @@ template <> struct OutT<1> {
 //                 row perm[s] of the output;
 //   GROUPED_DW    dweights: (expert, n tile, k tile), contraction over the
 //                 expert's rows in 64-row blocks read in place, the partial
-//                 last block read from a zero-padded tail buffer (tmA2/tmB2).
+//                 last block read from a zero-padded tail buffer (tmA2/tmB2);
+//   ADAPTER       DENSE, and after a tile's contraction the low-rank terms of the
+//                 adapters among its 256 rows, accumulated into the same tile:
+//                 per adapter and 32 ranks one more ring stage, A = the rows'
+//                 inner products h in two 16-bit parts (32 high parts, 32
+//                 remainders: 64 columns, tmA2), B = 32 rows of the adapter's
+//                 Q [R, cols] (MN-major, tmB2).  The rows of other adapters are
+//                 lanes the MMA is told not to write (its disable-output-lane
+//                 operand), so a row gets its own adapter's terms only, whatever
+//                 values the others hold, at its own place in the chain: after
+//                 the contraction, ranks ascending.  The terms cost 2 R / 16
+//                 MMAs per adapter of a tile beside the contraction's K / 16
+//                 and no pass over Y: a separate pass that adds them would
+//                 read and write Y again and round it twice.
 //
 // Barriers: full[s] (CTA 0, count 1, 64 KB expected from both CTAs' copies),
 // empty[s] (each CTA, released by CTA 0's commit multicast to both), tfull[b]
@@ -286,7 +180,6 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 template <int N>
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Raster of the dense tiles: GROUP_M row pairs share a sweep over the column
 // tiles (L2 reuse of the B columns).
@@ -339,7 +232,7 @@ __device__ __forceinline__ bool pair_tile(const Params& p, int t, PairTile& u) {
     const int units_m = (p.num_m + 1) / 2;
     u.part = -1;
     u.npiece = 1;
-    if (MODE == DENSE) {
+    if (MODE == DENSE || MODE == ADAPTER) {
         // tiles [0, split_from) whole; each later tile as split_s consecutive
         // units, chunk j contracting blocks [j nkb / s, (j + 1) nkb / s)
         int tile = t, chunk = -1;
@@ -414,6 +307,19 @@ __device__ __forceinline__ bool pair_tile(const Params& p, int t, PairTile& u) {
     }
     u.npiece = u.nkb == 0 ? 1 : (u.kb0 + u.nkb - 1) / DW_PIECE_KB - u.kb0 / DW_PIECE_KB + 1;
     return true;
+}
+
+// The f16 / bf16 MMA that leaves the accumulator lanes (rows) of `off` alone: bit
+// i of off[0..3] is row i of CTA 0's half of the tile, off[4..7] CTA 1's.
+__device__ __forceinline__ void mma_pair_masked(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                const uint32_t (&off)[8]) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]), "r"(off[5]),
+        "r"(off[6]), "r"(off[7])
+        : "memory");
 }
 
 template <int IN>
@@ -491,7 +397,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int ES = IN == 2 ? 1 : (IN == 3 ? 4 : 2);  // operand element size, bytes
     // the tf32 operands are always staged K-major (the split kernel transposes)
     static_assert(IN != 3 || (!A_MN && !B_MN), "3xTF32 takes K-major operands only");
-    static_assert(MODE == DENSE || IN <= 1, "grouped passes take bf16 / f16 operands");
+    static_assert(MODE == DENSE || IN <= 1, "grouped and adapter passes take bf16 / f16 operands");
+    static_assert(MODE != ADAPTER || (!A_MN && BNT == 256), "adapter passes: K-major rows, 256-column tiles");
     // tile widths: 256, or for 16-bit operands any multiple of 16 from 128 up;
     // an MN-major B tile is whole 64-column swizzle atoms per CTA (128 or 256)
     static_assert(BNT == 256 || (IN <= 1 && BNT % 16 == 0 && BNT >= 128 && BNT < 256 && MODE != GROUPED_DW &&
@@ -616,6 +523,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (++s == P_STAGES) { s = 0; ph ^= 1u; }
             }
             }
+            if (MODE == ADAPTER) {
+                const uint32_t* ids = p.plan.ids + static_cast<int64_t>(u.mpair) * ADAPTER_TILE;
+                const int n = static_cast<int>(p.plan.count[u.mpair]);
+                for (int e = 0; e < n; ++e) {
+                    const int g = static_cast<int>(ids[e]);
+                    for (int c = 0; c < (p.rank + 31) / 32; ++c) {
+                        if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) goto done_p;
+                        const uint32_t fb_leader = mapa_rank(full_bar(s), 0);
+                        const uint32_t a_dst = sbase + s * P_STAGE_BYTES, b_dst = a_dst + P_A_BYTES;
+                        if (crank == 0) mbar_expect_tx(full_bar(s), 2 * (P_A_BYTES + P_B_BYTES / 2));
+                        tma_load_2d_pair(a_dst, &tmA2, c * 64, arow, fb_leader);
+                        for (int b = 0; b < B_ATOMS; ++b)
+                            tma_load_3d_pair(b_dst + b * (BKE * 128), &tmB2, bcol + b * 64, c * 32, g, fb_leader);
+                        if (++s == P_STAGES) { s = 0; ph ^= 1u; }
+                    }
+                }
+            }
         }
     done_p:;
         // Copies of this CTA complete on CTA 0's barriers; CTA 0's MMA thread
@@ -664,6 +588,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 mma_commit_pair_mc(empty_bar(s), 0x3);
                 if (++s == P_STAGES) { s = 0; ph ^= 1u; }
+            }
+            if (MODE == ADAPTER) {  // the tile's low-rank terms
+                constexpr uint32_t idesc_q = instr_desc_pair<IN, false, true, BN>();
+                const int64_t tile = static_cast<int64_t>(u.mpair) * ADAPTER_TILE;
+                const int n = static_cast<int>(p.plan.count[u.mpair]);
+                for (int e = 0; e < n; ++e) {
+                    const uint4* mk = reinterpret_cast<const uint4*>(p.plan.masks + (tile + e) * 8);
+                    const uint4 lo = mk[0], hi = mk[1];
+                    const uint32_t off[8] = {~lo.x, ~lo.y, ~lo.z, ~lo.w, ~hi.x, ~hi.y, ~hi.z, ~hi.w};
+                    for (int c = 0; c < (p.rank + 31) / 32; ++c) {
+                        if (!mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA)) goto done_m;
+                        tc_fence_after();
+                        const uint32_t a_s = sbase + s * P_STAGE_BYTES, b_s = a_s + P_A_BYTES;
+                        const int steps = p.rank - 32 * c > 16 ? 2 : 1;  // K = 16 steps with ranks in them
+                        for (int part = 0; part < 2; ++part)
+                            for (int j = 0; j < steps; ++j)
+                                mma_pair_masked(d_tmem, smem_desc(a_s + (2 * part + j) * 32, 16, 1024),
+                                                smem_desc(b_s + j * 2048, BKE * 128, 1024), idesc_q, off);
+                        mma_commit_pair_mc(empty_bar(s), 0x3);
+                        if (++s == P_STAGES) { s = 0; ph ^= 1u; }
+                    }
+                }
             }
             mma_commit_pair_mc(tfull_bar(ab), 0x3);
             if (++ab == NACC) { ab = 0; aph ^= 1u; }
@@ -1021,60 +967,6 @@ cudaError_t launch_chunk_sum(const LaunchCtx& c, const float* ws, int split_from
 
 // ---------------------------------------------------------------- host side
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// 16-bit row-major tensor [outer][inner] (optionally [depth][outer][inner]),
-// box {64, box_outer(, 1)}, 128-byte swizzle, zero fill out of bounds.
-cudaError_t make_map(CUtensorMap* m, bi_dtype dt, const void* ptr, uint64_t inner, uint64_t outer,
-                     uint64_t depth, uint32_t box_outer, bool rank3 = false) {
-    auto enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    const CUtensorMapDataType t =
-        dt == BI_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    cuuint64_t dims[3] = {inner, outer, depth};
-    cuuint64_t strides[2] = {inner * 2, inner * outer * 2};
-    cuuint32_t box[3] = {64, box_outer, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    const cuuint32_t rank = rank3 ? 3 : 2;
-    CUresult r = enc(m, t, rank, const_cast<void*>(ptr), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-// Output [depth][outer][inner] (row stride ld elements; out_fmt 0 f16, 1 bf16,
-// 2 f32) for the TMA-store epilogue: box {128 bytes of columns, 32 rows (, 1)},
-// 128-byte swizzle; stores past the extents are clipped.
-cudaError_t make_out_map(CUtensorMap* m, int out_fmt, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld,
-                         uint64_t depth = 1, bool rank3 = false) {
-    auto enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    const CUtensorMapDataType t = out_fmt == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                : out_fmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const uint64_t es = out_fmt == 2 ? 4 : 2;
-    cuuint64_t dims[3] = {inner, outer, depth};
-    cuuint64_t strides[2] = {ld * es, ld * outer * es};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 32, 1};
-    cuuint32_t el[3] = {1, 1, 1};
-    CUresult r = enc(m, t, rank3 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, el,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // units: work units (or an upper bound, for the grouped modes, whose count is
 // known only on the device); -1 = the dense count.
 // o: the output's tensor map for the TMA-store epilogue (every mode but the
@@ -1181,6 +1073,31 @@ cudaError_t dx_impl(const LaunchCtx& c, bi_dtype dt, void* dx, const void* dy, c
     CUtensorMap o;
     if ((e = make_out_map(&o, FMT, dx, K, M, K)) != cudaSuccess) return e;
     return launch_pair<FMT, FMT, false, false, DENSE, BNT>(c, a, b, p, &o);
+}
+
+// Forward (B = W [K,N] with the columns contiguous) or dX (W's rows are the
+// columns) with the adapters' terms: z the rows [M,L], hh [M, 64 ceil(R/32)] the
+// inner products in two parts, q the adapters' [G,R,C].
+template <int FMT>
+cudaError_t adapter_rows_t(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
+                           const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
+                           int64_t K, int64_t N, int R, int64_t G) {
+    const int64_t L = dx ? N : K, C = dx ? K : N;
+    CUtensorMap a, b, a2, b2, o;
+    cudaError_t e;
+    if ((e = make_map(&a, dt, z, L, M, 1, BM)) != cudaSuccess) return e;
+    if ((e = dx ? make_map(&b, dt, w, N, K, 1, BN / 2) : make_map(&b, dt, w, N, K, 1, BK)) != cudaSuccess) return e;
+    if ((e = make_map(&a2, dt, hh, adapter_part_cols(R), M, 1, BM)) != cudaSuccess) return e;
+    if ((e = make_map(&b2, dt, q, C, R, G, 32, true)) != cudaSuccess) return e;
+    if ((e = make_out_map(&o, FMT, out, C, M, C)) != cudaSuccess) return e;
+    Params p{};
+    p.out = out; p.ldo = C; p.rows = M; p.cols = C; p.bias = bias;
+    p.plan = plan; p.rank = R;
+    p.num_m = static_cast<int>((M + BM - 1) / BM);
+    p.num_n = static_cast<int>((C + BN - 1) / BN);
+    p.num_kb = static_cast<int>((L + BK - 1) / BK);
+    return dx ? launch_pair<FMT, FMT, false, false, ADAPTER>(c, a, b, p, &o, &a2, &b2)
+              : launch_pair<FMT, FMT, false, true, ADAPTER>(c, a, b, p, &o, &a2, &b2);
 }
 
 template <int FMT>
@@ -1483,6 +1400,13 @@ cudaError_t tc_forward(const LaunchCtx& c, bi_dtype dt, void* y, const void* x, 
 cudaError_t tc_dx(const LaunchCtx& c, bi_dtype dt, void* dx, const void* dy, const void* w,
                   int64_t M, int64_t K, int64_t N) {
     return dt == BI_BF16 ? dx_t<1>(c, dt, dx, dy, w, M, K, N) : dx_t<0>(c, dt, dx, dy, w, M, K, N);
+}
+
+cudaError_t tc_adapter_rows(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
+                            const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
+                            int64_t K, int64_t N, int R, int64_t G) {
+    return dt == BI_BF16 ? adapter_rows_t<1>(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G)
+                         : adapter_rows_t<0>(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G);
 }
 
 int64_t tc_dw_workspace_bytes(const LaunchCtx& c, int dw_f32, int64_t M, int64_t K, int64_t N) {

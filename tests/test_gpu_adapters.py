@@ -198,7 +198,7 @@ def test_one_request_cannot_reach_another(eng, dtype, tc, bad):
 
 def test_rows_without_adapter_are_the_shared_projection(eng):
     """No id in range: y and dx are the plain layer's, bit for bit, h, dA and dB are 0."""
-    for dtype, tc in (("f32", 0), ("f32", 1), ("bf16", 0)):
+    for dtype, tc in (("f32", 0), ("f32", 1), ("bf16", 0), ("bf16", 1), ("f16", 1)):
         d = inputs(200, 136, 264, 8, 4, dtype, seed=6)
         d["ids"].fill_(4)
         y, h = forward(eng, d, tc)
@@ -264,6 +264,8 @@ def test_empty_batch_and_refusals(eng):
                    dict(a=None), dict(b=None), dict(ids=None)):
         assert status(**change) == bi.BI_ERR_INVALID_ARG, change
     assert status(r=257) == bi.BI_ERR_UNSUPPORTED and status(g=65536) == bi.BI_ERR_UNSUPPORTED
+    odd = torch.empty(4 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(4, 64)
+    assert status(x=odd) == bi.BI_ERR_MISALIGNED
     with pytest.raises(ValueError):
         status(a=d["a"].transpose(1, 2))
     with pytest.raises(bi.BiError):
