@@ -23,7 +23,7 @@ namespace {
 
 constexpr int RT_THREADS = 256;
 constexpr int RT_WARPS = RT_THREADS / 32;
-constexpr int64_t RT_BLOCKS = 1024;   // blocks aimed at: about 7 per SM for a long batch
+constexpr int64_t RT_BLOCKS = 608;    // blocks aimed at for a long batch: four on each of 152 SMs, one wave
 constexpr int64_t RT_MAX_E = 1024;
 constexpr int64_t RT_MAX_K = 64;
 constexpr int FIN_E = 8, FIN_SLOTS = 32;  // finishing kernel: experts per block, partial sums per expert
@@ -37,23 +37,33 @@ template <> __device__ __forceinline__ float down<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 down<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half down<__half>(float v) { return __float2half_rn(v); }
 
-// V consecutive elements from index e0 of a row of E; elements past E are `fill`.
+// V consecutive elements of a row of E from index e0 on, as loaded: unpacked
+// only when the row's turn comes, so a row's loads run under the one before.
+// Elements past E, and all of them when `in` is false, are -inf.
 template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int e0, int E, bool vec, float fill, float (&x)[V]) {
-    constexpr int PER = 16 / sizeof(T);  // V is a multiple of PER
-    if (vec && e0 + V <= E) {
+struct Raw {
+    uint32_t w[V * sizeof(T) / 4];
+    __device__ __forceinline__ void load(const T* row, int e0, int E, bool vec, bool in) {
+        constexpr int WORDS = V * sizeof(T) / 4;
+        if (vec && in && e0 + V <= E) {
+            if constexpr (WORDS == 2) {
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + e0));
+                w[0] = q.x; w[1] = q.y;
+            } else {
 #pragma unroll
-        for (int i = 0; i < V; i += PER) {
-            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(row + e0 + i));
-            const T* v = reinterpret_cast<const T*>(&raw);
+                for (int i = 0; i < WORDS; i += 4) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + e0) + i / 4);
+                    w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+                }
+            }
+        } else {
+            T* v = reinterpret_cast<T*>(w);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) x[i + j] = up<T>(v[j]);
+            for (int i = 0; i < V; ++i) v[i] = in && e0 + i < E ? __ldg(row + e0 + i) : down<T>(-INFINITY);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = e0 + i < E ? up<T>(__ldg(row + e0 + i)) : fill;
     }
-}
+    __device__ __forceinline__ float get(int i) const { return up<T>(reinterpret_cast<const T*>(w)[i]); }
+};
 
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
@@ -62,12 +72,36 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// A logit's place in the order of choice: larger logits have larger keys, the
-// two zeros the same one; -inf and NaN are 0 (never chosen).
-__device__ __forceinline__ uint32_t order_key(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-    return x > -INFINITY ? k : 0u;
+constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
+// 2^x, within 2 ulp; exponents are kept in base 2, so a probability costs one FMA
+// and one of these.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The largest value of a row's L lanes (NaN passed over).
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+    if constexpr (L == 32) {
+        float y;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+        return y;
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// loss = E / (k V) * the sum of the experts' terms counts[e] mean[e], by one warp
+// in a fixed order.
+__device__ __forceinline__ void write_loss(const volatile float* terms, int E, int k, uint32_t v, float* loss) {
+    const int lane = threadIdx.x & 31;
+    float s = 0.0f;
+    for (int q = lane; q < E; q += 32) s += terms[q];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) *loss = v ? s * (static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(v))) : 0.0f;
 }
 
 struct RouteArgs {
@@ -80,133 +114,191 @@ struct RouteArgs {
     uint32_t* pcnt;       // [blocks, E] choices
     uint32_t* prow;       // [blocks] rows counted
     uint32_t* ticket;
+    uint32_t* counts;     // the results, which a lone block writes itself
+    uint32_t* rows;
+    float* mean;
+    float* loss;
     int64_t T, rows_per_block;
     int E, k, normalize, vec;
 };
 
+// The choice, k experts of a row.  For rows of one warp (more than 64 experts):
+// the k-th largest of the 32 lanes' largest logits bounds the k-th largest logit
+// from below, so the logits at or above it, usually a dozen, hold the choice; they
+// are packed into shared memory and each ranked against the others, without a
+// chain of dependent steps.  Otherwise (shorter rows, k > 32, or more than 32
+// logits at or above the bound): k times the largest logit of the row's lanes.
+// 8 of 256 experts, 131072 rows in f32: 245 us by the second way.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a) {
     constexpr int GROUPS = 32 / L;             // rows per warp
     constexpr int STEP = RT_WARPS * GROUPS;    // rows per block and step
-    // choices kept per lane: slots li, li + L, ... (k is at most E <= L V)
-    constexpr int SLOTS = (RT_MAX_K + L - 1) / L < V ? (RT_MAX_K + L - 1) / L : V;
+    constexpr int MAXK = L * V < RT_MAX_K ? L * V : static_cast<int>(RT_MAX_K);
     __shared__ float s_sum[RT_WARPS][L * V];
     __shared__ uint32_t s_cnt[L * V];
     __shared__ uint32_t s_rows[RT_WARPS];
+    __shared__ uint2 s_pick[RT_WARPS * GROUPS][MAXK];  // slot -> (expert, weight's bits)
+    __shared__ __align__(16) float s_cand_v[L == 32 ? RT_WARPS : 1][32];
+    __shared__ uint16_t s_cand_i[L == 32 ? RT_WARPS : 1][32];  // (place in the lane, lane)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grp = lane / L, li = lane % L;
     const int e0 = li * V;
-    const int E = a.E;
+    const int E = a.E, k = a.k;
+    uint2* pick = s_pick[warp * GROUPS + grp];
     for (int i = threadIdx.x; i < L * V; i += RT_THREADS) s_cnt[i] = 0;
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && gridDim.x > 1) *a.ticket = 0;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     uint32_t rows = 0;
     const int64_t r0 = blockIdx.x * a.rows_per_block;
     const int64_t r1 = lmin(a.T, r0 + a.rows_per_block);
+    const T* logits = static_cast<const T*>(a.logits);
+    auto takes_part = [&](int64_t t) { return t < r1 && (a.valid == nullptr || a.valid[t] != 0); };
+    Raw<T, V> raw;
+    bool next = takes_part(r0 + warp * GROUPS + grp);
+    raw.load(logits + (r0 + warp * GROUPS + grp) * E, e0, E, a.vec != 0, next);
     for (int64_t base = r0; base < r1; base += STEP) {  // every warp runs every step: the shuffles need all lanes
         const int64_t t = base + warp * GROUPS + grp;
         const bool in = t < r1;
-        bool counted = in && (a.valid == nullptr || a.valid[t] != 0);
         float x[V];
-        if (counted) load_row<T, V>(static_cast<const T*>(a.logits) + t * E, e0, E, a.vec != 0, -INFINITY, x);
-        else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = -INFINITY;
-        }
-        uint32_t key[V];
-        float mx = -INFINITY;
-        bool nan = false;
+        float top = -INFINITY;  // this lane's largest
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            key[i] = order_key(x[i]);
-            mx = fmaxf(mx, x[i]);  // a NaN is passed over here and shows in the sum
-            nan = nan || x[i] != x[i];
+            x[i] = raw.get(i);
+            top = fmaxf(top, x[i]);  // a NaN is passed over here and shows in the sum
         }
+        bool counted = next;
+        next = takes_part(t + STEP);
+        raw.load(logits + (t + STEP) * E, e0, E, a.vec != 0, next);
+        const float mx = group_max<L>(top);
+        if (__any_sync(0xffffffffu, mx == -INFINITY)) {  // rows of -inf alone have no expert, rows of NaN and -inf are counted
+            bool nan = false;
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            nan = __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), o) != 0 || nan;
+            for (int i = 0; i < V; ++i) nan = nan || x[i] != x[i];
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) nan = __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), o) != 0 || nan;
+            counted = counted && (mx > -INFINITY || nan);
         }
-        counted = counted && (mx > -INFINITY || nan);  // a row of -inf alone has no expert
+        const float m2 = mx > -INFINITY ? mx * LOG2E : 0.0f;
         float p[V], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = counted && e0 + i < E ? __expf(x[i] - mx) : 0.0f;
+            p[i] = exp2_approx(fmaf(x[i], LOG2E, -m2));
             sum += p[i];
         }
         sum = group_sum<L>(sum);
         const float inv = counted ? 1.0f / sum : 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            p[i] *= inv;
-            acc[i] += p[i];
-        }
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
         if (in && li == 0) {
-            a.lse[t] = counted ? mx + logf(sum) : INFINITY;
+            a.lse[t] = counted ? (m2 + log2f(sum)) * LN2 : INFINITY;
             rows += counted;
         }
-        // the choice: k times the group's largest key, the lowest index among equals
+        auto weight = [&](float v) { return exp2_approx(fmaf(v, LOG2E, -m2)) * inv; };
         float wsum = 0.0f;
-        uint32_t my_id[SLOTS];
-        float my_w[SLOTS];
+        bool done = false;
+        if constexpr (L == 32) {
+            if (k <= 32) {
+                float most = top, bound = -INFINITY;
+                for (int j = 0; j < k; ++j) {
+                    bound = group_max<32>(most);
+                    if (most == bound) most = -INFINITY;
+                }
+                bound = fmaxf(bound, -3.402823466e38f);  // -inf and NaN are no candidates
+                int own = 0;
 #pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            my_id[s] = static_cast<uint32_t>(E);
-            my_w[s] = 0.0f;
-        }
-        uint32_t best = 0;
-        int bi_ = 0;
-        auto scan = [&] {
-            best = 0;
-            bi_ = 0;
+                for (int i = 0; i < V; ++i) own += x[i] >= bound;
+                int at = own;  // candidates of the lanes up to this one
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (key[i] > best) { best = key[i]; bi_ = i; }
-        };
-        scan();
-        for (int j = 0; j < a.k; ++j) {
-            uint32_t gk = best;
-            int ge = e0 + bi_;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, at, o);
+                    if (lane >= o) at += y;
+                }
+                const int total = __shfl_sync(0xffffffffu, at, 31);
+                if (total <= 32) {
+                    done = true;
+                    float* cv = s_cand_v[warp];
+                    uint16_t* ce = s_cand_i[warp];
+                    at -= own;
+                    cv[lane] = -INFINITY;
+                    __syncwarp();
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) {
-                const uint32_t ok = __shfl_xor_sync(0xffffffffu, gk, o);
-                const int oe = __shfl_xor_sync(0xffffffffu, ge, o);
-                if (ok > gk || (ok == gk && oe < ge)) { gk = ok; ge = oe; }
-            }
-            float w = 0.0f;
-            const bool mine = gk != 0 && ge / V == li;
-            if (mine) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i == bi_) { w = p[i]; key[i] = 0; }
-                scan();
-                atomicAdd(&s_cnt[ge], 1u);
-            }
-            w = __shfl_sync(0xffffffffu, w, (lane & ~(L - 1)) + (gk != 0 ? ge / V : 0));
-            if (gk == 0) w = 0.0f;
-            wsum += w;
-            if (j % L == li) {
-#pragma unroll
-                for (int s = 0; s < SLOTS; ++s)
-                    if (s == j / L) { my_id[s] = gk != 0 ? static_cast<uint32_t>(ge) : static_cast<uint32_t>(E); my_w[s] = w; }
-            }
-        }
-        if (in) {
-#pragma unroll
-            for (int s = 0; s < SLOTS; ++s) {
-                const int j = s * L + li;
-                if (j < a.k) {
-                    const bool picked = my_id[s] != static_cast<uint32_t>(E);
-                    a.ids[t * a.k + j] = my_id[s];
-                    a.weights[t * a.k + j] = a.normalize && picked ? my_w[s] / wsum : my_w[s];
+                    for (int i = 0; i < V; ++i)
+                        if (x[i] >= bound) {
+                            cv[at] = x[i];
+                            ce[at] = static_cast<uint16_t>(i * 32 + lane);
+                            ++at;
+                        }
+                    __syncwarp();
+                    const float mine = cv[lane];  // candidates stand in order of their expert
+                    int rank = 0;
+                    for (int j = 0; j < total; j += 4) {
+                        const float4 o = *reinterpret_cast<const float4*>(cv + j);
+                        rank += o.x > mine || (o.x == mine && j < lane);
+                        rank += o.y > mine || (o.y == mine && j + 1 < lane);
+                        rank += o.z > mine || (o.z == mine && j + 2 < lane);
+                        rank += o.w > mine || (o.w == mine && j + 3 < lane);
+                    }
+                    const bool chosen = lane < total && rank < k;
+                    const float w = chosen ? weight(mine) : 0.0f;
+                    wsum = group_sum<32>(w);
+                    if (lane >= total && lane < k) pick[lane] = make_uint2(E, 0);  // choices it cannot make
+                    if (chosen) {
+                        const int c = ce[lane];
+                        const uint32_t e = static_cast<uint32_t>((c & 31) * V + (c >> 5));
+                        pick[rank] = make_uint2(e, __float_as_uint(w));
+                        atomicAdd(&s_cnt[e], 1u);
+                    }
                 }
             }
         }
+        if (!done) {
+            float best;
+            int at;
+            auto scan = [&] {
+                best = -INFINITY;
+                at = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (x[i] > best) { best = x[i]; at = i; }
+            };
+            scan();
+            for (int j = 0; j < k; ++j) {
+                float gv = best;
+                int ge = e0 + at;
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) {
+                    const float ov = __shfl_xor_sync(0xffffffffu, gv, o);
+                    const int oe = __shfl_xor_sync(0xffffffffu, ge, o);
+                    if (ov > gv || (ov == gv && oe < ge)) { gv = ov; ge = oe; }
+                }
+                const bool can = gv > -INFINITY;
+                const float w = can ? weight(gv) : 0.0f;
+                wsum += w;
+                if (j % L == li) pick[j] = make_uint2(can ? ge : E, __float_as_uint(w));
+                if (can && ge / V == li) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (i == at) x[i] = -INFINITY;
+                    scan();
+                    atomicAdd(&s_cnt[ge], 1u);
+                }
+            }
+        }
+        __syncwarp();
+        if (in) {
+            for (int j = li; j < k; j += L) {
+                const uint2 q = pick[j];
+                const float w = __uint_as_float(q.y);
+                a.ids[t * k + j] = q.x;
+                a.weights[t * k + j] = a.normalize && q.x != static_cast<uint32_t>(E) ? w / wsum : w;
+            }
+        }
+        __syncwarp();  // pick and cand are free again
     }
     // the block's sums: rows of a warp by a shuffle tree, then the warps in order
 #pragma unroll
@@ -218,18 +310,30 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a) {
     for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
     if (lane == 0) s_rows[warp] = rows;
     __syncthreads();
+    uint32_t v = 0;
+    for (int w = 0; w < RT_WARPS; ++w) v += s_rows[w];
+    const bool alone = gridDim.x == 1;  // a short batch: this block's sums are the result
     for (int e = threadIdx.x; e < E; e += RT_THREADS) {
         float s = s_sum[0][e];
 #pragma unroll
         for (int w = 1; w < RT_WARPS; ++w) s += s_sum[w][e];
-        a.psum[static_cast<int64_t>(blockIdx.x) * E + e] = s;
-        a.pcnt[static_cast<int64_t>(blockIdx.x) * E + e] = s_cnt[e];
+        if (alone) {
+            const float m = v ? s / static_cast<float>(v) : 0.0f;
+            a.mean[e] = m;
+            a.counts[e] = s_cnt[e];
+            s_sum[0][e] = static_cast<float>(s_cnt[e]) * m;
+        } else {
+            a.psum[static_cast<int64_t>(blockIdx.x) * E + e] = s;
+            a.pcnt[static_cast<int64_t>(blockIdx.x) * E + e] = s_cnt[e];
+        }
     }
-    if (threadIdx.x == 0) {
-        uint32_t r = 0;
-        for (int w = 0; w < RT_WARPS; ++w) r += s_rows[w];
-        a.prow[blockIdx.x] = r;
+    if (!alone) {
+        if (threadIdx.x == 0) a.prow[blockIdx.x] = v;
+        return;
     }
+    __syncthreads();
+    if (warp == 0) write_loss(s_sum[0], E, k, v, a.loss);
+    if (threadIdx.x == 0) *a.rows = v;
 }
 
 // Adds the blocks' sums: 8 experts per block, 32 slots per expert (slot s takes
@@ -252,7 +356,7 @@ __global__ void __launch_bounds__(FIN_E * FIN_SLOTS)
     float p = 0.0f;
     uint32_t c = 0;
     if (e < E) {
-#pragma unroll 4
+#pragma unroll 16
         for (int b = slot; b < blocks; b += FIN_SLOTS) {
             p += psum[static_cast<int64_t>(b) * E + e];
             c += pcnt[static_cast<int64_t>(b) * E + e];
@@ -285,10 +389,7 @@ __global__ void __launch_bounds__(FIN_E * FIN_SLOTS)
     __syncthreads();
     if (!s_last || tid >= 32) return;
     __threadfence();
-    float s = 0.0f;
-    for (int q = tid; q < E; q += 32) s += __ldcg(terms + q);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (tid == 0) *loss = v ? s * (static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(v))) : 0.0f;
+    write_loss(terms, E, k, v, loss);
 }
 
 struct RouteBackArgs {
@@ -334,70 +435,97 @@ __global__ void __launch_bounds__(RT_THREADS) route_back_kernel(const RouteBackA
         for (int i = 0; i < V; ++i) q[i] = e0 + i < E ? s * static_cast<float>(a.counts[e0 + i]) : 0.0f;
     }
     const int64_t stride = static_cast<int64_t>(gridDim.x) * STEP;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * STEP; base < a.T; base += stride) {
-        const int64_t t = base + warp * GROUPS + grp;
-        const bool in = t < a.T;
-        const float lse = in ? a.lse[t] : INFINITY;
-        const bool counted = lse != INFINITY;  // false: the forward left the row out
-        float x[V];
-        if (counted) load_row<T, V>(static_cast<const T*>(a.logits) + t * E, e0, E, a.vec != 0, -INFINITY, x);
-        else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = -INFINITY;
+    const T* logits = static_cast<const T*>(a.logits);
+    // the next row's operands load under this one's arithmetic
+    int64_t t = static_cast<int64_t>(blockIdx.x) * STEP + warp * GROUPS + grp;
+    struct Slot {  // the row's choice li
+        uint32_t id;
+        float w, dw;
+    };
+    auto load_slot = [&](int64_t row) {
+        Slot z{0xffffffffu, 0.0f, 0.0f};
+        if (row < a.T && li < a.k) {
+            z.id = a.ids[row * a.k + li];
+            z.dw = a.dweights[row * a.k + li];
+            if (a.normalize) z.w = a.weights[row * a.k + li];
         }
+        return z;
+    };
+    Slot slot{0xffffffffu, 0.0f, 0.0f};
+    if (a.dweights != nullptr) slot = load_slot(t);
+    Raw<T, V> raw;
+    float lse_next = t < a.T ? a.lse[t] : INFINITY;
+    raw.load(logits + t * E, e0, E, a.vec != 0, t < a.T);
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * STEP; base < a.T; base += stride, t += stride) {
+        const bool in = t < a.T;
+        const float lse = lse_next;
+        const bool counted = lse != INFINITY;  // false: the forward left the row out
+        const float lse2 = lse * LOG2E;
+        float p[V], d[V], dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = counted ? exp2_approx(fmaf(raw.get(i), LOG2E, -lse2)) : 0.0f;
+        lse_next = t + stride < a.T ? a.lse[t + stride] : INFINITY;
+        raw.load(logits + (t + stride) * E, e0, E, a.vec != 0, t + stride < a.T);
+        float ex[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) ex[i] = 0.0f;
         if (a.dweights != nullptr) {
+            const Slot now = slot;
+            slot = load_slot(t + stride);
             float inner = 0.0f;
-            if (a.normalize && counted) {
-                for (int j = li; j < a.k; j += L)
-                    if (a.ids[t * a.k + j] < static_cast<uint32_t>(E)) inner += a.weights[t * a.k + j] * a.dweights[t * a.k + j];
+            if (a.normalize) {
+                if (counted && now.id < static_cast<uint32_t>(E)) inner = now.w * now.dw;
+                for (int j = li + L; j < a.k; j += L) {  // more choices than lanes
+                    if (counted && a.ids[t * a.k + j] < static_cast<uint32_t>(E))
+                        inner += a.weights[t * a.k + j] * a.dweights[t * a.k + j];
+                }
+                inner = group_sum<L>(inner);
             }
-            inner = group_sum<L>(inner);
             if (counted) {
-                for (int j = li; j < a.k; j += L) {
+                if (now.id < static_cast<uint32_t>(E)) extra[now.id] = a.normalize ? now.w * (now.dw - inner) : now.dw;
+                for (int j = li + L; j < a.k; j += L) {
                     const uint32_t id = a.ids[t * a.k + j];
-                    if (id < static_cast<uint32_t>(E)) {
-                        const float dw = a.dweights[t * a.k + j];
-                        extra[id] = a.normalize ? a.weights[t * a.k + j] * (dw - inner) : dw;
-                    }
+                    const float dw = a.dweights[t * a.k + j];
+                    if (id < static_cast<uint32_t>(E)) extra[id] = a.normalize ? a.weights[t * a.k + j] * (dw - inner) : dw;
                 }
             }
             __syncwarp();
-        }
-        float p[V], d[V], dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            p[i] = counted && e0 + i < E ? __expf(x[i] - lse) : 0.0f;
-            const float ex = extra[e0 + i];
-            d[i] = a.normalize ? q[i] : q[i] + ex;
-            dot += p[i] * d[i];
-        }
-        dot = group_sum<L>(dot);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float g = p[i] * (d[i] - dot);
-            d[i] = counted ? (a.normalize ? g + extra[e0 + i] : g) : 0.0f;
-        }
-        if (a.dweights != nullptr) {
+            for (int i = 0; i < V; ++i) ex[i] = extra[e0 + i];
             __syncwarp();
             if (counted) {
-                for (int j = li; j < a.k; j += L) {
+                if (now.id < static_cast<uint32_t>(E)) extra[now.id] = 0.0f;
+                for (int j = li + L; j < a.k; j += L) {
                     const uint32_t id = a.ids[t * a.k + j];
                     if (id < static_cast<uint32_t>(E)) extra[id] = 0.0f;
                 }
             }
             __syncwarp();
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            d[i] = a.normalize ? q[i] : q[i] + ex[i];
+            dot = fmaf(p[i], d[i], dot);
+        }
+        dot = group_sum<L>(dot);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float g = p[i] * (d[i] - dot);
+            d[i] = a.normalize ? g + ex[i] : g;
+        }
         if (!in) continue;
         T* out = static_cast<T*>(a.dlogits) + t * E + e0;
-        constexpr int PER = 16 / sizeof(T);
         if (a.vec && e0 + V <= E) {
+            constexpr int WORDS = V * sizeof(T) / 4;
+            uint32_t w[WORDS];
 #pragma unroll
-            for (int i = 0; i < V; i += PER) {
-                uint4 raw;
-                T* o = reinterpret_cast<T*>(&raw);
+            for (int i = 0; i < V; ++i) reinterpret_cast<T*>(w)[i] = down<T>(d[i]);
+            if constexpr (WORDS == 2) {
+                *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+            } else {
 #pragma unroll
-                for (int j = 0; j < PER; ++j) o[j] = down<T>(d[i + j]);
-                *reinterpret_cast<uint4*>(out + i) = raw;
+                for (int i = 0; i < WORDS; i += 4)
+                    reinterpret_cast<uint4*>(out)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
             }
         } else {
 #pragma unroll
@@ -415,18 +543,20 @@ cudaError_t with_layout(int64_t E, F&& f) {
     if (E <= 16) BI_LAYOUT(2, 8);
     if (E <= 32) BI_LAYOUT(4, 8);
     if (E <= 64) BI_LAYOUT(8, 8);
-    if (E <= 128) BI_LAYOUT(16, 8);
+    if (E <= 128) BI_LAYOUT(32, 4);
     if (E <= 256) BI_LAYOUT(32, 8);
     if (E <= 512) BI_LAYOUT(32, 16);
     BI_LAYOUT(32, 32);
 #undef BI_LAYOUT
 }
 
-int64_t lanes_for(int64_t E) { return E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : E <= 64 ? 8 : E <= 128 ? 16 : 32; }
+int64_t lanes_for(int64_t E) { return E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : E <= 64 ? 8 : 32; }
 
-// Rows per block: a whole number of block steps, about RT_BLOCKS blocks.
+// Rows per block: a whole number of block steps, about RT_BLOCKS blocks; up to
+// four steps of rows go to one block, which then needs no second kernel.
 int64_t rows_per_block(int64_t T, int64_t E) {
     const int64_t step = RT_WARPS * (32 / lanes_for(E));
+    if (T <= 4 * step) return 4 * step;
     const int64_t per = (T + RT_BLOCKS - 1) / RT_BLOCKS;
     return lmax(1, (per + step - 1) / step) * step;
 }
@@ -488,23 +618,27 @@ bi_status bi_router_forward(bi_engine eng, uint32_t* ids, float* weights, uint32
         return err == cudaSuccess ? BI_OK : cuda_fail(eng, err, "bi_router_forward");
     }
     const int64_t per = rows_per_block(t, e), blocks = (t + per - 1) / per;
-    // scratch: block sums | block counts | block rows | loss terms | ticket
-    Scratch sc(eng, s, static_cast<size_t>(4 * (2 * blocks * e + blocks + e + 1)));
+    // scratch (more than one block): block sums | block counts | block rows | loss terms | ticket
+    Scratch sc(eng, s, blocks > 1 ? static_cast<size_t>(4 * (2 * blocks * e + blocks + e + 1)) : 0);
     if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "router scratch");
     RouteArgs a{};
     a.ids = ids; a.weights = weights; a.lse = lse; a.logits = logits; a.valid = valid;
-    a.psum = static_cast<float*>(sc.ptr);
-    a.pcnt = reinterpret_cast<uint32_t*>(a.psum + blocks * e);
-    a.prow = a.pcnt + blocks * e;
-    float* terms = reinterpret_cast<float*>(a.prow + blocks);
-    a.ticket = reinterpret_cast<uint32_t*>(terms + e);
+    float* terms = nullptr;
+    if (blocks > 1) {
+        a.psum = static_cast<float*>(sc.ptr);
+        a.pcnt = reinterpret_cast<uint32_t*>(a.psum + blocks * e);
+        a.prow = a.pcnt + blocks * e;
+        terms = reinterpret_cast<float*>(a.prow + blocks);
+        a.ticket = reinterpret_cast<uint32_t*>(terms + e);
+    }
+    a.counts = counts; a.rows = rows; a.mean = mean_prob; a.loss = loss;
     a.T = t; a.rows_per_block = per;
     a.E = static_cast<int>(e); a.k = static_cast<int>(k); a.normalize = normalize != 0;
     a.vec = row_vectors(logits, e, dtype);
     err = dtype == BI_F32 ? forward_t<float>(c, a, blocks)
         : dtype == BI_BF16 ? forward_t<__nv_bfloat16>(c, a, blocks) : forward_t<__half>(c, a, blocks);
-    if (err == cudaSuccess) {
-        c.count();
+    if (err == cudaSuccess) c.count();
+    if (err == cudaSuccess && blocks > 1) {
         err = launch_pdl(route_finish_kernel, dim3(static_cast<unsigned>((e + FIN_E - 1) / FIN_E)),
                          dim3(FIN_E * FIN_SLOTS), 0, c.stream, a.psum, a.pcnt, a.prow, terms, a.ticket, counts, rows,
                          mean_prob, loss, static_cast<int>(blocks), a.E, a.k);

@@ -221,9 +221,11 @@ def test_empty_and_refusals(eng):
     assert bi.bi_router_backward(eng.handle, None, x, o["lse"], o["ids"], o["weights"], o["counts"], o["rows"], None, None,
                                  4, 8, 2, 1, "f32") == bi.BI_ERR_INVALID_ARG
     assert bi.bi_router_forward(None, *[16] * 9, 1, 1, 1, 1, "f32", 0) == bi.BI_ERR_INVALID_ARG
-    bi.bi_engine_fail_allocations(eng.handle, 1)
-    assert st() == bi.BI_ERR_OOM
+    bi.bi_engine_fail_allocations(eng.handle, 1)  # a batch of several blocks takes scratch
+    q, big = outputs(5000, 8, 2), torch.randn(5000, 8, device="cuda")
+    assert bi.bi_router_forward(eng.handle, *[q[v] for v in NAMES], big, None, 5000, 8, 2, 1, "f32") == bi.BI_ERR_OOM
     bi.bi_engine_fail_allocations(eng.handle, 0)
+    assert (q["ids"] == -7).all()
 
 
 def test_unaligned_rows(eng):
