@@ -199,8 +199,10 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     narrow_finish_tc_kernel(const float* partial, const float* h_in, const uint32_t* ids, const float* scales, float* h,
                             T* hh, T* v4, int64_t M, int R, int rp, uint32_t G, int pieces, int width) {
-    grid_dep_wait();
+    // the dependents first: a small-tile product starts on the shared weight while
+    // h is still in the making, and waits for this kernel before it reads it
     grid_dep_launch();
+    grid_dep_wait();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= M * width) return;
     const int64_t m = i / width;

@@ -71,6 +71,12 @@ __host__ __device__ inline int64_t adapter_grad_cols(int R) { return (R + 63) / 
 cudaError_t tc_adapter_rows(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
                             const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
                             int64_t K, int64_t N, int R, int64_t G);
+// The same by 128 x 64 tiles on single CTAs (adapter_tc.cu): identical bits, for
+// outputs that the 256 x 256 tiles of CTA pairs spread over too few SMs.
+bool adapter_small_tiles(const LaunchCtx& c, int64_t M, int64_t C);
+cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
+                                  const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
+                                  int64_t K, int64_t N, int R, int64_t G);
 // The narrow product on the tensor cores (adapter_tc.cu): partial[piece][m][rp] =
 // the piece's sum of z[m,l] p[g][r,l], rp = R rounded up to 16 the row stride.
 cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, const void* z, const void* p,

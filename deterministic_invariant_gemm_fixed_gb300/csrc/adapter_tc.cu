@@ -250,6 +250,302 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     }
 }
 
+// ---------------------------------------------------------------- small tiles
+//
+// The projection with its adapters' terms by tiles of 128 rows x 64 columns, one
+// per CTA (cta_group::1), for few rows or narrow outputs.  A decoding batch is
+// bound by reading W once (4096 x 4096: 33.5 MB, 5 us at the copy rate); 256-column
+// tiles would read it with a quarter of the SMs.  Every output element is the
+// same chain as in the CTA-pair kernel (64-wide blocks of the contraction
+// ascending, then the adapter's ranks ascending, high part before remainder), so
+// its bits are the same.  Measured, bf16 4096 x 4096, rank 16: see
+// adapter_small_tiles.
+//
+// For up to 64 rows the A tiles hold 64 rows: the MMA's other 64 rows are whatever
+// stands behind them in shared memory, and their accumulator lanes are not read.
+// The rows' inner products (up to rank 64) stay in shared memory, and a ring
+// stage then carries four adapters' 16 ranks of B: a batch in which every row has
+// an adapter of its own reads little besides these.
+//
+// The base product needs nothing of the kernels just before this one (plan,
+// narrow product, finish), so it starts under them (programmatic launch): only
+// the adapters' part waits for the previous kernel (grid_dep_wait), and x and w
+// are complete because the plan kernel waited for whatever wrote them before
+// anything that depends on it could start.
+constexpr int SM_THREADS = 192, SM_COLS = 64, SM_B = 64 * 128, SM_MAX_STAGES = 12;
+constexpr int SM_BARS = 2 * SM_MAX_STAGES + 3;
+constexpr int SM_TAIL = SM_BARS * 8 + 16 + 128 * 4 + 128 * 16 + 64;  // barriers, slots, adapter list and masks
+
+struct SmallParams {
+    AdapterPlan plan;
+    void* out;
+    const void* bias;
+    int64_t M, C;
+    int R, num_kb, stages, resident;  // resident: 32-rank parts of h kept in shared memory (0: streamed)
+    int* status;
+    unsigned long long wait_limit;
+};
+
+__device__ __forceinline__ void mma_one_masked(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint4 off) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
+        : "memory");
+}
+
+template <int FMT, int AR, bool B_MN>
+__global__ void __launch_bounds__(SM_THREADS, 1)
+    small_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmQ, const SmallParams p) {
+    constexpr int A_BYTES = AR * 128, STAGE = A_BYTES + SM_B;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_u32(smem);
+    const int stages = p.stages;
+    const uint32_t hbase = sbase + stages * STAGE;
+    // (a 128-row MMA on a 64-row tile at the very end reads up to 8 KB of what follows)
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * STAGE + p.resident * A_BYTES);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (SM_MAX_STAGES + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * SM_MAX_STAGES), h_bar = done_bar + 8, list_bar = done_bar + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile uint32_t* s_count = tmem_slot + 2;
+    uint4* s_mask = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 15) & ~uintptr_t(15));
+    uint32_t* s_id = reinterpret_cast<uint32_t*>(s_mask + 128);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row0 = static_cast<int>(blockIdx.y) * 128, col0 = static_cast<int>(blockIdx.x) * SM_COLS;
+    const int rg = (p.R + 15) / 16;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        mbar_init(h_bar, 1);
+        mbar_init(list_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<64>(smem_u32(tmem_slot));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    grid_dep_launch();
+
+    if (warp == 0 && lane == 0) {
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        auto claim = [&](uint32_t bytes) {  // the next stage, free and expecting `bytes`
+            ok = mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+            if (!ok) return;
+            ++issued;
+            mbar_expect_tx(full_bar(s), bytes);
+        };
+        auto advance = [&] {
+            if (++s == stages) { s = 0; ph ^= 1u; }
+        };
+        for (int kb = 0; kb < p.num_kb && ok; ++kb) {
+            claim(STAGE);
+            if (!ok) break;
+            const uint32_t a = sbase + s * STAGE;
+            tma_load_2d(a, &tmX, kb * BK, row0, full_bar(s));
+            if (B_MN) tma_load_2d(a + A_BYTES, &tmW, col0, kb * BK, full_bar(s));
+            else tma_load_2d(a + A_BYTES, &tmW, kb * BK, col0, full_bar(s));
+            advance();
+        }
+        if (ok) ok = mbar_wait(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+        if (ok) {
+            grid_dep_wait();
+            const int steps = static_cast<int>(*s_count) * rg;
+            if (p.resident && steps) {
+                mbar_expect_tx(h_bar, p.resident * A_BYTES);
+                for (int c = 0; c < p.resident; ++c) tma_load_2d(hbase + c * A_BYTES, &tmH, c * 64, row0, h_bar);
+                for (int f = 0; f < steps && ok; f += 4) {
+                    const int n = min(4, steps - f);
+                    claim(n * 2048);
+                    if (!ok) break;
+                    for (int i = 0; i < n; ++i)
+                        tma_load_3d(sbase + s * STAGE + A_BYTES + i * 2048, &tmQ, col0, ((f + i) % rg) * 16,
+                                    static_cast<int>(s_id[(f + i) / rg]), full_bar(s));
+                    advance();
+                }
+            } else {
+                for (int f = 0; f < steps && ok;) {  // one 32-rank part of one adapter
+                    const int j = f % rg, n = min(2, rg - j);
+                    claim(A_BYTES + n * 2048);
+                    if (!ok) break;
+                    const uint32_t a = sbase + s * STAGE;
+                    tma_load_2d(a, &tmH, (j / 2) * 64, row0, full_bar(s));
+                    for (int i = 0; i < n; ++i)
+                        tma_load_3d(a + A_BYTES + i * 2048, &tmQ, col0, (j + i) * 16, static_cast<int>(s_id[f / rg]), full_bar(s));
+                    f += n;
+                    advance();
+                }
+            }
+        }
+        if (!ok) drain_copies(full_bar, issued, stages);
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t idesc = instr_desc(FMT, false, B_MN, SM_COLS), idesc_q = instr_desc(FMT, false, true, SM_COLS);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        auto take = [&] {
+            ok = mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA);
+            tc_fence_after();
+        };
+        auto release = [&] {
+            mma_commit(empty_bar(s));
+            if (++s == stages) { s = 0; ph ^= 1u; }
+        };
+        for (int kb = 0; kb < p.num_kb && ok; ++kb) {
+            take();
+            if (!ok) break;
+            const uint32_t a = sbase + s * STAGE, b = a + A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_one(tmem_base, smem_desc(a + kk * 32, 16, 1024),
+                        B_MN ? smem_desc(b + kk * 2048, 8192, 1024) : smem_desc(b + kk * 32, 16, 1024), idesc,
+                        (kb | kk) != 0 ? 1u : 0u);
+            release();
+        }
+        if (ok) ok = mbar_wait(list_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        if (ok) {
+            const int steps = static_cast<int>(*s_count) * rg;
+            if (p.resident && steps) ok = mbar_wait(h_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+            for (int f = 0; f < steps && ok;) {
+                take();
+                if (!ok) break;
+                const uint32_t st = sbase + s * STAGE;
+                const int n = p.resident ? min(4, steps - f) : min(2, rg - f % rg);
+                for (int i = 0; i < n; ++i) {
+                    const int e = (f + i) / rg, j = (f + i) % rg;
+                    const uint4 m = s_mask[e];
+                    const uint4 off = make_uint4(~m.x, ~m.y, ~m.z, ~m.w);
+                    const uint32_t a = (p.resident ? hbase + (j / 2) * A_BYTES : st) + (j % 2) * 32;
+                    const uint64_t bd = smem_desc(st + A_BYTES + i * 2048, 8192, 1024);
+                    mma_one_masked(tmem_base, smem_desc(a, 16, 1024), bd, idesc_q, off);
+                    mma_one_masked(tmem_base, smem_desc(a + 64, 16, 1024), bd, idesc_q, off);
+                }
+                f += n;
+                release();
+            }
+        }
+        mma_commit(done_bar);
+        mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+    } else if (warp >= 2) {
+        const int w = warp & 3;
+        if (warp == 2) {  // the adapters of this half of the plan tile, in the plan's order
+            grid_dep_wait();
+            const int64_t tile = blockIdx.y >> 1;
+            const int half = blockIdx.y & 1;
+            const uint32_t n = p.plan.count[tile];
+            uint4 m[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                m[q] = q * 32 + lane < n
+                           ? *reinterpret_cast<const uint4*>(p.plan.masks + (tile * ADAPTER_TILE + q * 32 + lane) * 8 + 4 * half)
+                           : make_uint4(0, 0, 0, 0);
+            uint32_t total = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const bool has = (m[q].x | m[q].y | m[q].z | m[q].w) != 0;
+                const uint32_t b = __ballot_sync(0xffffffffu, has);
+                if (has) {
+                    const uint32_t at = total + __popc(b & ((1u << lane) - 1));
+                    s_mask[at] = m[q];
+                    s_id[at] = p.plan.ids[tile * ADAPTER_TILE + q * 32 + lane];
+                }
+                total += __popc(b);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                *s_count = total;
+                mbar_arrive(list_bar);
+            }
+            __syncwarp();
+        }
+        bool ok = mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
+        ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+        if (ok) {
+            tc_fence_after();
+            using O = OutT<FMT>;
+            using T = typename O::T;
+            const int64_t row = row0 + 32 * w + lane;
+            T* dst = static_cast<T*>(p.out) + row * p.C + col0;
+            if (row0 + 32 * w < p.M && 32 * w < AR) {
+#pragma unroll
+                for (int c = 0; c < SM_COLS; c += 16) {
+                    if (col0 + c >= p.C) break;
+                    uint32_t v[16];
+                    tmem_ld16(tmem_base + (static_cast<uint32_t>(32 * w) << 16) + c, v);
+                    if (row < p.M) {
+                        float f[16];
+                        const int have = static_cast<int>(lmin(16, p.C - col0 - c));  // 8 or 16
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            f[i] = __uint_as_float(v[i]);
+                            if (p.bias != nullptr && i < have) f[i] = __fadd_rn(f[i], O::load(p.bias, col0 + c + i));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8)
+                            if (i < have)
+                                *reinterpret_cast<uint4*>(dst + c + i) =
+                                    make_uint4(O::pack(f[i], f[i + 1]), O::pack(f[i + 2], f[i + 3]), O::pack(f[i + 4], f[i + 5]),
+                                               O::pack(f[i + 6], f[i + 7]));
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<64>(tmem_base);
+    }
+}
+
+constexpr int SM_LIMIT = 227 * 1024;  // shared memory of one CTA
+
+template <int FMT, int AR, bool B_MN>
+cudaError_t small_rows_t(const LaunchCtx& c, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& h,
+                         const CUtensorMap& q, SmallParams p, dim3 grid) {
+    auto kern = small_rows_kernel<FMT, AR, B_MN>;
+    static PerDeviceOnce setup;
+    const cudaError_t e = setup.run(c.eng->device, [&](int&) {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_LIMIT);
+    });
+    if (e != cudaSuccess) return e;
+    // a whole SM's shared memory where the tiles leave SMs over, else half
+    const int budget = int64_t(grid.x) * grid.y <= c.sm_count ? SM_LIMIT : SM_LIMIT / 2 - 1024;
+    constexpr int STAGE = AR * 128 + SM_B;
+    const int pad = 1024 + SM_TAIL + (AR < 128 ? 8192 : 0);  // alignment; the 128-row MMA's reach
+    p.resident = p.R <= 64 ? (p.R + 31) / 32 : 0;
+    p.stages = min(SM_MAX_STAGES, (budget - pad - p.resident * AR * 128) / STAGE);
+    const int bytes = pad + p.resident * AR * 128 + p.stages * STAGE;
+    const cudaError_t r = launch_pdl(kern, grid, dim3(SM_THREADS), bytes, c.stream, x, w, h, q, p);
+    if (r == cudaSuccess) c.count();
+    return r;
+}
+
+template <int FMT>
+cudaError_t small_rows_fmt(const LaunchCtx& c, int dx, int64_t M, const CUtensorMap& x, const CUtensorMap& w,
+                           const CUtensorMap& h, const CUtensorMap& q, const SmallParams& p, dim3 grid) {
+    if (M <= 64)
+        return dx ? small_rows_t<FMT, 64, false>(c, x, w, h, q, p, grid) : small_rows_t<FMT, 64, true>(c, x, w, h, q, p, grid);
+    return dx ? small_rows_t<FMT, 128, false>(c, x, w, h, q, p, grid) : small_rows_t<FMT, 128, true>(c, x, w, h, q, p, grid);
+}
+
 // ---------------------------------------------------------------- gradients
 //
 // A CTA takes one chunk (at most 1024) of one adapter's sorted rows, 128 columns
@@ -476,6 +772,31 @@ cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, c
     e = launch_pdl(narrow_tc_kernel, grid, dim3(NP_THREADS), NP_SMEM, c.stream, x, w, p);
     if (e == cudaSuccess) c.count();
     return e;
+}
+
+bool adapter_small_tiles(const LaunchCtx& c, int64_t M, int64_t C) {
+    const int64_t pairs = (M + 255) / 256 * ((C + 255) / 256);
+    return pairs <= c.sm_count / 4;
+}
+
+cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
+                                  const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
+                                  int64_t K, int64_t N, int R, int64_t G) {
+    const int64_t L = dx ? N : K, C = dx ? K : N;
+    const uint32_t ar = M <= 64 ? 64 : 128;
+    CUtensorMap mx, mw, mh, mq;
+    cudaError_t e;
+    if ((e = make_map(&mx, dt, z, L, M, 1, ar)) != cudaSuccess) return e;
+    if ((e = make_map(&mw, dt, w, N, K, 1, 64)) != cudaSuccess) return e;
+    if ((e = make_map(&mh, dt, hh, adapter_part_cols(R), M, 1, ar)) != cudaSuccess) return e;
+    if ((e = make_map(&mq, dt, q, C, R, G, 16, true)) != cudaSuccess) return e;
+    SmallParams p{};
+    p.plan = plan; p.out = out; p.bias = bias; p.M = M; p.C = C; p.R = R;
+    p.num_kb = static_cast<int>((L + BK - 1) / BK);
+    p.status = c.status; p.wait_limit = c.wait_limit_ns;
+    const dim3 grid(static_cast<unsigned>((C + SM_COLS - 1) / SM_COLS), static_cast<unsigned>((M + 127) / 128));
+    return dt == BI_BF16 ? small_rows_fmt<1>(c, dx, M, mx, mw, mh, mq, p, grid)
+                         : small_rows_fmt<0>(c, dx, M, mx, mw, mh, mq, p, grid);
 }
 
 cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, float* out, float* parts, const void* v4, const void* z,

@@ -130,7 +130,7 @@ struct RouteArgs {
 // logits at or above the bound): k times the largest logit of the row's lanes.
 // 8 of 256 experts, 131072 rows in f32: 245 us by the second way.
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(RT_THREADS, V <= 8 ? 4 : 1) route_kernel(const RouteArgs a) {
     constexpr int GROUPS = 32 / L;             // rows per warp
     constexpr int STEP = RT_WARPS * GROUPS;    // rows per block and step
     constexpr int MAXK = L * V < RT_MAX_K ? L * V : static_cast<int>(RT_MAX_K);
@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a) {
             sum += p[i];
         }
         sum = group_sum<L>(sum);
-        const float inv = counted ? 1.0f / sum : 0.0f;
+        const float inv = counted ? __fdividef(1.0f, sum) : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
         if (in && li == 0) {
-            a.lse[t] = counted ? (m2 + log2f(sum)) * LN2 : INFINITY;
+            a.lse[t] = counted ? (m2 + __log2f(sum)) * LN2 : INFINITY;
             rows += counted;
         }
         auto weight = [&](float v) { return exp2_approx(fmaf(v, LOG2E, -m2)) * inv; };
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a) {
                 const uint2 q = pick[j];
                 const float w = __uint_as_float(q.y);
                 a.ids[t * k + j] = q.x;
-                a.weights[t * k + j] = a.normalize && q.x != static_cast<uint32_t>(E) ? w / wsum : w;
+                a.weights[t * k + j] = a.normalize && q.x != static_cast<uint32_t>(E) ? __fdividef(w, wsum) : w;
             }
         }
         __syncwarp();  // pick and cand are free again

@@ -602,8 +602,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tc_fence_after();
                         const uint32_t a_s = sbase + s * P_STAGE_BYTES, b_s = a_s + P_A_BYTES;
                         const int steps = p.rank - 32 * c > 16 ? 2 : 1;  // K = 16 steps with ranks in them
-                        for (int part = 0; part < 2; ++part)
-                            for (int j = 0; j < steps; ++j)
+                        for (int j = 0; j < steps; ++j)
+                            for (int part = 0; part < 2; ++part)
                                 mma_pair_masked(d_tmem, smem_desc(a_s + (2 * part + j) * 32, 16, 1024),
                                                 smem_desc(b_s + j * 2048, BKE * 128, 1024), idesc_q, off);
                         mma_commit_pair_mc(empty_bar(s), 0x3);
@@ -1405,6 +1405,8 @@ cudaError_t tc_dx(const LaunchCtx& c, bi_dtype dt, void* dx, const void* dy, con
 cudaError_t tc_adapter_rows(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
                             const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
                             int64_t K, int64_t N, int R, int64_t G) {
+    if (forced_cols(c) == 0 && adapter_small_tiles(c, M, dx ? K : N))
+        return tc_adapter_rows_small(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G);
     return dt == BI_BF16 ? adapter_rows_t<1>(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G)
                          : adapter_rows_t<0>(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G);
 }

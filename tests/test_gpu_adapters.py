@@ -326,3 +326,20 @@ def test_nothing_is_written_outside_the_outputs(eng, dtype, tc):
     torch.cuda.synchronize()
     for buf, _ in outs.values():
         assert bool((buf[:pad] == 7).all() and (buf[-pad:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,k,n,r,g", [(1, 512, 256, 16, 2), (37, 1032, 328, 20, 9), (64, 136, 1000, 64, 64), (65, 264, 72, 8, 3),
+                                       (200, 520, 640, 100, 30), (300, 64, 64, 33, 200), (513, 768, 264, 48, 4)])
+def test_small_and_paired_tiles_give_the_same_bits(eng, m, k, n, r, g, dtype):
+    """The tile shape is chosen from the number of tiles; forcing the CTA pairs' width must not change a bit."""
+    d = inputs(m, k, n, r, g, dtype, seed=11, order="random")
+    y, h = forward(eng, d, 1)
+    dx = backward(eng, d, h, 1, ("dx",))[0]
+    bi.bi_engine_set_tile_cols(eng.handle, 256)
+    try:
+        y2, h2 = forward(eng, d, 1)
+        dx2 = backward(eng, d, h2, 1, ("dx",))[0]
+    finally:
+        bi.bi_engine_set_tile_cols(eng.handle, 0)
+    assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(dx, dx2)
