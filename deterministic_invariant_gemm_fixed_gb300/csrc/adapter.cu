@@ -23,6 +23,7 @@
 
 #include "abi_util.h"
 #include "adapter.h"
+#include "adapter_plan.cuh"
 
 namespace bi {
 namespace {
@@ -38,59 +39,12 @@ template <> __device__ __forceinline__ __half down<__half>(float v) { return __f
 
 // ---------------------------------------------------------------- plan
 
-// One block per 256-row tile, one thread per row.  Rows of a warp with the same
-// adapter are found by a match; the first of them stands for the group and
-// looks for its adapter among the groups of the warps before (then it is no
-// new entry), and gathers the masks of the warps after.
 __global__ void __launch_bounds__(256) adapter_plan_kernel(const uint32_t* ids, int64_t M, uint32_t G, AdapterPlan plan) {
-    __shared__ uint32_t s_id[256], s_mask[256];  // groups of warp w at [32 w, 32 w + s_n[w])
-    __shared__ uint32_t s_n[8], s_new[8];
+    __shared__ PlanSmem sm;
     grid_dep_wait();
     grid_dep_launch();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 256 + tid;
-    const uint32_t id = row < M ? ids[row] : G;
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    const bool lead = id < G && (same & ((1u << lane) - 1)) == 0;
-    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
-    if (lead) {
-        const int k = 32 * warp + __popc(leads & ((1u << lane) - 1));
-        s_id[k] = id;
-        s_mask[k] = same;
-    }
-    if (lane == 0) s_n[warp] = __popc(leads);
-    __syncthreads();
-    uint32_t mask[8];
-    bool fresh = lead;
-    if (lead) {
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            mask[w] = 0;
-            for (uint32_t i = 0; i < s_n[w]; ++i)
-                if (s_id[32 * w + i] == id) {
-                    mask[w] = s_mask[32 * w + i];
-                    break;
-                }
-            if (w < warp && mask[w] != 0) fresh = false;
-        }
-    }
-    const uint32_t fr = __ballot_sync(0xffffffffu, fresh);
-    if (lane == 0) s_new[warp] = __popc(fr);
-    __syncthreads();
-    uint32_t at = __popc(fr & ((1u << lane) - 1));
-    for (int w = 0; w < warp; ++w) at += s_new[w];
-    if (fresh) {
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 256 + at;
-        plan.ids[slot] = id;
-        uint4* m = reinterpret_cast<uint4*>(plan.masks + slot * 8);
-        m[0] = make_uint4(mask[0], mask[1], mask[2], mask[3]);
-        m[1] = make_uint4(mask[4], mask[5], mask[6], mask[7]);
-    }
-    if (tid == 0) {
-        uint32_t n = 0;
-        for (int w = 0; w < 8; ++w) n += s_new[w];
-        plan.count[blockIdx.x] = n;
-    }
+    plan_tile<8>(ids, M, G, blockIdx.x, threadIdx.x >> 5, sm, [] { __syncthreads(); });
+    plan_store(plan, blockIdx.x, sm, threadIdx.x, 256);
 }
 
 // Chunk tables of the sorted rows (AdapterChunks), one block.
@@ -504,8 +458,13 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
         uint8_t* p = static_cast<uint8_t*>(sc.ptr);
         const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
         float* part = reinterpret_cast<float*>(p + o_part);
-        cudaError_t e = build_plan(c, row_adapters, m, g, plan);
-        if (e == cudaSuccess) e = tc_adapter_narrow(c, dtype, part, x, a, plan, m, k, R, g);
+        cudaError_t e = tc_adapter_narrow(c, dtype, part, x, a, row_adapters, plan, m, k, R, g);
+        if (adapter_small_fuses(c, m, n, k, R)) {
+            const AdapterPieces fuse{part, row_adapters, scales, h, pieces};
+            if (e == cudaSuccess)
+                e = tc_adapter_rows_small(c, dtype, 0, y, x, w, bias, nullptr, b, plan, m, k, n, R, g, &fuse);
+            return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
+        }
         if (e == cudaSuccess)
             e = narrow_finish_tc(c, dtype, part, nullptr, row_adapters, scales, h, p + o_hh, nullptr, m, R, g, pieces);
         if (e == cudaSuccess) e = tc_adapter_rows(c, dtype, 0, y, x, w, bias, p + o_hh, b, plan, m, k, n, R, g);
@@ -597,8 +556,7 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         float* sums = reinterpret_cast<float*>(p + o_sum);
         cudaError_t e = cudaSuccess;
         if (need_u) {
-            e = build_plan(c, row_adapters, m, g, plan);
-            if (e == cudaSuccess) e = tc_adapter_narrow(c, dtype, part, dy, b, plan, m, n, R, g);
+            e = tc_adapter_narrow(c, dtype, part, dy, b, row_adapters, plan, m, n, R, g);
             if (e == cudaSuccess)
                 e = narrow_finish_tc(c, dtype, part, nullptr, row_adapters, scales, nullptr, dx ? p + o_uu : nullptr,
                                      da ? p + o_u3 : nullptr, m, R, g, pieces);

@@ -17,7 +17,7 @@ constexpr int64_t ADAPTER_CHUNK = 1024;
 constexpr int ADAPTER_TILE = 256;  // rows per plan tile
 
 // Which adapters the rows of each 256-row tile have: per tile the number of
-// distinct ones (in order of their first row), and for each its index and a bit
+// distinct ones, and for each its index and a bit
 // per row.
 struct AdapterPlan {
     uint32_t* count;  // [tiles]
@@ -74,13 +74,23 @@ cudaError_t tc_adapter_rows(const LaunchCtx& c, bi_dtype dt, int dx, void* out, 
 // The same by 128 x 64 tiles on single CTAs (adapter_tc.cu): identical bits, for
 // outputs that the 256 x 256 tiles of CTA pairs spread over too few SMs.
 bool adapter_small_tiles(const LaunchCtx& c, int64_t M, int64_t C);
+// ... and whether they also add up the pieces of h (then no finish kernel runs).
+bool adapter_small_fuses(const LaunchCtx& c, int64_t M, int64_t C, int64_t L, int R);
+struct AdapterPieces {
+    const float* partial;
+    const uint32_t* ids;
+    const float* scales;
+    float* h;
+    int pieces;
+};
 cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
                                   const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
-                                  int64_t K, int64_t N, int R, int64_t G);
+                                  int64_t K, int64_t N, int R, int64_t G, const AdapterPieces* fuse = nullptr);
 // The narrow product on the tensor cores (adapter_tc.cu): partial[piece][m][rp] =
 // the piece's sum of z[m,l] p[g][r,l], rp = R rounded up to 16 the row stride.
+// Also makes the plan of the rows' adapters.
 cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, const void* z, const void* p,
-                              const AdapterPlan& plan, int64_t M, int64_t L, int R, int64_t G);
+                              const uint32_t* ids, const AdapterPlan& plan, int64_t M, int64_t L, int R, int64_t G);
 // dA and dB on the tensor cores: out[g][r,c] (or its chunks' partial slots) =
 // sum over the adapter's sorted rows of v[m,r] z[m,c], v in four parts [M,
 // adapter_grad_cols(R)].

@@ -2,6 +2,7 @@
 // adapters' gradients.  The wide product runs inside the projection's own kernel
 // (tc.cu, mode ADAPTER).
 #include "adapter.h"
+#include "adapter_plan.cuh"
 #include "tc_common.cuh"
 
 namespace bi {
@@ -21,16 +22,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
-        : "memory");
+// 1 in one lane of the warp, always the same.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r;
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(lead)
+                 : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -44,12 +45,40 @@ template <int COLS>
 __device__ __forceinline__ void tmem_free(uint32_t base) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(COLS) : "memory");
 }
-// kind::f16, f32 accumulation, M = 128; format 0 f16, 1 bf16.
-__device__ __forceinline__ uint32_t instr_desc(int fmt, bool a_mn, bool b_mn, int n) {
+// kind::f16, f32 accumulation; format 0 f16, 1 bf16.
+__device__ __forceinline__ uint32_t instr_desc(int fmt, bool a_mn, bool b_mn, int n, int m = 128) {
     const uint32_t f = static_cast<uint32_t>(fmt);
     return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
+
+// One 64-wide contraction block: four K = 16 MMAs, the operands' descriptors (low
+// words; the high words do not change) advancing by astep, bstep.  The issuing
+// thread's own instructions are what a small tile waits for (a block's four MMAs
+// of N = 64 take 130 cycles), so this is one asm statement without 64-bit
+// arithmetic.
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a, uint32_t ahi, uint32_t astep, uint32_t b, uint32_t bhi,
+                                          uint32_t bstep, uint32_t idesc, uint32_t acc, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %8, 0;\n\tsetp.eq.b32 q, 0, 0;\n\tsetp.ne.b32 e, %9, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%4, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %7, p;\n\t"
+        "add.u32 x, %1, %3;\n\tadd.u32 y, %4, %6;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %7, q;\n\t"
+        "add.u32 x, x, %3;\n\tadd.u32 y, y, %6;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %7, q;\n\t"
+        "add.u32 x, x, %3;\n\tadd.u32 y, y, %6;\n\tmov.b64 da, {x, %2};\n\tmov.b64 db, {y, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %7, q;\n\t}\n" ::"r"(d_tmem),
+        "r"(a), "r"(ahi), "r"(astep), "r"(b), "r"(bhi), "r"(bstep), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+// Low and high word of a tile's descriptor (128-byte swizzle, 8-row groups 1024
+// bytes apart): K-major, or MN-major with 8192 bytes from one 64-column atom to
+// the next.  One MMA's step along K: 32 bytes, or 16 rows of 128.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, bool mn) { return ((saddr & 0x3FFFFu) >> 4) | ((mn ? 512u : 1u) << 16); }
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t K_STEP = 32 >> 4, MN_STEP = 2048 >> 4;
 
 // A producer that gives up waits (a bounded number of tries) for the copies it
 // has issued before its CTA's shared memory goes away: the last min(issued,
@@ -73,16 +102,22 @@ __device__ __forceinline__ void drain_copies(Bar&& full_bar, int issued, int sta
 // small enough that a batch of 8192 rows gives 512 of them, and one of 64 rows
 // with an own adapter each 128.
 //
-// Roles: warp 0 TMA, warp 1 MMA, warps 2-5 epilogue; two CTAs per SM, so one
-// CTA's set-up and drain run beside the other's loads.
+// Roles: warp 0 TMA, warp 1 MMA, warps 2-5 plan and epilogue; two CTAs per SM, so
+// one CTA's set-up and drain run beside the other's loads.  Every CTA finds its
+// tile's adapters itself, while the first blocks of X are on their way (a kernel
+// of its own took 3 to 9 us before this one could start); the first CTA of each
+// tile leaves them in the plan for the kernels after.
 constexpr int NP_THREADS = 192, NP_STAGES = 4;
 constexpr int NP_A = 128 * 128, NP_B = 64 * 128, NP_STAGE = NP_A + NP_B;
-constexpr int NP_BARS = 2 * NP_STAGES + 5;
-constexpr int NP_SMEM = 1024 + NP_STAGES * NP_STAGE + NP_BARS * 8 + 16 + 128 * 8 + 256;
+constexpr int NP_BARS = 2 * NP_STAGES + 6;
+constexpr int NP_SMEM = 1024 + NP_STAGES * NP_STAGE + static_cast<int>(sizeof(PlanSmem)) + NP_BARS * 8 + 16 + 128 * 8 + 256;
+static_assert(NP_SMEM <= 113 * 1024, "two CTAs per SM");
 constexpr int NP_KB = static_cast<int>(ADAPTER_PIECE / BK);
 
 struct NarrowParams {
     AdapterPlan plan;
+    const uint32_t* ids;
+    uint32_t G;
     float* partial;
     int64_t M;
     int R, rp, num_kb, fmt;
@@ -96,20 +131,21 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sbase = smem_u32(smem);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NP_STAGES * NP_STAGE);
+    PlanSmem& pl = *reinterpret_cast<PlanSmem*>(smem + NP_STAGES * NP_STAGE);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NP_STAGES * NP_STAGE + sizeof(PlanSmem));
     const uint32_t bar0 = smem_u32(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (NP_STAGES + s); };
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * NP_STAGES + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * NP_STAGES + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * NP_STAGES + 4);
+    const uint32_t drain_bar = bar0 + 8u * (2 * NP_STAGES + 4), list_bar = drain_bar + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NP_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    uint32_t* s_count = tmem_slot + 2;
-    uint32_t* s_ent = tmem_slot + 4;  // the tile's entries with a row in this half: plan slot
+    volatile uint32_t* s_count = tmem_slot + 2;
+    uint32_t* s_ent = tmem_slot + 4;  // the tile's entries with a row in this half: their masks' place
     uint32_t* s_id = s_ent + 128;     // ... and adapter
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int64_t tile = blockIdx.x >> 1;
     const int half = blockIdx.x & 1;
     const int row0 = static_cast<int>(blockIdx.x) * 128;
@@ -123,6 +159,7 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
             mbar_init(tempty_bar(b), 4);
         }
         mbar_init(drain_bar, 1);
+        mbar_init(list_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -132,47 +169,41 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     tc_fence_after();
     grid_dep_wait();
     grid_dep_launch();
-    if (warp == 2) {
-        const uint32_t n = p.plan.count[tile];
-        uint32_t total = 0;
-        for (uint32_t i0 = 0; i0 < n; i0 += 32) {
-            const uint32_t i = i0 + lane;
-            bool has = false;
-            if (i < n) {
-                const uint4 m = *reinterpret_cast<const uint4*>(p.plan.masks + (tile * ADAPTER_TILE + i) * 8 + 4 * half);
-                has = (m.x | m.y | m.z | m.w) != 0;
-            }
-            const uint32_t b = __ballot_sync(0xffffffffu, has);
-            if (has) {
-                const uint32_t at = total + __popc(b & ((1u << lane) - 1));
-                s_ent[at] = i;
-                s_id[at] = p.plan.ids[tile * ADAPTER_TILE + i];
-            }
-            total += __popc(b);
-        }
-        if (lane == 0) *s_count = total;
-    }
-    __syncthreads();
-    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-    const int rg = p.rp / 16;                                    // groups of 16 ranks per adapter
-    const int groups = static_cast<int>(*s_count) * rg;          // of this tile
-    const int batches = (groups + 3) / 4;                        // four groups at a time
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
+    const int rg = p.rp / 16;  // groups of 16 ranks per adapter
     const int kb0 = blockIdx.y * NP_KB, nkb = min(NP_KB, p.num_kb - kb0);
 
     if (warp == 0 && lane == 0) {
-        int s = 0, issued = 0;
+        // the first blocks of X need no list: their bytes are expected and the
+        // copies issued now, the stages' own arrivals follow with the adapters'
+        const int early = min(NP_STAGES, nkb);
+        for (int kb = 0; kb < early; ++kb) {
+            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full_bar(kb)), "r"(NP_A) : "memory");
+            tma_load_2d(sbase + kb * NP_STAGE, &tmX, (kb0 + kb) * BK, row0, full_bar(kb));
+        }
+        const bool listed = mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+        const int groups = listed ? static_cast<int>(*s_count) * rg : 0, batches = (groups + 3) / 4;
+        int s = 0, fills = 0;
         uint32_t ph = 0;
+        if (static_cast<int>(blockIdx.z) >= batches) {  // nothing to multiply: let the early copies land
+            for (int kb = 0; kb < early; ++kb) mbar_expect_tx(full_bar(kb), 0);
+            drain_copies(full_bar, early, NP_STAGES);
+        }
         for (int q = blockIdx.z; q < batches; q += gridDim.z) {
             const int n = min(4, groups - 4 * q);
             for (int kb = 0; kb < nkb; ++kb) {
-                if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) {
-                    drain_copies(full_bar, issued, NP_STAGES);
-                    goto done_p;
-                }
-                ++issued;
-                mbar_expect_tx(full_bar(s), NP_A + n * 2048);
                 const uint32_t a = sbase + s * NP_STAGE;
-                tma_load_2d(a, &tmX, (kb0 + kb) * BK, row0, full_bar(s));
+                if (fills < early) {
+                    mbar_expect_tx(full_bar(s), n * 2048);
+                } else {
+                    if (!mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) {
+                        drain_copies(full_bar, fills, NP_STAGES);
+                        goto done_p;
+                    }
+                    mbar_expect_tx(full_bar(s), NP_A + n * 2048);
+                    tma_load_2d(a, &tmX, (kb0 + kb) * BK, row0, full_bar(s));
+                }
+                ++fills;
                 for (int i = 0; i < n; ++i) {
                     const int gi = 4 * q + i;
                     tma_load_3d(a + NP_A + i * 2048, &tmP, (kb0 + kb) * BK, (gi % rg) * 16, static_cast<int>(s_id[gi / rg]),
@@ -182,46 +213,71 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
             }
         }
     done_p:;
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
+        const uint32_t lead = elect_lane();
+        const bool listed = __all_sync(0xffffffffu, mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA));
+        const int groups = listed ? static_cast<int>(*s_count) * rg : 0, batches = (groups + 3) / 4;
         int s = 0, ab = 0;
         uint32_t ph = 0, aph = 0;
         for (int q = blockIdx.z; q < batches; q += gridDim.z) {
             const uint32_t idesc = instr_desc(p.fmt, false, false, 16 * min(4, groups - 4 * q));
-            if (!mbar_wait(tempty_bar(ab), aph ^ 1u, abort_flag, p, DEV_TIMEOUT_MMA)) goto done_m;
+            if (!__all_sync(0xffffffffu, mbar_wait_fast(tempty_bar(ab), aph ^ 1u, abort_flag, p, DEV_TIMEOUT_MMA))) goto done_m;
             tc_fence_after();
             for (int kb = 0; kb < nkb; ++kb) {
-                if (!mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA)) goto done_m;
+                if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA))) goto done_m;
                 tc_fence_after();
                 const uint32_t a = sbase + s * NP_STAGE, b = a + NP_A;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_one(tmem_base + ab * 64, smem_desc(a + kk * 32, 16, 1024), smem_desc(b + kk * 32, 16, 1024), idesc,
-                            (kb | kk) != 0 ? 1u : 0u);
-                mma_commit(empty_bar(s));
+                mma_block(tmem_base + ab * 64, desc_lo(a, false), DESC_HI, K_STEP, desc_lo(b, false), DESC_HI, K_STEP, idesc,
+                          kb != 0 ? 1u : 0u, lead);
+                mma_commit(empty_bar(s), lead);
                 if (++s == NP_STAGES) { s = 0; ph ^= 1u; }
             }
-            mma_commit(tfull_bar(ab));
+            mma_commit(tfull_bar(ab), lead);
             if (++ab == 2) { ab = 0; aph ^= 1u; }
         }
     done_m:
         // the MMAs issued above have finished before the CTA leaves, and with
         // them the copies they waited for
-        mma_commit(drain_bar);
-        mbar_wait(drain_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        mma_commit(drain_bar, lead);
+        mbar_wait_fast(drain_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
     } else if (warp >= 2) {
         const int w = warp & 3;  // the TMEM lanes a warp may read
+        auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        plan_tile<4>(p.ids, p.M, p.G, tile, warp - 2, pl, sync4);
+        if (half == 0 && blockIdx.y == 0 && blockIdx.z == 0) plan_store(p.plan, tile, pl, threadIdx.x - 64, 128);
+        if (warp == 2) {  // those with a row in this CTA's half
+            uint32_t total = 0;
+            for (uint32_t i0 = 0; i0 < pl.count; i0 += 32) {
+                const uint32_t i = i0 + lane;
+                const uint32_t place = i < pl.count ? pl.slot[i] : 0;
+                const uint4 m = i < pl.count ? pl.masks[place][half] : make_uint4(0, 0, 0, 0);
+                const bool has = (m.x | m.y | m.z | m.w) != 0;
+                const uint32_t b = __ballot_sync(0xffffffffu, has);
+                if (has) {
+                    const uint32_t at = total + __popc(b & ((1u << lane) - 1));
+                    s_ent[at] = place;
+                    s_id[at] = pl.ids[i];
+                }
+                total += __popc(b);
+            }
+            if (lane == 0) *s_count = total;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(list_bar);
+        }
+        sync4();
+        const int groups = static_cast<int>(*s_count) * rg, batches = (groups + 3) / 4;
         const int64_t row = row0 + 32 * w + lane;
         int ab = 0;
         uint32_t aph = 0;
         for (int q = blockIdx.z; q < batches; q += gridDim.z) {
             const int n = min(4, groups - 4 * q);
-            bool ok = mbar_wait(tfull_bar(ab), aph, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
+            bool ok = mbar_wait_fast(tfull_bar(ab), aph, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             for (int i = 0; i < n; ++i) {
                 const int gi = 4 * q + i;
-                const uint32_t mask = p.plan.masks[(tile * ADAPTER_TILE + s_ent[gi / rg]) * 8 + 4 * half + w];
+                const uint32_t mask = reinterpret_cast<const uint32_t*>(&pl.masks[s_ent[gi / rg]][half])[w];
                 if (mask == 0) continue;  // the same for the whole warp
                 __syncwarp();
                 uint32_t v[16];
@@ -261,11 +317,15 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
 // its bits are the same.  Measured, bf16 4096 x 4096, rank 16: see
 // adapter_small_tiles.
 //
-// For up to 64 rows the A tiles hold 64 rows: the MMA's other 64 rows are whatever
-// stands behind them in shared memory, and their accumulator lanes are not read.
+// Up to 64 rows take MMAs of 64 rows, which read half as much of A: a block's MMAs
+// of M = 128, N = 64 are bound by their operands' reads from shared memory.
 // The rows' inner products (up to rank 64) stay in shared memory, and a ring
 // stage then carries four adapters' 16 ranks of B: a batch in which every row has
 // an adapter of its own reads little besides these.
+//
+// Where the pieces of h are few (up to SM_FUSE sums for the tile's rows) the
+// epilogue warps add them up and lay them out in shared memory themselves, in the
+// finish kernel's order, and the first CTA of the row writes h: one launch less.
 //
 // The base product needs nothing of the kernels just before this one (plan,
 // narrow product, finish), so it starts under them (programmatic launch): only
@@ -281,6 +341,13 @@ struct SmallParams {
     void* out;
     const void* bias;
     int64_t M, C;
+    const float* partial;  // fused: the pieces of h [pieces][M][rp], and what makes s h of them
+    const uint32_t* ids;
+    const float* scales;
+    float* h;
+    uint32_t G;
+    int pieces, rp;
+    int a_bytes;  // of one A tile's rows that exist (a multiple of 8 rows)
     int R, num_kb, stages, resident;  // resident: 32-rank parts of h kept in shared memory (0: streamed)
     int* status;
     unsigned long long wait_limit;
@@ -306,7 +373,6 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     const uint32_t sbase = smem_u32(smem);
     const int stages = p.stages;
     const uint32_t hbase = sbase + stages * STAGE;
-    // (a 128-row MMA on a 64-row tile at the very end reads up to 8 KB of what follows)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * STAGE + p.resident * A_BYTES);
     const uint32_t bar0 = smem_u32(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -317,7 +383,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     volatile uint32_t* s_count = tmem_slot + 2;
     uint4* s_mask = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 15) & ~uintptr_t(15));
     uint32_t* s_id = reinterpret_cast<uint32_t*>(s_mask + 128);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int row0 = static_cast<int>(blockIdx.y) * 128, col0 = static_cast<int>(blockIdx.x) * SM_COLS;
     const int rg = (p.R + 15) / 16;
 
@@ -336,7 +402,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     grid_dep_launch();
 
     if (warp == 0 && lane == 0) {
@@ -344,7 +410,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
         uint32_t ph = 0;
         bool ok = true;
         auto claim = [&](uint32_t bytes) {  // the next stage, free and expecting `bytes`
-            ok = mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+            ok = mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER);
             if (!ok) return;
             ++issued;
             mbar_expect_tx(full_bar(s), bytes);
@@ -353,7 +419,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             if (++s == stages) { s = 0; ph ^= 1u; }
         };
         for (int kb = 0; kb < p.num_kb && ok; ++kb) {
-            claim(STAGE);
+            claim(p.a_bytes + SM_B);
             if (!ok) break;
             const uint32_t a = sbase + s * STAGE;
             tma_load_2d(a, &tmX, kb * BK, row0, full_bar(s));
@@ -361,13 +427,15 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             else tma_load_2d(a + A_BYTES, &tmW, kb * BK, col0, full_bar(s));
             advance();
         }
-        if (ok) ok = mbar_wait(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+        if (ok) ok = mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER);
         if (ok) {
             grid_dep_wait();
             const int steps = static_cast<int>(*s_count) * rg;
             if (p.resident && steps) {
-                mbar_expect_tx(h_bar, p.resident * A_BYTES);
-                for (int c = 0; c < p.resident; ++c) tma_load_2d(hbase + c * A_BYTES, &tmH, c * 64, row0, h_bar);
+                if (p.partial == nullptr) {
+                    mbar_expect_tx(h_bar, p.resident * p.a_bytes);
+                    for (int c = 0; c < p.resident; ++c) tma_load_2d(hbase + c * A_BYTES, &tmH, c * 64, row0, h_bar);
+                }
                 for (int f = 0; f < steps && ok; f += 4) {
                     const int n = min(4, steps - f);
                     claim(n * 2048);
@@ -380,7 +448,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             } else {
                 for (int f = 0; f < steps && ok;) {  // one 32-rank part of one adapter
                     const int j = f % rg, n = min(2, rg - j);
-                    claim(A_BYTES + n * 2048);
+                    claim(p.a_bytes + n * 2048);
                     if (!ok) break;
                     const uint32_t a = sbase + s * STAGE;
                     tma_load_2d(a, &tmH, (j / 2) * 64, row0, full_bar(s));
@@ -392,54 +460,57 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             }
         }
         if (!ok) drain_copies(full_bar, issued, stages);
-    } else if (warp == 1 && lane == 0) {
-        const uint32_t idesc = instr_desc(FMT, false, B_MN, SM_COLS), idesc_q = instr_desc(FMT, false, true, SM_COLS);
+    } else if (warp == 1) {
+        const uint32_t idesc = instr_desc(FMT, false, B_MN, SM_COLS, AR), idesc_q = instr_desc(FMT, false, true, SM_COLS, AR);
+        // the whole warp runs this, one lane issues: warp-uniform code keeps the
+        // descriptors in uniform registers, where the MMA takes them from
+        const uint32_t lead = elect_lane();
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
         auto take = [&] {
-            ok = mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA);
+            ok = __all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA));
             tc_fence_after();
         };
         auto release = [&] {
-            mma_commit(empty_bar(s));
+            mma_commit(empty_bar(s), lead);
             if (++s == stages) { s = 0; ph ^= 1u; }
         };
         for (int kb = 0; kb < p.num_kb && ok; ++kb) {
             take();
             if (!ok) break;
             const uint32_t a = sbase + s * STAGE, b = a + A_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_one(tmem_base, smem_desc(a + kk * 32, 16, 1024),
-                        B_MN ? smem_desc(b + kk * 2048, 8192, 1024) : smem_desc(b + kk * 32, 16, 1024), idesc,
-                        (kb | kk) != 0 ? 1u : 0u);
+            mma_block(tmem_base, desc_lo(a, false), DESC_HI, K_STEP, desc_lo(b, B_MN), DESC_HI, B_MN ? MN_STEP : K_STEP, idesc,
+                      kb != 0 ? 1u : 0u, lead);
             release();
         }
-        if (ok) ok = mbar_wait(list_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA));
         if (ok) {
             const int steps = static_cast<int>(*s_count) * rg;
-            if (p.resident && steps) ok = mbar_wait(h_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+            if (p.resident && steps) ok = __all_sync(0xffffffffu, mbar_wait_fast(h_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA));
             for (int f = 0; f < steps && ok;) {
                 take();
                 if (!ok) break;
                 const uint32_t st = sbase + s * STAGE;
                 const int n = p.resident ? min(4, steps - f) : min(2, rg - f % rg);
-                for (int i = 0; i < n; ++i) {
+                for (int i = 0; i < n && lead; ++i) {
                     const int e = (f + i) / rg, j = (f + i) % rg;
                     const uint4 m = s_mask[e];
-                    const uint4 off = make_uint4(~m.x, ~m.y, ~m.z, ~m.w);
+                    // 64 rows: row i is lane 32 (i / 16) + i % 16
+                    const uint4 off = AR == 64 ? make_uint4(~m.x, ~m.x >> 16, ~m.y, ~m.y >> 16) : make_uint4(~m.x, ~m.y, ~m.z, ~m.w);
                     const uint32_t a = (p.resident ? hbase + (j / 2) * A_BYTES : st) + (j % 2) * 32;
                     const uint64_t bd = smem_desc(st + A_BYTES + i * 2048, 8192, 1024);
                     mma_one_masked(tmem_base, smem_desc(a, 16, 1024), bd, idesc_q, off);
                     mma_one_masked(tmem_base, smem_desc(a + 64, 16, 1024), bd, idesc_q, off);
                 }
+                __syncwarp();
                 f += n;
                 release();
             }
         }
-        mma_commit(done_bar);
-        mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        __syncwarp();
+        mma_commit(done_bar, lead);
+        mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
     } else if (warp >= 2) {
         const int w = warp & 3;
         if (warp == 2) {  // the adapters of this half of the plan tile, in the plan's order
@@ -472,21 +543,69 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             }
             __syncwarp();
         }
-        bool ok = mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
+        if (p.partial != nullptr) {  // s h of the tile's rows, 8 ranks (16 bytes of each part) per thread and turn
+            grid_dep_wait();
+            const int per_row = p.resident * 4;
+            const int rows = static_cast<int>(lmin(AR, p.M - row0));
+            for (int i = threadIdx.x - 64; i < rows * per_row; i += 128) {
+                const int row = i / per_row, r0 = (i % per_row) * 8;
+                const uint32_t g = p.ids[row0 + row];
+                float v[8], sv[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+                if (g < p.G && r0 < p.rp) {
+                    const float* src = p.partial + static_cast<int64_t>(row0 + row) * p.rp + r0;
+#pragma unroll 4
+                    for (int q = 0; q < p.pieces; ++q) {
+                        const float4 lo = reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * p.M * p.rp)[0];
+                        const float4 hi = reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * p.M * p.rp)[1];
+                        const float t[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[u] = q == 0 ? t[u] : v[u] + t[u];
+                    }
+                }
+                const float s = g < p.G && p.scales != nullptr ? p.scales[g] : 1.0f;
+                uint32_t w_hi[4], w_lo[4];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (r0 + u >= p.R) v[u] = 0.0f;  // ranks past R hold zeros of the padded rows
+                    else if (p.h != nullptr && blockIdx.x == 0) p.h[static_cast<int64_t>(row0 + row) * p.R + r0 + u] = v[u];
+                    sv[u] = v[u] * s;
+                }
+#pragma unroll
+                for (int u = 0; u < 8; u += 2) {
+                    w_hi[u / 2] = OutT<FMT>::pack(sv[u], sv[u + 1]);
+                    const typename OutT<FMT>::T* t = reinterpret_cast<const typename OutT<FMT>::T*>(&w_hi[u / 2]);
+                    const float h0 = OutT<FMT>::load(t, 0), h1 = OutT<FMT>::load(t, 1);
+                    w_lo[u / 2] = OutT<FMT>::pack(isinf(h0) ? 0.0f : sv[u] - h0, isinf(h1) ? 0.0f : sv[u + 1] - h1);
+                }
+                const uint32_t at = hbase + (r0 / 32) * A_BYTES + row * 128;
+                const uint32_t c = (r0 % 32) / 8;  // 16-byte piece of the high parts; the remainders' is 4 on
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((c ^ (row & 7)) * 16)), "r"(w_hi[0]),
+                             "r"(w_hi[1]), "r"(w_hi[2]), "r"(w_hi[3]) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((c + 4) ^ (row & 7)) * 16)), "r"(w_lo[0]),
+                             "r"(w_lo[1]), "r"(w_lo[2]), "r"(w_lo[3]) : "memory");
+            }
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (threadIdx.x == 64) mbar_arrive(h_bar);
+        }
+        bool ok = mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
         ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
         if (ok) {
             tc_fence_after();
             using O = OutT<FMT>;
             using T = typename O::T;
-            const int64_t row = row0 + 32 * w + lane;
+            constexpr int RPW = AR / 4;  // rows per warp: 32, or 16 in the first lanes of a 64-row tile's
+            const int64_t row = row0 + RPW * w + lane;
             T* dst = static_cast<T*>(p.out) + row * p.C + col0;
-            if (row0 + 32 * w < p.M && 32 * w < AR) {
+            if (row0 + RPW * w < p.M) {
 #pragma unroll
                 for (int c = 0; c < SM_COLS; c += 16) {
                     if (col0 + c >= p.C) break;
                     uint32_t v[16];
                     tmem_ld16(tmem_base + (static_cast<uint32_t>(32 * w) << 16) + c, v);
-                    if (row < p.M) {
+                    if (row < p.M && lane < RPW) {
                         float f[16];
                         const int have = static_cast<int>(lmin(16, p.C - col0 - c));  // 8 or 16
 #pragma unroll
@@ -529,7 +648,7 @@ cudaError_t small_rows_t(const LaunchCtx& c, const CUtensorMap& x, const CUtenso
     // a whole SM's shared memory where the tiles leave SMs over, else half
     const int budget = int64_t(grid.x) * grid.y <= c.sm_count ? SM_LIMIT : SM_LIMIT / 2 - 1024;
     constexpr int STAGE = AR * 128 + SM_B;
-    const int pad = 1024 + SM_TAIL + (AR < 128 ? 8192 : 0);  // alignment; the 128-row MMA's reach
+    const int pad = 1024 + SM_TAIL;  // alignment, barriers and lists
     p.resident = p.R <= 64 ? (p.R + 31) / 32 : 0;
     p.stages = min(SM_MAX_STAGES, (budget - pad - p.resident * AR * 128) / STAGE);
     const int bytes = pad + p.resident * AR * 128 + p.stages * STAGE;
@@ -600,7 +719,7 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
     const uint32_t done_bar = bar0 + 8u * (2 * STAGES);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     grid_dep_wait();
     const uint32_t chunk = p.chunk0 + blockIdx.x / p.strips;
     if (chunk >= p.ch.first[p.G]) return;
@@ -629,7 +748,7 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     grid_dep_launch();  // after the CTA has its TMEM: a dependent kernel may ask for some
 
     if (warp < 4) {
@@ -653,7 +772,7 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
         uint32_t ph = 0;
         for (int b = 0; b < blocks + LAG; ++b) {
             if (b < blocks) {
-                ok = ok && mbar_wait(empty_bar(st), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+                ok = ok && mbar_wait_fast(empty_bar(st), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER);
                 if (ok) {
                     const uint32_t a = sbase + st * STAGE;
 #pragma unroll
@@ -680,7 +799,7 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         // epilogue: this thread's column, ranks ascending, the parts added from the smallest
-        ok = mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE) && ok;
+        ok = mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             tc_fence_after();
@@ -707,23 +826,21 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
                 __syncwarp();
             }
         }
-    } else if (lane == 0) {
+    } else {
+        const uint32_t lead = elect_lane();
         const uint32_t idesc = instr_desc(p.fmt, true, true, 4 * RUN);
         int s = 0;
         uint32_t ph = 0;
         for (int b = 0; b < blocks; ++b) {
-            if (!mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA))) break;
             tc_fence_after();
             const uint32_t a = sbase + s * STAGE, v = a + GT_A;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_one(tmem_base, smem_desc(a + kk * 2048, 8192, 1024), smem_desc(v + kk * 2048, 8192, 1024), idesc,
-                        (b | kk) != 0 ? 1u : 0u);
-            mma_commit(empty_bar(s));
+            mma_block(tmem_base, desc_lo(a, true), DESC_HI, MN_STEP, desc_lo(v, true), DESC_HI, MN_STEP, idesc, b != 0 ? 1u : 0u, lead);
+            mma_commit(empty_bar(s), lead);
             if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
-        mma_commit(done_bar);
-        mbar_wait(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        mma_commit(done_bar, lead);
+        mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
     }
     __syncwarp();
     tc_fence_before();
@@ -749,7 +866,7 @@ cudaError_t grad_run(const LaunchCtx& c, const GradParams& p, dim3 grid) {
 }  // namespace
 
 cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, const void* z, const void* pw,
-                              const AdapterPlan& plan, int64_t M, int64_t L, int R, int64_t G) {
+                              const uint32_t* ids, const AdapterPlan& plan, int64_t M, int64_t L, int R, int64_t G) {
     static PerDeviceOnce setup;
     cudaError_t e = setup.run(c.eng->device, [](int&) {
         return cudaFuncSetAttribute(narrow_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NP_SMEM);
@@ -759,7 +876,7 @@ cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, c
     if ((e = make_map(&x, dt, z, L, M, 1, 128)) != cudaSuccess) return e;
     if ((e = make_map(&w, dt, pw, L, R, G, 16, true)) != cudaSuccess) return e;
     NarrowParams p{};
-    p.plan = plan; p.partial = partial; p.M = M; p.R = R; p.rp = (R + 15) / 16 * 16;
+    p.plan = plan; p.ids = ids; p.G = static_cast<uint32_t>(G); p.partial = partial; p.M = M; p.R = R; p.rp = (R + 15) / 16 * 16;
     p.num_kb = static_cast<int>((L + BK - 1) / BK);
     p.fmt = dt == BI_BF16 ? 1 : 0;
     p.status = c.status; p.wait_limit = c.wait_limit_ns;
@@ -774,24 +891,44 @@ cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, c
     return e;
 }
 
+// Which tiles (both give the same bits).  A wave of CTA pairs takes 390 ns per
+// contraction block; single CTAs take 150 ns (four dependent MMAs), or what their
+// operands take to come from L2, 1.5 ns per tile and block, if that is more.
+// Measured, bf16, K = 4096, the whole call: N = 4096, 64 rows 25 us against 45,
+// 512 rows 37 against 41, 1333 rows 70 against 65; N = 11008, 128 rows 36 against
+// 46, 512 rows 90 against 67.
 bool adapter_small_tiles(const LaunchCtx& c, int64_t M, int64_t C) {
-    const int64_t pairs = (M + 255) / 256 * ((C + 255) / 256);
-    return pairs <= c.sm_count / 4;
+    const int64_t pairs = (M + 255) / 256 * ((C + 255) / 256), tiles = (M + 127) / 128 * ((C + 63) / 64);
+    const int64_t wave_p = (pairs + c.sm_count / 2 - 1) / (c.sm_count / 2), wave_s = (tiles + c.sm_count - 1) / c.sm_count;
+    return (M + 127) / 128 <= 65535 && lmax(300 * wave_s, 3 * tiles) < 780 * wave_p;
+}
+
+// Sums of pieces that a small tile's CTA takes on itself: 64 KB of L2 reads.
+constexpr int64_t SM_FUSE = 16384;
+bool adapter_small_fuses(const LaunchCtx& c, int64_t M, int64_t C, int64_t L, int R) {
+    const int64_t pieces = (L + ADAPTER_PIECE - 1) / ADAPTER_PIECE, rp = (R + 15) / 16 * 16;
+    return (!c.eng || c.eng->tile_cols == 0) && R <= 64 && adapter_small_tiles(c, M, C) &&
+           lmin(M, 128) * rp * pieces <= SM_FUSE;
 }
 
 cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
                                   const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
-                                  int64_t K, int64_t N, int R, int64_t G) {
+                                  int64_t K, int64_t N, int R, int64_t G, const AdapterPieces* fuse) {
     const int64_t L = dx ? N : K, C = dx ? K : N;
-    const uint32_t ar = M <= 64 ? 64 : 128;
+    const uint32_t ar = static_cast<uint32_t>(lmin(128, (M + 7) / 8 * 8));
     CUtensorMap mx, mw, mh, mq;
     cudaError_t e;
     if ((e = make_map(&mx, dt, z, L, M, 1, ar)) != cudaSuccess) return e;
     if ((e = make_map(&mw, dt, w, N, K, 1, 64)) != cudaSuccess) return e;
-    if ((e = make_map(&mh, dt, hh, adapter_part_cols(R), M, 1, ar)) != cudaSuccess) return e;
+    if (!fuse && (e = make_map(&mh, dt, hh, adapter_part_cols(R), M, 1, ar)) != cudaSuccess) return e;
     if ((e = make_map(&mq, dt, q, C, R, G, 16, true)) != cudaSuccess) return e;
     SmallParams p{};
-    p.plan = plan; p.out = out; p.bias = bias; p.M = M; p.C = C; p.R = R;
+    if (fuse) {
+        mh = mx;  // not read
+        p.partial = fuse->partial; p.ids = fuse->ids; p.scales = fuse->scales; p.h = fuse->h;
+        p.G = static_cast<uint32_t>(G); p.pieces = fuse->pieces; p.rp = (R + 15) / 16 * 16;
+    }
+    p.plan = plan; p.out = out; p.bias = bias; p.M = M; p.C = C; p.R = R; p.a_bytes = static_cast<int>(ar) * 128;
     p.num_kb = static_cast<int>((L + BK - 1) / BK);
     p.status = c.status; p.wait_limit = c.wait_limit_ns;
     const dim3 grid(static_cast<unsigned>((C + SM_COLS - 1) / SM_COLS), static_cast<unsigned>((M + 127) / 128));

@@ -64,6 +64,9 @@ static __device__ __noinline__ bool mbar_wait_impl(uint32_t bar, uint32_t parity
 }
 #define mbar_wait(bar, parity, abort_flag, p, code) \
     mbar_wait_impl((bar), (parity), (abort_flag), (p).status, (p).wait_limit, (code))
+// The same with the first try inline: a barrier that is complete costs no call.
+#define mbar_wait_fast(bar, parity, abort_flag, p, code) \
+    (mbar_try_wait((bar), (parity)) || mbar_wait((bar), (parity), (abort_flag), p, (code)))
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
