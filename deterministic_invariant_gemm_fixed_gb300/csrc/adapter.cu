@@ -23,7 +23,6 @@
 
 #include "abi_util.h"
 #include "adapter.h"
-#include "adapter_plan.cuh"
 
 namespace bi {
 namespace {
@@ -37,15 +36,7 @@ template <> __device__ __forceinline__ float down<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 down<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half down<__half>(float v) { return __float2half_rn(v); }
 
-// ---------------------------------------------------------------- plan
-
-__global__ void __launch_bounds__(256) adapter_plan_kernel(const uint32_t* ids, int64_t M, uint32_t G, AdapterPlan plan) {
-    __shared__ PlanSmem sm;
-    grid_dep_wait();
-    grid_dep_launch();
-    plan_tile<8>(ids, M, G, blockIdx.x, threadIdx.x >> 5, sm, [] { __syncthreads(); });
-    plan_store(plan, blockIdx.x, sm, threadIdx.x, 256);
-}
+// ---------------------------------------------------------------- chunk tables
 
 // Chunk tables of the sorted rows (AdapterChunks), one block.
 __global__ void __launch_bounds__(1024) adapter_chunks_kernel(const uint32_t* off, uint32_t G, AdapterChunks ch) {
@@ -85,39 +76,88 @@ __global__ void __launch_bounds__(1024) adapter_chunks_kernel(const uint32_t* of
 
 // ---------------------------------------------------------------- narrow product, scalar
 
-// partial[piece][m][r] = sum over the piece's l ascending of X[m,l] P[g][r,l]
-// (one fmaf chain from +0).  A block has 16 rows and 16 ranks, one result per
-// thread; for each adapter among its rows it stages 64 steps of both operands.
-constexpr int NP_STEPS = 64;
+// partial[piece][m][r] = sum over the piece's l of X[m,l] P[g][r,l].  A warp has
+// four rows and one piece, the rows' 512 values in registers (lane j holds l = 128 i
+// + 4 j + 0..3), and for each of up to 16 ranks reads P's 512 values once, for all
+// four rows if they have one adapter: lane sums (16 FMAs, l ascending) and a
+// shuffle tree, the same order for a row alone or among others.  Rows of other
+// warps find P in L1.  (One result per thread, operands staged in shared memory
+// per adapter among 16 rows, took 81 us where this takes 6: 999 x 1000, rank 5,
+// seven adapters in no order.)
+constexpr int NS_ROWS = 4, NS_RANKS = 16, NS_WARPS = 4;
 template <typename T>
-__global__ void __launch_bounds__(256)
-    narrow_scalar_kernel(const T* x, const T* p, AdapterPlan plan, float* partial, int64_t M, int64_t L, int R) {
-    __shared__ float s_x[16][NP_STEPS + 1], s_p[16][NP_STEPS + 1];
-    const int tid = threadIdx.x, i = tid >> 4, j = tid & 15;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, tile = m0 / ADAPTER_TILE;
-    const int r0 = blockIdx.y * 16, word = static_cast<int>(m0 % ADAPTER_TILE) / 32;
-    const int shift = static_cast<int>(m0 % 32);
-    const int64_t l0 = static_cast<int64_t>(blockIdx.z) * ADAPTER_PIECE, l1 = lmin(L, l0 + ADAPTER_PIECE);
-    const uint32_t n = plan.count[tile];
-    for (uint32_t e = 0; e < n; ++e) {
-        const uint32_t mask = (plan.masks[(tile * 256 + e) * 8 + word] >> shift) & 0xffffu;
-        if (mask == 0) continue;
-        const T* pg = p + static_cast<int64_t>(plan.ids[tile * 256 + e]) * R * L;
-        const bool mine = (mask >> i) & 1u;
-        float acc = 0.0f;
-        for (int64_t l = l0; l < l1; l += NP_STEPS) {
-            __syncthreads();
-            for (int q = tid; q < 16 * NP_STEPS; q += 256) {
-                const int a = q / NP_STEPS, s = q % NP_STEPS;
-                const bool in = l + s < l1;
-                s_x[a][s] = in && m0 + a < M ? up<T>(x[(m0 + a) * L + l + s]) : 0.0f;
-                s_p[a][s] = in && r0 + a < R ? up<T>(pg[static_cast<int64_t>(r0 + a) * L + l + s]) : 0.0f;
+__device__ __forceinline__ void load_lane(const T* p, int64_t l0, int64_t L, bool vec, int lane, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t l = l0 + 128 * i + 4 * lane;
+        if (vec && l + 4 <= L) {  // L % 4 == 0 and aligned rows
+            if constexpr (sizeof(T) == 4) {
+                const float4 q = *reinterpret_cast<const float4*>(p + l);
+                v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+            } else {
+                const uint2 q = *reinterpret_cast<const uint2*>(p + l);
+                const T* e = reinterpret_cast<const T*>(&q);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * i + j] = up<T>(e[j]);
             }
-            __syncthreads();
-            const int steps = static_cast<int>(lmin(NP_STEPS, l1 - l));
-            for (int s = 0; s < steps; ++s) acc = fmaf(s_x[i][s], s_p[j][s], acc);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = l + j < L ? up<T>(p[l + j]) : 0.0f;
         }
-        if (mine && r0 + j < R) partial[(static_cast<int64_t>(blockIdx.z) * M + m0 + i) * R + r0 + j] = acc;
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(32 * NS_WARPS)
+    narrow_scalar_kernel(const T* x, const T* p, const uint32_t* ids, float* partial, int64_t M, int64_t L, int R, uint32_t G,
+                         int vec) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t m0 = (static_cast<int64_t>(blockIdx.x) * NS_WARPS + warp) * NS_ROWS;
+    if (m0 >= M) return;
+    const int r0 = blockIdx.z * NS_RANKS, r1 = min(R, r0 + NS_RANKS);
+    const int64_t l0 = static_cast<int64_t>(blockIdx.y) * ADAPTER_PIECE, l1 = lmin(L, l0 + ADAPTER_PIECE);
+    uint32_t g[NS_ROWS];
+    float v[NS_ROWS][16];
+#pragma unroll
+    for (int i = 0; i < NS_ROWS; ++i) {
+        g[i] = m0 + i < M ? ids[m0 + i] : G;
+        if (g[i] < G) load_lane(x + (m0 + i) * L, l0, l1, vec != 0, lane, v[i]);
+    }
+    // values past l1 are 0 in v and in P: they add +0 products
+    auto row_sum = [&](const float (&a)[16], const float (&b)[16]) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) s = fmaf(a[k], b[k], s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    };
+    float* out = partial + (static_cast<int64_t>(blockIdx.y) * M + m0) * R;
+    if (g[0] < G && g[1] == g[0] && g[2] == g[0] && g[3] == g[0]) {
+        const T* pg = p + static_cast<int64_t>(g[0]) * R * L;
+        for (int r = r0; r < r1; ++r) {
+            float b[16];
+            load_lane(pg + static_cast<int64_t>(r) * L, l0, l1, vec != 0, lane, b);
+#pragma unroll
+            for (int i = 0; i < NS_ROWS; ++i) {
+                const float s = row_sum(v[i], b);
+                if (lane == i) out[static_cast<int64_t>(i) * R + r] = s;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS_ROWS; ++i) {
+            if (g[i] >= G) continue;
+            const T* pg = p + static_cast<int64_t>(g[i]) * R * L;
+#pragma unroll 2
+            for (int r = r0; r < r1; ++r) {
+                float b[16];
+                load_lane(pg + static_cast<int64_t>(r) * L, l0, l1, vec != 0, lane, b);
+                const float s = row_sum(v[i], b);
+                if (lane == 0) out[static_cast<int64_t>(i) * R + r] = s;
+            }
+        }
     }
 }
 
@@ -126,6 +166,8 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     narrow_finish_kernel(const float* partial, const uint32_t* ids, const float* scales, float* h, float* hs,
                          int64_t M, int R, uint32_t G, int pieces) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= M * R) return;
     const uint32_t g = ids[i / R];
@@ -223,28 +265,42 @@ __global__ void __launch_bounds__(256) scale_rows_kernel(const float* h, const u
 // that adapter.
 template <typename T>
 __global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* base, const float* hs, const T* q,
-                                                          AdapterPlan plan, int64_t M, int64_t C, int R) {
+                                                          const uint32_t* ids, int64_t M, int64_t C, int R, uint32_t G) {
     extern __shared__ float s_h[];  // [R][16]
+    __shared__ uint32_t s_id[16], s_mask[16];  // row i's adapter; the rows with it, at the first of them (else 0)
+    grid_dep_wait();
+    grid_dep_launch();
     const int tid = threadIdx.x;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16, tile = m0 / ADAPTER_TILE;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + tid;
-    const int word = static_cast<int>(m0 % ADAPTER_TILE) / 32, shift = static_cast<int>(m0 % 32);
+    if (tid < 32) {
+        const uint32_t id = tid < 16 && m0 + tid < M ? ids[m0 + tid] : G;
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        if (tid < 16) {
+            s_id[tid] = id;
+            s_mask[tid] = id < G && (same & ((1u << tid) - 1)) == 0 ? same : 0;
+        }
+    }
     for (int i = tid; i < 16 * R; i += 256) {
         const int row = i / R, r = i % R;
         s_h[r * 16 + row] = m0 + row < M ? hs[(m0 + row) * R + r] : 0.0f;
     }
     __syncthreads();
-    const uint32_t n = plan.count[tile];
+    if (c >= C) return;
+    const bool in_place = reinterpret_cast<const void*>(base) == reinterpret_cast<const void*>(out);
+    float b[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = m0 + i < M ? base[(m0 + i) * C + c] : 0.0f;
     uint32_t any = 0;
-    for (uint32_t e = 0; e < n; ++e) {
-        const uint32_t mask = (plan.masks[(tile * 256 + e) * 8 + word] >> shift) & 0xffffu;
+    for (int e = 0; e < 16; ++e) {
+        const uint32_t mask = s_mask[e];
         if (mask == 0) continue;
         any |= mask;
-        if (c >= C) continue;
-        const T* qg = q + static_cast<int64_t>(plan.ids[tile * 256 + e]) * R * C + c;
+        const T* qg = q + static_cast<int64_t>(s_id[e]) * R * C + c;
         float acc[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+#pragma unroll 8
         for (int r = 0; r < R; ++r) {
             const float v = up<T>(qg[static_cast<int64_t>(r) * C]);
 #pragma unroll
@@ -252,11 +308,12 @@ __global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* b
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if ((mask >> i) & 1u) out[(m0 + i) * C + c] = down<T>(base[(m0 + i) * C + c] + acc[i]);
+            if ((mask >> i) & 1u) out[(m0 + i) * C + c] = down<T>(b[i] + acc[i]);
     }
-    if (c >= C || reinterpret_cast<const void*>(base) == reinterpret_cast<const void*>(out)) return;
+    if (in_place) return;
+#pragma unroll
     for (int i = 0; i < 16; ++i)  // rows without adapter
-        if (!((any >> i) & 1u) && m0 + i < M) out[(m0 + i) * C + c] = down<T>(base[(m0 + i) * C + c]);
+        if (!((any >> i) & 1u) && m0 + i < M) out[(m0 + i) * C + c] = down<T>(b[i]);
 }
 
 // ---------------------------------------------------------------- dA, dB, scalar
@@ -337,30 +394,39 @@ cudaError_t launched(const LaunchCtx& c) {
     return cudaGetLastError();
 }
 
-cudaError_t build_plan(const LaunchCtx& c, const uint32_t* ids, int64_t M, int64_t G, const AdapterPlan& plan) {
-    const cudaError_t e = launch_pdl(adapter_plan_kernel, dim3(static_cast<unsigned>(AdapterPlan::tiles(M))), dim3(256), 0,
-                                     c.stream, ids, M, static_cast<uint32_t>(G), plan);
-    if (e == cudaSuccess) c.count();
-    return e;
-}
-
 unsigned grid1(int64_t n) { return static_cast<unsigned>((n + 255) / 256); }
 int pieces_of(int64_t L) { return static_cast<int>((L + ADAPTER_PIECE - 1) / ADAPTER_PIECE); }
 
 template <typename T>
-cudaError_t narrow_scalar(const LaunchCtx& c, const T* x, const T* p, const AdapterPlan& plan, float* partial, int64_t M,
-                          int64_t L, int R) {
-    const dim3 grid(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>((R + 15) / 16), static_cast<unsigned>(pieces_of(L)));
-    narrow_scalar_kernel<T><<<grid, 256, 0, c.stream>>>(x, p, plan, partial, M, L, R);
-    return launched(c);
+cudaError_t narrow_scalar(const LaunchCtx& c, const T* x, const T* p, const uint32_t* ids, float* partial, int64_t M,
+                          int64_t L, int R, int64_t G) {
+    const int64_t rows = NS_ROWS * NS_WARPS;
+    const dim3 grid(static_cast<unsigned>((M + rows - 1) / rows), static_cast<unsigned>(pieces_of(L)),
+                    static_cast<unsigned>((R + NS_RANKS - 1) / NS_RANKS));
+    const int vec = L % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0 &&
+                    reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
+    const cudaError_t e = launch_pdl(narrow_scalar_kernel<T>, grid, dim3(32 * NS_WARPS), 0, c.stream, x, p, ids, partial, M, L, R,
+                                     static_cast<uint32_t>(G), vec);
+    if (e == cudaSuccess) c.count();
+    return e;
+}
+
+cudaError_t narrow_finish(const LaunchCtx& c, const float* partial, const uint32_t* ids, const float* scales, float* h, float* hs,
+                          int64_t M, int R, int64_t G, int pieces) {
+    const cudaError_t e = launch_pdl(narrow_finish_kernel, dim3(grid1(M * R)), dim3(256), 0, c.stream, partial, ids, scales, h, hs,
+                                     M, R, static_cast<uint32_t>(G), pieces);
+    if (e == cudaSuccess) c.count();
+    return e;
 }
 
 template <typename T>
-cudaError_t wide_scalar(const LaunchCtx& c, T* out, const float* base, const float* hs, const T* q, const AdapterPlan& plan,
-                        int64_t M, int64_t C, int R) {
+cudaError_t wide_scalar(const LaunchCtx& c, T* out, const float* base, const float* hs, const T* q, const uint32_t* ids,
+                        int64_t M, int64_t C, int R, int64_t G) {
     const dim3 grid(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>((C + 255) / 256));
-    wide_scalar_kernel<T><<<grid, 256, static_cast<size_t>(16 * R * 4), c.stream>>>(out, base, hs, q, plan, M, C, R);
-    return launched(c);
+    const cudaError_t e = launch_pdl(wide_scalar_kernel<T>, grid, dim3(256), static_cast<size_t>(16 * R * 4), c.stream, out, base,
+                                     hs, q, ids, M, C, R, static_cast<uint32_t>(G));
+    if (e == cudaSuccess) c.count();
+    return e;
 }
 
 template <typename T>
@@ -470,14 +536,13 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
         if (e == cudaSuccess) e = tc_adapter_rows(c, dtype, 0, y, x, w, bias, p + o_hh, b, plan, m, k, n, R, g);
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
     }
-    // scratch: plan | pieces of h | s h | the shared product in f32 (16-bit types)
+    // scratch: pieces of h | s h | the shared product in f32 (16-bit types)
     Cut cut;
-    const int64_t o_plan = cut.take(AdapterPlan::words(m) * 4), o_part = cut.take(pieces * m * r * 4),
-                  o_hs = cut.take(m * r * 4), o_base = cut.take(dtype == BI_F32 ? 0 : m * n * 4);
+    const int64_t o_part = cut.take(pieces * m * r * 4), o_hs = cut.take(m * r * 4),
+                  o_base = cut.take(dtype == BI_F32 ? 0 : m * n * 4);
     Scratch sc(eng, s, static_cast<size_t>(cut.at));
     if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "adapter scratch");
     uint8_t* p = static_cast<uint8_t*>(sc.ptr);
-    const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
     float* part = reinterpret_cast<float*>(p + o_part);
     float* hs = reinterpret_cast<float*>(p + o_hs);
     float* base = dtype == BI_F32 ? static_cast<float*>(y) : reinterpret_cast<float*>(p + o_base);
@@ -490,20 +555,16 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
     } else {
         e = scalar_rows(c, dtype, base, x, w, bias, m, k, n, 0, 1);
     }
-    if (e == cudaSuccess) e = build_plan(c, row_adapters, m, g, plan);
     if (e == cudaSuccess)
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return narrow_scalar<T>(c, static_cast<const T*>(x), static_cast<const T*>(a), plan, part, m, k, R);
+            return narrow_scalar<T>(c, static_cast<const T*>(x), static_cast<const T*>(a), row_adapters, part, m, k, R, g);
         });
-    if (e == cudaSuccess) {
-        narrow_finish_kernel<<<grid1(m * r), 256, 0, s>>>(part, row_adapters, scales, h, hs, m, R, static_cast<uint32_t>(g), pieces);
-        e = launched(c);
-    }
+    if (e == cudaSuccess) e = narrow_finish(c, part, row_adapters, scales, h, hs, m, R, g, pieces);
     if (e == cudaSuccess)
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return wide_scalar<T>(c, static_cast<T*>(y), base, hs, static_cast<const T*>(b), plan, m, n, R);
+            return wide_scalar<T>(c, static_cast<T*>(y), base, hs, static_cast<const T*>(b), row_adapters, m, n, R, g);
         });
     return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
 }
@@ -580,10 +641,10 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         }
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_backward");
     }
-    // scratch: plan | pieces of u | u | s h | sorted rows | chunk tables | chunk
+    // scratch: pieces of u | u | s h | sorted rows | chunk tables | chunk
     // sums (of dA, then of dB) | the shared product in f32 (16-bit types)
     Cut cut;
-    const int64_t o_plan = cut.take(need_u ? AdapterPlan::words(m) * 4 : 0), o_part = cut.take(need_u ? pieces * m * r * 4 : 0),
+    const int64_t o_part = cut.take(need_u ? pieces * m * r * 4 : 0),
                   o_u = cut.take(need_u ? m * r * 4 : 0), o_hs = cut.take(db ? m * r * 4 : 0);
     const bool grads = da || db;
     const int64_t o_seg = cut.take(grads ? seg_table_len(g) * 4 : 0), o_perm = cut.take(grads ? m * 4 : 0),
@@ -594,7 +655,6 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     Scratch sc(eng, s, static_cast<size_t>(cut.at));
     if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "adapter scratch");
     uint8_t* p = static_cast<uint8_t*>(sc.ptr);
-    const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
     float* part = reinterpret_cast<float*>(p + o_part);
     float* u = reinterpret_cast<float*>(p + o_u);
     float* hs = reinterpret_cast<float*>(p + o_hs);
@@ -612,21 +672,16 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         e = scalar_rows(c, dtype, base, dy, w, nullptr, m, n, k, 1, 1);
     }
     if (e == cudaSuccess && need_u) {
-        e = build_plan(c, row_adapters, m, g, plan);
-        if (e == cudaSuccess)
-            e = with_type(dtype, [&](auto* t) {
-                using T = std::remove_pointer_t<decltype(t)>;
-                return narrow_scalar<T>(c, static_cast<const T*>(dy), static_cast<const T*>(b), plan, part, m, n, R);
-            });
-        if (e == cudaSuccess) {
-            narrow_finish_kernel<<<grid1(m * r), 256, 0, s>>>(part, row_adapters, scales, nullptr, u, m, R, G, pieces);
-            e = launched(c);
-        }
+        e = with_type(dtype, [&](auto* t) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            return narrow_scalar<T>(c, static_cast<const T*>(dy), static_cast<const T*>(b), row_adapters, part, m, n, R, g);
+        });
+        if (e == cudaSuccess) e = narrow_finish(c, part, row_adapters, scales, nullptr, u, m, R, g, pieces);
     }
     if (e == cudaSuccess && dx) {
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return wide_scalar<T>(c, static_cast<T*>(dx), base, u, static_cast<const T*>(a), plan, m, k, R);
+            return wide_scalar<T>(c, static_cast<T*>(dx), base, u, static_cast<const T*>(a), row_adapters, m, k, R, g);
         });
     }
     if (e == cudaSuccess && grads) {

@@ -87,10 +87,11 @@ __device__ __forceinline__ float group_max(float v) {
         float y;
         asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
         return y;
-    }
+    } else {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+        for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    }
 }
 
 // loss = E / (k V) * the sum of the experts' terms counts[e] mean[e], by one warp
