@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(1024) adapter_chunks_kernel(const uint32_t* of
 // four rows if they have one adapter: lane sums (16 FMAs, l ascending) and a
 // shuffle tree, the same order for a row alone or among others.  Rows of other
 // warps find P in L1.  (One result per thread, operands staged in shared memory
-// per adapter among 16 rows, took 81 us where this takes 6: 999 x 1000, rank 5,
+// per adapter among 16 rows, took 81 us where this takes 13: 999 x 1000, rank 5,
 // seven adapters in no order.)
 constexpr int NS_ROWS = 4, NS_RANKS = 16, NS_WARPS = 4;
 template <typename T>

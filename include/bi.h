@@ -357,10 +357,10 @@ bi_status bi_router_backward(bi_engine engine, void* dlogits, const void* logits
  * call only.  Tensors need the alignment of their element type; tensors that
  * are 16-byte aligned are faster. */
 
-/* *norm = sqrt(sum of all squares), norm [1] f32 on the device.  Chunks of 32768
- * elements are summed in f32 (again in f64 where f32's range does not hold
- * their squares), the chunks in f64, all in a fixed order: bit-identical run
- * to run.  An empty set has norm 0. */
+/* *norm = sqrt(sum of all squares), norm [1] f32 on the device.  Up to 32
+ * squares at a time are summed in f32 (in f64 where f32's range does not hold
+ * them), these sums in f64, all in an order fixed by the sizes: bit-identical
+ * run to run.  An empty set has norm 0. */
 bi_status bi_grad_norm(bi_engine engine, float* norm, const void* const* tensors, const int64_t* counts,
                        const int* dtypes, int64_t n, void* stream);
 
