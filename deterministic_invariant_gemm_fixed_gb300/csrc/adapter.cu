@@ -184,67 +184,113 @@ __global__ void __launch_bounds__(256)
 // The same for the tensor cores: v = the pieces' sums (row stride rp), or h_in;
 // h = v; then s_g v in two parts (hh, for the wide product) and in four (v4, for
 // dA and dB), any of them nullable.  A part that would be an infinity's
-// remainder is 0, so an infinity stays one.  One thread per row and rank up to
-// `width`, which covers both formats' padding (zeros).
+// remainder is 0, so an infinity stays one.  One thread per row and 8 ranks
+// (16-byte stores) up to the formats' padded width (zeros past R); block row y
+// does job y.
+struct FinishJob {
+    const float* partial;
+    const float* h_in;
+    float* h;
+    void* hh;
+    void* v4;
+};
+struct FinishJobs {
+    FinishJob job[2];
+};
 template <typename T>
 __device__ __forceinline__ float part_rest(float v, T hi, float scale) {
     const float h = up<T>(hi) * scale;
     return isinf(h) ? 0.0f : v - h;
 }
 template <typename T>
+__device__ __forceinline__ void four_parts(float s, T (&part)[4]) {
+    part[0] = down<T>(0.0f);
+    if (std::is_same<T, __half>::value) {  // see adapter.h
+        float rest = s, scale = 0x1p11f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i, scale *= 0x1p-11f) {
+            const float x = rest * (1.0f / scale);
+            const bool none = i == 0 ? !(fabsf(s) > 65504.0f) : (i < 3 && fabsf(x) < 0x1p-14f);
+            part[i] = down<T>(none ? 0.0f : x);
+            rest = none ? rest : part_rest<T>(rest, part[i], scale);
+        }
+    } else {
+        part[1] = down<T>(s);
+        const float r1 = part_rest<T>(s, part[1], 1.0f);
+        part[2] = down<T>(r1);
+        part[3] = down<T>(part_rest<T>(r1, part[2], 1.0f));
+    }
+}
+template <typename T>
 __global__ void __launch_bounds__(256)
-    narrow_finish_tc_kernel(const float* partial, const float* h_in, const uint32_t* ids, const float* scales, float* h,
-                            T* hh, T* v4, int64_t M, int R, int rp, uint32_t G, int pieces, int width) {
+    narrow_finish_tc_kernel(const __grid_constant__ FinishJobs jobs, const uint32_t* ids, const float* scales, int64_t M, int R,
+                            int rp, uint32_t G, int pieces, int per_row) {
     // the dependents first: a small-tile product starts on the shared weight while
     // h is still in the making, and waits for this kernel before it reads it
     grid_dep_launch();
     grid_dep_wait();
+    const FinishJob& jb = jobs.job[blockIdx.y];
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= M * width) return;
-    const int64_t m = i / width;
-    const int r = static_cast<int>(i - m * width);
+    if (i >= M * per_row) return;
+    const int64_t m = M * per_row <= 0x7fffffff ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(per_row))
+                                                : i / per_row;
+    const int r0 = static_cast<int>(i - m * per_row) * 8;
     const uint32_t g = ids[m];
-    float v = 0.0f, s = 0.0f;
-    if (g < G && r < R) {
-        if (partial != nullptr) {
-            const float* p = partial + m * rp + r;
-            v = *p;
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = 0.0f;
+    if (g < G && r0 < R) {
+        if (jb.partial != nullptr) {  // rp - r0 is a multiple of 8: whole vectors
+            const float* p = jb.partial + m * rp + r0;
+            const int64_t step = M * rp;
 #pragma unroll 8
-            for (int q = 1; q < pieces; ++q) v += p[static_cast<int64_t>(q) * M * rp];
+            for (int q = 0; q < pieces; ++q) {
+                const float4 a = reinterpret_cast<const float4*>(p + q * step)[0];
+                const float4 b = reinterpret_cast<const float4*>(p + q * step)[1];
+                const float t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = q == 0 ? t[u] : v[u] + t[u];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (r0 + u >= R) v[u] = 0.0f;
         } else {
-            v = h_in[m * R + r];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (r0 + u < R) v[u] = jb.h_in[m * R + r0 + u];
         }
-        s = scales != nullptr ? v * scales[g] : v;
     }
-    if (h != nullptr && r < R) h[m * R + r] = v;
-    if (hh != nullptr && r < (R + 31) / 32 * 32) {
-        const T hi = down<T>(s);
-        T* o = hh + m * ((R + 31) / 32 * 64) + (r / 32) * 64 + r % 32;
-        o[0] = hi;
-        o[32] = down<T>(part_rest<T>(s, hi, 1.0f));
+    if (jb.h != nullptr) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (r0 + u < R) jb.h[m * R + r0 + u] = v[u];
+    }
+    const float scale = g < G && scales != nullptr ? scales[g] : 1.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] *= scale;
+    __align__(16) T out[4][8];
+    if (jb.hh != nullptr && r0 < (R + 31) / 32 * 32) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            out[0][u] = down<T>(v[u]);
+            out[1][u] = down<T>(part_rest<T>(v[u], out[0][u], 1.0f));
+        }
+        T* o = static_cast<T*>(jb.hh) + m * ((R + 31) / 32 * 64) + (r0 / 32) * 64 + r0 % 32;
+        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(out[0]);
+        *reinterpret_cast<uint4*>(o + 32) = *reinterpret_cast<const uint4*>(out[1]);
     }
     const int run = adapter_rank_run(R);
-    if (v4 != nullptr && r < (R + 63) / 64 * run) {
-        T part[4];
-        part[0] = down<T>(0.0f);
-        if (std::is_same<T, __half>::value) {  // see adapter.h
-            float rest = s, scale = 0x1p11f;
+    if (jb.v4 != nullptr && r0 < (R + 63) / 64 * run) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i, scale *= 0x1p-11f) {
-                const float x = rest * (1.0f / scale);
-                const bool none = i == 0 ? !(fabsf(s) > 65504.0f) : (i < 3 && fabsf(x) < 0x1p-14f);
-                part[i] = down<T>(none ? 0.0f : x);
-                rest = none ? rest : part_rest<T>(rest, part[i], scale);
-            }
-        } else {
-            part[1] = down<T>(s);
-            const float r1 = part_rest<T>(s, part[1], 1.0f);
-            part[2] = down<T>(r1);
-            part[3] = down<T>(part_rest<T>(r1, part[2], 1.0f));
+        for (int u = 0; u < 8; ++u) {
+            T part[4];
+            four_parts<T>(v[u], part);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) out[q][u] = part[q];
         }
-        T* o = v4 + m * adapter_grad_cols(R) + (r / 64) * 256 + r % 64;
+        T* o = static_cast<T*>(jb.v4) + m * adapter_grad_cols(R) + (r0 / 64) * 256 + r0 % 64;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i * run] = part[i];
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(o + q * run) = *reinterpret_cast<const uint4*>(out[q]);
     }
 }
 
@@ -368,19 +414,24 @@ __global__ void __launch_bounds__(128)
         if (r0 + i < R) dst[static_cast<int64_t>(r0 + i) * C + c] = acc[i];
 }
 
-// out[g] = the chunks' sums added in order; +0 for an adapter without rows.
-__global__ void __launch_bounds__(256) grad_sum_kernel(float* out, const float* parts, AdapterChunks ch, int64_t RC) {
+// out[g] = the chunks' sums added in order; +0 for an adapter without rows.  An
+// adapter of one chunk has its result already.  Block row z does job z.
+__global__ void __launch_bounds__(256)
+    grad_sum_kernel(const __grid_constant__ AdapterGradJobs jobs, AdapterChunks ch, int R) {
     grid_dep_wait();
     grid_dep_launch();
     const uint32_t g = blockIdx.x;
     const uint32_t n = ch.first[g + 1] - ch.first[g];
     if (n == 1) return;
-    float* o = out + static_cast<int64_t>(g) * RC;
-    const float* p = parts + static_cast<int64_t>(ch.part[g]) * RC;
+    const AdapterGradJob& jb = jobs.job[blockIdx.z];
+    const int64_t RC = R * jb.C;
+    float* o = jb.out + static_cast<int64_t>(g) * RC;
+    const float* p = jb.parts + static_cast<int64_t>(ch.part[g]) * RC;
     for (int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; i < RC; i += static_cast<int64_t>(gridDim.y) * 256) {
         float v = 0.0f;
         if (n > 1) {
             v = p[i];
+#pragma unroll 4
             for (uint32_t j = 1; j < n; ++j) v += p[static_cast<int64_t>(j) * RC + i];
         }
         o[i] = v;
@@ -438,25 +489,33 @@ cudaError_t grad_scalar(const LaunchCtx& c, float* out, float* parts, const floa
     return launched(c);
 }
 
-cudaError_t grad_sum(const LaunchCtx& c, float* out, const float* parts, const AdapterChunks& ch, int64_t RC, int64_t G) {
-    const dim3 grid(static_cast<unsigned>(G), static_cast<unsigned>(lmin((RC + 255) / 256, 1024)));
-    const cudaError_t e = launch_pdl(grad_sum_kernel, grid, dim3(256), 0, c.stream, out, parts, ch, RC);
+cudaError_t grad_sum(const LaunchCtx& c, const AdapterGradJob* jobs, int count, const AdapterChunks& ch, int R, int64_t M,
+                     int64_t G) {
+    AdapterGradJobs js{};
+    int64_t most = 0;
+    for (int i = 0; i < count; ++i) {
+        js.job[i] = jobs[i];
+        most = lmax(most, R * jobs[i].C);
+    }
+    const dim3 grid(static_cast<unsigned>(G), static_cast<unsigned>(lmin((most + 255) / 256, 1024)), static_cast<unsigned>(count));
+    const cudaError_t e = launch_pdl(grad_sum_kernel, grid, dim3(256), 0, c.stream, js, ch, R);
     if (e == cudaSuccess) c.count();
     return e;
 }
 
-cudaError_t narrow_finish_tc(const LaunchCtx& c, bi_dtype dt, const float* partial, const float* h_in, const uint32_t* ids,
-                             const float* scales, float* h, void* hh, void* v4, int64_t M, int R, int64_t G, int pieces) {
+// One or two jobs over the same rows: the second's partial is null.
+cudaError_t narrow_finish_tc(const LaunchCtx& c, bi_dtype dt, const FinishJob& a, const FinishJob* b, const uint32_t* ids,
+                             const float* scales, int64_t M, int R, int64_t G, int pieces) {
+    const FinishJobs jobs{{a, b ? *b : FinishJob{}}};
     const int rp = (R + 15) / 16 * 16;
-    const int width = static_cast<int>(lmax(hh ? (R + 31) / 32 * 32 : R, v4 ? (R + 63) / 64 * adapter_rank_run(R) : R));
-    const dim3 grid(static_cast<unsigned>((M * width + 255) / 256));
+    const bool hh = a.hh || (b && b->hh), v4 = a.v4 || (b && b->v4);
+    const int per_row = static_cast<int>(lmax(hh ? (R + 31) / 32 * 32 : rp, v4 ? (R + 63) / 64 * adapter_rank_run(R) : rp)) / 8;
+    const dim3 grid(static_cast<unsigned>((M * per_row + 255) / 256), b ? 2 : 1);
     const cudaError_t e =
-        dt == BI_BF16 ? launch_pdl(narrow_finish_tc_kernel<__nv_bfloat16>, grid, dim3(256), 0, c.stream, partial, h_in, ids, scales,
-                                   h, static_cast<__nv_bfloat16*>(hh), static_cast<__nv_bfloat16*>(v4), M, R, rp,
-                                   static_cast<uint32_t>(G), pieces, width)
-                      : launch_pdl(narrow_finish_tc_kernel<__half>, grid, dim3(256), 0, c.stream, partial, h_in, ids, scales, h,
-                                   static_cast<__half*>(hh), static_cast<__half*>(v4), M, R, rp, static_cast<uint32_t>(G), pieces,
-                                   width);
+        dt == BI_BF16 ? launch_pdl(narrow_finish_tc_kernel<__nv_bfloat16>, grid, dim3(256), 0, c.stream, jobs, ids, scales, M, R,
+                                   rp, static_cast<uint32_t>(G), pieces, per_row)
+                      : launch_pdl(narrow_finish_tc_kernel<__half>, grid, dim3(256), 0, c.stream, jobs, ids, scales, M, R, rp,
+                                   static_cast<uint32_t>(G), pieces, per_row);
     if (e == cudaSuccess) c.count();
     return e;
 }
@@ -532,7 +591,7 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
             return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
         }
         if (e == cudaSuccess)
-            e = narrow_finish_tc(c, dtype, part, nullptr, row_adapters, scales, h, p + o_hh, nullptr, m, R, g, pieces);
+            e = narrow_finish_tc(c, dtype, {part, nullptr, h, p + o_hh, nullptr}, nullptr, row_adapters, scales, m, R, g, pieces);
         if (e == cudaSuccess) e = tc_adapter_rows(c, dtype, 0, y, x, w, bias, p + o_hh, b, plan, m, k, n, R, g);
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
     }
@@ -595,7 +654,7 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
             (dx && (!aligned16(dx) || !aligned16(w) || !aligned16(a))))
             return fail(eng, BI_ERR_MISALIGNED, "tensor-core tier needs 16-byte aligned dx, x, w, dy, a, b");
         // scratch: plan | pieces of u | u in two parts | u, s h in four parts |
-        // sorted rows | chunk tables | chunk sums (of dA, then of dB)
+        // sorted rows | chunk tables | chunk sums
         const bool grads = da || db;
         Cut cut;
         const int64_t o_plan = cut.take(need_u ? AdapterPlan::words(m) * 4 : 0),
@@ -605,7 +664,7 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
                       o_seg = cut.take(grads ? seg_table_len(g) * 4 : 0), o_perm = cut.take(grads ? m * 4 : 0),
                       o_hist = cut.take(grads ? segment_scratch_bytes(m, g) : 0),
                       o_ch = cut.take(grads ? AdapterChunks::words(g) * 4 : 0),
-                      o_sum = cut.take(grads ? AdapterChunks::max_parts(m) * r * lmax(da ? k : 0, db ? n : 0) * 4 : 0);
+                      o_sum = cut.take(grads ? AdapterChunks::max_parts(m) * r * ((da ? k : 0) + (db ? n : 0)) * 4 : 0);
         Scratch sc(eng, s, static_cast<size_t>(cut.at));
         if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "adapter scratch");
         uint8_t* p = static_cast<uint8_t*>(sc.ptr);
@@ -615,29 +674,57 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         uint32_t* perm = reinterpret_cast<uint32_t*>(p + o_perm);
         const AdapterChunks ch = AdapterChunks::at(p + o_ch, g);
         float* sums = reinterpret_cast<float*>(p + o_sum);
-        cudaError_t e = cudaSuccess;
-        if (need_u) {
-            e = tc_adapter_narrow(c, dtype, part, dy, b, row_adapters, plan, m, n, R, g);
-            if (e == cudaSuccess)
-                e = narrow_finish_tc(c, dtype, part, nullptr, row_adapters, scales, nullptr, dx ? p + o_uu : nullptr,
-                                     da ? p + o_u3 : nullptr, m, R, g, pieces);
-        }
-        if (e == cudaSuccess && dx) e = tc_adapter_rows(c, dtype, 1, dx, dy, w, nullptr, p + o_uu, a, plan, m, k, n, R, g);
-        if (e == cudaSuccess && grads) {
-            e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
+        // the sorting of the rows for dA and dB runs on the engine's side stream
+        // beside the narrow product; the caller's stream waits for it before
+        // those (and before the scratch is released)
+        cudaError_t e = cudaSuccess, side = cudaSuccess;
+        cudaEvent_t fork = nullptr, join = nullptr;
+        auto sort_rows = [&](const LaunchCtx& cc) {
+            cudaError_t r = segment(cc, row_adapters, m, g, seg, perm, p + o_hist);
+            if (r == cudaSuccess) {
+                r = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, cc.stream, seg, static_cast<uint32_t>(g), ch);
+                if (r == cudaSuccess) cc.count();
+            }
+            return r;
+        };
+        const bool overlap = grads && need_u;
+        if (overlap) {
+            e = cudaEventCreateWithFlags(&fork, cudaEventDisableTiming);
+            if (e == cudaSuccess) e = cudaEventCreateWithFlags(&join, cudaEventDisableTiming);
+            if (e == cudaSuccess) e = cudaEventRecord(fork, s);
+            if (e == cudaSuccess) e = cudaStreamWaitEvent(eng->side, fork, 0);
             if (e == cudaSuccess) {
-                e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, static_cast<uint32_t>(g), ch);
-                if (e == cudaSuccess) c.count();
+                side = sort_rows(ctx(eng, eng->side));
+                const cudaError_t r = cudaEventRecord(join, eng->side);  // recorded whatever happened above
+                if (side == cudaSuccess) side = r;
             }
         }
-        if (e == cudaSuccess && da) {
-            e = tc_adapter_grad(c, dtype, da, sums, p + o_u3, x, seg, perm, ch, m, k, R, g);
-            if (e == cudaSuccess) e = grad_sum(c, da, sums, ch, r * k, g);
+        if (e == cudaSuccess && need_u) {
+            e = tc_adapter_narrow(c, dtype, part, dy, b, row_adapters, plan, m, n, R, g);
+            const FinishJob u{part, nullptr, nullptr, dx ? p + o_uu : nullptr, da ? p + o_u3 : nullptr};
+            const FinishJob hs{nullptr, h, nullptr, nullptr, p + o_h3};
+            if (e == cudaSuccess) e = narrow_finish_tc(c, dtype, u, db ? &hs : nullptr, row_adapters, scales, m, R, g, pieces);
         }
-        if (e == cudaSuccess && db) {
-            e = narrow_finish_tc(c, dtype, nullptr, h, row_adapters, scales, nullptr, nullptr, p + o_h3, m, R, g, 0);
-            if (e == cudaSuccess) e = tc_adapter_grad(c, dtype, db, sums, p + o_h3, dy, seg, perm, ch, m, n, R, g);
-            if (e == cudaSuccess) e = grad_sum(c, db, sums, ch, r * n, g);
+        if (e == cudaSuccess && dx) e = tc_adapter_rows(c, dtype, 1, dx, dy, w, nullptr, p + o_uu, a, plan, m, k, n, R, g);
+        if (join) {  // always joined before anything below and before the scratch is freed
+            const cudaError_t r = cudaStreamWaitEvent(s, join, 0);
+            if (e == cudaSuccess) e = side != cudaSuccess ? side : r;
+        }
+        if (fork) cudaEventDestroy(fork);
+        if (join) cudaEventDestroy(join);
+        if (e == cudaSuccess && grads && !overlap) e = sort_rows(c);
+        if (e == cudaSuccess && db && !need_u) {
+            const FinishJob hs{nullptr, h, nullptr, nullptr, p + o_h3};
+            e = narrow_finish_tc(c, dtype, hs, nullptr, row_adapters, scales, m, R, g, 0);
+        }
+        if (e == cudaSuccess && grads) {
+            AdapterGradJob jobs[2];
+            int count = 0;
+            float* db_sums = sums + (da ? AdapterChunks::max_parts(m) * r * k : 0);
+            if (da) jobs[count++] = {da, sums, p + o_u3, x, k};
+            if (db) jobs[count++] = {db, db_sums, p + o_h3, dy, n};
+            e = tc_adapter_grad(c, dtype, jobs, count, seg, perm, ch, m, R, g);
+            if (e == cudaSuccess) e = grad_sum(c, jobs, count, ch, R, m, g);
         }
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_backward");
     }
@@ -695,7 +782,8 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
                 using T = std::remove_pointer_t<decltype(t)>;
                 return grad_scalar<T>(c, out, sums, f, static_cast<const T*>(z), seg, perm, ch, m, C, R, g);
             });
-            if (err == cudaSuccess) err = grad_sum(c, out, sums, ch, r * C, g);
+            const AdapterGradJob job{out, sums, nullptr, z, C};
+            if (err == cudaSuccess) err = grad_sum(c, &job, 1, ch, R, m, g);
             return err;
         };
         if (e == cudaSuccess && da) e = one(da, u, x, k);

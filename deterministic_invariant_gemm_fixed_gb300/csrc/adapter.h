@@ -93,9 +93,18 @@ cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, c
                               const uint32_t* ids, const AdapterPlan& plan, int64_t M, int64_t L, int R, int64_t G);
 // dA and dB on the tensor cores: out[g][r,c] (or its chunks' partial slots) =
 // sum over the adapter's sorted rows of v[m,r] z[m,c], v in four parts [M,
-// adapter_grad_cols(R)].
-cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, float* out, float* parts, const void* v4, const void* z,
-                            const uint32_t* off, const uint32_t* perm, const AdapterChunks& ch, int64_t M, int64_t C,
-                            int R, int64_t G);
+// adapter_grad_cols(R)]; up to two such products in one launch.
+struct AdapterGradJob {
+    float* out;
+    float* parts;
+    const void* v4;
+    const void* z;
+    int64_t C;
+};
+struct AdapterGradJobs {
+    AdapterGradJob job[2];
+};
+cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, const AdapterGradJob* jobs, int count, const uint32_t* off,
+                            const uint32_t* perm, const AdapterChunks& ch, int64_t M, int R, int64_t G);
 
 }  // namespace bi

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     if (warp == 0 && lane == 0) {
         // the first blocks of X need no list: their bytes are expected and the
         // copies issued now, the stages' own arrivals follow with the adapters'
-        const int early = min(NP_STAGES, nkb);
+        // (the first CTA of a tile and piece; others may have no adapters left)
+        const int early = blockIdx.z == 0 ? min(NP_STAGES, nkb) : 0;
         for (int kb = 0; kb < early; ++kb) {
             asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full_bar(kb)), "r"(NP_A) : "memory");
             tma_load_2d(sbase + kb * NP_STAGE, &tmX, (kb0 + kb) * BK, row0, full_bar(kb));
@@ -685,15 +686,12 @@ __host__ __device__ constexpr int gt_smem(int run) { return 1024 + gt_stages(run
 static_assert(gt_stages(16) == 4 && gt_stages(32) == 3 && gt_stages(64) == 2, "ring depths");
 
 struct GradParams {
-    float* out;
-    float* parts;
-    const uint16_t* v4;  // [M, vcols]
-    const uint16_t* z;   // [M, C]
+    AdapterGradJob job[2];  // v4 [M, vcols], z [M, C]
     const uint32_t* off;
     const uint32_t* perm;
     AdapterChunks ch;
-    int64_t C, vcols;
-    uint32_t chunk0, strips;  // block x: strip x % strips of chunk chunk0 + x / strips
+    int64_t vcols;
+    uint32_t chunk0, strips0, strips;  // block x: strip x % strips (job 0's first) of chunk chunk0 + x / strips
     int R, G, fmt;
     int* status;
     unsigned long long wait_limit;
@@ -732,7 +730,10 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
     const uint32_t s0 = p.off[g] + j * static_cast<uint32_t>(ADAPTER_CHUNK);
     const uint32_t s1 = min(p.off[g + 1], s0 + static_cast<uint32_t>(ADAPTER_CHUNK));
     const int blocks = static_cast<int>((s1 - s0 + GT_ROWS - 1) / GT_ROWS);
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x % p.strips) * 128;
+    const uint32_t strip = blockIdx.x % p.strips;
+    const AdapterGradJob& jb = p.job[strip >= p.strips0];
+    const int64_t C = jb.C;
+    const int64_t c0 = static_cast<int64_t>(strip >= p.strips0 ? strip - p.strips0 : strip) * 128;
     const int r0 = blockIdx.y * 64;
 
     if (tid == 0) {
@@ -755,9 +756,10 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
         // thread t copies 16-byte piece t % 8 of each 128-byte atom row, rows t / 8 + 16 i
         const int piece = tid & 7, rr = tid >> 3;
         const uint32_t sw = static_cast<uint32_t>((piece ^ (rr & 7)) * 16);  // rr + 16 i has the same low bits
-        const bool in0 = c0 + piece * 8 < p.C, in1 = c0 + 64 + piece * 8 < p.C;
-        const uint16_t* zc = p.z + c0 + piece * 8;
-        const uint16_t* vc = p.v4 + static_cast<int64_t>(blockIdx.y) * (4 * RUN) + piece * 8;
+        const bool in0 = c0 + piece * 8 < C, in1 = c0 + 64 + piece * 8 < C;
+        const uint16_t* z = static_cast<const uint16_t*>(jb.z);
+        const uint16_t* zc = z + c0 + piece * 8;
+        const uint16_t* vc = static_cast<const uint16_t*>(jb.v4) + static_cast<int64_t>(blockIdx.y) * (4 * RUN) + piece * 8;
         uint32_t row[4];
         auto rows_of = [&](int b) {
 #pragma unroll
@@ -780,8 +782,8 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
                         const bool in = row[i] != 0xffffffffu;
                         const int64_t m = in ? row[i] : 0;
                         const uint32_t dst = a + (rr + 16 * i) * 128 + sw;
-                        copy16(dst, in && in0 ? zc + m * p.C : p.z, in && in0);
-                        copy16(dst + 8192, in && in1 ? zc + m * p.C + 64 : p.z, in && in1);
+                        copy16(dst, in && in0 ? zc + m * C : z, in && in0);
+                        copy16(dst + 8192, in && in1 ? zc + m * C + 64 : z, in && in1);
 #pragma unroll
                         for (int q = 0; q < ATOMS; ++q) copy16(dst + GT_A + q * 8192, vc + m * p.vcols + q * 64, in);
                     }
@@ -804,8 +806,8 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
         if (ok) {
             tc_fence_after();
             const int64_t col = c0 + 32 * warp + lane;
-            float* dst = nchunks > 1 ? p.parts + static_cast<int64_t>(p.ch.part[g] + j) * p.R * p.C
-                                     : p.out + static_cast<int64_t>(g) * p.R * p.C;
+            float* dst = nchunks > 1 ? jb.parts + static_cast<int64_t>(p.ch.part[g] + j) * p.R * C
+                                     : jb.out + static_cast<int64_t>(g) * p.R * C;
             const uint32_t t = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
             for (int q = 0; q < RUN && r0 + q < p.R; q += 16) {
                 uint32_t v0[16], v1[16], v2[16], v3[16];
@@ -813,14 +815,14 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
                 tmem_ld16(t + RUN + q, v1);
                 tmem_ld16(t + 2 * RUN + q, v2);
                 tmem_ld16(t + 3 * RUN + q, v3);
-                if (col < p.C) {
+                if (col < C) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float a = __uint_as_float(v0[i]), m = __uint_as_float(v1[i]), l = __uint_as_float(v2[i]);
                         const float t = __uint_as_float(v3[i]);
                         const float s = p.fmt ? m + (l + t)
                                               : fmaf(a, 0x1p11f, fmaf(fmaf(t, 0x1p-11f, l), 0x1p-11f, m));
-                        if (r0 + q + i < p.R) dst[static_cast<int64_t>(r0 + q + i) * p.C + col] = s;
+                        if (r0 + q + i < p.R) dst[static_cast<int64_t>(r0 + q + i) * C + col] = s;
                     }
                 }
                 __syncwarp();
@@ -936,16 +938,20 @@ cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void*
                          : small_rows_fmt<0>(c, dx, M, mx, mw, mh, mq, p, grid);
 }
 
-cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, float* out, float* parts, const void* v4, const void* z,
-                            const uint32_t* off, const uint32_t* perm, const AdapterChunks& ch, int64_t M, int64_t C,
-                            int R, int64_t G) {
+cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, const AdapterGradJob* jobs, int count, const uint32_t* off,
+                            const uint32_t* perm, const AdapterChunks& ch, int64_t M, int R, int64_t G) {
     GradParams p{};
-    p.out = out; p.parts = parts; p.v4 = static_cast<const uint16_t*>(v4); p.z = static_cast<const uint16_t*>(z);
-    p.off = off; p.perm = perm; p.ch = ch; p.C = C; p.vcols = adapter_grad_cols(R); p.R = R; p.G = static_cast<int>(G);
+    int64_t strips = 0;
+    for (int i = 0; i < count; ++i) {
+        p.job[i] = jobs[i];
+        strips += (jobs[i].C + 127) / 128;
+        if (i == 0) p.strips0 = static_cast<uint32_t>(strips);
+    }
+    p.off = off; p.perm = perm; p.ch = ch; p.vcols = adapter_grad_cols(R); p.R = R; p.G = static_cast<int>(G);
     p.fmt = dt == BI_BF16 ? 1 : 0;
     p.status = c.status; p.wait_limit = c.wait_limit_ns;
-    const int64_t strips = (C + 127) / 128, chunks = AdapterChunks::max_chunks(M, G);
     p.strips = static_cast<uint32_t>(strips);
+    const int64_t chunks = AdapterChunks::max_chunks(M, G);
     const int64_t slice = ((int64_t(1) << 31) - 1) / strips;  // chunks per launch
     for (int64_t q = 0; q < chunks; q += slice) {
         p.chunk0 = static_cast<uint32_t>(q);
