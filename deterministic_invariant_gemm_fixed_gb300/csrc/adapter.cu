@@ -77,14 +77,14 @@ __global__ void __launch_bounds__(1024) adapter_chunks_kernel(const uint32_t* of
 // ---------------------------------------------------------------- narrow product, scalar
 
 // partial[piece][m][r] = sum over the piece's l of X[m,l] P[g][r,l].  A warp has
-// four rows and one piece, the rows' 512 values in registers (lane j holds l = 128 i
-// + 4 j + 0..3), and for each of up to 16 ranks reads P's 512 values once, for all
-// four rows if they have one adapter: lane sums (16 FMAs, l ascending) and a
-// shuffle tree, the same order for a row alone or among others.  Rows of other
-// warps find P in L1.  (One result per thread, operands staged in shared memory
-// per adapter among 16 rows, took 81 us where this takes 13: 999 x 1000, rank 5,
-// seven adapters in no order.)
-constexpr int NS_ROWS = 4, NS_RANKS = 16, NS_WARPS = 4;
+// ROWS rows (four; one where that leaves SMs without warps) and one piece, the
+// rows' 512 values in registers (lane j holds l = 128 i + 4 j + 0..3), and for each
+// of up to 16 ranks reads P's 512 values once, for all of its rows if they have
+// one adapter: lane sums (16 FMAs, l ascending) and a shuffle tree, the same order
+// for a row alone or among others.  Rows of other warps find P in L1.  (One result
+// per thread, operands staged in shared memory per adapter among 16 rows, took 81
+// us where this takes 7: 999 x 1000, rank 5, seven adapters in no order.)
+constexpr int NS_RANKS = 16, NS_WARPS = 4;
 template <typename T>
 __device__ __forceinline__ void load_lane(const T* p, int64_t l0, int64_t L, bool vec, int lane, float (&v)[16]) {
 #pragma unroll
@@ -106,21 +106,21 @@ __device__ __forceinline__ void load_lane(const T* p, int64_t l0, int64_t L, boo
         }
     }
 }
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(32 * NS_WARPS)
     narrow_scalar_kernel(const T* x, const T* p, const uint32_t* ids, float* partial, int64_t M, int64_t L, int R, uint32_t G,
                          int vec) {
     grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t m0 = (static_cast<int64_t>(blockIdx.x) * NS_WARPS + warp) * NS_ROWS;
+    const int64_t m0 = (static_cast<int64_t>(blockIdx.x) * NS_WARPS + warp) * ROWS;
     if (m0 >= M) return;
     const int r0 = blockIdx.z * NS_RANKS, r1 = min(R, r0 + NS_RANKS);
     const int64_t l0 = static_cast<int64_t>(blockIdx.y) * ADAPTER_PIECE, l1 = lmin(L, l0 + ADAPTER_PIECE);
-    uint32_t g[NS_ROWS];
-    float v[NS_ROWS][16];
+    uint32_t g[ROWS];
+    float v[ROWS][16];
 #pragma unroll
-    for (int i = 0; i < NS_ROWS; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         g[i] = m0 + i < M ? ids[m0 + i] : G;
         if (g[i] < G) load_lane(x + (m0 + i) * L, l0, l1, vec != 0, lane, v[i]);
     }
@@ -134,20 +134,24 @@ __global__ void __launch_bounds__(32 * NS_WARPS)
         return s;
     };
     float* out = partial + (static_cast<int64_t>(blockIdx.y) * M + m0) * R;
-    if (g[0] < G && g[1] == g[0] && g[2] == g[0] && g[3] == g[0]) {
+    bool one = g[0] < G;
+#pragma unroll
+    for (int i = 1; i < ROWS; ++i) one = one && g[i] == g[0];
+    if (one) {
         const T* pg = p + static_cast<int64_t>(g[0]) * R * L;
+#pragma unroll 2
         for (int r = r0; r < r1; ++r) {
             float b[16];
             load_lane(pg + static_cast<int64_t>(r) * L, l0, l1, vec != 0, lane, b);
 #pragma unroll
-            for (int i = 0; i < NS_ROWS; ++i) {
+            for (int i = 0; i < ROWS; ++i) {
                 const float s = row_sum(v[i], b);
                 if (lane == i) out[static_cast<int64_t>(i) * R + r] = s;
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NS_ROWS; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             if (g[i] >= G) continue;
             const T* pg = p + static_cast<int64_t>(g[i]) * R * L;
 #pragma unroll 2
@@ -306,59 +310,59 @@ __global__ void __launch_bounds__(256) scale_rows_kernel(const float* h, const u
 // ---------------------------------------------------------------- wide product, scalar
 
 // out[m,c] = round( base[m,c] + sum over r ascending of hs[m,r] Q[g][r,c] ), base
-// in f32 (for f32 it is out itself).  16 rows by 256 columns per block, a column
-// per thread: an element of Q is read once for all of the block's rows with
+// in f32 (for f32 it is out itself).  ROWS rows by 256 columns per block (16; 4
+// where that leaves SMs without blocks), a column per thread: an element of Q is read once for all of the block's rows with
 // that adapter.
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* base, const float* hs, const T* q,
                                                           const uint32_t* ids, int64_t M, int64_t C, int R, uint32_t G) {
-    extern __shared__ float s_h[];  // [R][16]
-    __shared__ uint32_t s_id[16], s_mask[16];  // row i's adapter; the rows with it, at the first of them (else 0)
+    extern __shared__ float s_h[];  // [R][ROWS]
+    __shared__ uint32_t s_id[ROWS], s_mask[ROWS];  // row i's adapter; the rows with it, at the first of them (else 0)
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * ROWS;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + tid;
     if (tid < 32) {
-        const uint32_t id = tid < 16 && m0 + tid < M ? ids[m0 + tid] : G;
+        const uint32_t id = tid < ROWS && m0 + tid < M ? ids[m0 + tid] : G;
         const uint32_t same = __match_any_sync(0xffffffffu, id);
-        if (tid < 16) {
+        if (tid < ROWS) {
             s_id[tid] = id;
             s_mask[tid] = id < G && (same & ((1u << tid) - 1)) == 0 ? same : 0;
         }
     }
-    for (int i = tid; i < 16 * R; i += 256) {
+    for (int i = tid; i < ROWS * R; i += 256) {
         const int row = i / R, r = i % R;
-        s_h[r * 16 + row] = m0 + row < M ? hs[(m0 + row) * R + r] : 0.0f;
+        s_h[r * ROWS + row] = m0 + row < M ? hs[(m0 + row) * R + r] : 0.0f;
     }
     __syncthreads();
     if (c >= C) return;
     const bool in_place = reinterpret_cast<const void*>(base) == reinterpret_cast<const void*>(out);
-    float b[16];
+    float b[ROWS];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) b[i] = m0 + i < M ? base[(m0 + i) * C + c] : 0.0f;
+    for (int i = 0; i < ROWS; ++i) b[i] = m0 + i < M ? base[(m0 + i) * C + c] : 0.0f;
     uint32_t any = 0;
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < ROWS; ++e) {
         const uint32_t mask = s_mask[e];
         if (mask == 0) continue;
         any |= mask;
         const T* qg = q + static_cast<int64_t>(s_id[e]) * R * C + c;
-        float acc[16];
+        float acc[ROWS];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < ROWS; ++i) acc[i] = 0.0f;
 #pragma unroll 8
         for (int r = 0; r < R; ++r) {
             const float v = up<T>(qg[static_cast<int64_t>(r) * C]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = fmaf(s_h[r * 16 + i], v, acc[i]);
+            for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(s_h[r * ROWS + i], v, acc[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < ROWS; ++i)
             if ((mask >> i) & 1u) out[(m0 + i) * C + c] = down<T>(b[i] + acc[i]);
     }
     if (in_place) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)  // rows without adapter
+    for (int i = 0; i < ROWS; ++i)  // rows without adapter
         if (!((any >> i) & 1u) && m0 + i < M) out[(m0 + i) * C + c] = down<T>(b[i]);
 }
 
@@ -451,12 +455,13 @@ int pieces_of(int64_t L) { return static_cast<int>((L + ADAPTER_PIECE - 1) / ADA
 template <typename T>
 cudaError_t narrow_scalar(const LaunchCtx& c, const T* x, const T* p, const uint32_t* ids, float* partial, int64_t M,
                           int64_t L, int R, int64_t G) {
-    const int64_t rows = NS_ROWS * NS_WARPS;
+    const bool few = (M + 3) / 4 * pieces_of(L) < 16 * int64_t(c.sm_count);  // too few warps of four rows
+    const int64_t rows = (few ? 1 : 4) * NS_WARPS;
     const dim3 grid(static_cast<unsigned>((M + rows - 1) / rows), static_cast<unsigned>(pieces_of(L)),
                     static_cast<unsigned>((R + NS_RANKS - 1) / NS_RANKS));
     const int vec = L % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0 &&
                     reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
-    const cudaError_t e = launch_pdl(narrow_scalar_kernel<T>, grid, dim3(32 * NS_WARPS), 0, c.stream, x, p, ids, partial, M, L, R,
+    const cudaError_t e = launch_pdl(few ? narrow_scalar_kernel<T, 1> : narrow_scalar_kernel<T, 4>, grid, dim3(32 * NS_WARPS), 0, c.stream, x, p, ids, partial, M, L, R,
                                      static_cast<uint32_t>(G), vec);
     if (e == cudaSuccess) c.count();
     return e;
@@ -473,8 +478,11 @@ cudaError_t narrow_finish(const LaunchCtx& c, const float* partial, const uint32
 template <typename T>
 cudaError_t wide_scalar(const LaunchCtx& c, T* out, const float* base, const float* hs, const T* q, const uint32_t* ids,
                         int64_t M, int64_t C, int R, int64_t G) {
-    const dim3 grid(static_cast<unsigned>((M + 15) / 16), static_cast<unsigned>((C + 255) / 256));
-    const cudaError_t e = launch_pdl(wide_scalar_kernel<T>, grid, dim3(256), static_cast<size_t>(16 * R * 4), c.stream, out, base,
+    const bool few = (M + 15) / 16 * ((C + 255) / 256) < 4 * int64_t(c.sm_count);
+    const int rows = few ? 4 : 16;
+    const dim3 grid(static_cast<unsigned>((M + rows - 1) / rows), static_cast<unsigned>((C + 255) / 256));
+    const cudaError_t e = launch_pdl(few ? wide_scalar_kernel<T, 4> : wide_scalar_kernel<T, 16>, grid, dim3(256),
+                                     static_cast<size_t>(rows * R * 4), c.stream, out, base,
                                      hs, q, ids, M, C, R, static_cast<uint32_t>(G));
     if (e == cudaSuccess) c.count();
     return e;
@@ -497,7 +505,9 @@ cudaError_t grad_sum(const LaunchCtx& c, const AdapterGradJob* jobs, int count, 
         js.job[i] = jobs[i];
         most = lmax(most, R * jobs[i].C);
     }
-    const dim3 grid(static_cast<unsigned>(G), static_cast<unsigned>(lmin((most + 255) / 256, 1024)), static_cast<unsigned>(count));
+    // about eight blocks per SM in all: most adapters have one chunk and nothing to add
+    const int64_t y = lmax(1, lmin((most + 255) / 256, 8 * int64_t(c.sm_count) / (G * count)));
+    const dim3 grid(static_cast<unsigned>(G), static_cast<unsigned>(y), static_cast<unsigned>(count));
     const cudaError_t e = launch_pdl(grad_sum_kernel, grid, dim3(256), 0, c.stream, js, ch, R);
     if (e == cudaSuccess) c.count();
     return e;
