@@ -313,10 +313,20 @@ __global__ void __launch_bounds__(256) scale_rows_kernel(const float* h, const u
 // in f32 (for f32 it is out itself).  ROWS rows by 256 columns per block (16; 4
 // where that leaves SMs without blocks), a column per thread: an element of Q is read once for all of the block's rows with
 // that adapter.
+//
+// hs comes from the finish kernel, or (hs null) from the pieces themselves, added
+// and scaled here in the same order; then the first column of blocks writes h.
+struct WideSource {
+    const float* hs;
+    const float* partial;  // [pieces][M][R]
+    const float* scales;
+    float* h;
+    int pieces;
+};
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* base, const float* hs, const T* q,
+__global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* base, const WideSource src, const T* q,
                                                           const uint32_t* ids, int64_t M, int64_t C, int R, uint32_t G) {
-    extern __shared__ float s_h[];  // [R][ROWS]
+    extern __shared__ float s_h[];  // [R rounded up to 8][ROWS], zeros past R
     __shared__ uint32_t s_id[ROWS], s_mask[ROWS];  // row i's adapter; the rows with it, at the first of them (else 0)
     grid_dep_wait();
     grid_dep_launch();
@@ -331,16 +341,56 @@ __global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* b
             s_mask[tid] = id < G && (same & ((1u << tid) - 1)) == 0 ? same : 0;
         }
     }
-    for (int i = tid; i < ROWS * R; i += 256) {
-        const int row = i / R, r = i % R;
-        s_h[r * ROWS + row] = m0 + row < M ? hs[(m0 + row) * R + r] : 0.0f;
+    const int R8 = (R + 7) / 8 * 8;
+    for (int i = tid; i < ROWS * R8; i += 256) {
+        const int row = i / R8, r = i % R8;
+        const int64_t at = (m0 + row) * R + r;
+        float v = 0.0f;
+        if (m0 + row < M && r < R) {
+            if (src.hs != nullptr) {
+                v = src.hs[at];
+            } else {
+                const uint32_t g = ids[m0 + row];
+                if (g < G) {
+                    v = src.partial[at];
+                    for (int p = 1; p < src.pieces; ++p) v += src.partial[static_cast<int64_t>(p) * M * R + at];
+                }
+                if (src.h != nullptr && blockIdx.y == 0) src.h[at] = v;
+                if (g < G && src.scales != nullptr) v *= src.scales[g];
+            }
+        }
+        s_h[r * ROWS + row] = v;
+    }
+    float b[ROWS];
+    if (c < C) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) b[i] = m0 + i < M ? base[(m0 + i) * C + c] : 0.0f;
     }
     __syncthreads();
     if (c >= C) return;
     const bool in_place = reinterpret_cast<const void*>(base) == reinterpret_cast<const void*>(out);
-    float b[ROWS];
+    if constexpr (ROWS == 4) {  // few blocks: each row reads its own adapter, all loads in flight at once
+        float acc[ROWS] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < R; r += 8) {
+            float v[ROWS][8];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) b[i] = m0 + i < M ? base[(m0 + i) * C + c] : 0.0f;
+            for (int i = 0; i < ROWS; ++i) {
+                const T* qg = q + (static_cast<int64_t>(s_id[i]) * R + r) * C + c;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[i][u] = s_id[i] < G && r + u < R ? up<T>(qg[static_cast<int64_t>(u) * C]) : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(s_h[(r + u) * ROWS + i], v[i][u], acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (s_id[i] < G) out[(m0 + i) * C + c] = down<T>(b[i] + acc[i]);
+            else if (!in_place && m0 + i < M) out[(m0 + i) * C + c] = down<T>(b[i]);
+        }
+        return;
+    }
     uint32_t any = 0;
     for (int e = 0; e < ROWS; ++e) {
         const uint32_t mask = s_mask[e];
@@ -350,11 +400,14 @@ __global__ void __launch_bounds__(256) wide_scalar_kernel(T* out, const float* b
         float acc[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) acc[i] = 0.0f;
-#pragma unroll 8
-        for (int r = 0; r < R; ++r) {
-            const float v = up<T>(qg[static_cast<int64_t>(r) * C]);
+        for (int r = 0; r < R; r += 8) {  // eight loads in flight; past R both factors are 0
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(s_h[r * ROWS + i], v, acc[i]);
+            for (int u = 0; u < 8; ++u) v[u] = r + u < R ? up<T>(qg[static_cast<int64_t>(r + u) * C]) : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) acc[i] = fmaf(s_h[(r + u) * ROWS + i], v[u], acc[i]);
         }
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
@@ -476,17 +529,21 @@ cudaError_t narrow_finish(const LaunchCtx& c, const float* partial, const uint32
 }
 
 template <typename T>
-cudaError_t wide_scalar(const LaunchCtx& c, T* out, const float* base, const float* hs, const T* q, const uint32_t* ids,
+cudaError_t wide_scalar(const LaunchCtx& c, T* out, const float* base, const WideSource& src, const T* q, const uint32_t* ids,
                         int64_t M, int64_t C, int R, int64_t G) {
     const bool few = (M + 15) / 16 * ((C + 255) / 256) < 4 * int64_t(c.sm_count);
     const int rows = few ? 4 : 16;
     const dim3 grid(static_cast<unsigned>((M + rows - 1) / rows), static_cast<unsigned>((C + 255) / 256));
     const cudaError_t e = launch_pdl(few ? wide_scalar_kernel<T, 4> : wide_scalar_kernel<T, 16>, grid, dim3(256),
-                                     static_cast<size_t>(rows * R * 4), c.stream, out, base,
-                                     hs, q, ids, M, C, R, static_cast<uint32_t>(G));
+                                     static_cast<size_t>(rows * ((R + 7) / 8 * 8) * 4), c.stream, out, base, src, q, ids, M, C,
+                                     R, static_cast<uint32_t>(G));
     if (e == cudaSuccess) c.count();
     return e;
 }
+
+// A row's sums of pieces that the wide kernel's blocks take on themselves, each
+// for its own columns (then no finish kernel runs): few enough to be noise there.
+constexpr int64_t WIDE_FUSE = 512;
 
 template <typename T>
 cudaError_t grad_scalar(const LaunchCtx& c, float* out, float* parts, const float* hs, const T* z, const uint32_t* seg,
@@ -619,7 +676,7 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
     // the shared product first: it may need scratch of its own, and a call that
     // gets none must leave nothing enqueued
     if (dtype == BI_F32) {
-        st = bi_forward(eng, y, x, w, bias, m, k, n, dtype, stream, tensor_cores);
+        st = adapter_projection_f32(eng, c, 0, y, x, w, bias, m, k, n, tensor_cores);
         if (st != BI_OK) return st;
     } else {
         e = scalar_rows(c, dtype, base, x, w, bias, m, k, n, 0, 1);
@@ -629,11 +686,13 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
             using T = std::remove_pointer_t<decltype(t)>;
             return narrow_scalar<T>(c, static_cast<const T*>(x), static_cast<const T*>(a), row_adapters, part, m, k, R, g);
         });
-    if (e == cudaSuccess) e = narrow_finish(c, part, row_adapters, scales, h, hs, m, R, g, pieces);
+    const bool fuse = pieces * r <= WIDE_FUSE;
+    if (e == cudaSuccess && !fuse) e = narrow_finish(c, part, row_adapters, scales, h, hs, m, R, g, pieces);
     if (e == cudaSuccess)
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return wide_scalar<T>(c, static_cast<T*>(y), base, hs, static_cast<const T*>(b), row_adapters, m, n, R, g);
+            return wide_scalar<T>(c, static_cast<T*>(y), base, WideSource{fuse ? nullptr : hs, part, scales, h, pieces},
+                                  static_cast<const T*>(b), row_adapters, m, n, R, g);
         });
     return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
 }
@@ -763,7 +822,7 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     const uint32_t G = static_cast<uint32_t>(g);
     cudaError_t e = cudaSuccess;
     if (dx && dtype == BI_F32) {  // first, as in the forward
-        st = bi_backward_dx(eng, dx, dy, w, m, k, n, dtype, stream, tensor_cores);
+        st = adapter_projection_f32(eng, c, 1, dx, dy, w, nullptr, m, k, n, tensor_cores);
         if (st != BI_OK) return st;
     } else if (dx) {
         e = scalar_rows(c, dtype, base, dy, w, nullptr, m, n, k, 1, 1);
@@ -778,7 +837,8 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     if (e == cudaSuccess && dx) {
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return wide_scalar<T>(c, static_cast<T*>(dx), base, u, static_cast<const T*>(a), row_adapters, m, k, R, g);
+            return wide_scalar<T>(c, static_cast<T*>(dx), base, WideSource{u, nullptr, nullptr, nullptr, 0},
+                                  static_cast<const T*>(a), row_adapters, m, k, R, g);
         });
     }
     if (e == cudaSuccess && grads) {

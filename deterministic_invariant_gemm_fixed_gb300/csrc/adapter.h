@@ -86,6 +86,15 @@ struct AdapterPieces {
 cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
                                   const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
                                   int64_t K, int64_t N, int R, int64_t G, const AdapterPieces* fuse = nullptr);
+// The shared product of f32 adapters, as bi_forward / bi_backward_dx compute it
+// (engine.cu), with the 3xTF32 tiles chosen by their number: single CTAs' 128 x
+// 64 tiles (adapter_tc.cu; contractions up to one piece) give the same bits.
+bi_status adapter_projection_f32(bi_engine eng, const LaunchCtx& c, int dx, void* out, const void* z, const void* w,
+                                 const void* bias, int64_t m, int64_t k, int64_t n, int tensor_cores);
+bool tf32x3_small_tiles(const LaunchCtx& c, int64_t rows, int64_t cols, int64_t depth);
+cudaError_t tc_tf32x3_small(const LaunchCtx& c, const float* a_hi, const float* a_lo, int64_t lda, const float* b_hi,
+                            const float* b_lo, int64_t ldb, float* out, int64_t ldo, const float* bias, int64_t rows,
+                            int64_t cols, int64_t depth);
 // The narrow product on the tensor cores (adapter_tc.cu): partial[piece][m][rp] =
 // the piece's sum of z[m,l] p[g][r,l], rp = R rounded up to 16 the row stride.
 // Also makes the plan of the rows' adapters.

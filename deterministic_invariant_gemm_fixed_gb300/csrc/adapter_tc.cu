@@ -666,6 +666,149 @@ cudaError_t small_rows_fmt(const LaunchCtx& c, int dx, int64_t M, const CUtensor
     return dx ? small_rows_t<FMT, 128, false>(c, x, w, h, q, p, grid) : small_rows_t<FMT, 128, true>(c, x, w, h, q, p, grid);
 }
 
+// ---------------------------------------------------------------- small tiles, f32
+//
+// The 3xTF32 product of the CTA-pair kernel (operands split into hi and lo parts,
+// both K-major) by tiles of 128 rows x 64 columns on single CTAs: per 32-wide
+// block and K = 8 step lo hi and hi lo into one accumulator, hi hi into another,
+// in the pair kernel's order, so the bits are the same.  Two accumulators make two
+// chains of dependent MMAs; a block takes 0.3 us of them, the pairs' 256 x 256
+// tile 1.14 us.  999 x 1000 x 1000: 36 us on 16 pairs, 15 on 128 CTAs.
+constexpr int SF_STAGE = 2 * (128 * 128 + SM_B), SF_STAGES = 4, SF_BARS = 2 * SF_STAGES + 1;
+constexpr int SF_SMEM = 1024 + SF_STAGES * SF_STAGE + SF_BARS * 8 + 16;
+
+struct SmallF32Params {
+    float* out;
+    const float* bias;
+    int64_t M, C, ldo;
+    int num_kb;
+    int* status;
+    unsigned long long wait_limit;
+};
+
+__device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], da, db, %4, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+
+__global__ void __launch_bounds__(SM_THREADS, 1)
+    small_f32_kernel(const __grid_constant__ CUtensorMap tmAh, const __grid_constant__ CUtensorMap tmAl,
+                     const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmBl, const SmallF32Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SF_STAGES * SF_STAGE);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (SF_STAGES + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * SF_STAGES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SF_BARS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int row0 = static_cast<int>(blockIdx.y) * 128, col0 = static_cast<int>(blockIdx.x) * SM_COLS;
+    constexpr int A_HI = 0, B_HI = 128 * 128, A_LO = B_HI + SM_B, B_LO = A_LO + 128 * 128;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SF_STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<128>(smem_u32(tmem_slot));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
+    grid_dep_wait();
+    grid_dep_launch();
+    if (warp == 0 && lane == 0) {
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+            if (!mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) {
+                drain_copies(full_bar, kb, SF_STAGES);
+                break;
+            }
+            mbar_expect_tx(full_bar(s), SF_STAGE);
+            const uint32_t a = sbase + s * SF_STAGE;
+            tma_load_2d(a + A_HI, &tmAh, kb * 32, row0, full_bar(s));
+            tma_load_2d(a + B_HI, &tmBh, kb * 32, col0, full_bar(s));
+            tma_load_2d(a + A_LO, &tmAl, kb * 32, row0, full_bar(s));
+            tma_load_2d(a + B_LO, &tmBl, kb * 32, col0, full_bar(s));
+            if (++s == SF_STAGES) { s = 0; ph ^= 1u; }
+        }
+    } else if (warp == 1) {
+        const uint32_t lead = elect_lane();
+        const uint32_t idesc = instr_desc(2, false, false, SM_COLS);  // 2: tf32 in kind::tf32
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA))) break;
+            tc_fence_after();
+            const uint32_t st = sbase + s * SF_STAGE;
+            const uint32_t ah = desc_lo(st + A_HI, false), bh = desc_lo(st + B_HI, false), al = desc_lo(st + A_LO, false),
+                           bl = desc_lo(st + B_LO, false);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t acc = (kb | kk) != 0 ? 1u : 0u, o = kk * K_STEP;
+                mma_tf32(tmem_base + SM_COLS, al + o, bh + o, idesc, acc, lead);
+                mma_tf32(tmem_base + SM_COLS, ah + o, bl + o, idesc, 1u, lead);
+                mma_tf32(tmem_base, ah + o, bh + o, idesc, acc, lead);
+            }
+            mma_commit(empty_bar(s), lead);
+            if (++s == SF_STAGES) { s = 0; ph ^= 1u; }
+        }
+        mma_commit(done_bar, lead);
+        mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+    } else if (warp >= 2) {
+        const int w = warp & 3;
+        bool ok = mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
+        ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+        if (ok && row0 + 32 * w < p.M) {
+            tc_fence_after();
+            const int64_t row = row0 + 32 * w + lane;
+            float* dst = p.out + row * p.ldo + col0;
+            const uint32_t t = tmem_base + (static_cast<uint32_t>(32 * w) << 16);
+#pragma unroll
+            for (int c = 0; c < SM_COLS; c += 16) {
+                if (col0 + c >= p.C) break;
+                uint32_t v[16], x[16];
+                tmem_ld16(t + c, v);
+                tmem_ld16(t + SM_COLS + c, x);
+                if (row < p.M) {
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        f[i] = __uint_as_float(v[i]);
+                        // an infinite hi hi sum is the result: the cross terms of an
+                        // infinite operand carry no value
+                        if (!isinf(f[i])) f[i] = __fadd_rn(f[i], __uint_as_float(x[i]));
+                        if (p.bias != nullptr && col0 + c + i < p.C) f[i] = __fadd_rn(f[i], p.bias[col0 + c + i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)  // C is a multiple of 4
+                        if (col0 + c + i < p.C) *reinterpret_cast<float4*>(dst + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<128>(tmem_base);
+    }
+}
+
 // ---------------------------------------------------------------- gradients
 //
 // A CTA takes one chunk (at most 1024) of one adapter's sorted rows, 128 columns
@@ -936,6 +1079,38 @@ cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void*
     const dim3 grid(static_cast<unsigned>((C + SM_COLS - 1) / SM_COLS), static_cast<unsigned>((M + 127) / 128));
     return dt == BI_BF16 ? small_rows_fmt<1>(c, dx, M, mx, mw, mh, mq, p, grid)
                          : small_rows_fmt<0>(c, dx, M, mx, mw, mh, mq, p, grid);
+}
+
+// A wave of pairs takes 1.14 us per 32-wide block, one of single CTAs 0.3 us, or
+// what their 48 KB per block take from L2, 4.8 ns per tile.
+bool tf32x3_small_tiles(const LaunchCtx& c, int64_t rows, int64_t cols, int64_t depth) {
+    const int64_t pairs = (rows + 255) / 256 * ((cols + 255) / 256), tiles = (rows + 127) / 128 * ((cols + 63) / 64);
+    const int64_t wave_p = (pairs + c.sm_count / 2 - 1) / (c.sm_count / 2), wave_s = (tiles + c.sm_count - 1) / c.sm_count;
+    return c.eng->tile_cols == 0 && depth <= TF32X3_PIECE && (rows + 127) / 128 <= 65535 &&
+           lmax(3000 * wave_s, 48 * tiles) < 11400 * wave_p;
+}
+
+cudaError_t tc_tf32x3_small(const LaunchCtx& c, const float* a_hi, const float* a_lo, int64_t lda, const float* b_hi,
+                            const float* b_lo, int64_t ldb, float* out, int64_t ldo, const float* bias, int64_t rows,
+                            int64_t cols, int64_t depth) {
+    static PerDeviceOnce setup;
+    cudaError_t e = setup.run(c.eng->device, [](int&) {
+        return cudaFuncSetAttribute(small_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SF_SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    CUtensorMap ah, al, bh, bl;
+    if ((e = make_map32(&ah, a_hi, depth, rows, lda, 128)) != cudaSuccess) return e;
+    if ((e = make_map32(&al, a_lo, depth, rows, lda, 128)) != cudaSuccess) return e;
+    if ((e = make_map32(&bh, b_hi, depth, cols, ldb, 64)) != cudaSuccess) return e;
+    if ((e = make_map32(&bl, b_lo, depth, cols, ldb, 64)) != cudaSuccess) return e;
+    SmallF32Params p{};
+    p.out = out; p.bias = bias; p.M = rows; p.C = cols; p.ldo = ldo;
+    p.num_kb = static_cast<int>((depth + 31) / 32);
+    p.status = c.status; p.wait_limit = c.wait_limit_ns;
+    const dim3 grid(static_cast<unsigned>((cols + SM_COLS - 1) / SM_COLS), static_cast<unsigned>((rows + 127) / 128));
+    e = launch_pdl(small_f32_kernel, grid, dim3(SM_THREADS), SF_SMEM, c.stream, ah, al, bh, bl, p);
+    if (e == cudaSuccess) c.count();
+    return e;
 }
 
 cudaError_t tc_adapter_grad(const LaunchCtx& c, bi_dtype dt, const AdapterGradJob* jobs, int count, const uint32_t* off,

@@ -6,6 +6,7 @@
 #include <string>
 
 #include "abi_util.h"
+#include "adapter.h"
 
 namespace {
 
@@ -42,7 +43,8 @@ struct Tf32Operand {
 };
 
 bi_status tf32x3(bi_engine eng, const bi::LaunchCtx& c, const Tf32Operand& a, const Tf32Operand& b, void* out,
-                 int64_t ldo, const void* bias, int64_t rows, int64_t cols, int64_t depth, const char* name) {
+                 int64_t ldo, const void* bias, int64_t rows, int64_t cols, int64_t depth, const char* name,
+                 bool small_tiles = false) {
     const int64_t a_b = a.bytes(), b_b = b.bytes();
     Scratch sc(eng, c.stream, static_cast<size_t>(2 * (a_b + b_b)));
     if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "3xTF32 scratch");
@@ -55,8 +57,11 @@ bi_status tf32x3(bi_engine eng, const bi::LaunchCtx& c, const Tf32Operand& a, co
     if (e == cudaSuccess)
         e = bi::tf32_split(c, static_cast<const float*>(b.src), bh, bl, b.rows, b.cols, b.transpose, b.ld());
     if (e == cudaSuccess)
-        e = bi::tc_tf32x3_pass(c, ah, al, a.ld(), bh, bl, b.ld(), static_cast<float*>(out), ldo,
-                               static_cast<const float*>(bias), rows, cols, depth);
+        e = small_tiles && bi::tf32x3_small_tiles(c, rows, cols, depth)
+                ? bi::tc_tf32x3_small(c, ah, al, a.ld(), bh, bl, b.ld(), static_cast<float*>(out), ldo,
+                                      static_cast<const float*>(bias), rows, cols, depth)
+                : bi::tc_tf32x3_pass(c, ah, al, a.ld(), bh, bl, b.ld(), static_cast<float*>(out), ldo,
+                                     static_cast<const float*>(bias), rows, cols, depth);
     return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, name);
 }
 
@@ -76,6 +81,20 @@ bi_status fail(bi_engine eng, bi_status st, const std::string& msg) {
 bi_status cuda_fail(bi_engine eng, cudaError_t e, const char* where) {
     return fail(eng, e == cudaErrorMemoryAllocation ? BI_ERR_OOM : BI_ERR_CUDA,
                 std::string(where) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
+}
+
+bi_status adapter_projection_f32(bi_engine eng, const LaunchCtx& c, int dx, void* out, const void* z, const void* w,
+                                 const void* bias, int64_t m, int64_t k, int64_t n, int tensor_cores) {
+    const int tier = bi_dispatch_tier(dx ? BI_PASS_DX : BI_PASS_FORWARD, BI_F32, tensor_cores, k, n);
+    if (!tier) {
+        const cudaError_t e = dx ? scalar_rows(c, BI_F32, out, z, w, nullptr, m, n, k, 1)
+                                 : scalar_rows(c, BI_F32, out, z, w, bias, m, k, n, 0);
+        return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "adapter projection");
+    }
+    if (!aligned16(out) || !aligned16(z) || !aligned16(w))
+        return fail(eng, BI_ERR_MISALIGNED, "tensor-core tier needs 16-byte aligned rows, weight and result");
+    return dx ? tf32x3(eng, c, {z, m, n, false}, {w, k, n, false}, out, k, nullptr, m, k, n, "adapter projection", true)
+              : tf32x3(eng, c, {z, m, k, false}, {w, k, n, true}, out, n, bias, m, n, k, "adapter projection", true);
 }
 
 bi_status set_thread_error(bi_status st, const std::string& msg) { return fail(nullptr, st, msg); }

@@ -1374,21 +1374,6 @@ cudaError_t fp8_pass_t(const LaunchCtx& c, int pass, void* out, const uint8_t* a
     return cudaSuccess;
 }
 
-// 32-bit K-major tensor [outer][inner] with row stride ld elements (ld >= inner,
-// a multiple of 4), box {32, 128}, 128-byte swizzle.
-cudaError_t make_map32(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t ld) {
-    auto enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {ld * 4};
-    cuuint32_t box[2] = {32, 128};
-    cuuint32_t es[2] = {1, 1};
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(ptr), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 cudaError_t tc_forward(const LaunchCtx& c, bi_dtype dt, void* y, const void* x, const void* w,
@@ -1445,10 +1430,10 @@ cudaError_t tc_tf32x3_pass(const LaunchCtx& c, const float* a_hi, const float* a
         const int64_t len = lmin(TF32X3_PIECE, depth - d0);
         CUtensorMap ah, al, bh, bl;
         cudaError_t e;
-        if ((e = make_map32(&ah, a_hi + d0, len, rows, lda)) != cudaSuccess) return e;
-        if ((e = make_map32(&al, a_lo + d0, len, rows, lda)) != cudaSuccess) return e;
-        if ((e = make_map32(&bh, b_hi + d0, len, cols, ldb)) != cudaSuccess) return e;
-        if ((e = make_map32(&bl, b_lo + d0, len, cols, ldb)) != cudaSuccess) return e;
+        if ((e = make_map32(&ah, a_hi + d0, len, rows, lda, 128)) != cudaSuccess) return e;
+        if ((e = make_map32(&al, a_lo + d0, len, rows, lda, 128)) != cudaSuccess) return e;
+        if ((e = make_map32(&bh, b_hi + d0, len, cols, ldb, 128)) != cudaSuccess) return e;
+        if ((e = make_map32(&bl, b_lo + d0, len, cols, ldb, 128)) != cudaSuccess) return e;
         Params p{};
         p.out = out; p.ldo = ldo; p.rows = rows; p.cols = cols;
         p.bias = d0 + len == depth ? bias : nullptr;

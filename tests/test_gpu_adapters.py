@@ -328,7 +328,7 @@ def test_nothing_is_written_outside_the_outputs(eng, dtype, tc):
         assert bool((buf[:pad] == 7).all() and (buf[-pad:] == 7).all())
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("m,k,n,r,g", [(1, 512, 256, 16, 2), (37, 1032, 328, 20, 9), (64, 136, 1000, 64, 64), (65, 264, 72, 8, 3),
                                        (200, 520, 640, 100, 30), (300, 64, 64, 33, 200), (513, 768, 264, 48, 4)])
 def test_small_and_paired_tiles_give_the_same_bits(eng, m, k, n, r, g, dtype):
