@@ -817,16 +817,21 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 // z: four warps copy them 16 bytes at a time (cp.async) into the swizzled tiles,
 // rows past the chunk's end as zeros, so rows of other adapters are never read.
 // v comes in four 16-bit parts whose products stand in columns of their own and
-// are added at the end, so dA and dB keep f32's precision.  z is read once per 64
-// ranks, which bounds the pass (8192 rows of 4096: 67 MB, 10 us at the copy
+// are added at the end, and each 512 rows have an accumulator of their own (the
+// tensor core's accumulation rounds towards zero, an error that grows with the
+// length: dA of 8192 x 4096 rows was off by 1.3e-6 with one, 0.9e-6 with two), so
+// dA and dB keep f32's precision.  z is read once per 64 ranks, which bounds the pass (8192 rows of 4096: 67 MB, 10 us at the copy
 // rate); two CTAs per SM keep about 190 KB in flight.
 constexpr int GT_THREADS = 160, GT_ROWS = 64;
 constexpr int GT_A = 2 * 8192;  // 64 rows x 128 columns, two 64-column atoms
 __host__ __device__ constexpr int gt_atoms(int run) { return 4 * run / 64; }
 __host__ __device__ constexpr int gt_stage(int run) { return GT_A + gt_atoms(run) * 8192; }
-__host__ __device__ constexpr int gt_stages(int run) { return 98304 / gt_stage(run); }
+// two CTAs per SM, or (more ranks, whose two accumulators fill the tensor memory) one
+__host__ __device__ constexpr int gt_ctas(int run) { return run > 32 ? 1 : 2; }
+__host__ __device__ constexpr int gt_stages(int run) { return (run > 32 ? 196608 : 98304) / gt_stage(run); }
 __host__ __device__ constexpr int gt_smem(int run) { return 1024 + gt_stages(run) * gt_stage(run) + 256; }
-static_assert(gt_stages(16) == 4 && gt_stages(32) == 3 && gt_stages(64) == 2, "ring depths");
+static_assert(gt_stages(16) == 4 && gt_stages(32) == 3 && gt_stages(48) == 4 && gt_stages(64) == 4, "ring depths");
+constexpr int GT_HALF = 8;  // blocks per accumulator
 
 struct GradParams {
     AdapterGradJob job[2];  // v4 [M, vcols], z [M, C]
@@ -846,9 +851,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
 }
 
 template <int RUN>
-__global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams p) {
+__global__ void __launch_bounds__(GT_THREADS, gt_ctas(RUN)) grad_tc_kernel(const GradParams p) {
     constexpr int ATOMS = gt_atoms(RUN), STAGE = gt_stage(RUN), STAGES = gt_stages(RUN), LAG = STAGES - 1;
-    constexpr int COLS = 4 * RUN <= 128 ? 4 * RUN : 256;  // TMEM columns, a power of two
+    constexpr int ACC = 4 * RUN <= 128 ? 4 * RUN : 256, COLS = 2 * ACC;  // TMEM columns of an accumulator, of both
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -953,20 +958,27 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
                                      : jb.out + static_cast<int64_t>(g) * p.R * C;
             const uint32_t t = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
             for (int q = 0; q < RUN && r0 + q < p.R; q += 16) {
-                uint32_t v0[16], v1[16], v2[16], v3[16];
-                tmem_ld16(t + q, v0);
-                tmem_ld16(t + RUN + q, v1);
-                tmem_ld16(t + 2 * RUN + q, v2);
-                tmem_ld16(t + 3 * RUN + q, v3);
-                if (col < C) {
+                float sum[16];
+                for (int half = 0; half < (blocks > GT_HALF ? 2 : 1); ++half) {
+                    const uint32_t th = t + half * ACC + q;
+                    uint32_t v0[16], v1[16], v2[16], v3[16];
+                    tmem_ld16(th, v0);
+                    tmem_ld16(th + RUN, v1);
+                    tmem_ld16(th + 2 * RUN, v2);
+                    tmem_ld16(th + 3 * RUN, v3);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float a = __uint_as_float(v0[i]), m = __uint_as_float(v1[i]), l = __uint_as_float(v2[i]);
-                        const float t = __uint_as_float(v3[i]);
-                        const float s = p.fmt ? m + (l + t)
-                                              : fmaf(a, 0x1p11f, fmaf(fmaf(t, 0x1p-11f, l), 0x1p-11f, m));
-                        if (r0 + q + i < p.R) dst[static_cast<int64_t>(r0 + q + i) * C + col] = s;
+                        const float z3 = __uint_as_float(v3[i]);
+                        const float r = p.fmt ? m + (l + z3)
+                                              : fmaf(a, 0x1p11f, fmaf(fmaf(z3, 0x1p-11f, l), 0x1p-11f, m));
+                        sum[i] = half == 0 ? r : sum[i] + r;
                     }
+                }
+                if (col < C) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (r0 + q + i < p.R) dst[static_cast<int64_t>(r0 + q + i) * C + col] = sum[i];
                 }
                 __syncwarp();
             }
@@ -980,7 +992,8 @@ __global__ void __launch_bounds__(GT_THREADS, 2) grad_tc_kernel(const GradParams
             if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA))) break;
             tc_fence_after();
             const uint32_t a = sbase + s * STAGE, v = a + GT_A;
-            mma_block(tmem_base, desc_lo(a, true), DESC_HI, MN_STEP, desc_lo(v, true), DESC_HI, MN_STEP, idesc, b != 0 ? 1u : 0u, lead);
+            mma_block(tmem_base + (b < GT_HALF ? 0 : ACC), desc_lo(a, true), DESC_HI, MN_STEP, desc_lo(v, true), DESC_HI, MN_STEP,
+                      idesc, b % GT_HALF != 0 ? 1u : 0u, lead);
             mma_commit(empty_bar(s), lead);
             if (++s == STAGES) { s = 0; ph ^= 1u; }
         }

@@ -297,7 +297,8 @@ bi_status bi_grouped_forward_noalloc(void* y, const void* x, const void* w,
  * row's h, Y and dX depend on that row, W, bias and its own adapter alone:
  * they are bit-identical for any M and any other rows beside it, and an
  * infinity or NaN in another adapter does not reach them.  dA and dB add an
- * adapter's rows in ascending order in chunks of 1024, the chunks in order;
+ * adapter's rows in ascending order in chunks of 1024 (on the tensor cores as two
+ * halves of 512 rows), the chunks in order;
  * run-to-run identical.  The tiers and their conditions are those of bi_forward
  * (forward) and bi_backward_dx (backward).  On the tensor-core tier with 16-bit
  * operands h and u enter the second product as two 16-bit parts (high part and
