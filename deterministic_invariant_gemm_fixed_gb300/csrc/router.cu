@@ -157,24 +157,29 @@ __global__ void __launch_bounds__(RT_THREADS, V <= 8 ? 4 : 1) route_kernel(const
     uint32_t rows = 0;
     const int64_t r0 = blockIdx.x * a.rows_per_block;
     const int64_t r1 = lmin(a.T, r0 + a.rows_per_block);
-    const T* logits = static_cast<const T*>(a.logits);
-    auto takes_part = [&](int64_t t) { return t < r1 && (a.valid == nullptr || a.valid[t] != 0); };
+    // The next row's logits and flag load under this one's arithmetic (a row that
+    // is left out is loaded too, and not looked at: its flag comes no earlier).
+    int64_t t = r0 + warp * GROUPS + grp;
+    const T* row = static_cast<const T*>(a.logits) + t * E;
     Raw<T, V> raw;
-    bool next = takes_part(r0 + warp * GROUPS + grp);
-    raw.load(logits + (r0 + warp * GROUPS + grp) * E, e0, E, a.vec != 0, next);
-    for (int64_t base = r0; base < r1; base += STEP) {  // every warp runs every step: the shuffles need all lanes
-        const int64_t t = base + warp * GROUPS + grp;
+    raw.load(row, e0, E, a.vec != 0, t < r1);
+    uint32_t flag = t < r1 && a.valid != nullptr ? a.valid[t] : 1u;
+    for (int64_t base = r0; base < r1; base += STEP, t += STEP) {  // every warp runs every step: the shuffles need all lanes
         const bool in = t < r1;
+        bool counted = in && flag != 0;
         float x[V];
         float top = -INFINITY;  // this lane's largest
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            x[i] = raw.get(i);
-            top = fmaxf(top, x[i]);  // a NaN is passed over here and shows in the sum
+        for (int i = 0; i < V; ++i) x[i] = raw.get(i);
+        if (!counted) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = -INFINITY;
         }
-        bool counted = next;
-        next = takes_part(t + STEP);
-        raw.load(logits + (t + STEP) * E, e0, E, a.vec != 0, next);
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);  // a NaN is passed over here and shows in the sum
+        row += static_cast<int64_t>(STEP) * E;
+        raw.load(row, e0, E, a.vec != 0, t + STEP < r1);
+        flag = t + STEP < r1 && a.valid != nullptr ? a.valid[t + STEP] : 1u;
         const float mx = group_max<L>(top);
         if (__any_sync(0xffffffffu, mx == -INFINITY)) {  // rows of -inf alone have no expert, rows of NaN and -inf are counted
             bool nan = false;
@@ -292,11 +297,13 @@ __global__ void __launch_bounds__(RT_THREADS, V <= 8 ? 4 : 1) route_kernel(const
         }
         __syncwarp();
         if (in) {
+            uint32_t* ids = a.ids + t * k;
+            float* weights = a.weights + t * k;
             for (int j = li; j < k; j += L) {
                 const uint2 q = pick[j];
                 const float w = __uint_as_float(q.y);
-                a.ids[t * k + j] = q.x;
-                a.weights[t * k + j] = a.normalize && q.x != static_cast<uint32_t>(E) ? __fdividef(w, wsum) : w;
+                ids[j] = q.x;
+                weights[j] = a.normalize && q.x != static_cast<uint32_t>(E) ? __fdividef(w, wsum) : w;
             }
         }
         __syncwarp();  // pick and cand are free again

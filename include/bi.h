@@ -329,7 +329,7 @@ bi_status bi_adapter_backward(bi_engine engine, void* dx, float* da, float* db, 
  *   p[:,e] over them;  loss = E * sum_e counts[e] / (k V) * mean_prob[e]
  *
  * logits [T,E] of dtype, E <= 1024, k <= min(E, 64); valid [T] u8 (nullable:
- * all rows), a row with valid 0 is left out and its logits are not read.  A
+ * all rows), a row with valid 0 is left out whatever its logits hold.  A
  * logit of -inf or NaN is never chosen.  A choice that a row cannot make (fewer
  * than k such logits) has id E and weight 0, and so have all choices of a row
  * left out; id E is a padding row for the grouped calls, which take ids as
