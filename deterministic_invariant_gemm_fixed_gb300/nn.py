@@ -21,6 +21,12 @@ f32 product by scale_x * scale_w, then adds the bias and rounds once; the
 backward quantizes the output gradient with scale_g and computes dX and dW from
 the saved codes the same way.  The bias gradient is the fixed-order column sum
 of the unquantized output gradient.
+
+Beside the layer: `adapter_linear` (a shared projection with the low-rank adapter
+of each row), `route` (a router's expert choice, weights, counts and balance
+loss, whose ids the grouped matmul takes) and `clip_grad_norm_` (global gradient
+norm and clipping of a parameter list), each over its own entry points of the
+library, so a training step made of them is bit-reproducible too.
 """
 from __future__ import annotations
 
@@ -30,7 +36,7 @@ import threading
 
 import torch
 
-from . import Engine
+from . import Engine, TensorSet
 
 _engines: dict[int, Engine] = {}
 _engines_lock = threading.Lock()
@@ -234,3 +240,128 @@ class Linear(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"bias={self.bias is not None}, tensor_cores={self.tensor_cores}")
+
+
+class _AdapterLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, a, b, scales, ids, tensor_cores):
+        _check(x, weight, bias)
+        k, n = weight.shape
+        if a.dim() != 3 or b.dim() != 3 or a.shape[2] != k or b.shape != (a.shape[0], a.shape[1], n):
+            raise ValueError("a must be [adapters, rank, in] and b [adapters, rank, out]")
+        if a.dtype != x.dtype or b.dtype != x.dtype:
+            raise TypeError("x, weight, a and b must share one dtype")
+        g, r, _ = a.shape
+        if ids.dtype not in (torch.int32, torch.uint32) or ids.shape != x.shape[:-1]:
+            raise ValueError("ids must be int32 or uint32, one per row of x")
+        if scales is not None and (scales.dtype != torch.float32 or scales.shape != (g,)):
+            raise ValueError("scales must be float32 [adapters]")
+        if not all(t is None or (t.is_cuda and t.device == x.device) for t in (a, b, scales, ids)):
+            raise ValueError("adapter_linear needs all tensors on x's CUDA device")
+        x2, w, a, b = x.reshape(-1, k).contiguous(), weight.contiguous(), a.contiguous(), b.contiguous()
+        ids2 = ids.reshape(-1).contiguous()
+        sc = scales.contiguous() if scales is not None else None
+        m = x2.shape[0]
+        y = torch.empty(m, n, dtype=x.dtype, device=x.device)
+        h = torch.empty(m, r, dtype=torch.float32, device=x.device)
+        engine_for(x.device).adapter_forward(y, h, x2, w, bias.contiguous() if bias is not None else None, a, b, sc, ids2,
+                                             m, k, n, r, g, x.dtype, torch.cuda.current_stream(x.device), int(tensor_cores))
+        ctx.save_for_backward(x2, w, a, b, sc, ids2, h)
+        ctx.has_bias, ctx.tensor_cores, ctx.x_shape = bias is not None, int(tensor_cores), x.shape
+        return y.reshape(*x.shape[:-1], n)
+
+    @staticmethod
+    def backward(ctx, gy):
+        x2, w, a, b, sc, ids2, h = ctx.saved_tensors
+        (k, n), (g, r, _) = w.shape, a.shape
+        dt, dev, m = w.dtype, w.device, x2.shape[0]
+        gy2 = gy.reshape(-1, n).to(dt).contiguous()
+        eng, stream, tc = engine_for(dev), torch.cuda.current_stream(dev), ctx.tensor_cores
+        need = ctx.needs_input_grad
+        gx = torch.empty(m, k, dtype=dt, device=dev) if need[0] else None
+        ga = torch.empty(g, r, k, dtype=torch.float32, device=dev) if need[3] else None
+        gb = torch.empty(g, r, n, dtype=torch.float32, device=dev) if need[4] else None
+        eng.adapter_backward(gx, ga, gb, x2, h, w, gy2, a, b, sc, ids2, m, k, n, r, g, dt, stream, tc)
+        gw = gbias = None
+        f32 = int(dt == torch.float32)
+        if need[1]:
+            gw = torch.empty(k, n, dtype=dt, device=dev)
+            eng.backward_dw(gw, f32, x2, gy2, m, k, n, dt, stream, tc)
+        if ctx.has_bias and need[2]:
+            gbias = torch.empty(n, dtype=dt, device=dev)
+            eng.bias_grad(gbias, f32, gy2, m, n, dt, stream)
+        return (gx.reshape(ctx.x_shape) if gx is not None else None, gw, gbias, ga.to(dt) if ga is not None else None,
+                gb.to(dt) if gb is not None else None, None, None, None)
+
+
+def adapter_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, a: torch.Tensor, b: torch.Tensor,
+                   scales: torch.Tensor | None, ids: torch.Tensor, tensor_cores: bool = True) -> torch.Tensor:
+    """y = x @ weight (+ bias) + scales[g] * (x @ a[g].T) @ b[g] with g = ids[row]:
+    weight [in, out] shared by all rows, adapters a [G, rank, in] and b [G, rank,
+    out], scales [G] float32 (None: 1), ids int32 or uint32 of x's leading shape;
+    a row whose id is outside [0, G) gets the shared projection alone.  Gradients
+    for x, weight, bias, a and b; a row's y and dx do not depend on other rows."""
+    return _AdapterLinear.apply(x, weight, bias, a, b, scales, ids, tensor_cores)
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, normalize, valid):
+        if not logits.is_cuda:
+            raise ValueError("route needs CUDA tensors")
+        e = logits.shape[-1]
+        x = logits.reshape(-1, e).contiguous()
+        t, dev = x.shape[0], x.device
+        if valid is not None:
+            if valid.shape != logits.shape[:-1] or valid.dtype not in (torch.bool, torch.uint8) or valid.device != dev:
+                raise ValueError("valid must be bool or uint8, one per row of logits")
+            valid = valid.reshape(-1).contiguous()
+        def new(*shape, dtype=torch.float32):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+        ids, weights, lse = new(t, k, dtype=torch.int32), new(t, k), new(t)
+        counts, rows, mean, loss = new(e, dtype=torch.int32), new(1, dtype=torch.int32), new(e), new(1)
+        engine_for(dev).router_forward(ids, weights, counts, rows, mean, loss, lse, x, valid, t, e, k, normalize, x.dtype,
+                                       torch.cuda.current_stream(dev))
+        ctx.save_for_backward(x, lse, ids, weights, counts, rows)
+        ctx.k, ctx.normalize, ctx.shape = k, normalize, logits.shape
+        ids_out, counts_out = ids.reshape(*logits.shape[:-1], k), counts.clone()
+        ctx.mark_non_differentiable(ids_out, counts_out)
+        return ids_out, weights.clone().reshape(*logits.shape[:-1], k), loss.reshape(()), counts_out
+
+    @staticmethod
+    def backward(ctx, _ids, gweights, gloss, _counts):
+        x, lse, ids, weights, counts, rows = ctx.saved_tensors
+        t, e = x.shape
+        d = torch.empty_like(x)
+        gw = gweights.reshape(t, ctx.k).float().contiguous() if gweights is not None else None
+        gl = gloss.reshape(1).float().contiguous() if gloss is not None else None
+        engine_for(x.device).router_backward(d, x, lse, ids, weights, counts, rows, gw, gl, t, e, ctx.k, ctx.normalize,
+                                             x.dtype, torch.cuda.current_stream(x.device))
+        return d.reshape(ctx.shape), None, None, None
+
+
+def route(logits: torch.Tensor, k: int, normalize: bool = True, valid: torch.Tensor | None = None):
+    """A softmax router's choice of k experts per row of logits [..., E]: (ids int32
+    [..., k], weights float32 [..., k], balance loss [], counts int32 [E]).  ids of
+    rows with valid = 0 are E, which the grouped matmul takes as padding; the loss is
+    E * sum_e (counts_e / kV) * mean_t p_te over the V rows that take part.
+    Gradients of the weights and the loss reach the logits."""
+    return _Route.apply(logits, k, normalize, valid)
+
+
+def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
+    """Scale the gradients of `parameters` in place so that their global norm is at
+    most max_norm; returns the norm before (a float32 tensor of one element, on the
+    device; nothing synchronises).  The gradients must be contiguous and on one
+    device."""
+    params = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
+    grads = [p.grad for p in params if p.grad is not None]
+    if not grads:
+        return torch.zeros(1)
+    dev = grads[0].device
+    if any(g.device != dev for g in grads):
+        raise ValueError("clip_grad_norm_: gradients must be on one device")
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    s = TensorSet(grads)
+    engine_for(dev).clip_gradients(s, s, norm, max_norm, torch.cuda.current_stream(dev))
+    return norm
