@@ -173,43 +173,40 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     const int rg = p.rp / 16;  // groups of 16 ranks per adapter
     const int kb0 = blockIdx.y * NP_KB, nkb = min(NP_KB, p.num_kb - kb0);
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {  // a lane for each of a stage's copies, as in the small tiles' kernel below
         // the first blocks of X need no list: their bytes are expected and the
         // copies issued now, the stages' own arrivals follow with the adapters'
         // (the first CTA of a tile and piece; others may have no adapters left)
         const int early = blockIdx.z == 0 ? min(NP_STAGES, nkb) : 0;
-        for (int kb = 0; kb < early; ++kb) {
-            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full_bar(kb)), "r"(NP_A) : "memory");
-            tma_load_2d(sbase + kb * NP_STAGE, &tmX, (kb0 + kb) * BK, row0, full_bar(kb));
+        if (lane < early) {
+            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full_bar(lane)), "r"(NP_A) : "memory");
+            tma_load_2d(sbase + lane * NP_STAGE, &tmX, (kb0 + lane) * BK, row0, full_bar(lane));
         }
-        const bool listed = mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+        __syncwarp();
+        const bool listed = __all_sync(0xffffffffu, mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER));
         const int groups = listed ? static_cast<int>(*s_count) * rg : 0, batches = (groups + 3) / 4;
         int s = 0, fills = 0;
         uint32_t ph = 0;
-        if (static_cast<int>(blockIdx.z) >= batches) {  // nothing to multiply: let the early copies land
+        if (static_cast<int>(blockIdx.z) >= batches && lane == 0) {  // nothing to multiply: let the early copies land
             for (int kb = 0; kb < early; ++kb) mbar_expect_tx(full_bar(kb), 0);
             drain_copies(full_bar, early, NP_STAGES);
         }
         for (int q = blockIdx.z; q < batches; q += gridDim.z) {
             const int n = min(4, groups - 4 * q);
+            const int gi = 4 * q + lane, e = gi / rg, r16 = (gi - e * rg) * 16;
+            const int g = lane < n ? static_cast<int>(s_id[e]) : 0;
             for (int kb = 0; kb < nkb; ++kb) {
                 const uint32_t a = sbase + s * NP_STAGE;
-                if (fills < early) {
-                    mbar_expect_tx(full_bar(s), n * 2048);
-                } else {
-                    if (!mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) {
-                        drain_copies(full_bar, fills, NP_STAGES);
-                        goto done_p;
-                    }
-                    mbar_expect_tx(full_bar(s), NP_A + n * 2048);
-                    tma_load_2d(a, &tmX, (kb0 + kb) * BK, row0, full_bar(s));
+                const bool have_x = fills < early;
+                if (!have_x && !__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER))) {
+                    if (lane == 0) drain_copies(full_bar, fills, NP_STAGES);
+                    goto done_p;
                 }
+                if (lane == 0) mbar_expect_tx(full_bar(s), (have_x ? 0 : NP_A) + n * 2048);
+                __syncwarp();
+                if (!have_x && lane == 4) tma_load_2d(a, &tmX, (kb0 + kb) * BK, row0, full_bar(s));
+                if (lane < n) tma_load_3d(a + NP_A + lane * 2048, &tmP, (kb0 + kb) * BK, r16, g, full_bar(s));
                 ++fills;
-                for (int i = 0; i < n; ++i) {
-                    const int gi = 4 * q + i;
-                    tma_load_3d(a + NP_A + i * 2048, &tmP, (kb0 + kb) * BK, (gi % rg) * 16, static_cast<int>(s_id[gi / rg]),
-                                full_bar(s));
-                }
                 if (++s == NP_STAGES) { s = 0; ph ^= 1u; }
             }
         }
@@ -354,12 +351,17 @@ struct SmallParams {
     unsigned long long wait_limit;
 };
 
-__device__ __forceinline__ void mma_one_masked(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint4 off) {
+// Sixteen ranks of one adapter: the high parts' MMA and the remainders' (64 bytes on
+// in the rows of h), on the accumulator lanes that `off` does not exclude.
+__device__ __forceinline__ void mma_masked(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint4 off, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tsetp.ne.b32 e, %9, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, {%5, %6, %7, %8}, p;\n\t"
+        "add.u32 x, %1, 4;\n\tmov.b64 da, {x, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w), "r"(lead)
         : "memory");
 }
 
@@ -382,8 +384,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + SM_BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile uint32_t* s_count = tmem_slot + 2;
-    uint4* s_mask = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 15) & ~uintptr_t(15));
-    uint32_t* s_id = reinterpret_cast<uint32_t*>(s_mask + 128);
+    // per adapter of this half the accumulator lanes that are not its rows', and its index
+    uint4* s_off = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 15) & ~uintptr_t(15));
+    uint32_t* s_id = reinterpret_cast<uint32_t*>(s_off + 128);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int row0 = static_cast<int>(blockIdx.y) * 128, col0 = static_cast<int>(blockIdx.x) * SM_COLS;
     const int rg = (p.R + 15) / 16;
@@ -406,61 +409,65 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     grid_dep_launch();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+        // the whole warp runs this: lane 0 expects a stage's bytes, then a lane for
+        // each of its copies issues them side by side (one lane issuing four copies
+        // per stage, with their addresses, took 0.2 us a copy)
         int s = 0, issued = 0;
         uint32_t ph = 0;
         bool ok = true;
         auto claim = [&](uint32_t bytes) {  // the next stage, free and expecting `bytes`
-            ok = mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+            ok = __all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER));
             if (!ok) return;
             ++issued;
-            mbar_expect_tx(full_bar(s), bytes);
+            if (lane == 0) mbar_expect_tx(full_bar(s), bytes);
+            __syncwarp();
         };
         auto advance = [&] {
             if (++s == stages) { s = 0; ph ^= 1u; }
         };
+        const CUtensorMap* map = lane == 0 ? &tmX : &tmW;
+        const uint32_t to = sbase + (lane == 0 ? 0 : A_BYTES);
+        const uint32_t bytes = p.a_bytes + SM_B;
         for (int kb = 0; kb < p.num_kb && ok; ++kb) {
-            claim(p.a_bytes + SM_B);
+            claim(bytes);
             if (!ok) break;
-            const uint32_t a = sbase + s * STAGE;
-            tma_load_2d(a, &tmX, kb * BK, row0, full_bar(s));
-            if (B_MN) tma_load_2d(a + A_BYTES, &tmW, col0, kb * BK, full_bar(s));
-            else tma_load_2d(a + A_BYTES, &tmW, kb * BK, col0, full_bar(s));
+            const int kx = kb * BK;
+            if (lane < 2) tma_load_2d(to + s * STAGE, map, B_MN && lane ? col0 : kx, lane == 0 ? row0 : (B_MN ? kx : col0), full_bar(s));
             advance();
         }
-        if (ok) ok = mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER));
         if (ok) {
             grid_dep_wait();
             const int steps = static_cast<int>(*s_count) * rg;
             if (p.resident && steps) {
-                if (p.partial == nullptr) {
+                if (p.partial == nullptr && lane == 0) {
                     mbar_expect_tx(h_bar, p.resident * p.a_bytes);
                     for (int c = 0; c < p.resident; ++c) tma_load_2d(hbase + c * A_BYTES, &tmH, c * 64, row0, h_bar);
                 }
                 for (int f = 0; f < steps && ok; f += 4) {
                     const int n = min(4, steps - f);
+                    const int e = (f + lane) / rg, jr = f + lane - e * rg;
+                    const int g = lane < n ? static_cast<int>(s_id[e]) : 0;
                     claim(n * 2048);
                     if (!ok) break;
-                    for (int i = 0; i < n; ++i)
-                        tma_load_3d(sbase + s * STAGE + A_BYTES + i * 2048, &tmQ, col0, ((f + i) % rg) * 16,
-                                    static_cast<int>(s_id[(f + i) / rg]), full_bar(s));
+                    if (lane < n) tma_load_3d(sbase + s * STAGE + A_BYTES + lane * 2048, &tmQ, col0, jr * 16, g, full_bar(s));
                     advance();
                 }
             } else {
                 for (int f = 0; f < steps && ok;) {  // one 32-rank part of one adapter
-                    const int j = f % rg, n = min(2, rg - j);
+                    const int e = f / rg, jr = f - e * rg, n = min(2, rg - jr);
                     claim(p.a_bytes + n * 2048);
                     if (!ok) break;
                     const uint32_t a = sbase + s * STAGE;
-                    tma_load_2d(a, &tmH, (j / 2) * 64, row0, full_bar(s));
-                    for (int i = 0; i < n; ++i)
-                        tma_load_3d(a + A_BYTES + i * 2048, &tmQ, col0, (j + i) * 16, static_cast<int>(s_id[f / rg]), full_bar(s));
+                    if (lane < n) tma_load_3d(a + A_BYTES + lane * 2048, &tmQ, col0, (jr + lane) * 16, static_cast<int>(s_id[e]), full_bar(s));
+                    if (lane == n) tma_load_2d(a, &tmH, (jr / 2) * 64, row0, full_bar(s));
                     f += n;
                     advance();
                 }
             }
         }
-        if (!ok) drain_copies(full_bar, issued, stages);
+        if (!ok && lane == 0) drain_copies(full_bar, issued, stages);
     } else if (warp == 1) {
         const uint32_t idesc = instr_desc(FMT, false, B_MN, SM_COLS, AR), idesc_q = instr_desc(FMT, false, true, SM_COLS, AR);
         // the whole warp runs this, one lane issues: warp-uniform code keeps the
@@ -489,22 +496,26 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
         if (ok) {
             const int steps = static_cast<int>(*s_count) * rg;
             if (p.resident && steps) ok = __all_sync(0xffffffffu, mbar_wait_fast(h_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA));
+            // step f: 16-rank group jr of adapter e; four steps per stage (h resident),
+            // or up to two of one 32-rank part
+            const uint32_t h_desc = desc_lo(hbase, false);
+            int e = 0, jr = 0;
+            uint4 off = s_off[0], next = s_off[1];
             for (int f = 0; f < steps && ok;) {
                 take();
                 if (!ok) break;
                 const uint32_t st = sbase + s * STAGE;
-                const int n = p.resident ? min(4, steps - f) : min(2, rg - f % rg);
-                for (int i = 0; i < n && lead; ++i) {
-                    const int e = (f + i) / rg, j = (f + i) % rg;
-                    const uint4 m = s_mask[e];
-                    // 64 rows: row i is lane 32 (i / 16) + i % 16
-                    const uint4 off = AR == 64 ? make_uint4(~m.x, ~m.x >> 16, ~m.y, ~m.y >> 16) : make_uint4(~m.x, ~m.y, ~m.z, ~m.w);
-                    const uint32_t a = (p.resident ? hbase + (j / 2) * A_BYTES : st) + (j % 2) * 32;
-                    const uint64_t bd = smem_desc(st + A_BYTES + i * 2048, 8192, 1024);
-                    mma_one_masked(tmem_base, smem_desc(a, 16, 1024), bd, idesc_q, off);
-                    mma_one_masked(tmem_base, smem_desc(a + 64, 16, 1024), bd, idesc_q, off);
+                const int n = p.resident ? min(4, steps - f) : min(2, rg - jr);
+                const uint32_t a0 = p.resident ? h_desc : desc_lo(st, false), b0 = desc_lo(st + A_BYTES, true);
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t part = p.resident ? static_cast<uint32_t>(jr >> 1) * (A_BYTES >> 4) : 0u;
+                    mma_masked(tmem_base, a0 + part + (jr & 1) * K_STEP, b0 + i * MN_STEP, idesc_q, off, lead);
+                    if (++jr == rg) {
+                        jr = 0;
+                        off = next;
+                        next = s_off[min(++e + 1, 127)];
+                    }
                 }
-                __syncwarp();
                 f += n;
                 release();
             }
@@ -532,7 +543,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 const uint32_t b = __ballot_sync(0xffffffffu, has);
                 if (has) {
                     const uint32_t at = total + __popc(b & ((1u << lane) - 1));
-                    s_mask[at] = m[q];
+                    // 64 rows: row i is lane 32 (i / 16) + i % 16
+                    s_off[at] = AR == 64 ? make_uint4(~m[q].x, ~(m[q].x >> 16), ~m[q].y, ~(m[q].y >> 16))
+                                         : make_uint4(~m[q].x, ~m[q].y, ~m[q].z, ~m[q].w);
                     s_id[at] = p.plan.ids[tile * ADAPTER_TILE + q * 32 + lane];
                 }
                 total += __popc(b);
