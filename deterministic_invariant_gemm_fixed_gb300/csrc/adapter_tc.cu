@@ -22,12 +22,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// 1 in one lane of the warp, always the same.
-__device__ __forceinline__ uint32_t elect_lane() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
     asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
                  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(lead)
@@ -73,13 +67,6 @@ __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a, uint32_t 
         "r"(a), "r"(ahi), "r"(astep), "r"(b), "r"(bhi), "r"(bstep), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
 }
-// Low and high word of a tile's descriptor (128-byte swizzle, 8-row groups 1024
-// bytes apart): K-major, or MN-major with 8192 bytes from one 64-column atom to
-// the next.  One MMA's step along K: 32 bytes, or 16 rows of 128.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, bool mn) { return ((saddr & 0x3FFFFu) >> 4) | ((mn ? 512u : 1u) << 16); }
-constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-constexpr uint32_t K_STEP = 32 >> 4, MN_STEP = 2048 >> 4;
-
 // A producer that gives up waits (a bounded number of tries) for the copies it
 // has issued before its CTA's shared memory goes away: the last min(issued,
 // stages) fills, fill f on stage f % stages in phase f / stages.
@@ -488,7 +475,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             take();
             if (!ok) break;
             const uint32_t a = sbase + s * STAGE, b = a + A_BYTES;
-            mma_block(tmem_base, desc_lo(a, false), DESC_HI, K_STEP, desc_lo(b, B_MN), DESC_HI, B_MN ? MN_STEP : K_STEP, idesc,
+            mma_block(tmem_base, desc_lo(a, false), DESC_HI, K_STEP, desc_lo(b, B_MN), DESC_HI, B_MN ? MN_STEP_16 : K_STEP, idesc,
                       kb != 0 ? 1u : 0u, lead);
             release();
         }
@@ -509,7 +496,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 const uint32_t a0 = p.resident ? h_desc : desc_lo(st, false), b0 = desc_lo(st + A_BYTES, true);
                 for (int i = 0; i < n; ++i) {
                     const uint32_t part = p.resident ? static_cast<uint32_t>(jr >> 1) * (A_BYTES >> 4) : 0u;
-                    mma_masked(tmem_base, a0 + part + (jr & 1) * K_STEP, b0 + i * MN_STEP, idesc_q, off, lead);
+                    mma_masked(tmem_base, a0 + part + (jr & 1) * K_STEP, b0 + i * MN_STEP_16, idesc_q, off, lead);
                     if (++jr == rg) {
                         jr = 0;
                         off = next;
@@ -741,20 +728,19 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     grid_dep_wait();
     grid_dep_launch();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {  // a lane for each of a block's four copies
+        const CUtensorMap* map = lane == 0 ? &tmAh : lane == 1 ? &tmBh : lane == 2 ? &tmAl : &tmBl;
+        const uint32_t to = sbase + (lane == 0 ? A_HI : lane == 1 ? B_HI : lane == 2 ? A_LO : B_LO);
         int s = 0;
         uint32_t ph = 0;
         for (int kb = 0; kb < p.num_kb; ++kb) {
-            if (!mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) {
-                drain_copies(full_bar, kb, SF_STAGES);
+            if (!__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER))) {
+                if (lane == 0) drain_copies(full_bar, kb, SF_STAGES);
                 break;
             }
-            mbar_expect_tx(full_bar(s), SF_STAGE);
-            const uint32_t a = sbase + s * SF_STAGE;
-            tma_load_2d(a + A_HI, &tmAh, kb * 32, row0, full_bar(s));
-            tma_load_2d(a + B_HI, &tmBh, kb * 32, col0, full_bar(s));
-            tma_load_2d(a + A_LO, &tmAl, kb * 32, row0, full_bar(s));
-            tma_load_2d(a + B_LO, &tmBl, kb * 32, col0, full_bar(s));
+            if (lane == 0) mbar_expect_tx(full_bar(s), SF_STAGE);
+            __syncwarp();
+            if (lane < 4) tma_load_2d(to + s * SF_STAGE, map, kb * 32, lane & 1 ? col0 : row0, full_bar(s));
             if (++s == SF_STAGES) { s = 0; ph ^= 1u; }
         }
     } else if (warp == 1) {
@@ -1005,7 +991,7 @@ __global__ void __launch_bounds__(GT_THREADS, gt_ctas(RUN)) grad_tc_kernel(const
             if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA))) break;
             tc_fence_after();
             const uint32_t a = sbase + s * STAGE, v = a + GT_A;
-            mma_block(tmem_base + (b < GT_HALF ? 0 : ACC), desc_lo(a, true), DESC_HI, MN_STEP, desc_lo(v, true), DESC_HI, MN_STEP,
+            mma_block(tmem_base + (b < GT_HALF ? 0 : ACC), desc_lo(a, true), DESC_HI, MN_STEP_16, desc_lo(v, true), DESC_HI, MN_STEP_16,
                       idesc, b % GT_HALF != 0 ? 1u : 0u, lead);
             mma_commit(empty_bar(s), lead);
             if (++s == STAGES) { s = 0; ph ^= 1u; }

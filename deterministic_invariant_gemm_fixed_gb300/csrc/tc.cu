@@ -309,16 +309,38 @@ __device__ __forceinline__ bool pair_tile(const Params& p, int t, PairTile& u) {
     return true;
 }
 
-// The f16 / bf16 MMA that leaves the accumulator lanes (rows) of `off` alone: bit
-// i of off[0..3] is row i of CTA 0's half of the tile, off[4..7] CTA 1's.
-__device__ __forceinline__ void mma_pair_masked(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                const uint32_t (&off)[8]) {
+// The adapter passes' MMAs, issued by one lane (`lead`) of warp-uniform code from
+// the low words of the operands' descriptors: a 64-wide block, and sixteen ranks
+// of one adapter (the high parts and, 64 bytes on, the remainders) that leave the
+// accumulator lanes (rows) of `off` alone: bit i of off[0..3] is row i of CTA 0's
+// half of the tile, off[4..7] CTA 1's.
+__device__ __forceinline__ void mma_pair_block(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t bstep, uint32_t idesc,
+                                               uint32_t acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]), "r"(off[5]),
-        "r"(off[6]), "r"(off[7])
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 q, 0, 0;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, %4;\n\tmov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, q;\n\t"
+        "add.u32 x, x, 2;\n\tadd.u32 y, y, %4;\n\tmov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, q;\n\t"
+        "add.u32 x, x, 2;\n\tadd.u32 y, y, %4;\n\tmov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, q;\n\t}\n" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(bstep), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair_masked(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                                const uint32_t (&off)[8], uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tsetp.ne.b32 e, %13, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t"
+        "add.u32 x, %1, 4;\n\tmov.b64 da, {x, %3};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]), "r"(off[5]),
+        "r"(off[6]), "r"(off[7]), "r"(lead)
         : "memory");
 }
 
@@ -353,6 +375,15 @@ __device__ __forceinline__ void mma_commit_pair_mc(uint32_t bar, uint16_t mask) 
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(bar), "h"(mask)
+        : "memory");
+}
+
+// The same from warp-uniform code, issued by one lane.
+__device__ __forceinline__ void mma_commit_pair_lead(uint32_t bar, uint16_t mask, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
+        "h"(mask), "r"(lead)
         : "memory");
 }
 
@@ -434,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * P_STAGES + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = MODE == ADAPTER ? __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0) : threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t crank = blockIdx.x & 1u;
     const int cidx = static_cast<int>(blockIdx.x >> 1);
@@ -464,13 +495,121 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    if (MODE == ADAPTER) tmem_base = __shfl_sync(0xffffffffu, tmem_base, 0);
     // set-up above touches no global memory; everything below may read what
     // the previous kernel in the stream wrote
     grid_dep_wait();
     grid_dep_launch();
 
-    if (warp == 0 && lane == 0) {
+    if (MODE == ADAPTER && warp == 0) {
+        // ------------------------------------------------------------ producer (both CTAs), adapter passes
+        // A lane issues each of a stage's copies (A, and B's one or two), the
+        // addresses computed side by side; lane 0 waits and expects the bytes.
+        constexpr int COPIES = 1 + (B_MN ? B_ATOMS : 1);
+        const CUtensorMap* map = lane == 0 ? &tmA : &tmB;
+        const CUtensorMap* map2 = lane == 0 ? &tmA2 : &tmB2;
+        const uint32_t to = sbase + (lane == 0 ? 0 : P_A_BYTES + (lane - 1) * (BKE * 128));
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        auto claim = [&](uint32_t bytes) {
+            ok = __all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER));
+            if (ok && crank == 0 && lane == 0) mbar_expect_tx(full_bar(s), 2 * bytes);
+            __syncwarp();
+        };
+        auto advance = [&] {
+            if (++s == P_STAGES) { s = 0; ph ^= 1u; }
+        };
+        PairTile u;
+        for (int t = cidx; ok && pair_tile<MODE>(p, t, u); t += ncl) {
+            const int arow = u.mpair * 256 + static_cast<int>(crank) * 128;
+            const int bcol = u.nb * BN + static_cast<int>(crank) * (BN / 2);
+            const int col = bcol + (lane - 1) * 64;
+            for (int kb = 0; kb < u.nkb; ++kb) {
+                claim(P_LOAD_BYTES);
+                if (!ok) break;
+                const int kofs = kb * BKE;
+                if (lane < COPIES)
+                    tma_load_2d_pair(to + s * P_STAGE_BYTES, map, B_MN && lane ? col : kofs, lane == 0 ? arow : (B_MN ? kofs : bcol),
+                                     mapa_rank(full_bar(s), 0));
+                advance();
+            }
+            const int n = static_cast<int>(p.plan.count[u.mpair]);
+            for (int e = 0; e < n && ok; ++e) {
+                const int g = static_cast<int>(p.plan.ids[static_cast<int64_t>(u.mpair) * ADAPTER_TILE + e]);
+                for (int c = 0; c < (p.rank + 31) / 32; ++c) {
+                    claim(P_A_BYTES + P_B_BYTES / 2);
+                    if (!ok) break;
+                    const uint32_t fb = mapa_rank(full_bar(s), 0), dst = to + s * P_STAGE_BYTES;
+                    if (lane == 0) tma_load_2d_pair(dst, map2, c * 64, arow, fb);
+                    else if (lane <= (BN / 2) / 64) tma_load_3d_pair(dst, map2, col, c * 32, g, fb);
+                    advance();
+                }
+            }
+        }
+    } else if (MODE == ADAPTER && warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (CTA 0), adapter passes
+        // Warp-uniform code with one issuing lane: the descriptors stay in uniform
+        // registers, where the MMA takes them from.
+        if (crank == 0) {
+            constexpr uint32_t idesc = instr_desc_pair<IN, A_MN, B_MN, BN>(), idesc_q = instr_desc_pair<IN, false, true, BN>();
+            const uint32_t lead = elect_lane();
+            int s = 0, ab = 0;
+            uint32_t ph = 0, aph = 0;
+            bool ok = true;
+            auto take = [&] {
+                ok = __all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA));
+                tc_fence_after();
+            };
+            auto release = [&] {
+                mma_commit_pair_lead(empty_bar(s), 0x3, lead);
+                if (++s == P_STAGES) { s = 0; ph ^= 1u; }
+            };
+            PairTile u;
+            for (int t = cidx; ok && pair_tile<MODE>(p, t, u); t += ncl) {
+                ok = __all_sync(0xffffffffu, mbar_wait_fast(tempty_bar(ab), aph ^ 1u, abort_flag, p, DEV_TIMEOUT_MMA));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(ab * ACC_STRIDE);
+                for (int kb = 0; kb < u.nkb; ++kb) {
+                    take();
+                    if (!ok) break;
+                    const uint32_t st = sbase + s * P_STAGE_BYTES;
+                    mma_pair_block(d_tmem, desc_lo(st, false), desc_lo(st + P_A_BYTES, B_MN), B_MN ? MN_STEP_16 : K_STEP, idesc,
+                                   kb != 0 ? 1u : 0u, lead);
+                    release();
+                }
+                // the tile's low-rank terms
+                const int64_t tile = static_cast<int64_t>(u.mpair) * ADAPTER_TILE;
+                const int n = static_cast<int>(p.plan.count[u.mpair]);
+                for (int e = 0; e < n && ok; ++e) {
+                    const uint4* mk = reinterpret_cast<const uint4*>(p.plan.masks + (tile + e) * 8);
+                    const uint4 lo = mk[0], hi = mk[1];
+                    const uint32_t off[8] = {~lo.x, ~lo.y, ~lo.z, ~lo.w, ~hi.x, ~hi.y, ~hi.z, ~hi.w};
+                    for (int c = 0; c < (p.rank + 31) / 32; ++c) {
+                        take();
+                        if (!ok) break;
+                        const uint32_t st = sbase + s * P_STAGE_BYTES;
+                        const int steps = p.rank - 32 * c > 16 ? 2 : 1;  // 16-rank groups with ranks in them
+                        for (int j = 0; j < steps; ++j)
+                            mma_pair_masked(d_tmem, desc_lo(st, false) + j * K_STEP, desc_lo(st + P_A_BYTES, true) + j * MN_STEP_16,
+                                            idesc_q, off, lead);
+                        release();
+                    }
+                }
+                if (!ok) break;
+                mma_commit_pair_lead(tfull_bar(ab), 0x3, lead);
+                if (++ab == NACC) { ab = 0; aph ^= 1u; }
+            }
+            __syncwarp();
+            if (lead) {  // the commit covers what its own thread issued
+                mma_commit_pair(drain_bar);
+                mbar_wait(drain_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 0 && lane == 0) {
         // ------------------------------------------------------------ producer (both CTAs)
         int s = 0;
         uint32_t ph = 0;
@@ -523,23 +662,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (++s == P_STAGES) { s = 0; ph ^= 1u; }
             }
             }
-            if (MODE == ADAPTER) {
-                const uint32_t* ids = p.plan.ids + static_cast<int64_t>(u.mpair) * ADAPTER_TILE;
-                const int n = static_cast<int>(p.plan.count[u.mpair]);
-                for (int e = 0; e < n; ++e) {
-                    const int g = static_cast<int>(ids[e]);
-                    for (int c = 0; c < (p.rank + 31) / 32; ++c) {
-                        if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)) goto done_p;
-                        const uint32_t fb_leader = mapa_rank(full_bar(s), 0);
-                        const uint32_t a_dst = sbase + s * P_STAGE_BYTES, b_dst = a_dst + P_A_BYTES;
-                        if (crank == 0) mbar_expect_tx(full_bar(s), 2 * (P_A_BYTES + P_B_BYTES / 2));
-                        tma_load_2d_pair(a_dst, &tmA2, c * 64, arow, fb_leader);
-                        for (int b = 0; b < B_ATOMS; ++b)
-                            tma_load_3d_pair(b_dst + b * (BKE * 128), &tmB2, bcol + b * 64, c * 32, g, fb_leader);
-                        if (++s == P_STAGES) { s = 0; ph ^= 1u; }
-                    }
-                }
-            }
         }
     done_p:;
         // Copies of this CTA complete on CTA 0's barriers; CTA 0's MMA thread
@@ -588,28 +710,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 mma_commit_pair_mc(empty_bar(s), 0x3);
                 if (++s == P_STAGES) { s = 0; ph ^= 1u; }
-            }
-            if (MODE == ADAPTER) {  // the tile's low-rank terms
-                constexpr uint32_t idesc_q = instr_desc_pair<IN, false, true, BN>();
-                const int64_t tile = static_cast<int64_t>(u.mpair) * ADAPTER_TILE;
-                const int n = static_cast<int>(p.plan.count[u.mpair]);
-                for (int e = 0; e < n; ++e) {
-                    const uint4* mk = reinterpret_cast<const uint4*>(p.plan.masks + (tile + e) * 8);
-                    const uint4 lo = mk[0], hi = mk[1];
-                    const uint32_t off[8] = {~lo.x, ~lo.y, ~lo.z, ~lo.w, ~hi.x, ~hi.y, ~hi.z, ~hi.w};
-                    for (int c = 0; c < (p.rank + 31) / 32; ++c) {
-                        if (!mbar_wait(full_bar(s), ph, abort_flag, p, DEV_TIMEOUT_MMA)) goto done_m;
-                        tc_fence_after();
-                        const uint32_t a_s = sbase + s * P_STAGE_BYTES, b_s = a_s + P_A_BYTES;
-                        const int steps = p.rank - 32 * c > 16 ? 2 : 1;  // K = 16 steps with ranks in them
-                        for (int j = 0; j < steps; ++j)
-                            for (int part = 0; part < 2; ++part)
-                                mma_pair_masked(d_tmem, smem_desc(a_s + (2 * part + j) * 32, 16, 1024),
-                                                smem_desc(b_s + j * 2048, BKE * 128, 1024), idesc_q, off);
-                        mma_commit_pair_mc(empty_bar(s), 0x3);
-                        if (++s == P_STAGES) { s = 0; ph ^= 1u; }
-                    }
-                }
             }
             mma_commit_pair_mc(tfull_bar(ab), 0x3);
             if (++ab == NACC) { ab = 0; aph ^= 1u; }

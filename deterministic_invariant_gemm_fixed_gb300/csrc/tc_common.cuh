@@ -93,6 +93,19 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
     return d;
 }
 
+// Low and high word of a tile's descriptor (128-byte swizzle, 8-row groups 1024
+// bytes apart): K-major, or MN-major with 8192 bytes from one 64-column atom to
+// the next.  One MMA's step along K: 32 bytes, or 16 rows of 128.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, bool mn) { return ((saddr & 0x3FFFFu) >> 4) | ((mn ? 512u : 1u) << 16); }
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t K_STEP = 32 >> 4, MN_STEP_16 = 2048 >> 4;
+
+// 1 in one lane of the warp, always the same.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32"
