@@ -62,6 +62,7 @@ SIGNATURES = {
     "bi_router_backward": (_i32, [_p] * 10 + [_i64] * 3 + [_i32, _i32, _p]),
     "bi_grad_norm": (_i32, [_p, _p, _p, _p, _p, _i64, _p]),
     "bi_grad_clip": (_i32, [_p, _p, _p, _p, _p, _i64, _p, ctypes.c_float, _p]),
+    "bi_grad_norm_clip": (_i32, [_p, _p, _p, _p, _p, _i64, _p, ctypes.c_float, _p]),
     "bi_grouped_forward_noalloc": (_i32, [_p, _p, _p, _p, _i64, _i64, _i64, _i64, _i32, _p]),
 }
 
@@ -312,13 +313,24 @@ def bi_grad_norm(engine, norm, tensors, stream=None) -> int:
     return _lib.bi_grad_norm(engine, _ptr(norm), t.ptrs, t.counts, t.dtypes, t.n, _stream(stream))
 
 
+def _set_pair(dst, src):
+    s = _set(src)
+    d = s if dst is src else _set(dst)
+    if d is not s and (d.n != s.n or d.counts[:] != s.counts[:] or d.dtypes[:] != s.dtypes[:]):
+        raise ValueError("bi: dst and src must hold tensors of the same sizes and dtypes")
+    return d, s
+
+
 def bi_grad_clip(engine, dst, src, norm, max_norm, stream=None) -> int:
     """dst and src: TensorSets (or sequences) of the same shapes and dtypes; dst
     may be src."""
-    s, d = _set(src), _set(dst)
-    if d is not s and (d.n != s.n or d.counts[:] != s.counts[:] or d.dtypes[:] != s.dtypes[:]):
-        raise ValueError("bi: dst and src must hold tensors of the same sizes and dtypes")
+    d, s = _set_pair(dst, src)
     return _lib.bi_grad_clip(engine, d.ptrs, s.ptrs, s.counts, s.dtypes, s.n, _ptr(norm), max_norm, _stream(stream))
+
+
+def bi_grad_norm_clip(engine, dst, src, norm, max_norm, stream=None) -> int:
+    d, s = _set_pair(dst, src)
+    return _lib.bi_grad_norm_clip(engine, d.ptrs, s.ptrs, s.counts, s.dtypes, s.n, _ptr(norm), max_norm, _stream(stream))
 
 
 def bi_dispatch_tier(pass_, dtype, tensor_cores, k, n) -> int:
@@ -432,9 +444,7 @@ class Engine:
 
     def clip_gradients(self, dst, src, norm, max_norm, stream=None):
         """norm = the set's global norm, then dst = src scaled to at most max_norm."""
-        src = _set(src)
-        self.grad_norm(norm, src, stream)
-        self.grad_clip(dst, src, norm, max_norm, stream)
+        self._ok(bi_grad_norm_clip(self.handle, dst, src, norm, max_norm, stream))
 
     def check(self, stream=None):
         self._ok(bi_engine_check(self.handle, stream))

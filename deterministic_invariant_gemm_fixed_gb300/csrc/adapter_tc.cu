@@ -1048,16 +1048,16 @@ cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, c
     return e;
 }
 
-// Which tiles (both give the same bits).  A wave of CTA pairs takes 390 ns per
-// contraction block; single CTAs take 150 ns (four dependent MMAs), or what their
-// operands take to come from L2, 1.5 ns per tile and block, if that is more.
-// Measured, bf16, K = 4096, the whole call: N = 4096, 64 rows 25 us against 45,
-// 512 rows 37 against 41, 1333 rows 70 against 65; N = 11008, 128 rows 36 against
-// 46, 512 rows 90 against 67.
+// Which tiles (both give the same bits).  A wave of CTA pairs takes 300 ns per
+// contraction block; single CTAs take 80 ns, or what their operands take to come
+// from L2, 7/6 ns per tile and block, if that is more.  Measured, bf16, K = 4096,
+// the whole call, single CTAs against pairs: N = 4096, 64 rows 16.5 us against 35,
+// 512 rows 26.7 against 33.1; N = 11008, 128 rows 31 against 37, 256 rows 53
+// against 38.
 bool adapter_small_tiles(const LaunchCtx& c, int64_t M, int64_t C) {
     const int64_t pairs = (M + 255) / 256 * ((C + 255) / 256), tiles = (M + 127) / 128 * ((C + 63) / 64);
     const int64_t wave_p = (pairs + c.sm_count / 2 - 1) / (c.sm_count / 2), wave_s = (tiles + c.sm_count - 1) / c.sm_count;
-    return (M + 127) / 128 <= 65535 && lmax(300 * wave_s, 3 * tiles) < 780 * wave_p;
+    return (M + 127) / 128 <= 65535 && lmax(480 * wave_s, 7 * tiles) < 1800 * wave_p;
 }
 
 // Sums of pieces that a small tile's CTA takes on itself: 64 KB of L2 reads.

@@ -146,24 +146,28 @@ __global__ void __launch_bounds__(GC_THREADS, 4) square_sum_kernel(const __grid_
     if (lane == 0) partials[warp] = d;
 }
 
-// norm = sqrt of the warps' sums, added thread-strided in order, then by a tree.
-__global__ void __launch_bounds__(1024) norm_finish_kernel(const double* partials, int64_t n, float* norm) {
-    __shared__ double s_w[32];
-    grid_dep_wait();
-    grid_dep_launch();
+// sqrt of the warps' sums, in every thread of a block of GC_THREADS: each thread
+// adds every GC_THREADS-th sum in order, then a tree.
+__device__ __forceinline__ float norm_of(const double* partials, int64_t n, double* s_w) {
     double a = 0.0;
 #pragma unroll 8
-    for (int64_t i = threadIdx.x; i < n; i += 1024) a += partials[i];
+    for (int64_t i = threadIdx.x; i < n; i += GC_THREADS) a += partials[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = a;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        a = s_w[threadIdx.x];
+    a = 0.0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-        if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(a));
-    }
+    for (int w = 0; w < GC_WARPS; ++w) a += s_w[w];
+    return static_cast<float>(sqrt(a));
+}
+
+__global__ void __launch_bounds__(GC_THREADS) norm_finish_kernel(const double* partials, int64_t n, float* norm) {
+    __shared__ double s_w[GC_WARPS];
+    grid_dep_wait();
+    grid_dep_launch();
+    const float v = norm_of(partials, n, s_w);
+    if (threadIdx.x == 0) *norm = v;
 }
 
 template <typename T>
@@ -199,11 +203,21 @@ __device__ __forceinline__ void scale_unit(const Tensor& t, int64_t e0, int len,
 
 // dst = round(src * coef), coef = norm > max_norm ? max_norm / norm : 1 (NaN for
 // a NaN norm).  coef = 1 copies the bits, and leaves a tensor in place alone.
+// With `partials` every block adds up the norm itself, and block 0 of the launch
+// that has `norm_out` writes it.
 __global__ void __launch_bounds__(GC_THREADS, 4)
-    scale_kernel(const __grid_constant__ Table t, const float* norm, float max_norm) {
+    scale_kernel(const __grid_constant__ Table t, const float* norm, float max_norm, const double* partials, int64_t sums,
+                 float* norm_out) {
+    __shared__ double s_w[GC_WARPS];
     grid_dep_wait();
     grid_dep_launch();
-    const float n = __ldg(norm);
+    float n;
+    if (partials != nullptr) {
+        n = norm_of(partials, sums, s_w);
+        if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = n;
+    } else {
+        n = __ldg(norm);
+    }
     const float coef = n > max_norm ? max_norm / n : (n == n ? 1.0f : n);
     const bool exact = coef == 1.0f;
     const int lane = threadIdx.x & 31, units = t.first[t.n];
@@ -294,6 +308,42 @@ cudaError_t over_set(const void* const* src, void* const* dst, const int64_t* co
     return cudaSuccess;
 }
 
+// The warps' sums of the set into partials; their number in *sums.
+cudaError_t launch_sums(const LaunchCtx& c, const void* const* tensors, const int64_t* counts, const int* dtypes, int64_t n,
+                        const Cuts& cuts, double* partials, int64_t* sums) {
+    *sums = 0;
+    return over_set(tensors, nullptr, counts, dtypes, n, false, cuts, [&](const Table& t, int64_t count) {
+        const cudaError_t r = launch_pdl(square_sum_kernel, dim3(static_cast<unsigned>(blocks_of(count))), dim3(GC_THREADS), 0,
+                                         c.stream, t, partials + *sums);
+        *sums += blocks_of(count) * GC_WARPS;
+        if (r == cudaSuccess) c.count();
+        return r;
+    });
+}
+
+cudaError_t launch_scale(const LaunchCtx& c, void* const* dst, const void* const* src, const int64_t* counts,
+                         const int* dtypes, int64_t n, const Cuts& cuts, const float* norm, float max_norm,
+                         const double* partials, int64_t sums, float* norm_out) {
+    return over_set(src, dst, counts, dtypes, n, true, cuts, [&](const Table& t, int64_t count) {
+        const cudaError_t r = launch_pdl(scale_kernel, dim3(static_cast<unsigned>(blocks_of(count))), dim3(GC_THREADS), 0,
+                                         c.stream, t, norm, max_norm, partials, sums, norm_out);
+        norm_out = nullptr;  // written by the first launch
+        if (r == cudaSuccess) c.count();
+        return r;
+    });
+}
+
+// One sum per warp of every launch over the set.
+int64_t sums_bytes(int64_t n, const Cuts& cuts) {
+    const int64_t groups = (n + GC_TENSORS - 1) / GC_TENSORS;
+    return lmin(cuts.units + groups * GC_WARPS, groups * GC_BLOCKS * GC_WARPS) * 8;
+}
+// Up to this many warps' sums are added up by every block of the scaling pass (a
+// small set, 24 tensors of 1.5 million f32: 14.7 us with a finishing kernel, 12.6
+// without); more would queue for the f64 units (4864 sums, 40 million f32: 80 us
+// against 87).
+constexpr int64_t GC_FUSE = 1024;
+
 }  // namespace
 }  // namespace bi
 
@@ -315,21 +365,13 @@ bi_status bi_grad_norm(bi_engine eng, float* norm, const void* const* tensors, c
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_grad_norm");
     }
     const LaunchCtx c = ctx(eng, stream);
-    // one sum per warp of every launch
-    const int64_t groups = (n + GC_TENSORS - 1) / GC_TENSORS;
-    Scratch sc(eng, s, static_cast<size_t>(lmin(cuts.units + groups * GC_WARPS, groups * GC_BLOCKS * GC_WARPS) * 8));
+    Scratch sc(eng, s, static_cast<size_t>(sums_bytes(n, cuts)));
     if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "norm scratch");
     double* partials = static_cast<double*>(sc.ptr);
     int64_t sums = 0;
-    cudaError_t e = over_set(tensors, nullptr, counts, dtypes, n, false, cuts, [&](const Table& t, int64_t count) {
-        const dim3 grid(static_cast<unsigned>(blocks_of(count)));
-        const cudaError_t r = launch_pdl(square_sum_kernel, grid, dim3(GC_THREADS), 0, c.stream, t, partials + sums);
-        sums += blocks_of(count) * GC_WARPS;
-        if (r == cudaSuccess) c.count();
-        return r;
-    });
+    cudaError_t e = launch_sums(c, tensors, counts, dtypes, n, cuts, partials, &sums);
     if (e == cudaSuccess) {
-        e = launch_pdl(norm_finish_kernel, dim3(1), dim3(1024), 0, c.stream, partials, sums, norm);
+        e = launch_pdl(norm_finish_kernel, dim3(1), dim3(GC_THREADS), 0, c.stream, partials, sums, norm);
         if (e == cudaSuccess) c.count();
     }
     return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_grad_norm");
@@ -345,15 +387,32 @@ bi_status bi_grad_clip(bi_engine eng, void* const* dst, const void* const* src, 
     if (cuts.units == 0) return BI_OK;
     DeviceGuard g(eng->device);
     if (!g.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
-    const LaunchCtx c = ctx(eng, stream);
-    const cudaError_t e = over_set(src, dst, counts, dtypes, n, true, cuts,
-                                   [&](const Table& t, int64_t count) {
-        const dim3 grid(static_cast<unsigned>(blocks_of(count)));
-        const cudaError_t r = launch_pdl(scale_kernel, grid, dim3(GC_THREADS), 0, c.stream, t, norm, max_norm);
-        if (r == cudaSuccess) c.count();
-        return r;
-    });
+    const cudaError_t e =
+        launch_scale(ctx(eng, stream), dst, src, counts, dtypes, n, cuts, norm, max_norm, nullptr, 0, nullptr);
     return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_grad_clip");
+}
+
+bi_status bi_grad_norm_clip(bi_engine eng, void* const* dst, const void* const* src, const int64_t* counts,
+                            const int* dtypes, int64_t n, float* norm, float max_norm, void* stream) {
+    Cuts cuts;
+    bi_status st = check_set(eng, src, dst, true, counts, dtypes, n, &cuts);
+    if (st != BI_OK) return st;
+    if (!norm) return fail(eng, BI_ERR_INVALID_ARG, "norm must not be NULL");
+    if (!(max_norm >= 0.0f)) return fail(eng, BI_ERR_INVALID_ARG, "max_norm must be >= 0");
+    if (cuts.units == 0 || sums_bytes(n, cuts) / 8 > GC_FUSE) {
+        st = bi_grad_norm(eng, norm, src, counts, dtypes, n, stream);
+        return st == BI_OK ? bi_grad_clip(eng, dst, src, counts, dtypes, n, norm, max_norm, stream) : st;
+    }
+    DeviceGuard g(eng->device);
+    if (!g.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
+    const LaunchCtx c = ctx(eng, stream);
+    Scratch sc(eng, static_cast<cudaStream_t>(stream), static_cast<size_t>(sums_bytes(n, cuts)));
+    if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "norm scratch");
+    double* partials = static_cast<double*>(sc.ptr);
+    int64_t sums = 0;
+    cudaError_t e = launch_sums(c, src, counts, dtypes, n, cuts, partials, &sums);
+    if (e == cudaSuccess) e = launch_scale(c, dst, src, counts, dtypes, n, cuts, nullptr, max_norm, partials, sums, norm);
+    return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_grad_norm_clip");
 }
 
 }  // extern "C"

@@ -371,6 +371,10 @@ bi_status bi_grad_norm(bi_engine engine, float* norm, const void* const* tensors
 bi_status bi_grad_clip(bi_engine engine, void* const* dst, const void* const* src, const int64_t* counts,
                        const int* dtypes, int64_t n, const float* norm, float max_norm, void* stream);
 
+/* Both in one call, with the same results: *norm of the src set, then dst. */
+bi_status bi_grad_norm_clip(bi_engine engine, void* const* dst, const void* const* src, const int64_t* counts,
+                            const int* dtypes, int64_t n, float* norm, float max_norm, void* stream);
+
 /* ---- introspection ---------------------------------------------------- */
 
 /* The dispatcher's choice for a call: 0 = scalar tier, 1 = tensor-core tier.

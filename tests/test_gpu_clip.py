@@ -168,3 +168,17 @@ def test_offsets_beyond_32_bits(eng):
     eng.clip_gradients([t], [t], norm, math.sqrt(34.0) / 2)
     assert abs(float(norm) - math.sqrt(34.0)) <= 10 * U * 6
     assert t[[0, n - 2, n - 1]].tolist() == [2.0, 1.5, 1.5] and not t[1:1000].any()
+
+
+@pytest.mark.parametrize("sizes,dtypes", SETS + [([4000] * 700, [F] * 700)])
+def test_one_call_equals_two(eng, sizes, dtypes):
+    src = make(sizes, dtypes, seed=9)
+    a, b = [torch.empty_like(t) for t in src], [torch.empty_like(t) for t in src]
+    n1, n2 = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    eng.grad_norm(n1, src)
+    eng.grad_clip(a, src, n1, 0.75)
+    eng.clip_gradients(b, src, n2, 0.75)
+    assert torch.equal(n1, n2) and all(torch.equal(p, q) for p, q in zip(a, b))
+    s = bi.TensorSet(src)
+    assert bi.bi_grad_norm_clip(eng.handle, s, s, n1, -1.0) == bi.BI_ERR_INVALID_ARG
+    assert bi.bi_grad_norm_clip(eng.handle, s, s, None, 1.0) == bi.BI_ERR_INVALID_ARG
