@@ -158,16 +158,17 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     grid_dep_launch();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     const int rg = p.rp / 16;  // groups of 16 ranks per adapter
-    const int kb0 = blockIdx.y * NP_KB, nkb = min(NP_KB, p.num_kb - kb0);
+    const int pieces = (p.num_kb + NP_KB - 1) / NP_KB;  // this CTA's: blockIdx.y, + gridDim.y, ...
+    auto piece_blocks = [&](int piece) { return min(NP_KB, p.num_kb - piece * NP_KB); };
 
     if (warp == 0) {  // a lane for each of a stage's copies, as in the small tiles' kernel below
         // the first blocks of X need no list: their bytes are expected and the
         // copies issued now, the stages' own arrivals follow with the adapters'
         // (the first CTA of a tile and piece; others may have no adapters left)
-        const int early = blockIdx.z == 0 ? min(NP_STAGES, nkb) : 0;
+        const int early = blockIdx.z == 0 ? min(NP_STAGES, piece_blocks(blockIdx.y)) : 0;
         if (lane < early) {
             asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full_bar(lane)), "r"(NP_A) : "memory");
-            tma_load_2d(sbase + lane * NP_STAGE, &tmX, (kb0 + lane) * BK, row0, full_bar(lane));
+            tma_load_2d(sbase + lane * NP_STAGE, &tmX, (static_cast<int>(blockIdx.y) * NP_KB + lane) * BK, row0, full_bar(lane));
         }
         __syncwarp();
         const bool listed = __all_sync(0xffffffffu, mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER));
@@ -178,10 +179,12 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
             for (int kb = 0; kb < early; ++kb) mbar_expect_tx(full_bar(kb), 0);
             drain_copies(full_bar, early, NP_STAGES);
         }
+        for (int piece = blockIdx.y; piece < pieces; piece += gridDim.y)
         for (int q = blockIdx.z; q < batches; q += gridDim.z) {
             const int n = min(4, groups - 4 * q);
             const int gi = 4 * q + lane, e = gi / rg, r16 = (gi - e * rg) * 16;
             const int g = lane < n ? static_cast<int>(s_id[e]) : 0;
+            const int kb0 = piece * NP_KB, nkb = piece_blocks(piece);
             for (int kb = 0; kb < nkb; ++kb) {
                 const uint32_t a = sbase + s * NP_STAGE;
                 const bool have_x = fills < early;
@@ -204,7 +207,9 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
         const int groups = listed ? static_cast<int>(*s_count) * rg : 0, batches = (groups + 3) / 4;
         int s = 0, ab = 0;
         uint32_t ph = 0, aph = 0;
+        for (int piece = blockIdx.y; piece < pieces; piece += gridDim.y)
         for (int q = blockIdx.z; q < batches; q += gridDim.z) {
+            const int nkb = piece_blocks(piece);
             const uint32_t idesc = instr_desc(p.fmt, false, false, 16 * min(4, groups - 4 * q));
             if (!__all_sync(0xffffffffu, mbar_wait_fast(tempty_bar(ab), aph ^ 1u, abort_flag, p, DEV_TIMEOUT_MMA))) goto done_m;
             tc_fence_after();
@@ -254,11 +259,13 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
         const int64_t row = row0 + 32 * w + lane;
         int ab = 0;
         uint32_t aph = 0;
+        bool going = true;
+        for (int piece = blockIdx.y; piece < pieces && going; piece += gridDim.y)
         for (int q = blockIdx.z; q < batches; q += gridDim.z) {
             const int n = min(4, groups - 4 * q);
             bool ok = mbar_wait_fast(tfull_bar(ab), aph, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            going = __all_sync(0xffffffffu, ok);
+            if (!going) break;
             tc_fence_after();
             for (int i = 0; i < n; ++i) {
                 const int gi = 4 * q + i;
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
                 uint32_t v[16];
                 tmem_ld16(tmem_base + (static_cast<uint32_t>(32 * w) << 16) + ab * 64 + 16 * i, v);
                 if ((mask >> lane) & 1u) {
-                    float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<int64_t>(blockIdx.y) * p.M + row) * p.rp +
+                    float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<int64_t>(piece) * p.M + row) * p.rp +
                                                             (gi % rg) * 16);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -1038,11 +1045,15 @@ cudaError_t tc_adapter_narrow(const LaunchCtx& c, bi_dtype dt, float* partial, c
     p.fmt = dt == BI_BF16 ? 1 : 0;
     p.status = c.status; p.wait_limit = c.wait_limit_ns;
     const int64_t tiles = (M + 127) / 128, pieces = (L + ADAPTER_PIECE - 1) / ADAPTER_PIECE;
-    // batches of four 16-rank groups: at most one adapter per row; a CTA takes
-    // several where the tiles and pieces alone fill the GPU
+    // A CTA per tile and piece, or, where those are more than the two CTAs that fit
+    // an SM, several pieces one after the other (its set-up once: 8192 rows of 4096
+    // in 18 us with a CTA per piece).  Where they are fewer, the batches of four
+    // 16-rank groups (at most one adapter per row) are split among CTAs as well.
+    const int64_t slots = 2 * int64_t(c.sm_count);
+    const int64_t each = (tiles * pieces + slots - 1) / slots, gy = (pieces + each - 1) / each;
     const int64_t most = (lmin(lmin(G, M), 128) * (p.rp / 16) + 3) / 4;
-    const int64_t want = (4 * int64_t(c.sm_count) + tiles * pieces - 1) / (tiles * pieces);
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(pieces), static_cast<unsigned>(lmin(most, want)));
+    const int64_t want = (2 * slots + tiles * gy - 1) / (tiles * gy);
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(gy), static_cast<unsigned>(lmin(most, want)));
     e = launch_pdl(narrow_tc_kernel, grid, dim3(NP_THREADS), NP_SMEM, c.stream, x, w, p);
     if (e == cudaSuccess) c.count();
     return e;

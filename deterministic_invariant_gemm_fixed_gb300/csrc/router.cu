@@ -130,23 +130,23 @@ struct RouteArgs {
 // chain of dependent steps.  Otherwise (shorter rows, k > 32, or more than 32
 // logits at or above the bound): k times the largest logit of the row's lanes.
 // 8 of 256 experts, 131072 rows in f32: 245 us by the second way.
-template <typename T, int L, int V>
-__global__ void __launch_bounds__(RT_THREADS, V <= 8 ? 4 : 1) route_kernel(const RouteArgs a) {
+template <typename T, int L, int V, int W>  // W warps per block
+__global__ void __launch_bounds__(32 * W, W == RT_WARPS && V <= 8 ? 4 : 1) route_kernel(const RouteArgs a) {
     constexpr int GROUPS = 32 / L;             // rows per warp
-    constexpr int STEP = RT_WARPS * GROUPS;    // rows per block and step
+    constexpr int STEP = W * GROUPS;    // rows per block and step
     constexpr int MAXK = L * V < RT_MAX_K ? L * V : static_cast<int>(RT_MAX_K);
-    __shared__ float s_sum[RT_WARPS][L * V];
+    __shared__ float s_sum[W][L * V];
     __shared__ uint32_t s_cnt[L * V];
-    __shared__ uint32_t s_rows[RT_WARPS];
-    __shared__ uint2 s_pick[RT_WARPS * GROUPS][MAXK];  // slot -> (expert, weight's bits)
-    __shared__ __align__(16) float s_cand_v[L == 32 ? RT_WARPS : 1][32];
-    __shared__ uint16_t s_cand_i[L == 32 ? RT_WARPS : 1][32];  // (place in the lane, lane)
+    __shared__ uint32_t s_rows[W];
+    __shared__ uint2 s_pick[W * GROUPS][MAXK];  // slot -> (expert, weight's bits)
+    __shared__ __align__(16) float s_cand_v[L == 32 ? W : 1][32];
+    __shared__ uint16_t s_cand_i[L == 32 ? W : 1][32];  // (place in the lane, lane)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grp = lane / L, li = lane % L;
     const int e0 = li * V;
     const int E = a.E, k = a.k;
     uint2* pick = s_pick[warp * GROUPS + grp];
-    for (int i = threadIdx.x; i < L * V; i += RT_THREADS) s_cnt[i] = 0;
+    for (int i = threadIdx.x; i < L * V; i += 32 * W) s_cnt[i] = 0;
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
@@ -319,12 +319,12 @@ __global__ void __launch_bounds__(RT_THREADS, V <= 8 ? 4 : 1) route_kernel(const
     if (lane == 0) s_rows[warp] = rows;
     __syncthreads();
     uint32_t v = 0;
-    for (int w = 0; w < RT_WARPS; ++w) v += s_rows[w];
+    for (int w = 0; w < W; ++w) v += s_rows[w];
     const bool alone = gridDim.x == 1;  // a short batch: this block's sums are the result
-    for (int e = threadIdx.x; e < E; e += RT_THREADS) {
+    for (int e = threadIdx.x; e < E; e += 32 * W) {
         float s = s_sum[0][e];
 #pragma unroll
-        for (int w = 1; w < RT_WARPS; ++w) s += s_sum[w][e];
+        for (int w = 1; w < W; ++w) s += s_sum[w][e];
         if (alone) {
             const float m = v ? s / static_cast<float>(v) : 0.0f;
             a.mean[e] = m;
@@ -572,8 +572,12 @@ int64_t rows_per_block(int64_t T, int64_t E) {
 template <typename T>
 cudaError_t forward_t(const LaunchCtx& c, const RouteArgs& a, int64_t blocks) {
     return with_layout(a.E, [&](auto l, auto v) {
-        return launch_pdl(route_kernel<T, l.value, v.value>, dim3(static_cast<unsigned>(blocks)), dim3(RT_THREADS), 0,
-                          c.stream, a);
+        // a lone block takes more warps, as far as its shared memory goes: fewer
+        // steps one after the other (64 rows of 64 experts: one instead of two)
+        constexpr int L = l.value, V = v.value, LONE = L * V <= 64 ? 32 : V <= 16 ? 16 : RT_WARPS;
+        return blocks == 1 ? launch_pdl(route_kernel<T, L, V, LONE>, dim3(1), dim3(32 * LONE), 0, c.stream, a)
+                           : launch_pdl(route_kernel<T, L, V, RT_WARPS>, dim3(static_cast<unsigned>(blocks)), dim3(RT_THREADS),
+                                        0, c.stream, a);
     });
 }
 
