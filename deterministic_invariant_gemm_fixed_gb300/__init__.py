@@ -1,4 +1,5 @@
-"""Deterministic, batch-invariant training matmul for GB300 (sm_103a).
+"""Deterministic, batch-invariant training matmul for GB300 (sm_103a), with the
+adapters, router and gradient clipping that go beside it.
 
 Thin ctypes binding over the C ABI in ``include/bi.h`` (libbi.so, built in-tree
 by ``deterministic_invariant_gemm_fixed_gb300.build``).  The functions below

@@ -10,6 +10,9 @@
  *             dX[m,:] = dY[m,:] * W[e(m)]        dW[e] = sum over rows of expert e
  *                                                 of dY[m,:]^T X[m,:] (always f32)
  *
+ * and beside them low-rank adapters of many requests, a router with its balance
+ * loss, and gradient norm and clipping, each described at its declarations.
+ *
  * Sources: sgemm-bi 0.1.1.post2 (PyPI page), sections "Use" (weight stored
  * [in, out]; the raw-pointer Engine.forward call with m, k, n, a dtype string,
  * a stream and a tensor-core flag) and "Determinism contracts" (the two tiers);
