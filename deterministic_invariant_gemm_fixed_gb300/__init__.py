@@ -295,6 +295,8 @@ class TensorSet:
     def __init__(self, tensors):
         self.tensors = list(tensors)
         n = self.n = len(self.tensors)
+        if len({t.device for t in self.tensors}) > 1:
+            raise ValueError("bi: the tensors of a set must be on one device")
         # an empty tensor has no storage to point at
         self.ptrs = (ctypes.c_void_p * n)(*[_ptr(t) if t.numel() else None for t in self.tensors])
         self.counts = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])

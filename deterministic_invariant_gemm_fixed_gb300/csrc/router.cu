@@ -73,8 +73,8 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
-// 2^x, within 2 ulp; exponents are kept in base 2, so a probability costs one FMA
-// and one of these.
+// 2^x, within 2 ulp.  Probabilities are 2^((x - m) log2 e), the difference taken
+// first: it is exact or nearly so, and overflows for no finite logits that matter.
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -189,11 +189,11 @@ __global__ void __launch_bounds__(32 * W, W == RT_WARPS && V <= 8 ? 4 : 1) route
             for (int o = L / 2; o > 0; o >>= 1) nan = __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), o) != 0 || nan;
             counted = counted && (mx > -INFINITY || nan);
         }
-        const float m2 = mx > -INFINITY ? mx * LOG2E : 0.0f;
+        const float m = mx > -INFINITY ? mx : 0.0f;
         float p[V], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = exp2_approx(fmaf(x[i], LOG2E, -m2));
+            p[i] = exp2_approx((x[i] - m) * LOG2E);
             sum += p[i];
         }
         sum = group_sum<L>(sum);
@@ -201,10 +201,10 @@ __global__ void __launch_bounds__(32 * W, W == RT_WARPS && V <= 8 ? 4 : 1) route
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
         if (in && li == 0) {
-            a.lse[t] = counted ? (m2 + __log2f(sum)) * LN2 : INFINITY;
+            a.lse[t] = counted ? fmaf(__log2f(sum), LN2, m) : INFINITY;
             rows += counted;
         }
-        auto weight = [&](float v) { return exp2_approx(fmaf(v, LOG2E, -m2)) * inv; };
+        auto weight = [&](float v) { return exp2_approx((v - m) * LOG2E) * inv; };
         float wsum = 0.0f;
         bool done = false;
         if constexpr (L == 32) {
@@ -468,10 +468,9 @@ __global__ void __launch_bounds__(RT_THREADS) route_back_kernel(const RouteBackA
         const bool in = t < a.T;
         const float lse = lse_next;
         const bool counted = lse != INFINITY;  // false: the forward left the row out
-        const float lse2 = lse * LOG2E;
         float p[V], d[V], dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = counted ? exp2_approx(fmaf(raw.get(i), LOG2E, -lse2)) : 0.0f;
+        for (int i = 0; i < V; ++i) p[i] = counted ? exp2_approx((raw.get(i) - lse) * LOG2E) : 0.0f;
         lse_next = t + stride < a.T ? a.lse[t + stride] : INFINITY;
         raw.load(logits + (t + stride) * E, e0, E, a.vec != 0, t + stride < a.T);
         float ex[V];

@@ -343,3 +343,61 @@ def test_small_and_paired_tiles_give_the_same_bits(eng, m, k, n, r, g, dtype):
     finally:
         bi.bi_engine_set_tile_cols(eng.handle, 0)
     assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(dx, dx2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_row_tiles(eng, dtype):
+    """More tiles and pieces than resident CTAs: each takes several pieces; rows equal those of a short batch."""
+    d = inputs(20011, 1040, 72, 8, 5, dtype, seed=12, order="random")
+    y, h = forward(eng, d, 1)
+    dx = backward(eng, d, h, 1, ("dx",))[0]
+    for lo in (0, 9984, 19900):
+        hi = min(lo + 111, d["m"])
+        e = dict(d, m=hi - lo, x=d["x"][lo:hi].contiguous(), dy=d["dy"][lo:hi].contiguous(), ids=d["ids"][lo:hi].contiguous())
+        ye, he = forward(eng, e, 1)
+        assert torch.equal(ye, y[lo:hi]) and torch.equal(he, h[lo:hi])
+        assert torch.equal(backward(eng, e, he, 1, ("dx",))[0], dx[lo:hi])
+        r = exact(e)
+        close(ye, r["y"], r["y_s"], dtype, 0, 1, r["y_in"])
+        close(he, r["h"], r["h_s"], "f32", 0, 1)
+
+
+def test_backward_in_a_graph_and_on_a_side_stream(eng):
+    d = inputs(700, 256, 320, 16, 6, "bf16", seed=13, order="random")
+    _, h = forward(eng, d, 1)
+    want = backward(eng, d, h, 1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = backward(eng, d, h, 1)
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    out = [torch.zeros_like(t) for t in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        eng.adapter_backward(*out, d["x"], h, d["w"], d["dy"], d["a"], d["b"], d["scales"], d["ids"], *sizes(d))
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, out))
+
+
+def test_calls_back_to_back_on_one_buffer(eng):
+    """Each call reads what the one before wrote (the kernels of the next may start early): a chain of projections."""
+    d = inputs(48, 256, 256, 16, 4, "bf16", seed=14, order="random", bias=False)
+    x = d["x"]
+    want = []
+    for _ in range(6):
+        y, _ = forward(eng, dict(d, x=x), 1)
+        torch.cuda.synchronize()
+        x = y
+        want.append(y)
+    bufs = [torch.empty_like(x) for _ in range(2)]
+    for rep in range(20):
+        src = d["x"]
+        for i in range(6):
+            eng.adapter_forward(bufs[i % 2], None, src, d["w"], None, d["a"], d["b"], d["scales"], d["ids"], *sizes(d))
+            src = bufs[i % 2]
+        assert torch.equal(src, want[-1]), rep

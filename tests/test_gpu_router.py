@@ -238,3 +238,21 @@ def test_unaligned_rows(eng):
     dw = torch.randn(50, 4, device="cuda")
     dl = torch.ones(1, device="cuda")
     assert torch.equal(route_back(eng, x, o, dw, dl, 4, 1), route_back(eng, x.clone(), p, dw, dl, 4, 1))
+
+
+@pytest.mark.parametrize("e", [8, 64, 200])
+def test_large_logits(eng, e):
+    """Logits of 1e4 and of 3e38 apart: the softmax is that of their differences."""
+    gen = torch.Generator(device="cuda").manual_seed(e)
+    x = torch.randint(0, 5, (40, e), device="cuda", generator=gen).float()
+    for shift in (1.0e4, -2.0e4):  # the sums are exact in f32
+        o, p = route(eng, x + shift, None, 2, 0), route(eng, x, None, 2, 0)
+        for v in ("ids", "counts", "weights", "mean", "loss"):
+            assert torch.equal(o[v], p[v]), v
+    y = torch.full((3, e), -3.0e38, device="cuda")
+    y[:, 5] = 3.0e38
+    y[1, 6] = 3.0e38
+    o = route(eng, y, None, 2, 0)
+    assert o["weights"].tolist() == [[1.0, 0.0], [0.5, 0.5], [1.0, 0.0]]
+    d = route_back(eng, y, o, torch.ones(3, 2, device="cuda"), torch.ones(1, device="cuda"), 2, 0)
+    assert torch.isfinite(d).all()
