@@ -605,6 +605,38 @@ bi_status check_adapter(bi_engine eng, bi_dtype dt, int64_t m, int64_t k, int64_
     return BI_OK;
 }
 
+// Work on the engine's side stream beside the caller's.  mark() notes what it may
+// start after; begin() makes the side stream wait for that; join(), always reached
+// before the call's scratch is freed, makes the caller's stream wait for the side.
+struct Side {
+    bi_engine eng;
+    cudaStream_t main;
+    cudaEvent_t fork = nullptr, done = nullptr;
+    bool begun = false;
+    Side(bi_engine e, cudaStream_t s) : eng(e), main(s) {}
+    cudaError_t mark() {
+        cudaError_t e = cudaEventCreateWithFlags(&fork, cudaEventDisableTiming);
+        if (e == cudaSuccess) e = cudaEventCreateWithFlags(&done, cudaEventDisableTiming);
+        return e == cudaSuccess ? cudaEventRecord(fork, main) : e;
+    }
+    cudaError_t begin() {
+        const cudaError_t e = cudaStreamWaitEvent(eng->side, fork, 0);
+        begun = e == cudaSuccess;
+        return e;
+    }
+    cudaError_t join() {
+        if (!begun) return cudaSuccess;
+        begun = false;
+        const cudaError_t e = cudaEventRecord(done, eng->side);
+        return e == cudaSuccess ? cudaStreamWaitEvent(main, done, 0) : e;
+    }
+    ~Side() {
+        join();
+        if (fork) cudaEventDestroy(fork);
+        if (done) cudaEventDestroy(done);
+    }
+};
+
 // Cuts of one scratch allocation.
 struct Cut {
     int64_t at = 0;
@@ -672,22 +704,27 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
     float* part = reinterpret_cast<float*>(p + o_part);
     float* hs = reinterpret_cast<float*>(p + o_hs);
     float* base = dtype == BI_F32 ? static_cast<float*>(y) : reinterpret_cast<float*>(p + o_base);
-    cudaError_t e = cudaSuccess;
     // the shared product first: it may need scratch of its own, and a call that
-    // gets none must leave nothing enqueued
-    if (dtype == BI_F32) {
+    // gets none must leave nothing enqueued; h on the side stream beside it
+    Side side(eng, s);
+    cudaError_t e = side.mark();
+    if (e == cudaSuccess && dtype == BI_F32) {
         st = adapter_projection_f32(eng, c, 0, y, x, w, bias, m, k, n, tensor_cores);
         if (st != BI_OK) return st;
-    } else {
+    } else if (e == cudaSuccess) {
         e = scalar_rows(c, dtype, base, x, w, bias, m, k, n, 0, 1);
     }
+    const LaunchCtx cs = ctx(eng, eng->side);
+    if (e == cudaSuccess) e = side.begin();
     if (e == cudaSuccess)
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return narrow_scalar<T>(c, static_cast<const T*>(x), static_cast<const T*>(a), row_adapters, part, m, k, R, g);
+            return narrow_scalar<T>(cs, static_cast<const T*>(x), static_cast<const T*>(a), row_adapters, part, m, k, R, g);
         });
     const bool fuse = pieces * r <= WIDE_FUSE;
-    if (e == cudaSuccess && !fuse) e = narrow_finish(c, part, row_adapters, scales, h, hs, m, R, g, pieces);
+    if (e == cudaSuccess && !fuse) e = narrow_finish(cs, part, row_adapters, scales, h, hs, m, R, g, pieces);
+    const cudaError_t joined = side.join();
+    if (e == cudaSuccess) e = joined;
     if (e == cudaSuccess)
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
@@ -743,29 +780,16 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         uint32_t* perm = reinterpret_cast<uint32_t*>(p + o_perm);
         const AdapterChunks ch = AdapterChunks::at(p + o_ch, g);
         float* sums = reinterpret_cast<float*>(p + o_sum);
-        // the sorting of the rows for dA and dB runs on the engine's side stream
-        // beside the narrow product; the caller's stream waits for it before
-        // those (and before the scratch is released)
-        cudaError_t e = cudaSuccess, side = cudaSuccess;
-        cudaEvent_t fork = nullptr, join = nullptr;
-        auto sort_rows = [&](const LaunchCtx& cc) {
-            cudaError_t r = segment(cc, row_adapters, m, g, seg, perm, p + o_hist);
-            if (r == cudaSuccess) {
-                r = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, cc.stream, seg, static_cast<uint32_t>(g), ch);
-                if (r == cudaSuccess) cc.count();
-            }
-            return r;
-        };
-        const bool overlap = grads && need_u;
-        if (overlap) {
-            e = cudaEventCreateWithFlags(&fork, cudaEventDisableTiming);
-            if (e == cudaSuccess) e = cudaEventCreateWithFlags(&join, cudaEventDisableTiming);
-            if (e == cudaSuccess) e = cudaEventRecord(fork, s);
-            if (e == cudaSuccess) e = cudaStreamWaitEvent(eng->side, fork, 0);
+        // the rows are sorted for dA and dB on the side stream, beside the narrow product
+        Side side(eng, s);
+        cudaError_t e = grads ? side.mark() : cudaSuccess;
+        if (e == cudaSuccess && grads) e = side.begin();
+        if (e == cudaSuccess && grads) {
+            const LaunchCtx cs = ctx(eng, eng->side);
+            e = segment(cs, row_adapters, m, g, seg, perm, p + o_hist);
             if (e == cudaSuccess) {
-                side = sort_rows(ctx(eng, eng->side));
-                const cudaError_t r = cudaEventRecord(join, eng->side);  // recorded whatever happened above
-                if (side == cudaSuccess) side = r;
+                e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, cs.stream, seg, static_cast<uint32_t>(g), ch);
+                if (e == cudaSuccess) c.count();
             }
         }
         if (e == cudaSuccess && need_u) {
@@ -775,13 +799,8 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
             if (e == cudaSuccess) e = narrow_finish_tc(c, dtype, u, db ? &hs : nullptr, row_adapters, scales, m, R, g, pieces);
         }
         if (e == cudaSuccess && dx) e = tc_adapter_rows(c, dtype, 1, dx, dy, w, nullptr, p + o_uu, a, plan, m, k, n, R, g);
-        if (join) {  // always joined before anything below and before the scratch is freed
-            const cudaError_t r = cudaStreamWaitEvent(s, join, 0);
-            if (e == cudaSuccess) e = side != cudaSuccess ? side : r;
-        }
-        if (fork) cudaEventDestroy(fork);
-        if (join) cudaEventDestroy(join);
-        if (e == cudaSuccess && grads && !overlap) e = sort_rows(c);
+        const cudaError_t joined = side.join();
+        if (e == cudaSuccess) e = joined;
         if (e == cudaSuccess && db && !need_u) {
             const FinishJob hs{nullptr, h, nullptr, nullptr, p + o_h3};
             e = narrow_finish_tc(c, dtype, hs, nullptr, row_adapters, scales, m, R, g, 0);
@@ -820,20 +839,32 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     float* sums = reinterpret_cast<float*>(p + o_sum);
     float* base = dtype == BI_F32 ? static_cast<float*>(dx) : reinterpret_cast<float*>(p + o_base);
     const uint32_t G = static_cast<uint32_t>(g);
-    cudaError_t e = cudaSuccess;
-    if (dx && dtype == BI_F32) {  // first, as in the forward
+    Side side(eng, s);
+    cudaError_t e = side.mark();
+    if (e == cudaSuccess && dx && dtype == BI_F32) {  // first, as in the forward
         st = adapter_projection_f32(eng, c, 1, dx, dy, w, nullptr, m, k, n, tensor_cores);
         if (st != BI_OK) return st;
-    } else if (dx) {
+    } else if (e == cudaSuccess && dx) {
         e = scalar_rows(c, dtype, base, dy, w, nullptr, m, n, k, 1, 1);
     }
+    const LaunchCtx cs = ctx(eng, eng->side);
+    if (e == cudaSuccess) e = side.begin();  // u, and the rows sorted by adapter
     if (e == cudaSuccess && need_u) {
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return narrow_scalar<T>(c, static_cast<const T*>(dy), static_cast<const T*>(b), row_adapters, part, m, n, R, g);
+            return narrow_scalar<T>(cs, static_cast<const T*>(dy), static_cast<const T*>(b), row_adapters, part, m, n, R, g);
         });
-        if (e == cudaSuccess) e = narrow_finish(c, part, row_adapters, scales, nullptr, u, m, R, g, pieces);
+        if (e == cudaSuccess) e = narrow_finish(cs, part, row_adapters, scales, nullptr, u, m, R, g, pieces);
     }
+    if (e == cudaSuccess && grads) {
+        e = segment(cs, row_adapters, m, g, seg, perm, p + o_hist);
+        if (e == cudaSuccess) {
+            e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, cs.stream, seg, G, ch);
+            if (e == cudaSuccess) c.count();
+        }
+    }
+    const cudaError_t joined = side.join();
+    if (e == cudaSuccess) e = joined;
     if (e == cudaSuccess && dx) {
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
@@ -842,11 +873,6 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         });
     }
     if (e == cudaSuccess && grads) {
-        e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
-        if (e == cudaSuccess) {
-            e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, G, ch);
-            if (e == cudaSuccess) c.count();
-        }
         auto one = [&](float* out, const float* f, const void* z, int64_t C) {
             cudaError_t err = with_type(dtype, [&](auto* t) {
                 using T = std::remove_pointer_t<decltype(t)>;
