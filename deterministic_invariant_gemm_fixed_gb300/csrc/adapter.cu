@@ -247,13 +247,21 @@ __global__ void __launch_bounds__(256)
         if (jb.partial != nullptr) {  // rp - r0 is a multiple of 8: whole vectors
             const float* p = jb.partial + m * rp + r0;
             const int64_t step = M * rp;
-#pragma unroll 8
-            for (int q = 0; q < pieces; ++q) {
-                const float4 a = reinterpret_cast<const float4*>(p + q * step)[0];
-                const float4 b = reinterpret_cast<const float4*>(p + q * step)[1];
-                const float t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            for (int q0 = 0; q0 < pieces; q0 += 4) {  // four pieces' loads in flight
+                float4 a[4], b[4];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] = q == 0 ? t[u] : v[u] + t[u];
+                for (int q = 0; q < 4; ++q) {
+                    if (q0 + q >= pieces) break;
+                    a[q] = reinterpret_cast<const float4*>(p + (q0 + q) * step)[0];
+                    b[q] = reinterpret_cast<const float4*>(p + (q0 + q) * step)[1];
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q0 + q >= pieces) break;
+                    const float t[8] = {a[q].x, a[q].y, a[q].z, a[q].w, b[q].x, b[q].y, b[q].z, b[q].w};
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) v[u] = q0 + q == 0 ? t[u] : v[u] + t[u];
+                }
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u)
@@ -486,10 +494,13 @@ __global__ void __launch_bounds__(256)
     const float* p = jb.parts + static_cast<int64_t>(ch.part[g]) * RC;
     for (int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; i < RC; i += static_cast<int64_t>(gridDim.y) * 256) {
         float v = 0.0f;
-        if (n > 1) {
-            v = p[i];
-#pragma unroll 4
-            for (uint32_t j = 1; j < n; ++j) v += p[static_cast<int64_t>(j) * RC + i];
+        for (uint32_t j0 = 0; j0 < n; j0 += 4) {  // four chunks' loads in flight
+            float t[4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) t[j] = j0 + j < n ? p[static_cast<int64_t>(j0 + j) * RC + i] : 0.0f;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                if (j0 + j < n) v = j0 + j == 0 ? t[j] : v + t[j];
         }
         o[i] = v;
     }

@@ -563,13 +563,22 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 for (int q = 0; q < 8; ++q) v[q] = 0.0f;
                 if (g < p.G && r0 < p.rp) {
                     const float* src = p.partial + static_cast<int64_t>(row0 + row) * p.rp + r0;
-#pragma unroll 4
-                    for (int q = 0; q < p.pieces; ++q) {
-                        const float4 lo = reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * p.M * p.rp)[0];
-                        const float4 hi = reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * p.M * p.rp)[1];
-                        const float t[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    const int64_t step = p.M * p.rp;
+                    for (int q0 = 0; q0 < p.pieces; q0 += 4) {  // four pieces' loads in flight
+                        float4 a[4], b[4];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = q == 0 ? t[u] : v[u] + t[u];
+                        for (int q = 0; q < 4; ++q) {
+                            if (q0 + q >= p.pieces) break;
+                            a[q] = reinterpret_cast<const float4*>(src + (q0 + q) * step)[0];
+                            b[q] = reinterpret_cast<const float4*>(src + (q0 + q) * step)[1];
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (q0 + q >= p.pieces) break;
+                            const float t[8] = {a[q].x, a[q].y, a[q].z, a[q].w, b[q].x, b[q].y, b[q].z, b[q].w};
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) v[u] = q0 + q == 0 ? t[u] : v[u] + t[u];
+                        }
                     }
                 }
                 const float s = g < p.G && p.scales != nullptr ? p.scales[g] : 1.0f;

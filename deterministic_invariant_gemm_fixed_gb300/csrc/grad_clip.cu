@@ -150,8 +150,13 @@ __global__ void __launch_bounds__(GC_THREADS, 4) square_sum_kernel(const __grid_
 // adds every GC_THREADS-th sum in order, then a tree.
 __device__ __forceinline__ float norm_of(const double* partials, int64_t n, double* s_w) {
     double a = 0.0;
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < n; i += GC_THREADS) a += partials[i];
+    for (int64_t i = threadIdx.x; i < n; i += 8 * GC_THREADS) {  // eight loads in flight
+        double t[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t[u] = i + u * GC_THREADS < n ? partials[i + u * GC_THREADS] : 0.0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) a += t[u];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = a;

@@ -26,7 +26,7 @@ constexpr int RT_WARPS = RT_THREADS / 32;
 constexpr int64_t RT_BLOCKS = 608;    // blocks aimed at for a long batch: four on each of 152 SMs, one wave
 constexpr int64_t RT_MAX_E = 1024;
 constexpr int64_t RT_MAX_K = 64;
-constexpr int FIN_E = 8, FIN_SLOTS = 32;  // finishing kernel: experts per block, partial sums per expert
+constexpr int FIN_E = 4, FIN_SLOTS = 64;  // finishing kernel: experts per block, partial sums per expert
 
 template <typename T> __device__ __forceinline__ float up(T v);
 template <> __device__ __forceinline__ float up<float>(float v) { return v; }
@@ -105,6 +105,17 @@ __device__ __forceinline__ void write_loss(const volatile float* terms, int E, i
     if (lane == 0) *loss = v ? s * (static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(v))) : 0.0f;
 }
 
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of another block of the cluster, at this block's address of it.
+__device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
+    uint32_t at, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
 struct RouteArgs {
     uint32_t* ids;        // [T, k]
     float* weights;       // [T, k]
@@ -150,7 +161,7 @@ __global__ void __launch_bounds__(32 * W, W == RT_WARPS && V <= 8 ? 4 : 1) route
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    if (blockIdx.x == 0 && threadIdx.x == 0 && gridDim.x > 1) *a.ticket = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.ticket != nullptr) *a.ticket = 0;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -320,32 +331,50 @@ __global__ void __launch_bounds__(32 * W, W == RT_WARPS && V <= 8 ? 4 : 1) route
     __syncthreads();
     uint32_t v = 0;
     for (int w = 0; w < W; ++w) v += s_rows[w];
-    const bool alone = gridDim.x == 1;  // a short batch: this block's sums are the result
     for (int e = threadIdx.x; e < E; e += 32 * W) {
         float s = s_sum[0][e];
 #pragma unroll
         for (int w = 1; w < W; ++w) s += s_sum[w][e];
-        if (alone) {
-            const float m = v ? s / static_cast<float>(v) : 0.0f;
-            a.mean[e] = m;
-            a.counts[e] = s_cnt[e];
-            s_sum[0][e] = static_cast<float>(s_cnt[e]) * m;
-        } else {
+        if (a.psum != nullptr) {
             a.psum[static_cast<int64_t>(blockIdx.x) * E + e] = s;
             a.pcnt[static_cast<int64_t>(blockIdx.x) * E + e] = s_cnt[e];
+        } else {
+            s_sum[0][e] = s;
         }
     }
-    if (!alone) {
+    if (a.psum != nullptr) {
         if (threadIdx.x == 0) a.prow[blockIdx.x] = v;
         return;
     }
+    // a short batch: the grid is one block, or one cluster whose first block adds
+    // the others' sums, in order, from their shared memory
+    __shared__ uint32_t s_v;
+    if (threadIdx.x == 0) s_v = v;
     __syncthreads();
-    if (warp == 0) write_loss(s_sum[0], E, k, v, a.loss);
-    if (threadIdx.x == 0) *a.rows = v;
+    if (gridDim.x > 1) cluster_barrier();
+    if (blockIdx.x == 0) {
+        for (uint32_t b = 1; b < gridDim.x; ++b) v += remote_u32(&s_v, b);
+        for (int e = threadIdx.x; e < E; e += 32 * W) {
+            float s = s_sum[0][e];
+            uint32_t n = s_cnt[e];
+            for (uint32_t b = 1; b < gridDim.x; ++b) {
+                s += __uint_as_float(remote_u32(&s_sum[0][e], b));
+                n += remote_u32(&s_cnt[e], b);
+            }
+            const float m = v ? s / static_cast<float>(v) : 0.0f;
+            a.mean[e] = m;
+            a.counts[e] = n;
+            s_sum[0][e] = static_cast<float>(n) * m;
+        }
+        __syncthreads();
+        if (warp == 0) write_loss(s_sum[0], E, k, v, a.loss);
+        if (threadIdx.x == 0) *a.rows = v;
+    }
+    if (gridDim.x > 1) cluster_barrier();  // no block leaves while its sums may be read
 }
 
-// Adds the blocks' sums: 8 experts per block, 32 slots per expert (slot s takes
-// blocks s, s + 32, ... in order), the slots by a fixed tree.  The block that
+// Adds the blocks' sums: FIN_E experts per block, FIN_SLOTS slots each (slot s takes
+// blocks s, s + FIN_SLOTS, ... in order), the slots by a fixed tree.  The block that
 // finishes last (a ticket) adds the experts' terms of the loss, in order of e.
 __global__ void __launch_bounds__(FIN_E * FIN_SLOTS)
     route_finish_kernel(const float* psum, const uint32_t* pcnt, const uint32_t* prow, float* terms, uint32_t* ticket,
@@ -357,18 +386,32 @@ __global__ void __launch_bounds__(FIN_E * FIN_SLOTS)
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, slot = tid / FIN_E, i = tid % FIN_E, e = blockIdx.x * FIN_E + i;
+    // (at most RT_BLOCKS blocks: all loads of a thread in flight at once)
+    constexpr int ROW_TURNS = static_cast<int>((RT_BLOCKS + FIN_E * FIN_SLOTS - 1) / (FIN_E * FIN_SLOTS));
+    constexpr int TURNS = static_cast<int>((RT_BLOCKS + FIN_SLOTS - 1) / FIN_SLOTS);
     uint32_t v = 0;
-    for (int b = tid; b < blocks; b += FIN_E * FIN_SLOTS) v += prow[b];
+#pragma unroll
+    for (int q = 0; q < ROW_TURNS; ++q) {
+        const int b = tid + q * FIN_E * FIN_SLOTS;
+        v += b < blocks ? prow[b] : 0u;
+    }
+    float ps[TURNS];
+    uint32_t cs[TURNS];
+#pragma unroll
+    for (int q = 0; q < TURNS; ++q) {
+        const int b = slot + q * FIN_SLOTS;
+        const bool in = e < E && b < blocks;
+        ps[q] = in ? psum[static_cast<int64_t>(b) * E + e] : 0.0f;
+        cs[q] = in ? pcnt[static_cast<int64_t>(b) * E + e] : 0u;
+    }
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((tid & 31) == 0) s_v[tid >> 5] = v;
     float p = 0.0f;
     uint32_t c = 0;
-    if (e < E) {
-#pragma unroll 16
-        for (int b = slot; b < blocks; b += FIN_SLOTS) {
-            p += psum[static_cast<int64_t>(b) * E + e];
-            c += pcnt[static_cast<int64_t>(b) * E + e];
-        }
+#pragma unroll
+    for (int q = 0; q < TURNS; ++q) {
+        p += ps[q];
+        c += cs[q];
     }
     s_p[slot][i] = p;
     s_c[slot][i] = c;
@@ -559,24 +602,52 @@ cudaError_t with_layout(int64_t E, F&& f) {
 
 int64_t lanes_for(int64_t E) { return E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : E <= 64 ? 8 : 32; }
 
-// Rows per block: a whole number of block steps, about RT_BLOCKS blocks; up to
-// four steps of rows go to one block, which then needs no second kernel.
-int64_t rows_per_block(int64_t T, int64_t E) {
-    const int64_t step = RT_WARPS * (32 / lanes_for(E));
-    if (T <= 4 * step) return 4 * step;
-    const int64_t per = (T + RT_BLOCKS - 1) / RT_BLOCKS;
-    return lmax(1, (per + step - 1) / step) * step;
+// Warps of a block in the short-batch form, as far as 48 KB of shared memory go.
+constexpr int short_warps(int V) { return V <= 16 ? 16 : RT_WARPS; }
+int short_warps_for(int64_t E) { return E <= 512 ? short_warps(16) : short_warps(32); }
+
+// How the rows are dealt.  Up to SHORT_STEPS steps of one cluster of up to
+// SHORT_BLOCKS large blocks: one launch, the sums through the cluster's shared
+// memory (64 rows of 64 experts 7 us; 16384 rows of 8, with the gradient, 17.5 us
+// by two kernels).  Longer batches: about RT_BLOCKS blocks of RT_WARPS warps and a
+// second kernel that adds their sums.  Either way a function of T and E.
+struct Deal {
+    int64_t per, blocks;  // rows per block (whole block steps), blocks
+    bool is_short;
+};
+constexpr int64_t SHORT_BLOCKS = 8, SHORT_STEPS = 4;
+Deal deal_rows(int64_t T, int64_t E) {
+    const int64_t rows = 32 / lanes_for(E), step = short_warps_for(E) * rows;
+    if (T <= SHORT_BLOCKS * SHORT_STEPS * step) {
+        int64_t n = 1;  // a power of two: a cluster
+        while (n < SHORT_BLOCKS && n * step < T) n *= 2;
+        const int64_t per = (T + n * step - 1) / (n * step) * step;
+        return {per, n, true};
+    }
+    const int64_t small = RT_WARPS * rows, per = ((T + RT_BLOCKS - 1) / RT_BLOCKS + small - 1) / small * small;
+    return {per, (T + per - 1) / per, false};
 }
 
 template <typename T>
-cudaError_t forward_t(const LaunchCtx& c, const RouteArgs& a, int64_t blocks) {
+cudaError_t forward_t(const LaunchCtx& c, const RouteArgs& a, const Deal& d) {
     return with_layout(a.E, [&](auto l, auto v) {
-        // a lone block takes more warps, as far as its shared memory goes: fewer
-        // steps one after the other (64 rows of 64 experts: one instead of two)
-        constexpr int L = l.value, V = v.value, LONE = L * V <= 64 ? 32 : V <= 16 ? 16 : RT_WARPS;
-        return blocks == 1 ? launch_pdl(route_kernel<T, L, V, LONE>, dim3(1), dim3(32 * LONE), 0, c.stream, a)
-                           : launch_pdl(route_kernel<T, L, V, RT_WARPS>, dim3(static_cast<unsigned>(blocks)), dim3(RT_THREADS),
-                                        0, c.stream, a);
+        constexpr int L = l.value, V = v.value, W = short_warps(V);
+        if (!d.is_short)
+            return launch_pdl(route_kernel<T, L, V, RT_WARPS>, dim3(static_cast<unsigned>(d.blocks)), dim3(RT_THREADS), 0,
+                              c.stream, a);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(d.blocks));
+        cfg.blockDim = dim3(32 * W);
+        cfg.stream = c.stream;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = static_cast<unsigned>(d.blocks);
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = d.blocks > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, route_kernel<T, L, V, W>, a);
     });
 }
 
@@ -628,14 +699,15 @@ bi_status bi_router_forward(bi_engine eng, uint32_t* ids, float* weights, uint32
         if (err == cudaSuccess) err = cudaMemsetAsync(loss, 0, 4, s);
         return err == cudaSuccess ? BI_OK : cuda_fail(eng, err, "bi_router_forward");
     }
-    const int64_t per = rows_per_block(t, e), blocks = (t + per - 1) / per;
-    // scratch (more than one block): block sums | block counts | block rows | loss terms | ticket
-    Scratch sc(eng, s, blocks > 1 ? static_cast<size_t>(4 * (2 * blocks * e + blocks + e + 1)) : 0);
+    const Deal d = deal_rows(t, e);
+    const int64_t per = d.per, blocks = d.blocks;
+    // scratch (a long batch): block sums | block counts | block rows | loss terms | ticket
+    Scratch sc(eng, s, !d.is_short ? static_cast<size_t>(4 * (2 * blocks * e + blocks + e + 1)) : 0);
     if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "router scratch");
     RouteArgs a{};
     a.ids = ids; a.weights = weights; a.lse = lse; a.logits = logits; a.valid = valid;
     float* terms = nullptr;
-    if (blocks > 1) {
+    if (!d.is_short) {
         a.psum = static_cast<float*>(sc.ptr);
         a.pcnt = reinterpret_cast<uint32_t*>(a.psum + blocks * e);
         a.prow = a.pcnt + blocks * e;
@@ -646,10 +718,10 @@ bi_status bi_router_forward(bi_engine eng, uint32_t* ids, float* weights, uint32
     a.T = t; a.rows_per_block = per;
     a.E = static_cast<int>(e); a.k = static_cast<int>(k); a.normalize = normalize != 0;
     a.vec = row_vectors(logits, e, dtype);
-    err = dtype == BI_F32 ? forward_t<float>(c, a, blocks)
-        : dtype == BI_BF16 ? forward_t<__nv_bfloat16>(c, a, blocks) : forward_t<__half>(c, a, blocks);
+    err = dtype == BI_F32 ? forward_t<float>(c, a, d)
+        : dtype == BI_BF16 ? forward_t<__nv_bfloat16>(c, a, d) : forward_t<__half>(c, a, d);
     if (err == cudaSuccess) c.count();
-    if (err == cudaSuccess && blocks > 1) {
+    if (err == cudaSuccess && !d.is_short) {
         err = launch_pdl(route_finish_kernel, dim3(static_cast<unsigned>((e + FIN_E - 1) / FIN_E)),
                          dim3(FIN_E * FIN_SLOTS), 0, c.stream, a.psum, a.pcnt, a.prow, terms, a.ticket, counts, rows,
                          mean_prob, loss, static_cast<int>(blocks), a.E, a.k);

@@ -101,7 +101,7 @@ def exact(x, ok, k, normalize, dw=None, dl=0.0):
 
 CASES = [  # t, e, k
     (1, 1, 1), (1, 8, 2), (3, 4, 4), (64, 64, 6), (257, 60, 5), (1000, 8, 2), (130, 16, 16), (77, 32, 3), (300, 128, 8),
-    (5000, 256, 8), (100, 160, 64), (50, 500, 33), (40, 1024, 64), (33, 1000, 7)]
+    (5000, 256, 8), (100, 160, 64), (40000, 8, 2), (9000, 64, 6), (20000, 16, 3), (700, 256, 8), (50, 500, 33), (40, 1024, 64), (33, 1000, 7)]
 
 
 @pytest.mark.parametrize("normalize", [0, 1])
@@ -222,8 +222,8 @@ def test_empty_and_refusals(eng):
                                  4, 8, 2, 1, "f32") == bi.BI_ERR_INVALID_ARG
     assert bi.bi_router_forward(None, *[16] * 9, 1, 1, 1, 1, "f32", 0) == bi.BI_ERR_INVALID_ARG
     bi.bi_engine_fail_allocations(eng.handle, 1)  # a batch of several blocks takes scratch
-    q, big = outputs(5000, 8, 2), torch.randn(5000, 8, device="cuda")
-    assert bi.bi_router_forward(eng.handle, *[q[v] for v in NAMES], big, None, 5000, 8, 2, 1, "f32") == bi.BI_ERR_OOM
+    q, big = outputs(50000, 8, 2), torch.randn(50000, 8, device="cuda")
+    assert bi.bi_router_forward(eng.handle, *[q[v] for v in NAMES], big, None, 50000, 8, 2, 1, "f32") == bi.BI_ERR_OOM
     bi.bi_engine_fail_allocations(eng.handle, 0)
     assert (q["ids"] == -7).all()
 
