@@ -229,10 +229,8 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     narrow_finish_tc_kernel(const __grid_constant__ FinishJobs jobs, const uint32_t* ids, const float* scales, int64_t M, int R,
                             int rp, uint32_t G, int pieces, int per_row) {
-    // the dependents first: a small-tile product starts on the shared weight while
-    // h is still in the making, and waits for this kernel before it reads it
-    grid_dep_launch();
     grid_dep_wait();
+    grid_dep_launch();
     const FinishJob& jb = jobs.job[blockIdx.y];
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= M * per_row) return;
@@ -616,38 +614,6 @@ bi_status check_adapter(bi_engine eng, bi_dtype dt, int64_t m, int64_t k, int64_
     return BI_OK;
 }
 
-// Work on the engine's side stream beside the caller's.  mark() notes what it may
-// start after; begin() makes the side stream wait for that; join(), always reached
-// before the call's scratch is freed, makes the caller's stream wait for the side.
-struct Side {
-    bi_engine eng;
-    cudaStream_t main;
-    cudaEvent_t fork = nullptr, done = nullptr;
-    bool begun = false;
-    Side(bi_engine e, cudaStream_t s) : eng(e), main(s) {}
-    cudaError_t mark() {
-        cudaError_t e = cudaEventCreateWithFlags(&fork, cudaEventDisableTiming);
-        if (e == cudaSuccess) e = cudaEventCreateWithFlags(&done, cudaEventDisableTiming);
-        return e == cudaSuccess ? cudaEventRecord(fork, main) : e;
-    }
-    cudaError_t begin() {
-        const cudaError_t e = cudaStreamWaitEvent(eng->side, fork, 0);
-        begun = e == cudaSuccess;
-        return e;
-    }
-    cudaError_t join() {
-        if (!begun) return cudaSuccess;
-        begun = false;
-        const cudaError_t e = cudaEventRecord(done, eng->side);
-        return e == cudaSuccess ? cudaStreamWaitEvent(main, done, 0) : e;
-    }
-    ~Side() {
-        join();
-        if (fork) cudaEventDestroy(fork);
-        if (done) cudaEventDestroy(done);
-    }
-};
-
 // Cuts of one scratch allocation.
 struct Cut {
     int64_t at = 0;
@@ -716,26 +682,21 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
     float* hs = reinterpret_cast<float*>(p + o_hs);
     float* base = dtype == BI_F32 ? static_cast<float*>(y) : reinterpret_cast<float*>(p + o_base);
     // the shared product first: it may need scratch of its own, and a call that
-    // gets none must leave nothing enqueued; h on the side stream beside it
-    Side side(eng, s);
-    cudaError_t e = side.mark();
-    if (e == cudaSuccess && dtype == BI_F32) {
+    // gets none must leave nothing enqueued
+    cudaError_t e = cudaSuccess;
+    if (dtype == BI_F32) {
         st = adapter_projection_f32(eng, c, 0, y, x, w, bias, m, k, n, tensor_cores);
         if (st != BI_OK) return st;
-    } else if (e == cudaSuccess) {
+    } else {
         e = scalar_rows(c, dtype, base, x, w, bias, m, k, n, 0, 1);
     }
-    const LaunchCtx cs = ctx(eng, eng->side);
-    if (e == cudaSuccess) e = side.begin();
     if (e == cudaSuccess)
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return narrow_scalar<T>(cs, static_cast<const T*>(x), static_cast<const T*>(a), row_adapters, part, m, k, R, g);
+            return narrow_scalar<T>(c, static_cast<const T*>(x), static_cast<const T*>(a), row_adapters, part, m, k, R, g);
         });
     const bool fuse = pieces * r <= WIDE_FUSE;
-    if (e == cudaSuccess && !fuse) e = narrow_finish(cs, part, row_adapters, scales, h, hs, m, R, g, pieces);
-    const cudaError_t joined = side.join();
-    if (e == cudaSuccess) e = joined;
+    if (e == cudaSuccess && !fuse) e = narrow_finish(c, part, row_adapters, scales, h, hs, m, R, g, pieces);
     if (e == cudaSuccess)
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
@@ -791,15 +752,11 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         uint32_t* perm = reinterpret_cast<uint32_t*>(p + o_perm);
         const AdapterChunks ch = AdapterChunks::at(p + o_ch, g);
         float* sums = reinterpret_cast<float*>(p + o_sum);
-        // the rows are sorted for dA and dB on the side stream, beside the narrow product
-        Side side(eng, s);
-        cudaError_t e = grads ? side.mark() : cudaSuccess;
-        if (e == cudaSuccess && grads) e = side.begin();
-        if (e == cudaSuccess && grads) {
-            const LaunchCtx cs = ctx(eng, eng->side);
-            e = segment(cs, row_adapters, m, g, seg, perm, p + o_hist);
+        cudaError_t e = cudaSuccess;
+        if (grads) {  // the rows sorted by adapter, for dA and dB
+            e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
             if (e == cudaSuccess) {
-                e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, cs.stream, seg, static_cast<uint32_t>(g), ch);
+                e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, static_cast<uint32_t>(g), ch);
                 if (e == cudaSuccess) c.count();
             }
         }
@@ -810,8 +767,6 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
             if (e == cudaSuccess) e = narrow_finish_tc(c, dtype, u, db ? &hs : nullptr, row_adapters, scales, m, R, g, pieces);
         }
         if (e == cudaSuccess && dx) e = tc_adapter_rows(c, dtype, 1, dx, dy, w, nullptr, p + o_uu, a, plan, m, k, n, R, g);
-        const cudaError_t joined = side.join();
-        if (e == cudaSuccess) e = joined;
         if (e == cudaSuccess && db && !need_u) {
             const FinishJob hs{nullptr, h, nullptr, nullptr, p + o_h3};
             e = narrow_finish_tc(c, dtype, hs, nullptr, row_adapters, scales, m, R, g, 0);
@@ -850,32 +805,27 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     float* sums = reinterpret_cast<float*>(p + o_sum);
     float* base = dtype == BI_F32 ? static_cast<float*>(dx) : reinterpret_cast<float*>(p + o_base);
     const uint32_t G = static_cast<uint32_t>(g);
-    Side side(eng, s);
-    cudaError_t e = side.mark();
-    if (e == cudaSuccess && dx && dtype == BI_F32) {  // first, as in the forward
+    cudaError_t e = cudaSuccess;
+    if (dx && dtype == BI_F32) {  // first, as in the forward
         st = adapter_projection_f32(eng, c, 1, dx, dy, w, nullptr, m, k, n, tensor_cores);
         if (st != BI_OK) return st;
-    } else if (e == cudaSuccess && dx) {
+    } else if (dx) {
         e = scalar_rows(c, dtype, base, dy, w, nullptr, m, n, k, 1, 1);
     }
-    const LaunchCtx cs = ctx(eng, eng->side);
-    if (e == cudaSuccess) e = side.begin();  // u, and the rows sorted by adapter
     if (e == cudaSuccess && need_u) {
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;
-            return narrow_scalar<T>(cs, static_cast<const T*>(dy), static_cast<const T*>(b), row_adapters, part, m, n, R, g);
+            return narrow_scalar<T>(c, static_cast<const T*>(dy), static_cast<const T*>(b), row_adapters, part, m, n, R, g);
         });
-        if (e == cudaSuccess) e = narrow_finish(cs, part, row_adapters, scales, nullptr, u, m, R, g, pieces);
+        if (e == cudaSuccess) e = narrow_finish(c, part, row_adapters, scales, nullptr, u, m, R, g, pieces);
     }
     if (e == cudaSuccess && grads) {
-        e = segment(cs, row_adapters, m, g, seg, perm, p + o_hist);
+        e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
         if (e == cudaSuccess) {
-            e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, cs.stream, seg, G, ch);
+            e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, G, ch);
             if (e == cudaSuccess) c.count();
         }
     }
-    const cudaError_t joined = side.join();
-    if (e == cudaSuccess) e = joined;
     if (e == cudaSuccess && dx) {
         e = with_type(dtype, [&](auto* t) {
             using T = std::remove_pointer_t<decltype(t)>;

@@ -319,11 +319,10 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
 // epilogue warps add them up and lay them out in shared memory themselves, in the
 // finish kernel's order, and the first CTA of the row writes h: one launch less.
 //
-// The base product needs nothing of the kernels just before this one (plan,
-// narrow product, finish), so it starts under them (programmatic launch): only
-// the adapters' part waits for the previous kernel (grid_dep_wait), and x and w
-// are complete because the plan kernel waited for whatever wrote them before
-// anything that depends on it could start.
+// The base product needs nothing of the kernel just before this one, so it starts
+// under it (programmatic launch): only the adapters' part waits for that kernel
+// (grid_dep_wait).  x and w are complete, because the narrow product (and the
+// finish kernel) waited for whatever came before it ere it let this one start.
 constexpr int SM_THREADS = 192, SM_COLS = 64, SM_B = 64 * 128, SM_MAX_STAGES = 12;
 constexpr int SM_BARS = 2 * SM_MAX_STAGES + 3;
 constexpr int SM_TAIL = SM_BARS * 8 + 16 + 128 * 4 + 128 * 16 + 64;  // barriers, slots, adapter list and masks
