@@ -608,8 +608,8 @@ int short_warps_for(int64_t E) { return E <= 512 ? short_warps(16) : short_warps
 
 // How the rows are dealt.  Up to SHORT_STEPS steps of one cluster of up to
 // SHORT_BLOCKS large blocks: one launch, the sums through the cluster's shared
-// memory (64 rows of 64 experts 7 us; 16384 rows of 8, with the gradient, 17.5 us
-// by two kernels).  Longer batches: about RT_BLOCKS blocks of RT_WARPS warps and a
+// memory (64 rows of 64 experts 7 us; 16384 rows of 8, with the gradient, 13.5 us
+// against 17.5 with a second kernel).  Longer batches: about RT_BLOCKS blocks of RT_WARPS warps and a
 // second kernel that adds their sums.  Either way a function of T and E.
 struct Deal {
     int64_t per, blocks;  // rows per block (whole block steps), blocks
