@@ -322,7 +322,9 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
 // The base product needs nothing of the kernel just before this one, so it starts
 // under it (programmatic launch): only the adapters' part waits for that kernel
 // (grid_dep_wait).  x and w are complete, because the narrow product (and the
-// finish kernel) waited for whatever came before it ere it let this one start.
+// finish kernel) waited for whatever came before it ere it let this one start: this
+// kernel is launched behind one of these two only.  The kernel behind it is let in
+// after that wait, like everywhere.
 constexpr int SM_THREADS = 192, SM_COLS = 64, SM_B = 64 * 128, SM_MAX_STAGES = 12;
 constexpr int SM_BARS = 2 * SM_MAX_STAGES + 3;
 constexpr int SM_TAIL = SM_BARS * 8 + 16 + 128 * 4 + 128 * 16 + 64;  // barriers, slots, adapter list and masks
@@ -400,7 +402,6 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
-    grid_dep_launch();
 
     if (warp == 0) {
         // the whole warp runs this: lane 0 expects a stage's bytes, then a lane for
@@ -520,6 +521,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
         const int w = warp & 3;
         if (warp == 2) {  // the adapters of this half of the plan tile, in the plan's order
             grid_dep_wait();
+            grid_dep_launch();
             const int64_t tile = blockIdx.y >> 1;
             const int half = blockIdx.y & 1;
             const uint32_t n = p.plan.count[tile];

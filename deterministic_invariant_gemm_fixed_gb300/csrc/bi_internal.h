@@ -51,8 +51,13 @@ struct PerDeviceOnce {
 // scheduled while the previous kernel in its stream is still finishing.  It
 // must call grid_dep_wait() before touching global memory (that waits for the
 // previous kernel to complete and its writes to be visible); grid_dep_launch()
-// lets the kernel after it be scheduled early in turn.  Both are no-ops for a
-// kernel launched the ordinary way.
+// lets the kernel after it be scheduled early in turn, and is called after
+// grid_dep_wait() only: then no more than two kernels of a stream are ever under
+// way at once, and what a kernel finds complete is complete for the ones after it.
+// Both are no-ops for a kernel launched the ordinary way.  One kernel reads before
+// its wait, the adapters' small tiles (adapter_tc.cu): the shared operands, which
+// were complete when the kernel before it, always the adapters' narrow product or
+// its finish, passed its own wait.
 #ifdef __CUDACC__
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
