@@ -67,13 +67,18 @@ __device__ __forceinline__ void mma_block(uint32_t d_tmem, uint32_t a, uint32_t 
         "r"(a), "r"(ahi), "r"(astep), "r"(b), "r"(bhi), "r"(bstep), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
 }
-// A producer that gives up waits (a bounded number of tries) for the copies it
-// has issued before its CTA's shared memory goes away: the last min(issued,
-// stages) fills, fill f on stage f % stages in phase f / stages.
+// Before a CTA that gave up (a wait ran out) lets its shared memory go, it waits for
+// the copies it has issued: the last min(issued, stages) fills, fill f on stage f %
+// stages in phase f / stages.
 template <typename Bar>
 __device__ __forceinline__ void drain_copies(Bar&& full_bar, int issued, int stages) {
-    for (int f = max(0, issued - stages); f < issued; ++f)
-        for (int i = 0; i < (1 << 20) && !mbar_try_wait(full_bar(f % stages), (f / stages) & 1); ++i) {}
+    for (int f = max(0, issued - stages); f < issued; ++f) mbar_drain(full_bar(f % stages), (f / stages) & 1);
+}
+// The MMAs issued by the electing lane have finished before the CTA goes on.
+template <typename P>
+__device__ __forceinline__ void drain_mmas(uint32_t bar, uint32_t lead, volatile int* abort_flag, const P& p) {
+    mma_commit(bar, lead);
+    if (!mbar_wait_fast(bar, 0, abort_flag, p, DEV_TIMEOUT_MMA)) mbar_drain(bar, 0);
 }
 
 // ---------------------------------------------------------------- narrow product
@@ -159,6 +164,7 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     const int rg = p.rp / 16;  // groups of 16 ranks per adapter
     const int pieces = (p.num_kb + NP_KB - 1) / NP_KB;  // this CTA's: blockIdx.y, + gridDim.y, ...
+    int fills = 0;  // stages the producer has filled
     auto piece_blocks = [&](int piece) { return min(NP_KB, p.num_kb - piece * NP_KB); };
 
     if (warp == 0) {  // a lane for each of a stage's copies, as in the small tiles' kernel below
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
         __syncwarp();
         const bool listed = __all_sync(0xffffffffu, mbar_wait_fast(list_bar, 0, abort_flag, p, DEV_TIMEOUT_PRODUCER));
         const int groups = listed ? static_cast<int>(*s_count) * rg : 0, batches = (groups + 3) / 4;
-        int s = 0, fills = 0;
+        int s = 0;
         uint32_t ph = 0;
         if (static_cast<int>(blockIdx.z) >= batches && lane == 0) {  // nothing to multiply: let the early copies land
             for (int kb = 0; kb < early; ++kb) mbar_expect_tx(full_bar(kb), 0);
@@ -188,10 +194,8 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
             for (int kb = 0; kb < nkb; ++kb) {
                 const uint32_t a = sbase + s * NP_STAGE;
                 const bool have_x = fills < early;
-                if (!have_x && !__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER))) {
-                    if (lane == 0) drain_copies(full_bar, fills, NP_STAGES);
+                if (!have_x && !__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER)))
                     goto done_p;
-                }
                 if (lane == 0) mbar_expect_tx(full_bar(s), (have_x ? 0 : NP_A) + n * 2048);
                 __syncwarp();
                 if (!have_x && lane == 4) tma_load_2d(a, &tmX, (kb0 + kb) * BK, row0, full_bar(s));
@@ -228,8 +232,7 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     done_m:
         // the MMAs issued above have finished before the CTA leaves, and with
         // them the copies they waited for
-        mma_commit(drain_bar, lead);
-        mbar_wait_fast(drain_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        drain_mmas(drain_bar, lead, abort_flag, p);
     } else if (warp >= 2) {
         const int w = warp & 3;  // the TMEM lanes a warp may read
         auto sync4 = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag != 0 && threadIdx.x == 0) drain_copies(full_bar, fills, NP_STAGES);
     if (warp == 1) {
         tc_fence_after();
         tmem_free<128>(tmem_base);
@@ -402,12 +406,14 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
+    int issued = 0;  // stages the producer has filled
+    bool h_issued = false;
 
     if (warp == 0) {
         // the whole warp runs this: lane 0 expects a stage's bytes, then a lane for
         // each of its copies issues them side by side (one lane issuing four copies
         // per stage, with their addresses, took 0.2 us a copy)
-        int s = 0, issued = 0;
+        int s = 0;
         uint32_t ph = 0;
         bool ok = true;
         auto claim = [&](uint32_t bytes) {  // the next stage, free and expecting `bytes`
@@ -435,7 +441,8 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             grid_dep_wait();
             const int steps = static_cast<int>(*s_count) * rg;
             if (p.resident && steps) {
-                if (p.partial == nullptr && lane == 0) {
+                h_issued = p.partial == nullptr;
+                if (h_issued && lane == 0) {
                     mbar_expect_tx(h_bar, p.resident * p.a_bytes);
                     for (int c = 0; c < p.resident; ++c) tma_load_2d(hbase + c * A_BYTES, &tmH, c * 64, row0, h_bar);
                 }
@@ -461,7 +468,6 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 }
             }
         }
-        if (!ok && lane == 0) drain_copies(full_bar, issued, stages);
     } else if (warp == 1) {
         const uint32_t idesc = instr_desc(FMT, false, B_MN, SM_COLS, AR), idesc_q = instr_desc(FMT, false, true, SM_COLS, AR);
         // the whole warp runs this, one lane issues: warp-uniform code keeps the
@@ -515,8 +521,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             }
         }
         __syncwarp();
-        mma_commit(done_bar, lead);
-        mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        drain_mmas(done_bar, lead, abort_flag, p);
     } else if (warp >= 2) {
         const int w = warp & 3;
         if (warp == 2) {  // the adapters of this half of the plan tile, in the plan's order
@@ -646,6 +651,10 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag != 0 && threadIdx.x == 0) {
+        drain_copies(full_bar, issued, stages);
+        if (h_issued) mbar_drain(h_bar, 0);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_free<64>(tmem_base);
@@ -745,16 +754,15 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
     grid_dep_wait();
     grid_dep_launch();
+    int issued = 0;  // stages the producer has filled
     if (warp == 0) {  // a lane for each of a block's four copies
         const CUtensorMap* map = lane == 0 ? &tmAh : lane == 1 ? &tmBh : lane == 2 ? &tmAl : &tmBl;
         const uint32_t to = sbase + (lane == 0 ? A_HI : lane == 1 ? B_HI : lane == 2 ? A_LO : B_LO);
         int s = 0;
         uint32_t ph = 0;
         for (int kb = 0; kb < p.num_kb; ++kb) {
-            if (!__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER))) {
-                if (lane == 0) drain_copies(full_bar, kb, SF_STAGES);
-                break;
-            }
+            if (!__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, p, DEV_TIMEOUT_PRODUCER))) break;
+            ++issued;
             if (lane == 0) mbar_expect_tx(full_bar(s), SF_STAGE);
             __syncwarp();
             if (lane < 4) tma_load_2d(to + s * SF_STAGE, map, kb * 32, lane & 1 ? col0 : row0, full_bar(s));
@@ -781,8 +789,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             mma_commit(empty_bar(s), lead);
             if (++s == SF_STAGES) { s = 0; ph ^= 1u; }
         }
-        mma_commit(done_bar, lead);
-        mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        drain_mmas(done_bar, lead, abort_flag, p);
     } else if (warp >= 2) {
         const int w = warp & 3;
         bool ok = mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
@@ -819,6 +826,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag != 0 && threadIdx.x == 0) drain_copies(full_bar, issued, SF_STAGES);
     if (warp == 1) {
         tc_fence_after();
         tmem_free<128>(tmem_base);
@@ -1013,8 +1021,7 @@ __global__ void __launch_bounds__(GT_THREADS, gt_ctas(RUN)) grad_tc_kernel(const
             mma_commit(empty_bar(s), lead);
             if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
-        mma_commit(done_bar, lead);
-        mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_MMA);
+        drain_mmas(done_bar, lead, abort_flag, p);
     }
     __syncwarp();
     tc_fence_before();

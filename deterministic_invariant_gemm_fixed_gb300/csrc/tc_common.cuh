@@ -68,6 +68,15 @@ static __device__ __noinline__ bool mbar_wait_impl(uint32_t bar, uint32_t parity
 #define mbar_wait_fast(bar, parity, abort_flag, p, code) \
     (mbar_try_wait((bar), (parity)) || mbar_wait((bar), (parity), (abort_flag), p, (code)))
 
+// A wait for what is in flight, by a CTA that gives up: nothing but the time ends it
+// early (the abort flag is up already, and the limit of the ordinary waits may have
+// been set to nearly nothing).
+constexpr unsigned long long DRAIN_LIMIT_NS = 2000000000ull;
+static __device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 <= DRAIN_LIMIT_NS) {}
+}
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -33,3 +33,11 @@ def test_dependents_start_after_the_wait(path):
         if launch >= 0:
             wait = body.find("grid_dep_wait()")
             assert 0 <= wait < launch, name
+
+
+def test_waits_are_bounded():
+    """Every loop on a barrier's try_wait stands in one of the helpers that watch the clock."""
+    for path in glob.glob(os.path.join(CSRC, "*.cu")):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for line in text.split("\n"):
+            assert not ("mbar_try_wait(" in line and re.search(r"\b(for|while)\b", line)), (os.path.basename(path), line)
