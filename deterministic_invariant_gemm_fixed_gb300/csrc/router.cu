@@ -462,8 +462,10 @@ struct RouteBackArgs {
 // chosen logits, so their part, w (dw - sum w dw), is added to dL instead.  The
 // chosen experts' values reach the lanes that own them through one row of
 // shared memory per row group (kept zero between rows).  Probabilities are
-// recomputed from the row's log-sum-exp: the pass reads the logits and writes
-// their gradient, nothing else of that size.
+// recomputed from the row, with its maximum and its sum, as in the forward: the pass
+// reads the logits and writes their gradient, nothing else of that size.  (From the
+// log-sum-exp they would be off by its rounding: 2^-24 of the logits' size, 2e-2 of
+// the gradient at logits of 1e6.)  The log-sum-exp says which rows were left out.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(RT_THREADS) route_back_kernel(const RouteBackArgs a) {
     constexpr int GROUPS = 32 / L;
@@ -512,8 +514,19 @@ __global__ void __launch_bounds__(RT_THREADS) route_back_kernel(const RouteBackA
         const float lse = lse_next;
         const bool counted = lse != INFINITY;  // false: the forward left the row out
         float p[V], d[V], dot = 0.0f;
+        float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = counted ? exp2_approx((raw.get(i) - lse) * LOG2E) : 0.0f;
+        for (int i = 0; i < V; ++i) top = fmaxf(top, raw.get(i));
+        top = group_max<L>(top);
+        const float m = top > -INFINITY ? top : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = exp2_approx((raw.get(i) - m) * LOG2E);
+            sum += p[i];
+        }
+        const float inv = __fdividef(1.0f, group_sum<L>(sum));
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = counted ? p[i] * inv : 0.0f;
         lse_next = t + stride < a.T ? a.lse[t + stride] : INFINITY;
         raw.load(logits + (t + stride) * E, e0, E, a.vec != 0, t + stride < a.T);
         float ex[V];

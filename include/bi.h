@@ -338,7 +338,7 @@ bi_status bi_adapter_backward(bi_engine engine, void* dx, float* da, float* db, 
  * left out; id E is a padding row for the grouped calls, which take ids as
  * [T*k].  A row of -inf alone is left out too; a row with a NaN or +inf counts
  * and its probabilities are NaN.  lse [T] f32 = log-sum-exp of the row (+inf
- * for a row left out), for the backward.  counts [E] and rows [1] (= V) are
+ * for a row left out, which is what the backward reads from it).  counts [E] and rows [1] (= V) are
  * u32, mean_prob [E], loss [1] and weights [T,k] f32.  V = 0 gives a loss of 0.
  * Sums over rows are f32 in a fixed order (a function of T and E):
  * bit-identical run to run. */

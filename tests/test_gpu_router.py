@@ -256,3 +256,51 @@ def test_large_logits(eng, e):
     assert o["weights"].tolist() == [[1.0, 0.0], [0.5, 0.5], [1.0, 0.0]]
     d = route_back(eng, y, o, torch.ones(3, 2, device="cuda"), torch.ones(1, device="cuda"), 2, 0)
     assert torch.isfinite(d).all()
+
+
+def _exact_gradient_check(x, valid, o, d, dw, dl, k, normalize, dtype):
+    """d against 64 bits, for probabilities from differences of logits: no term grows with the logits themselves."""
+    t, e = x.shape
+    x64 = x.double().cpu().numpy()
+    r = exact(x64, valid, k, normalize, dw.double().cpu().numpy(), float(dl.item()))
+    fin = np.where(np.isfinite(x64), x64, x64.max(1, keepdims=True))
+    # beyond 104 below the maximum a probability is under 2^-149 in either case
+    span = float(np.minimum(fin.max(1) - fin.min(1), 104.0).max())
+    grel = 2 * (2 * span + e + 8) * U + 16 * U + e * U
+    got = d.double().cpu().numpy()
+    tol = 4 * grel * r["mag"] + 1e-38 + (0.5 * ulp_of(np.maximum(abs(got), abs(r["d"])), dtype) if dtype != "f32" else 0.0)
+    assert (abs(got - r["d"]) <= tol).all(), float((abs(got - r["d"]) / tol).max())
+
+
+@pytest.mark.parametrize("normalize", [0, 1])
+@pytest.mark.parametrize("dtype,shift,step", [("f32", 1.0e4, 1.0), ("f32", -1.0e6, 1.0), ("f32", 1.0e7, 1.0),
+                                              ("bf16", 1024.0, 8.0), ("f16", 8192.0, 8.0)])
+@pytest.mark.parametrize("e,k", [(8, 2), (64, 6), (200, 8), (1000, 40)])
+def test_gradient_does_not_depend_on_a_shift_of_the_logits(eng, e, k, dtype, shift, step, normalize):
+    """Logits whose sums with the shift are exact: differences, hence probabilities and gradients, are the same bits."""
+    gen = torch.Generator(device="cuda").manual_seed(e + k)
+    x = (torch.randint(0, 5, (70, e), device="cuda", generator=gen) * step).to(TD[dtype])
+    y = (x.double() + shift).to(TD[dtype])
+    assert torch.equal(y.double() - shift, x.double())
+    dw = torch.randn(70, k, device="cuda", generator=gen)
+    dl = torch.tensor([0.7], device="cuda")
+    out = []
+    for v in (x, y):
+        o = route(eng, v, None, k, normalize)
+        out.append(route_back(eng, v, o, dw, dl, k, normalize))
+        _exact_gradient_check(v, np.ones(70, bool), o, out[-1], dw, dl, k, normalize, dtype)
+    assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("normalize", [0, 1])
+@pytest.mark.parametrize("e", [8, 64, 200])
+def test_gradient_of_the_largest_logits(eng, e, normalize):
+    """Two experts tied at 3e38 have probability 1/2 each, in the gradient too."""
+    y = torch.full((3, e), -3.0e38, device="cuda")
+    y[:, 5] = 3.0e38
+    y[1, 6] = 3.0e38
+    dw = torch.tensor([[1.0, 1.0], [1.0, -2.0], [0.5, 3.0]], device="cuda")
+    dl = torch.tensor([0.5], device="cuda")
+    o = route(eng, y, None, 2, normalize)
+    d = route_back(eng, y, o, dw, dl, 2, normalize)
+    _exact_gradient_check(y, np.ones(3, bool), o, d, dw, dl, 2, normalize, "f32")
