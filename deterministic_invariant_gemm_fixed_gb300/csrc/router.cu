@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(RT_THREADS) route_back_kernel(const RouteBackA
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float g = p[i] * (d[i] - dot);
-            d[i] = a.normalize ? g + ex[i] : g;
+            d[i] = counted ? (a.normalize ? g + ex[i] : g) : 0.0f;  // (0 * dloss is no 0 for every dloss)
         }
         if (!in) continue;
         T* out = static_cast<T*>(a.dlogits) + t * E + e0;

@@ -304,3 +304,21 @@ def test_gradient_of_the_largest_logits(eng, e, normalize):
     o = route(eng, y, None, 2, normalize)
     d = route_back(eng, y, o, dw, dl, 2, normalize)
     _exact_gradient_check(y, np.ones(3, bool), o, d, dw, dl, 2, normalize, "f32")
+
+
+@pytest.mark.parametrize("normalize", [0, 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dloss", [-1.0, float("inf"), float("nan")])
+@pytest.mark.parametrize("e,k", [(8, 2), (60, 5), (256, 8)])
+def test_rows_left_out_get_plus_zero(eng, e, k, dloss, dtype, normalize):
+    """Whatever the loss's gradient is (an overflowed loss scale), the gradient of a row left out is +0, bit for bit."""
+    x = torch.randn(40, e, device="cuda").to(TD[dtype])
+    x[7] = float("-inf")
+    valid = torch.ones(40, dtype=torch.uint8, device="cuda")
+    valid[::3] = 0
+    o = route(eng, x, valid, k, normalize)
+    d = route_back(eng, x, o, torch.randn(40, k, device="cuda"), torch.tensor([dloss], device="cuda"), k, normalize)
+    out = valid == 0
+    out[7] = True
+    bits = d.view(torch.int32 if dtype == "f32" else torch.int16)
+    assert not bits[out].any()
