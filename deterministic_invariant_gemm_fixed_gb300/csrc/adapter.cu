@@ -23,6 +23,7 @@
 
 #include "abi_util.h"
 #include "adapter.h"
+#include "adapter_parts.cuh"
 
 namespace bi {
 namespace {
@@ -186,9 +187,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // The same for the tensor cores: v = the pieces' sums (row stride rp), or h_in;
-// h = v; then s_g v in two parts (hh, for the wide product) and in four (v4, for
-// dA and dB), any of them nullable.  A part that would be an infinity's
-// remainder is 0, so an infinity stays one.  One thread per row and 8 ranks
+// h = v; then s_g v in two parts (hh, for the wide product; `over` gets a bit for a
+// row that they cannot carry) and in four (v4, for dA and dB), any of them nullable.
+// A part that would be an infinity's remainder is 0, so an infinity stays one.  One
+// thread per row and 8 ranks
 // (16-byte stores) up to the formats' padded width (zeros past R); block row y
 // does job y.
 struct FinishJob {
@@ -227,8 +229,8 @@ __device__ __forceinline__ void four_parts(float s, T (&part)[4]) {
 }
 template <typename T>
 __global__ void __launch_bounds__(256)
-    narrow_finish_tc_kernel(const __grid_constant__ FinishJobs jobs, const uint32_t* ids, const float* scales, int64_t M, int R,
-                            int rp, uint32_t G, int pieces, int per_row) {
+    narrow_finish_tc_kernel(const __grid_constant__ FinishJobs jobs, const uint32_t* ids, const float* scales, uint32_t* over,
+                            int64_t M, int R, int rp, uint32_t G, int pieces, int per_row) {
     grid_dep_wait();
     grid_dep_launch();
     const FinishJob& jb = jobs.job[blockIdx.y];
@@ -243,24 +245,7 @@ __global__ void __launch_bounds__(256)
     for (int u = 0; u < 8; ++u) v[u] = 0.0f;
     if (g < G && r0 < R) {
         if (jb.partial != nullptr) {  // rp - r0 is a multiple of 8: whole vectors
-            const float* p = jb.partial + m * rp + r0;
-            const int64_t step = M * rp;
-            for (int q0 = 0; q0 < pieces; q0 += 4) {  // four pieces' loads in flight
-                float4 a[4], b[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q0 + q >= pieces) break;
-                    a[q] = reinterpret_cast<const float4*>(p + (q0 + q) * step)[0];
-                    b[q] = reinterpret_cast<const float4*>(p + (q0 + q) * step)[1];
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q0 + q >= pieces) break;
-                    const float t[8] = {a[q].x, a[q].y, a[q].z, a[q].w, b[q].x, b[q].y, b[q].z, b[q].w};
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) v[u] = q0 + q == 0 ? t[u] : v[u] + t[u];
-                }
-            }
+            sum_pieces8(jb.partial + m * rp + r0, M * rp, pieces, v);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 if (r0 + u >= R) v[u] = 0.0f;
@@ -280,14 +265,11 @@ __global__ void __launch_bounds__(256)
     for (int u = 0; u < 8; ++u) v[u] *= scale;
     __align__(16) T out[4][8];
     if (jb.hh != nullptr && r0 < (R + 31) / 32 * 32) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            out[0][u] = down<T>(v[u]);
-            out[1][u] = down<T>(part_rest<T>(v[u], out[0][u], 1.0f));
-        }
+        uint32_t hi[4], lo[4];
+        if (two_parts8<std::is_same<T, __half>::value ? 0 : 1>(v, hi, lo)) atomicOr(over + (m >> 5), 1u << (m & 31));
         T* o = static_cast<T*>(jb.hh) + m * ((R + 31) / 32 * 64) + (r0 / 32) * 64 + r0 % 32;
-        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(out[0]);
-        *reinterpret_cast<uint4*>(o + 32) = *reinterpret_cast<const uint4*>(out[1]);
+        *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(o + 32) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     const int run = adapter_rank_run(R);
     if (jb.v4 != nullptr && r0 < (R + 63) / 64 * run) {
@@ -581,16 +563,16 @@ cudaError_t grad_sum(const LaunchCtx& c, const AdapterGradJob* jobs, int count, 
 
 // One or two jobs over the same rows: the second's partial is null.
 cudaError_t narrow_finish_tc(const LaunchCtx& c, bi_dtype dt, const FinishJob& a, const FinishJob* b, const uint32_t* ids,
-                             const float* scales, int64_t M, int R, int64_t G, int pieces) {
+                             const float* scales, uint32_t* over, int64_t M, int R, int64_t G, int pieces) {
     const FinishJobs jobs{{a, b ? *b : FinishJob{}}};
     const int rp = (R + 15) / 16 * 16;
     const bool hh = a.hh || (b && b->hh), v4 = a.v4 || (b && b->v4);
     const int per_row = static_cast<int>(lmax(hh ? (R + 31) / 32 * 32 : rp, v4 ? (R + 63) / 64 * adapter_rank_run(R) : rp)) / 8;
     const dim3 grid(static_cast<unsigned>((M * per_row + 255) / 256), b ? 2 : 1);
     const cudaError_t e =
-        dt == BI_BF16 ? launch_pdl(narrow_finish_tc_kernel<__nv_bfloat16>, grid, dim3(256), 0, c.stream, jobs, ids, scales, M, R,
-                                   rp, static_cast<uint32_t>(G), pieces, per_row)
-                      : launch_pdl(narrow_finish_tc_kernel<__half>, grid, dim3(256), 0, c.stream, jobs, ids, scales, M, R, rp,
+        dt == BI_BF16 ? launch_pdl(narrow_finish_tc_kernel<__nv_bfloat16>, grid, dim3(256), 0, c.stream, jobs, ids, scales, over, M,
+                                   R, rp, static_cast<uint32_t>(G), pieces, per_row)
+                      : launch_pdl(narrow_finish_tc_kernel<__half>, grid, dim3(256), 0, c.stream, jobs, ids, scales, over, M, R, rp,
                                    static_cast<uint32_t>(G), pieces, per_row);
     if (e == cudaSuccess) c.count();
     return e;
@@ -660,15 +642,16 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
         const AdapterPlan plan = AdapterPlan::at(p + o_plan, m);
         float* part = reinterpret_cast<float*>(p + o_part);
         cudaError_t e = tc_adapter_narrow(c, dtype, part, x, a, row_adapters, plan, m, k, R, g);
+        const AdapterPieces src{part, row_adapters, scales, h, pieces};
         if (adapter_small_fuses(c, m, n, k, R)) {
-            const AdapterPieces fuse{part, row_adapters, scales, h, pieces};
             if (e == cudaSuccess)
-                e = tc_adapter_rows_small(c, dtype, 0, y, x, w, bias, nullptr, b, plan, m, k, n, R, g, &fuse);
+                e = tc_adapter_rows_small(c, dtype, 0, y, x, w, bias, nullptr, b, plan, src, m, k, n, R, g, true);
             return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
         }
         if (e == cudaSuccess)
-            e = narrow_finish_tc(c, dtype, {part, nullptr, h, p + o_hh, nullptr}, nullptr, row_adapters, scales, m, R, g, pieces);
-        if (e == cudaSuccess) e = tc_adapter_rows(c, dtype, 0, y, x, w, bias, p + o_hh, b, plan, m, k, n, R, g);
+            e = narrow_finish_tc(c, dtype, {part, nullptr, h, p + o_hh, nullptr}, nullptr, row_adapters, scales, plan.over, m, R,
+                                 g, pieces);
+        if (e == cudaSuccess) e = tc_adapter_rows(c, dtype, 0, y, x, w, bias, p + o_hh, b, plan, src, m, k, n, R, g);
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
     }
     // scratch: pieces of h | s h | the shared product in f32 (16-bit types)
@@ -764,12 +747,15 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
             e = tc_adapter_narrow(c, dtype, part, dy, b, row_adapters, plan, m, n, R, g);
             const FinishJob u{part, nullptr, nullptr, dx ? p + o_uu : nullptr, da ? p + o_u3 : nullptr};
             const FinishJob hs{nullptr, h, nullptr, nullptr, p + o_h3};
-            if (e == cudaSuccess) e = narrow_finish_tc(c, dtype, u, db ? &hs : nullptr, row_adapters, scales, m, R, g, pieces);
+            if (e == cudaSuccess) e = narrow_finish_tc(c, dtype, u, db ? &hs : nullptr, row_adapters, scales, plan.over, m, R, g,
+                                                      pieces);
         }
-        if (e == cudaSuccess && dx) e = tc_adapter_rows(c, dtype, 1, dx, dy, w, nullptr, p + o_uu, a, plan, m, k, n, R, g);
+        if (e == cudaSuccess && dx)
+            e = tc_adapter_rows(c, dtype, 1, dx, dy, w, nullptr, p + o_uu, a, plan, {part, row_adapters, scales, nullptr, pieces}, m,
+                                k, n, R, g);
         if (e == cudaSuccess && db && !need_u) {
             const FinishJob hs{nullptr, h, nullptr, nullptr, p + o_h3};
-            e = narrow_finish_tc(c, dtype, hs, nullptr, row_adapters, scales, m, R, g, 0);
+            e = narrow_finish_tc(c, dtype, hs, nullptr, row_adapters, scales, nullptr, m, R, g, 0);
         }
         if (e == cudaSuccess && grads) {
             AdapterGradJob jobs[2];

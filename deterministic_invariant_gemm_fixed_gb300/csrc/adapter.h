@@ -17,19 +17,20 @@ constexpr int64_t ADAPTER_CHUNK = 1024;
 constexpr int ADAPTER_TILE = 256;  // rows per plan tile
 
 // Which adapters the rows of each 256-row tile have: per tile the number of
-// distinct ones, and for each its index and a bit
-// per row.
+// distinct ones, and for each its index and a bit per row.
 struct AdapterPlan {
     uint32_t* count;  // [tiles]
     uint32_t* ids;    // [tiles][256]
     uint32_t* masks;  // [tiles][256][8]
+    uint32_t* over;   // [tiles][8] a bit per row: an inner product of it is beyond f16 (adapter_parts.cuh)
     static int64_t tiles(int64_t M) { return (M + ADAPTER_TILE - 1) / ADAPTER_TILE; }
-    static int64_t words(int64_t M) { return tiles(M) * (1 + 256 + 256 * 8); }
+    static int64_t words(int64_t M) { return tiles(M) * (1 + 256 + 256 * 8 + 8); }
     static AdapterPlan at(void* p, int64_t M) {
         AdapterPlan r;
         r.masks = static_cast<uint32_t*>(p);  // 16-byte aligned masks first
         r.ids = r.masks + tiles(M) * 256 * 8;
-        r.count = r.ids + tiles(M) * 256;
+        r.over = r.ids + tiles(M) * 256;
+        r.count = r.over + tiles(M) * 8;
         return r;
     }
 };
@@ -54,7 +55,8 @@ struct AdapterChunks {
 
 // Tensor-core formats of an inner product v (h or u, scaled), 16-bit.
 // Two parts, for the wide product: row m holds per 32 ranks 32 high parts and 32
-// remainders, v ~ hi + lo (bf16: to 2^-17 of v, f16: to 2^-22 or 2^-25).
+// remainders, v ~ hi + lo (bf16: to 2^-17 of v, f16: to 2^-22 of v or, for small
+// ones, 2^-25; beyond f16's 65504 both are 0 and the epilogue adds the term).
 inline int64_t adapter_part_cols(int64_t R) { return (R + 31) / 32 * 64; }
 // Four parts, for dA and dB: row m holds per 64 ranks four runs of rank_run
 // columns whose products are summed apart.  bf16: v = p1 + p2 + p3, together f32's
@@ -66,26 +68,27 @@ inline int64_t adapter_part_cols(int64_t R) { return (R + 31) / 32 * 64; }
 __host__ __device__ inline int adapter_rank_run(int R) { return R > 64 ? 64 : (R + 15) / 16 * 16; }
 __host__ __device__ inline int64_t adapter_grad_cols(int R) { return (R + 63) / 64 * 4 * adapter_rank_run(R); }
 
+// The narrow product's pieces, and what makes h (u) of them.
+struct AdapterPieces {
+    const float* partial;
+    const uint32_t* ids;
+    const float* scales;
+    float* h;  // fused small tiles only: receives the unscaled sums (nullable)
+    int pieces;
+};
 // The wide product on the tensor cores: forward (dx = 0) or dX with the shared
 // product, its bias and the adapters' terms in one pass (tc.cu).
 cudaError_t tc_adapter_rows(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
-                            const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
-                            int64_t K, int64_t N, int R, int64_t G);
+                            const void* bias, const void* hh, const void* q, const AdapterPlan& plan,
+                            const AdapterPieces& src, int64_t M, int64_t K, int64_t N, int R, int64_t G);
 // The same by 128 x 64 tiles on single CTAs (adapter_tc.cu): identical bits, for
 // outputs that the 256 x 256 tiles of CTA pairs spread over too few SMs.
 bool adapter_small_tiles(const LaunchCtx& c, int64_t M, int64_t C);
 // ... and whether they also add up the pieces of h (then no finish kernel runs).
 bool adapter_small_fuses(const LaunchCtx& c, int64_t M, int64_t C, int64_t L, int R);
-struct AdapterPieces {
-    const float* partial;
-    const uint32_t* ids;
-    const float* scales;
-    float* h;
-    int pieces;
-};
 cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
-                                  const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
-                                  int64_t K, int64_t N, int R, int64_t G, const AdapterPieces* fuse = nullptr);
+                                  const void* bias, const void* hh, const void* q, const AdapterPlan& plan,
+                                  const AdapterPieces& src, int64_t M, int64_t K, int64_t N, int R, int64_t G, bool fuse);
 // The shared product of f32 adapters, as bi_forward / bi_backward_dx compute it
 // (engine.cu), with the 3xTF32 tiles chosen by their number: single CTAs' 128 x
 // 64 tiles (adapter_tc.cu; contractions up to one piece) give the same bits.

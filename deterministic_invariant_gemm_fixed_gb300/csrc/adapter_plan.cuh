@@ -136,6 +136,7 @@ __device__ __forceinline__ void plan_store(const AdapterPlan& plan, int64_t tile
     uint4* masks = reinterpret_cast<uint4*>(plan.masks + tile * ADAPTER_TILE * 8);
     for (int i = tid; i < 2 * n; i += threads) masks[i] = sm.masks[sm.slot[i >> 1]][i & 1];
     for (int i = tid; i < n; i += threads) plan.ids[tile * ADAPTER_TILE + i] = sm.ids[i];
+    if (tid < 8) plan.over[tile * 8 + tid] = 0;  // set by the finish kernel
     if (tid == 0) plan.count[tile] = sm.count;
 }
 

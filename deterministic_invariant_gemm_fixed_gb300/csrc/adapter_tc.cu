@@ -2,6 +2,7 @@
 // adapters' gradients.  The wide product runs inside the projection's own kernel
 // (tc.cu, mode ADAPTER).
 #include "adapter.h"
+#include "adapter_parts.cuh"
 #include "adapter_plan.cuh"
 #include "tc_common.cuh"
 
@@ -331,19 +332,17 @@ __global__ void __launch_bounds__(NP_THREADS, 2)
 // after that wait, like everywhere.
 constexpr int SM_THREADS = 192, SM_COLS = 64, SM_B = 64 * 128, SM_MAX_STAGES = 12;
 constexpr int SM_BARS = 2 * SM_MAX_STAGES + 3;
-constexpr int SM_TAIL = SM_BARS * 8 + 16 + 128 * 4 + 128 * 16 + 64;  // barriers, slots, adapter list and masks
+constexpr int SM_TAIL = SM_BARS * 8 + 16 + 128 * 4 + 128 * 16 + 64;  // barriers, slots, adapter list and masks, rows beyond f16
 
 struct SmallParams {
     AdapterPlan plan;
     void* out;
     const void* bias;
     int64_t M, C;
-    const float* partial;  // fused: the pieces of h [pieces][M][rp], and what makes s h of them
-    const uint32_t* ids;
-    const float* scales;
-    float* h;
+    AdapterFar far;  // the pieces of h and what makes s h of them (fused), and the terms beyond f16
+    float* h;        // fused
     uint32_t G;
-    int pieces, rp;
+    int fused;
     int a_bytes;  // of one A tile's rows that exist (a multiple of 8 rows)
     int R, num_kb, stages, resident;  // resident: 32-rank parts of h kept in shared memory (0: streamed)
     int* status;
@@ -386,6 +385,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     // per adapter of this half the accumulator lanes that are not its rows', and its index
     uint4* s_off = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 15) & ~uintptr_t(15));
     uint32_t* s_id = reinterpret_cast<uint32_t*>(s_off + 128);
+    uint32_t* s_over = s_id + 128;  // fused: a bit per row with a rank beyond f16
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int row0 = static_cast<int>(blockIdx.y) * 128, col0 = static_cast<int>(blockIdx.x) * SM_COLS;
     const int rg = (p.R + 15) / 16;
@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
         mbar_init(h_bar, 1);
         mbar_init(list_bar, 1);
         *abort_flag = 0;
+        for (int i = 0; i < 4; ++i) s_over[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<64>(smem_u32(tmem_slot));
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             grid_dep_wait();
             const int steps = static_cast<int>(*s_count) * rg;
             if (p.resident && steps) {
-                h_issued = p.partial == nullptr;
+                h_issued = !p.fused;
                 if (h_issued && lane == 0) {
                     mbar_expect_tx(h_bar, p.resident * p.a_bytes);
                     for (int c = 0; c < p.resident; ++c) tma_load_2d(hbase + c * A_BYTES, &tmH, c * 64, row0, h_bar);
@@ -557,51 +558,34 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             }
             __syncwarp();
         }
-        if (p.partial != nullptr) {  // s h of the tile's rows, 8 ranks (16 bytes of each part) per thread and turn
+        constexpr int RPW = AR / 4;  // rows per warp: 32, or 16 in the first lanes of a 64-row tile's
+        const int64_t row = row0 + RPW * w + lane;
+        uint32_t over = 0;  // f16: this lane's row has terms beyond the MMAs'
+        if (FMT == 0 && !p.fused) {
+            grid_dep_wait();
+            if (row < p.M) over = p.far.over[row >> 5];
+        }
+        if (p.fused) {  // s h of the tile's rows, 8 ranks (16 bytes of each part) per thread and turn
             grid_dep_wait();
             const int per_row = p.resident * 4;
             const int rows = static_cast<int>(lmin(AR, p.M - row0));
             for (int i = threadIdx.x - 64; i < rows * per_row; i += 128) {
                 const int row = i / per_row, r0 = (i % per_row) * 8;
-                const uint32_t g = p.ids[row0 + row];
+                const uint32_t g = p.far.ids[row0 + row];
                 float v[8], sv[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = 0.0f;
-                if (g < p.G && r0 < p.rp) {
-                    const float* src = p.partial + static_cast<int64_t>(row0 + row) * p.rp + r0;
-                    const int64_t step = p.M * p.rp;
-                    for (int q0 = 0; q0 < p.pieces; q0 += 4) {  // four pieces' loads in flight
-                        float4 a[4], b[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (q0 + q >= p.pieces) break;
-                            a[q] = reinterpret_cast<const float4*>(src + (q0 + q) * step)[0];
-                            b[q] = reinterpret_cast<const float4*>(src + (q0 + q) * step)[1];
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (q0 + q >= p.pieces) break;
-                            const float t[8] = {a[q].x, a[q].y, a[q].z, a[q].w, b[q].x, b[q].y, b[q].z, b[q].w};
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) v[u] = q0 + q == 0 ? t[u] : v[u] + t[u];
-                        }
-                    }
-                }
-                const float s = g < p.G && p.scales != nullptr ? p.scales[g] : 1.0f;
-                uint32_t w_hi[4], w_lo[4];
+                if (g < p.G && r0 < p.far.rp)
+                    sum_pieces8(p.far.partial + static_cast<int64_t>(row0 + row) * p.far.rp + r0, p.M * p.far.rp, p.far.pieces, v);
+                const float s = g < p.G && p.far.scales != nullptr ? p.far.scales[g] : 1.0f;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     if (r0 + u >= p.R) v[u] = 0.0f;  // ranks past R hold zeros of the padded rows
                     else if (p.h != nullptr && blockIdx.x == 0) p.h[static_cast<int64_t>(row0 + row) * p.R + r0 + u] = v[u];
                     sv[u] = v[u] * s;
                 }
-#pragma unroll
-                for (int u = 0; u < 8; u += 2) {
-                    w_hi[u / 2] = OutT<FMT>::pack(sv[u], sv[u + 1]);
-                    const typename OutT<FMT>::T* t = reinterpret_cast<const typename OutT<FMT>::T*>(&w_hi[u / 2]);
-                    const float h0 = OutT<FMT>::load(t, 0), h1 = OutT<FMT>::load(t, 1);
-                    w_lo[u / 2] = OutT<FMT>::pack(isinf(h0) ? 0.0f : sv[u] - h0, isinf(h1) ? 0.0f : sv[u + 1] - h1);
-                }
+                uint32_t w_hi[4], w_lo[4];
+                if (two_parts8<FMT>(sv, w_hi, w_lo)) atomicOr(&s_over[row >> 5], 1u << (row & 31));
                 const uint32_t at = hbase + (r0 / 32) * A_BYTES + row * 128;
                 const uint32_t c = (r0 % 32) / 8;  // 16-byte piece of the high parts; the remainders' is 4 on
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((c ^ (row & 7)) * 16)), "r"(w_hi[0]),
@@ -612,15 +596,15 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             fence_proxy_async_smem();
             asm volatile("bar.sync 1, 128;" ::: "memory");
             if (threadIdx.x == 64) mbar_arrive(h_bar);
+            if (FMT == 0) over = s_over[(row - row0) >> 5];
         }
+        const bool far = ((over >> (row & 31)) & 1u) != 0;
         bool ok = mbar_wait_fast(done_bar, 0, abort_flag, p, DEV_TIMEOUT_EPILOGUE);
         ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
         if (ok) {
             tc_fence_after();
             using O = OutT<FMT>;
             using T = typename O::T;
-            constexpr int RPW = AR / 4;  // rows per warp: 32, or 16 in the first lanes of a 64-row tile's
-            const int64_t row = row0 + RPW * w + lane;
             T* dst = static_cast<T*>(p.out) + row * p.C + col0;
             if (row0 + RPW * w < p.M) {
 #pragma unroll
@@ -632,8 +616,17 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                         float f[16];
                         const int have = static_cast<int>(lmin(16, p.C - col0 - c));  // 8 or 16
 #pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+                        if (FMT == 0 && far) {
+                            float t[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) t[i] = f[i];
+                            add_far_terms(p.far, row, col0 + c, t);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) f[i] = t[i];
+                        }
+#pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            f[i] = __uint_as_float(v[i]);
                             if (p.bias != nullptr && i < have) f[i] = __fadd_rn(f[i], O::load(p.bias, col0 + c + i));
                         }
 #pragma unroll
@@ -1097,8 +1090,8 @@ bool adapter_small_fuses(const LaunchCtx& c, int64_t M, int64_t C, int64_t L, in
 }
 
 cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
-                                  const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
-                                  int64_t K, int64_t N, int R, int64_t G, const AdapterPieces* fuse) {
+                                  const void* bias, const void* hh, const void* q, const AdapterPlan& plan,
+                                  const AdapterPieces& src, int64_t M, int64_t K, int64_t N, int R, int64_t G, bool fuse) {
     const int64_t L = dx ? N : K, C = dx ? K : N;
     const uint32_t ar = static_cast<uint32_t>(lmin(128, (M + 7) / 8 * 8));
     CUtensorMap mx, mw, mh, mq;
@@ -1108,11 +1101,9 @@ cudaError_t tc_adapter_rows_small(const LaunchCtx& c, bi_dtype dt, int dx, void*
     if (!fuse && (e = make_map(&mh, dt, hh, adapter_part_cols(R), M, 1, ar)) != cudaSuccess) return e;
     if ((e = make_map(&mq, dt, q, C, R, G, 16, true)) != cudaSuccess) return e;
     SmallParams p{};
-    if (fuse) {
-        mh = mx;  // not read
-        p.partial = fuse->partial; p.ids = fuse->ids; p.scales = fuse->scales; p.h = fuse->h;
-        p.G = static_cast<uint32_t>(G); p.pieces = fuse->pieces; p.rp = (R + 15) / 16 * 16;
-    }
+    if (fuse) mh = mx;  // not read
+    p.far = {src.partial, src.ids, src.scales, q, plan.over, M, C, src.pieces, (R + 15) / 16 * 16, R};
+    p.h = src.h; p.G = static_cast<uint32_t>(G); p.fused = fuse;
     p.plan = plan; p.out = out; p.bias = bias; p.M = M; p.C = C; p.R = R; p.a_bytes = static_cast<int>(ar) * 128;
     p.num_kb = static_cast<int>((L + BK - 1) / BK);
     p.status = c.status; p.wait_limit = c.wait_limit_ns;

@@ -29,6 +29,7 @@
 #include <cuda_fp8.h>
 
 #include "adapter.h"
+#include "adapter_parts.cuh"
 #include "tc_common.cuh"
 
 namespace bi {
@@ -61,6 +62,7 @@ struct Params {
     float* partials;         // ... whose f32 results go here, 256 x BN per (tile, chunk)
     AdapterPlan plan;        // adapter passes: the adapters of each 256-row tile
     int rank;
+    AdapterFar far;          // ... and in f16 the terms that the two parts of h cannot carry
     int* status;
     unsigned long long wait_limit;
 };
@@ -752,6 +754,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             : 0.0f;
             }
             static_assert(BN <= 8 * 32, "one 8-column bias slice per lane");
+            bool far = false;  // this row has terms beyond f16
+            if (MODE == ADAPTER && IN == 0) far = orow >= 0 && ((p.far.over[orow >> 5] >> (orow & 31)) & 1u) != 0;
           for (int pc = 0; pc < u.npiece; ++pc) {
             int pkb0, pnkb;
             unit_piece<MODE>(u, pc, pkb0, pnkb);
@@ -804,6 +808,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < 16; ++i) f[i] = __fmul_rn(f[i], scale);
                 }
                 const int64_t cb = col0 + c0;
+                if (MODE == ADAPTER && IN == 0 && far && cb < p.cols) {
+                    float t[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) t[i] = f[i];
+                    add_far_terms(p.far, orow, cb, t);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] = t[i];
+                }
                 if (OUT == 2 && add_prev && orow >= 0) {  // the earlier pieces' sum, left in the output
                     const float* prev = static_cast<const float*>(out) + orow * p.ldo + cb;
 #pragma unroll
@@ -1180,8 +1192,8 @@ cudaError_t dx_impl(const LaunchCtx& c, bi_dtype dt, void* dx, const void* dy, c
 // inner products in two parts, q the adapters' [G,R,C].
 template <int FMT>
 cudaError_t adapter_rows_t(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
-                           const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
-                           int64_t K, int64_t N, int R, int64_t G) {
+                           const void* bias, const void* hh, const void* q, const AdapterPlan& plan,
+                           const AdapterPieces& src, int64_t M, int64_t K, int64_t N, int R, int64_t G) {
     const int64_t L = dx ? N : K, C = dx ? K : N;
     CUtensorMap a, b, a2, b2, o;
     cudaError_t e;
@@ -1193,6 +1205,7 @@ cudaError_t adapter_rows_t(const LaunchCtx& c, bi_dtype dt, int dx, void* out, c
     Params p{};
     p.out = out; p.ldo = C; p.rows = M; p.cols = C; p.bias = bias;
     p.plan = plan; p.rank = R;
+    p.far = {src.partial, src.ids, src.scales, q, plan.over, M, C, src.pieces, (R + 15) / 16 * 16, R};
     p.num_m = static_cast<int>((M + BM - 1) / BM);
     p.num_n = static_cast<int>((C + BN - 1) / BN);
     p.num_kb = static_cast<int>((L + BK - 1) / BK);
@@ -1488,12 +1501,12 @@ cudaError_t tc_dx(const LaunchCtx& c, bi_dtype dt, void* dx, const void* dy, con
 }
 
 cudaError_t tc_adapter_rows(const LaunchCtx& c, bi_dtype dt, int dx, void* out, const void* z, const void* w,
-                            const void* bias, const void* hh, const void* q, const AdapterPlan& plan, int64_t M,
-                            int64_t K, int64_t N, int R, int64_t G) {
+                            const void* bias, const void* hh, const void* q, const AdapterPlan& plan,
+                            const AdapterPieces& src, int64_t M, int64_t K, int64_t N, int R, int64_t G) {
     if (forced_cols(c) == 0 && adapter_small_tiles(c, M, dx ? K : N))
-        return tc_adapter_rows_small(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G);
-    return dt == BI_BF16 ? adapter_rows_t<1>(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G)
-                         : adapter_rows_t<0>(c, dt, dx, out, z, w, bias, hh, q, plan, M, K, N, R, G);
+        return tc_adapter_rows_small(c, dt, dx, out, z, w, bias, hh, q, plan, src, M, K, N, R, G, false);
+    return dt == BI_BF16 ? adapter_rows_t<1>(c, dt, dx, out, z, w, bias, hh, q, plan, src, M, K, N, R, G)
+                         : adapter_rows_t<0>(c, dt, dx, out, z, w, bias, hh, q, plan, src, M, K, N, R, G);
 }
 
 int64_t tc_dw_workspace_bytes(const LaunchCtx& c, int dw_f32, int64_t M, int64_t K, int64_t N) {

@@ -304,9 +304,19 @@ bi_status bi_grouped_forward_noalloc(void* y, const void* x, const void* w,
  * halves of 512 rows), the chunks in order;
  * run-to-run identical.  The tiers and their conditions are those of bi_forward
  * (forward) and bi_backward_dx (backward).  On the tensor-core tier with 16-bit
- * operands h and u enter the second product as two 16-bit parts (high part and
- * remainder); with f16 a magnitude of s_g h or u beyond 65504 is not
- * representable there and gives an infinity. */
+ * operands s_g h and u enter the second product as two 16-bit parts (high part and
+ * remainder): to 2^-17 of the value with bf16, with f16 to 2^-22 of it or, for
+ * small ones, 2^-25 absolute.  With f16 a magnitude beyond 65504 enters as the f32
+ * value itself (added in f32 FMAs after the others: correct, but slow where most
+ * rows have such).  dA and dB take u and s_g h in four parts: f32's 24 bits, with f16 up
+ * to 2^27, beyond which they are infinite.  A non-finite operand of a row, or of its
+ * adapter, makes that row's results non-finite (an infinity or NaN).
+ *
+ * Scratch, taken from the engine's pool for the call: on the tensor cores about
+ * 4 ceil(L/512) M R bytes (L = K forward, N backward; R rounded up to 16) besides 37
+ * bytes a row and the parts (4 bytes per row and rank for the second product, 8 for
+ * each of dA and dB); in plain f32 the same pieces and, with 16-bit operands, the shared
+ * product in f32. */
 
 /* h (nullable) receives X A^T unscaled, which the backward's dB needs. */
 bi_status bi_adapter_forward(bi_engine engine, void* y, float* h, const void* x, const void* w, const void* bias,

@@ -401,3 +401,103 @@ def test_calls_back_to_back_on_one_buffer(eng):
             eng.adapter_forward(bufs[i % 2], None, src, d["w"], None, d["a"], d["b"], d["scales"], d["ids"], *sizes(d))
             src = bufs[i % 2]
         assert torch.equal(src, want[-1]), rep
+
+
+def far_inputs(m, k, n, r, g, seed, which):
+    """f16 whose inner products s h ("y") or u ("dx") pass 65504 in many places while the results stay finite."""
+    d = inputs(m, k, n, r, g, "f16", seed=seed, order="random", none=0.1)
+    rng = np.random.default_rng(seed + 1)
+    powers = rng.choice([0, 14, 17, 20], size=g)
+    powers[0] = 20
+    d["scales"] = torch.from_numpy((2.0 ** powers).astype(np.float32)).cuda()
+    if which == "y":  # h about 1: s h up to some 2^22, B about 2^-11
+        d["b"] = (torch.from_numpy(rng.standard_normal((g, r, n))) * 2.0 ** -11).half().cuda()
+    else:  # dY B^T about 1, A about 2^-11
+        d["b"] = (torch.from_numpy(rng.standard_normal((g, r, n))) * n ** -0.5).half().cuda()
+        d["a"] = (torch.from_numpy(rng.standard_normal((g, r, k))) * 2.0 ** -11).half().cuda()
+    return d
+
+
+FAR = [(1, 512, 256, 16, 2), (37, 1032, 328, 20, 9), (65, 264, 72, 8, 3), (200, 520, 640, 100, 30), (300, 64, 64, 33, 40), (1500, 128, 2048, 16, 6)]
+
+
+@pytest.mark.parametrize("which", ["y", "dx"])
+@pytest.mark.parametrize("m,k,n,r,g", FAR)
+def test_inner_products_beyond_f16(eng, m, k, n, r, g, which):
+    """s h and u are f32 values: those that f16 cannot hold count in full, and by any tile with the same bits.
+
+    Bound: 2e-6 S twice (the two products), 2^-21 of the inner terms and 2^-24 r max|Q|
+    for the remainders' own rounding, terms beyond f16 in f32 FMAs (r roundings), half an ulp."""
+    d = far_inputs(m, k, n, r, g, m + k, which)
+    if which == "y":
+        got, h = forward(eng, d, 1)
+        e = exact(d, h)
+        want, s, inner, q = e["y"], e["y_s"], e["y_in"], d["b"]
+        v = abs(e["h"]) * f64(torch.cat([d["scales"], d["scales"][:1]]))[np.minimum(d["ids"].cpu().numpy().view(np.uint32), g)][:, None]
+        if m > 1:
+            assert v.max() > 2.0 ** 18
+    else:
+        got = backward(eng, d, None, 1, ("dx",))[0]
+        e = exact(d)
+        want, s, inner, q = e["dx"], e["dx_s"], e["dx_in"], d["a"]
+    keep = abs(want) < 6.0e4
+    assert keep.mean() > 0.5
+    tol = 4e-6 * s + 2.0 ** -21 * inner + 2.0 ** -24 * r * float(q.abs().max()) + (r + 4) * U * inner
+    tol = tol + 0.5 * ulp_of(np.maximum(abs(f64(got)), abs(want)), "f16")
+    assert (abs(f64(got) - want) <= tol)[keep].all()
+    bi.bi_engine_set_tile_cols(eng.handle, 256)
+    try:
+        other = forward(eng, d, 1)[0] if which == "y" else backward(eng, d, None, 1, ("dx",))[0]
+    finally:
+        bi.bi_engine_set_tile_cols(eng.handle, 0)
+    assert torch.equal(got, other)
+    for lo, hi in ((0, 1), (m // 2, m)):  # rows alone
+        p = dict(d, m=hi - lo, x=d["x"][lo:hi].contiguous(), dy=d["dy"][lo:hi].contiguous(), ids=d["ids"][lo:hi].contiguous())
+        part = forward(eng, p, 1)[0] if which == "y" else backward(eng, p, None, 1, ("dx",))[0]
+        assert torch.equal(part, got[lo:hi])
+
+
+def test_zeros_beside_an_inner_product_beyond_f16(eng):
+    """A finite s h times 0 is 0, whatever its size."""
+    m, k, n, r, g = 5, 64, 128, 4, 1
+    d = inputs(m, k, n, r, g, "f16", seed=2, none=0.0)
+    d["bias"] = None
+    d["w"].zero_()
+    d["scales"] = torch.tensor([2.0 ** 16], device="cuda")
+    d["x"].fill_(0)
+    d["x"][:, 0] = 100.0
+    d["a"].fill_(0)
+    d["a"][:, :, 0] = 1.0  # s h = 100 * 2^16
+    d["b"].fill_(0)
+    d["b"][0, 0, :64] = 2.0 ** -14
+    y, _ = forward(eng, d, 1)
+    assert torch.equal(y, torch.cat([torch.full((m, 64), 400.0, device="cuda"), torch.zeros(m, 64, device="cuda")], 1).half())
+
+
+@pytest.mark.parametrize("which", ["y", "dx"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [3, 100, 300])
+def test_inner_products_keep_both_parts(eng, m, dtype, which):
+    """Whole numbers throughout: inner products of 22 bits (f16; bf16 16) that f32 holds exactly and that
+    cancel down to 2 z, so a bit lost in the remainder shows as it is."""
+    k = n = 64
+    rng = np.random.default_rng(m)
+    big, unit = (32.0, 2.0 ** -6) if dtype == "f16" else (256.0, 1.0)
+    rows = np.zeros((m, k))
+    rows[:, 0] = rng.integers(1, 2000 if dtype == "f16" else 255, size=m)
+    rows[:, 1] = rng.integers(1, 2000 if dtype == "f16" else 127, size=m) * unit
+    narrow, wide = np.zeros((1, 2, k)), np.zeros((1, 2, k))
+    narrow[0, 0, :2], narrow[0, 1, :2] = (big, 1.0), (big, -1.0)
+    wide[0, 0], wide[0, 1] = 1.0, -1.0
+    t = lambda v: torch.from_numpy(v).to(TD[dtype]).cuda()
+    d = dict(x=t(rows), dy=t(rows), w=t(np.zeros((k, n))), bias=None, scales=None, m=m, k=k, n=n, r=2, g=1, dtype=dtype,
+             a=t(narrow if which == "y" else wide), b=t(wide if which == "y" else narrow),
+             ids=torch.zeros(m, dtype=torch.int32, device="cuda"))
+    want = t(np.repeat(2 * rows[:, 1:2], 64, 1))
+    for cols in (0, 256):
+        bi.bi_engine_set_tile_cols(eng.handle, cols)
+        try:
+            got = forward(eng, d, 1)[0] if which == "y" else backward(eng, d, None, 1, ("dx",))[0]
+        finally:
+            bi.bi_engine_set_tile_cols(eng.handle, 0)
+        assert torch.equal(got, want)
