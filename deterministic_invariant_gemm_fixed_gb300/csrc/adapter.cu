@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(256)
     }
     const float scale = g < G && scales != nullptr ? scales[g] : 1.0f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] *= scale;
+    for (int u = 0; u < 8; ++u) v[u] = r0 + u < R ? v[u] * scale : 0.0f;  // (0 times an infinite scale is no padding)
     __align__(16) T out[4][8];
     if (jb.hh != nullptr && r0 < (R + 31) / 32 * 32) {
         uint32_t hi[4], lo[4];

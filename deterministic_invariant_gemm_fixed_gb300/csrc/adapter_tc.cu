@@ -580,9 +580,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 const float s = g < p.G && p.far.scales != nullptr ? p.far.scales[g] : 1.0f;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    if (r0 + u >= p.R) v[u] = 0.0f;  // ranks past R hold zeros of the padded rows
-                    else if (p.h != nullptr && blockIdx.x == 0) p.h[static_cast<int64_t>(row0 + row) * p.R + r0 + u] = v[u];
-                    sv[u] = v[u] * s;
+                    const bool is_rank = r0 + u < p.R;  // past R the padding stays 0 whatever the scale
+                    if (is_rank && p.h != nullptr && blockIdx.x == 0) p.h[static_cast<int64_t>(row0 + row) * p.R + r0 + u] = v[u];
+                    sv[u] = is_rank ? v[u] * s : 0.0f;
                 }
                 uint32_t w_hi[4], w_lo[4];
                 if (two_parts8<FMT>(sv, w_hi, w_lo)) atomicOr(&s_over[row >> 5], 1u << (row & 31));

@@ -501,3 +501,22 @@ def test_inner_products_keep_both_parts(eng, m, dtype, which):
         finally:
             bi.bi_engine_set_tile_cols(eng.handle, 0)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,tc", [("f32", 0), ("bf16", 0), ("bf16", 1), ("f16", 1)])
+@pytest.mark.parametrize("m", [5, 300])
+def test_an_infinite_scale_reaches_no_padding(eng, m, dtype, tc):
+    """Every term of the row is the same infinity: ranks that only pad a vector (rank 4 of 16) add nothing to it."""
+    k, n, r = 64, 128, 4
+    d = inputs(m, k, n, r, 1, dtype, seed=2, none=0.0)
+    for v, c in (("w", 0.0), ("x", 1.0), ("dy", 1.0), ("a", 1.0), ("b", -1.0)):
+        d[v].fill_(c)
+    d["scales"] = torch.tensor([float("inf")], device="cuda")
+    y, h = forward(eng, d, tc)
+    assert (y == float("-inf")).all() and (h == k).all()
+    assert (backward(eng, d, h, tc, ("dx",))[0] == float("-inf")).all()  # u = -inf, A = 1
+    bi.bi_engine_set_tile_cols(eng.handle, 256)
+    try:
+        assert torch.equal(forward(eng, d, tc)[0], y)
+    finally:
+        bi.bi_engine_set_tile_cols(eng.handle, 0)
