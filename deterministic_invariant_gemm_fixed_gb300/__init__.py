@@ -288,12 +288,18 @@ def bi_router_backward(engine, dlogits, logits, lse, ids, weights, counts, rows,
 
 class TensorSet:
     """A set of tensors as bi_grad_norm and bi_grad_clip take it: the host arrays
-    of device pointers, element counts and dtypes.  Holds its tensors, so the
-    pointers stay valid; a program whose gradient buffers persist makes one set
-    and uses it every step."""
+    of device pointers, element counts and dtypes.  A program whose gradient
+    buffers persist makes one set and uses it every step.  The set holds its
+    tensors, and a tensor whose storage was replaced or resized since (`.data =`,
+    `set_`, `resize_`) is looked up again by the next call (0.1 us a tensor)."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
+        self._ptr_of = [t.data_ptr for t in self.tensors]
+        self._count_of = [t.numel for t in self.tensors]
+        self._look_up()
+
+    def _look_up(self):
         n = self.n = len(self.tensors)
         if len({t.device for t in self.tensors}) > 1:
             raise ValueError("bi: the tensors of a set must be on one device")
@@ -301,13 +307,24 @@ class TensorSet:
         self.ptrs = (ctypes.c_void_p * n)(*[_ptr(t) if t.numel() else None for t in self.tensors])
         self.counts = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
         self.dtypes = (ctypes.c_int * n)(*[dtype_code(t.dtype) for t in self.tensors])
+        self._seen_ptrs, self._seen_counts = [f() for f in self._ptr_of], [f() for f in self._count_of]
+        self._kinds = [t.dtype for t in self.tensors]
+
+    def current(self):
+        """The set with its arrays as its tensors are now."""
+        if [f() for f in self._ptr_of] != self._seen_ptrs or [f() for f in self._count_of] != self._seen_counts:
+            self._look_up()
+        return self
+
+    def matches(self, other):
+        return self._seen_counts == other._seen_counts and self._kinds == other._kinds
 
     def __len__(self):
         return self.n
 
 
 def _set(tensors):
-    return tensors if isinstance(tensors, TensorSet) else TensorSet(tensors)
+    return tensors.current() if isinstance(tensors, TensorSet) else TensorSet(tensors)
 
 
 def bi_grad_norm(engine, norm, tensors, stream=None) -> int:
@@ -319,7 +336,7 @@ def bi_grad_norm(engine, norm, tensors, stream=None) -> int:
 def _set_pair(dst, src):
     s = _set(src)
     d = s if dst is src else _set(dst)
-    if d is not s and (d.n != s.n or d.counts[:] != s.counts[:] or d.dtypes[:] != s.dtypes[:]):
+    if d is not s and not d.matches(s):
         raise ValueError("bi: dst and src must hold tensors of the same sizes and dtypes")
     return d, s
 

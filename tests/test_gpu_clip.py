@@ -182,3 +182,29 @@ def test_one_call_equals_two(eng, sizes, dtypes):
     s = bi.TensorSet(src)
     assert bi.bi_grad_norm_clip(eng.handle, s, s, n1, -1.0) == bi.BI_ERR_INVALID_ARG
     assert bi.bi_grad_norm_clip(eng.handle, s, s, None, 1.0) == bi.BI_ERR_INVALID_ARG
+
+
+def test_a_set_follows_its_tensors(eng):
+    """A tensor whose storage was replaced or resized: the set's next call goes to the new one."""
+    a, b = torch.full((9,), 2.0, device="cuda"), torch.full((5,), 1.0, device="cuda", dtype=torch.bfloat16)
+    s, norm = bi.TensorSet([a, b]), torch.empty(1, device="cuda")
+    eng.grad_norm(norm, s)
+    assert abs(float(norm) - math.sqrt(41.0)) <= 10 * U * 7
+    old = a.data  # (kept, so that its memory is not given away while this test runs)
+    a.data = torch.full((4, 4), 3.0, device="cuda")
+    eng.clip_gradients(s, s, norm, math.sqrt(149.0) / 2)
+    assert abs(float(norm) - math.sqrt(149.0)) <= 10 * U * 13
+    assert torch.allclose(a, torch.full_like(a, 1.5)) and torch.equal(old, torch.full_like(old, 2.0))
+    with torch.no_grad():
+        b.set_(torch.full((70,), 4.0, device="cuda", dtype=torch.bfloat16).untyped_storage(), 8, (3,), (1,))
+        a.resize_(2)
+    eng.grad_norm(norm, s)
+    assert abs(float(norm) - math.sqrt(2 * 1.5 ** 2 + 3 * 16.0)) <= 10 * U * 8
+    d = bi.TensorSet([torch.empty_like(a), torch.empty_like(b)])
+    eng.grad_clip(d, s, norm, 1.0e9)
+    b.data = torch.ones(6, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        eng.grad_clip(d, s, norm, 1.0e9)  # the two sets no longer match
+    a.data = torch.ones(4, 4, device="cuda").t()[:2]
+    with pytest.raises(ValueError):
+        eng.grad_norm(norm, s)
