@@ -309,6 +309,8 @@ class TensorSet:
         self.dtypes = (ctypes.c_int * n)(*[dtype_code(t.dtype) for t in self.tensors])
         self._seen_ptrs, self._seen_counts = [f() for f in self._ptr_of], [f() for f in self._count_of]
         self._kinds = [t.dtype for t in self.tensors]
+        held = [p for p, c in zip(self._seen_ptrs, self._seen_counts) if c]
+        self.has_twice = len(set(held)) < len(held)
 
     def current(self):
         """The set with its arrays as its tensors are now."""
@@ -338,6 +340,8 @@ def _set_pair(dst, src):
     d = s if dst is src else _set(dst)
     if d is not s and not d.matches(s):
         raise ValueError("bi: dst and src must hold tensors of the same sizes and dtypes")
+    if d.has_twice:  # scaled by two warps at once, in place perhaps twice
+        raise ValueError("bi: a tensor stands twice in the set to be written")
     return d, s
 
 

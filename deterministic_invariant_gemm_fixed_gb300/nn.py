@@ -352,8 +352,8 @@ def route(logits: torch.Tensor, k: int, normalize: bool = True, valid: torch.Ten
 def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
     """Scale the gradients of `parameters` in place so that their global norm is at
     most max_norm; returns the norm before (a float32 tensor of one element, on the
-    device; nothing synchronises).  The gradients must be contiguous and on one
-    device."""
+    device; nothing synchronises).  The gradients must be contiguous, on one device,
+    and each parameter is given once."""
     params = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = [p.grad for p in params if p.grad is not None]
     if not grads:

@@ -380,7 +380,8 @@ bi_status bi_grad_norm(bi_engine engine, float* norm, const void* const* tensors
 
 /* dst[i] = round( src[i] * c ), c = *norm > max_norm ? max_norm / *norm : 1 (NaN
  * for a NaN norm; 0 for an infinite one).  c = 1 copies the bits.  dst[i] may be
- * src[i] itself (in place); otherwise no dst may overlap any src.  max_norm >= 0. */
+ * src[i] itself (in place); otherwise no dst may overlap any src or other dst.
+ * max_norm >= 0. */
 bi_status bi_grad_clip(bi_engine engine, void* const* dst, const void* const* src, const int64_t* counts,
                        const int* dtypes, int64_t n, const float* norm, float max_norm, void* stream);
 

@@ -208,3 +208,15 @@ def test_a_set_follows_its_tensors(eng):
     a.data = torch.ones(4, 4, device="cuda").t()[:2]
     with pytest.raises(ValueError):
         eng.grad_norm(norm, s)
+
+
+def test_a_tensor_twice_in_a_set(eng):
+    """Its squares count twice; scaling it in place would be a race, and is refused."""
+    t = torch.full((8,), 2.0, device="cuda")
+    norm = torch.empty(1, device="cuda")
+    eng.grad_norm(norm, [t, t])
+    assert float(norm) == 8.0
+    for call in (lambda: eng.clip_gradients([t, t], [t, t], norm, 1.0), lambda: eng.grad_clip([t, t], [t.clone(), t], norm, 1.0)):
+        with pytest.raises(ValueError):
+            call()
+    assert (t == 2).all()

@@ -124,3 +124,12 @@ def test_example_step_is_reproducible_and_learns(dtype):
     for u, v in zip(p1, p2):
         assert torch.equal(u, v)
     assert l1[-1] < l1[0] and all(n > 0 for n in n1)
+
+
+def test_clip_grad_norm_of_the_same_parameter_twice():
+    """Its gradient would be scaled by two warps at once: refused, and left as it is."""
+    p = torch.nn.Parameter(torch.ones(3, device="cuda"))
+    p.grad = torch.full_like(p, 2.0)
+    with pytest.raises(ValueError):
+        nn.clip_grad_norm_([p, p], 1.0)
+    assert (p.grad == 2).all()
