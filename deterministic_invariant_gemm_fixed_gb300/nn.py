@@ -357,7 +357,7 @@ def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
     params = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = [p.grad for p in params if p.grad is not None]
     if not grads:
-        return torch.zeros(1)
+        return torch.zeros(1, device=params[0].device if params else None)
     dev = grads[0].device
     if any(g.device != dev for g in grads):
         raise ValueError("clip_grad_norm_: gradients must be on one device")

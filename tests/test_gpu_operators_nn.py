@@ -133,3 +133,9 @@ def test_clip_grad_norm_of_the_same_parameter_twice():
     with pytest.raises(ValueError):
         nn.clip_grad_norm_([p, p], 1.0)
     assert (p.grad == 2).all()
+
+
+def test_clip_grad_norm_without_gradients_stays_on_the_device():
+    p = torch.nn.Parameter(torch.ones(3, device="cuda"))
+    norm = nn.clip_grad_norm_([p], 1.0)
+    assert norm.device == p.device and norm.shape == (1,) and norm.dtype == torch.float32 and float(norm) == 0.0
