@@ -300,7 +300,11 @@ def adapter_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     weight [in, out] shared by all rows, adapters a [G, rank, in] and b [G, rank,
     out], scales [G] float32 (None: 1), ids int32 or uint32 of x's leading shape;
     a row whose id is outside [0, G) gets the shared projection alone.  Gradients
-    for x, weight, bias, a and b; a row's y and dx do not depend on other rows."""
+    for x, weight, bias, a and b; a row's y and dx do not depend on other rows.
+    scales are constants: one that requires a gradient is refused (fold a trained
+    scale into b instead)."""
+    if scales is not None and scales.requires_grad and torch.is_grad_enabled():
+        raise ValueError("adapter_linear has no gradient for scales: pass scales.detach(), or fold them into b")
     return _AdapterLinear.apply(x, weight, bias, a, b, scales, ids, tensor_cores)
 
 

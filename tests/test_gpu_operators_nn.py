@@ -139,3 +139,17 @@ def test_clip_grad_norm_without_gradients_stays_on_the_device():
     p = torch.nn.Parameter(torch.ones(3, device="cuda"))
     norm = nn.clip_grad_norm_([p], 1.0)
     assert norm.device == p.device and norm.shape == (1,) and norm.dtype == torch.float32 and float(norm) == 0.0
+
+
+def test_adapter_linear_does_not_drop_the_gradient_of_scales():
+    """There is no gradient for the scales: one that asks for it is refused, not left without."""
+    x, w = torch.randn(6, 64, device="cuda"), torch.randn(64, 64, device="cuda")
+    a, b = torch.randn(2, 4, 64, device="cuda", requires_grad=True), torch.randn(2, 4, 64, device="cuda")
+    ids = torch.zeros(6, dtype=torch.int32, device="cuda")
+    scales = torch.ones(2, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError):
+        nn.adapter_linear(x, w, None, a, b, scales, ids)
+    nn.adapter_linear(x, w, None, a, b, scales.detach(), ids).sum().backward()
+    assert a.grad is not None
+    with torch.no_grad():  # no gradient is asked for here
+        nn.adapter_linear(x, w, None, a, b, scales, ids)
