@@ -35,6 +35,7 @@ import math
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import Engine, TensorSet
 
@@ -271,6 +272,7 @@ class _AdapterLinear(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], n)
 
     @staticmethod
+    @once_differentiable  # a second derivative is refused, not left out
     def backward(ctx, gy):
         x2, w, a, b, sc, ids2, h = ctx.saved_tensors
         (k, n), (g, r, _) = w.shape, a.shape
@@ -333,6 +335,7 @@ class _Route(torch.autograd.Function):
         return ids_out, weights.clone().reshape(*logits.shape[:-1], k), loss.reshape(()), counts_out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _ids, gweights, gloss, _counts):
         x, lse, ids, weights, counts, rows = ctx.saved_tensors
         t, e = x.shape

@@ -153,3 +153,19 @@ def test_adapter_linear_does_not_drop_the_gradient_of_scales():
     assert a.grad is not None
     with torch.no_grad():  # no gradient is asked for here
         nn.adapter_linear(x, w, None, a, b, scales, ids)
+
+
+def test_second_derivatives_are_refused():
+    """The backward passes are kernels without a backward of their own: a second derivative says so."""
+    x, w = torch.randn(6, 64, device="cuda", requires_grad=True), torch.randn(64, 64, device="cuda")
+    a, b = torch.randn(2, 4, 64, device="cuda"), torch.randn(2, 4, 64, device="cuda")
+    ids = torch.zeros(6, dtype=torch.int32, device="cuda")
+    y = nn.adapter_linear(x, w, None, a, b, None, ids)
+    gx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (gx.square().sum() + x.sum()).backward()
+    logits = torch.randn(6, 8, device="cuda", requires_grad=True)
+    _, weights, loss, _ = nn.route(logits, 2)
+    gl, = torch.autograd.grad(weights.square().sum() + loss, logits, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (gl.square().sum() + logits.sum()).backward()
