@@ -8,8 +8,9 @@
 // below its normal numbers) is summed again in f64 from the registers, so every
 // finite input has its norm.  A lane keeps its sum over all of its warp's units; the lanes'
 // sums are added by a tree, the warps' by a finishing block, in f64 in a fixed
-// order.  Cuts, dealing and orders depend on the sizes alone: the norm is the same
-// bit for bit from run to run.
+// order.  Cuts, dealing and orders depend on the sizes alone (a tensor off 16-byte
+// alignment has the same vectors, loaded element by element): the norm is the same
+// bit for bit from run to run and wherever in memory the tensors lie.
 //
 // Both passes are bound by memory.  No barrier stands between a warp's loads and
 // the next ones (512-thread blocks that reduced every 64 KB read 3.1 TB/s of the
@@ -21,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "abi_util.h"
 
@@ -73,55 +75,61 @@ template <> __device__ __forceinline__ __half down<__half>(float v) { return __f
 
 constexpr float GC_TINY = 0x1p-90f, GC_BIG = 3.0e38f;  // a batch sum outside may have lost squares
 
+// 16 bytes of elements, in one load where they are aligned.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load16(const T* src) {
+    if (VEC) return *reinterpret_cast<const uint4*>(src);
+    uint4 raw;
+    T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(16 / sizeof(T)); ++j) e[j] = src[j];
+    return raw;
+}
+
 // Adds one lane's part of a unit's sum of squares to `total`.
-template <typename T>
-__device__ __forceinline__ void lane_square_sum(const T* src, int len, bool vec, int lane, double& total) {
+template <typename T, bool VEC>
+__device__ __forceinline__ void lane_square_sum(const T* src, int len, int lane, double& total) {
     constexpr int PER = 16 / sizeof(T);
-    int done = 0;
-    if (vec) {
-        const int nv = len / PER;
-        const uint4* v = reinterpret_cast<const uint4*>(src);
-        for (int b = lane; b < nv; b += 32 * GC_VECS) {
-            uint4 raw[GC_VECS];
+    const int nv = len / PER;
+    for (int b = lane; b < nv; b += 32 * GC_VECS) {
+        uint4 raw[GC_VECS];
 #pragma unroll
-            for (int u = 0; u < GC_VECS; ++u)
-                raw[u] = b + 32 * u < nv ? v[b + 32 * u] : make_uint4(0, 0, 0, 0);
-            float acc[8];
+        for (int u = 0; u < GC_VECS; ++u)
+            raw[u] = b + 32 * u < nv ? load16<T, VEC>(src + static_cast<int64_t>(b + 32 * u) * PER) : make_uint4(0, 0, 0, 0);
+        float acc[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
 #pragma unroll
-            for (int u = 0; u < GC_VECS; ++u) {
-                const T* e = reinterpret_cast<const T*>(&raw[u]);
+        for (int u = 0; u < GC_VECS; ++u) {
+            const T* e = reinterpret_cast<const T*>(&raw[u]);
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const float f = up<T>(e[j]);
-                    acc[(u * PER + j) & 7] = fmaf(f, f, acc[(u * PER + j) & 7]);
-                }
+            for (int j = 0; j < PER; ++j) {
+                const float f = up<T>(e[j]);
+                acc[(u * PER + j) & 7] = fmaf(f, f, acc[(u * PER + j) & 7]);
             }
-            const float s = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
-            if (s >= GC_TINY && s <= GC_BIG) {
-                total += static_cast<double>(s);
-            } else {  // zeros, or squares (or their sum) that f32 does not hold, or not finite
-                constexpr uint32_t MAG = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
-                uint32_t bits = 0;
+        }
+        const float s = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        if (s >= GC_TINY && s <= GC_BIG) {
+            total += static_cast<double>(s);
+        } else {  // zeros, or squares (or their sum) that f32 does not hold, or not finite
+            constexpr uint32_t MAG = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
+            uint32_t bits = 0;
 #pragma unroll
-                for (int u = 0; u < GC_VECS; ++u) bits |= raw[u].x | raw[u].y | raw[u].z | raw[u].w;
-                if ((bits & MAG) != 0) {
+            for (int u = 0; u < GC_VECS; ++u) bits |= raw[u].x | raw[u].y | raw[u].z | raw[u].w;
+            if ((bits & MAG) != 0) {
 #pragma unroll
-                    for (int u = 0; u < GC_VECS; ++u) {
-                        const T* e = reinterpret_cast<const T*>(&raw[u]);
+                for (int u = 0; u < GC_VECS; ++u) {
+                    const T* e = reinterpret_cast<const T*>(&raw[u]);
 #pragma unroll
-                        for (int j = 0; j < PER; ++j) {
-                            const double f = up<T>(e[j]);
-                            total = fma(f, f, total);
-                        }
+                    for (int j = 0; j < PER; ++j) {
+                        const double f = up<T>(e[j]);
+                        total = fma(f, f, total);
                     }
                 }
             }
         }
-        done = nv * PER;
     }
-    for (int i = done + lane; i < len; i += 32) {  // the last elements, or a tensor off 16-byte alignment
+    for (int i = nv * PER + lane; i < len; i += 32) {  // the last elements
         const double f = up<T>(src[i]);
         total = fma(f, f, total);
     }
@@ -135,11 +143,15 @@ __global__ void __launch_bounds__(GC_THREADS, 4) square_sum_kernel(const __grid_
     double d = 0.0;
     for (int c = warp; c < units; c += warps) {
         const Piece p = piece_of(t, c);
-        const bool vec = t.vec[p.i] != 0;
         const void* src = t.t[p.i].src;
-        if (t.dtype[p.i] == BI_F32) lane_square_sum(static_cast<const float*>(src) + p.e0, p.len, vec, lane, d);
-        else if (t.dtype[p.i] == BI_BF16) lane_square_sum(static_cast<const __nv_bfloat16*>(src) + p.e0, p.len, vec, lane, d);
-        else lane_square_sum(static_cast<const __half*>(src) + p.e0, p.len, vec, lane, d);
+        auto add = [&](auto* e) {
+            using T = std::remove_const_t<std::remove_pointer_t<decltype(e)>>;
+            if (t.vec[p.i] != 0) lane_square_sum<T, true>(e + p.e0, p.len, lane, d);
+            else lane_square_sum<T, false>(e + p.e0, p.len, lane, d);
+        };
+        if (t.dtype[p.i] == BI_F32) add(static_cast<const float*>(src));
+        else if (t.dtype[p.i] == BI_BF16) add(static_cast<const __nv_bfloat16*>(src));
+        else add(static_cast<const __half*>(src));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);

@@ -220,3 +220,24 @@ def test_a_tensor_twice_in_a_set(eng):
         with pytest.raises(ValueError):
             call()
     assert (t == 2).all()
+
+
+@pytest.mark.parametrize("dtype", [F, B, H])
+@pytest.mark.parametrize("n", [5, 64, 1000, 2048 * 3 + 9, 700001])
+def test_results_do_not_depend_on_alignment(eng, n, dtype):
+    """The same values at any offset of a buffer: the same norm and the same scaled values, bit for bit.
+    (Few values each of many times: a long sum's rounding to f32 hides the order of its additions.)"""
+    for seed in range(40 if n < 5000 else 3):
+        val = make([n], [dtype], seed=seed)[0]
+        want, norm = torch.empty_like(val), torch.empty(1, device="cuda")
+        eng.clip_gradients([want], [val], norm, 0.5)
+        for off in (1, 2, 3, 5, 7):
+            buf = torch.zeros(n + 16, dtype=dtype, device="cuda")
+            v = buf[off:off + n]
+            v.copy_(val)
+            got = torch.empty(1, device="cuda")
+            eng.grad_norm(got, [v])
+            assert torch.equal(got, norm), (seed, off, float(got), float(norm))
+            eng.clip_gradients([v], [v], got, 0.5)
+            assert torch.equal(got, norm) and torch.equal(v, want)
+            assert not buf[:off].any() and not buf[off + n:].any()
