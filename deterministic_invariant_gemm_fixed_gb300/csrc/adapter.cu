@@ -596,6 +596,15 @@ bi_status check_adapter(bi_engine eng, bi_dtype dt, int64_t m, int64_t k, int64_
     return BI_OK;
 }
 
+// The f32-FMA kernels count pieces (512 elements), the wide product's columns (256) and
+// the gradients' (128) in a grid's second dimension.
+bool too_long(int64_t length, int64_t per_block) { return (length + per_block - 1) / per_block > 65535; }
+bi_status fail_too_long(bi_engine eng) {
+    return fail(eng, BI_ERR_UNSUPPORTED,
+                "adapters in plain f32: a contraction is limited to 33553920 elements, y's and dx's columns to 16776960, da's and "
+                "db's to 8388480");
+}
+
 // Cuts of one scratch allocation.
 struct Cut {
     int64_t at = 0;
@@ -654,6 +663,7 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
         if (e == cudaSuccess) e = tc_adapter_rows(c, dtype, 0, y, x, w, bias, p + o_hh, b, plan, src, m, k, n, R, g);
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_forward");
     }
+    if (too_long(k, ADAPTER_PIECE) || too_long(n, 256)) return fail_too_long(eng);
     // scratch: pieces of h | s h | the shared product in f32 (16-bit types)
     Cut cut;
     const int64_t o_part = cut.take(pieces * m * r * 4), o_hs = cut.take(m * r * 4),
@@ -768,6 +778,8 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         }
         return e == cudaSuccess ? BI_OK : cuda_fail(eng, e, "bi_adapter_backward");
     }
+    if ((need_u && too_long(n, ADAPTER_PIECE)) || (dx && too_long(k, 256)) || (da && too_long(k, 128)) || (db && too_long(n, 128)))
+        return fail_too_long(eng);
     // scratch: pieces of u | u | s h | sorted rows | chunk tables | chunk
     // sums (of dA, then of dB) | the shared product in f32 (16-bit types)
     Cut cut;

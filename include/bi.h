@@ -293,7 +293,9 @@ bi_status bi_grouped_forward_noalloc(void* y, const void* x, const void* w,
  * B [G,R,N] have the operands' type; scales [G] f32 (nullable: all 1);
  * row_adapters [M] u32, a row with an id >= G has no adapter (its h is +0 and
  * its Y and dX are the shared projection's).  Rows need not be sorted, and an
- * adapter may have none (its dA and dB are +0).  R <= 256, G <= 65535.
+ * adapter may have none (its dA and dB are +0).  R <= 256, G <= 65535; in plain f32
+ * (the scalar tier, and f32 operands on either) a contraction has at most 33553920
+ * elements, Y's and dX's rows 16776960 columns, dA's and dB's 8388480.
  *
  * h and u contract in pieces of 512 elements counted from 0, added in order in
  * f32; the R terms are added to the row's f32 sum before its one rounding.  A

@@ -520,3 +520,23 @@ def test_an_infinite_scale_reaches_no_padding(eng, m, dtype, tc):
         assert torch.equal(forward(eng, d, tc)[0], y)
     finally:
         bi.bi_engine_set_tile_cols(eng.handle, 0)
+
+
+def test_lengths_beyond_the_grids_are_refused(eng):
+    """Rows longer than the f32-FMA kernels' grids count: refused before anything is written."""
+    long = 65535 * 128 + 1
+    x, w = torch.ones(1, long, device="cuda"), torch.ones(8, 8, device="cuda")
+    a, dy, b = torch.ones(1, 1, long, device="cuda"), torch.ones(1, 8, device="cuda"), torch.ones(1, 1, 8, device="cuda")
+    ids = torch.zeros(1, dtype=torch.int32, device="cuda")
+    da = torch.full((1, 1, long), 7.0, device="cuda")
+    def status(k):
+        return bi.bi_adapter_backward(eng.handle, None, da, None, x, None, w, dy, a, b, None, ids, 1, k, 8, 1, 1, "f32", None, 0)
+    assert status(long) == bi.BI_ERR_UNSUPPORTED and (da == 7).all()
+    assert status(long - 1) == bi.BI_OK and (da[..., :-1] == 8).all() and float(da[0, 0, -1]) == 7  # u = 8, x = 1
+    # y of 65535 x 256 + 1 columns (refused on the host: nothing is read)
+    y = torch.full((8,), 7.0, device="cuda")
+    assert bi.bi_adapter_forward(eng.handle, y, None, x, w, None, a, b, None, ids, 1, 8, 65535 * 256 + 1, 1, 1, "f32", None,
+                                 0) == bi.BI_ERR_UNSUPPORTED
+    assert bi.bi_adapter_forward(eng.handle, y, None, x, w, None, a, b, None, ids, 1, 65535 * 512 + 1, 8, 1, 1, "f32", None,
+                                 0) == bi.BI_ERR_UNSUPPORTED
+    assert (y == 7).all()
