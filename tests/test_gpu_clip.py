@@ -241,3 +241,16 @@ def test_results_do_not_depend_on_alignment(eng, n, dtype):
             eng.clip_gradients([v], [v], got, 0.5)
             assert torch.equal(got, norm) and torch.equal(v, want)
             assert not buf[:off].any() and not buf[off + n:].any()
+
+
+@pytest.mark.parametrize("sizes,dtypes", SETS)
+def test_norm_within_its_own_bound(eng, sizes, dtypes):
+    """16 or 32 squares in 8 running sums: at most 2 roundings of an f32 square and its addition, or 3
+    additions of 16-bit squares (exact in f32), then 3 additions of the sums, 6 * 2^-24 on positive
+    terms; f64 from there (its own error below 2^-40); the root halves it and rounds once: 4 * 2^-24."""
+    for seed in range(5):
+        src = make(sizes, dtypes, seed=seed)
+        norm = torch.empty(1, device="cuda")
+        eng.grad_norm(norm, src)
+        want = norm64(src)
+        assert abs(float(norm) - want) <= (4 * U + 2.0 ** -40) * want
