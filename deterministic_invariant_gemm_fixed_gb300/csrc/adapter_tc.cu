@@ -88,10 +88,15 @@ __device__ __forceinline__ void drain_mmas(uint32_t bar, uint32_t lead, volatile
 // these the adapters among its rows, four groups of 16 ranks (64 accumulator
 // columns) at a time: D [128 rows x 64] += X [128 x 64] P^T, P the groups' rows
 // stacked.  Every row is multiplied with every adapter of the tile, and reads
-// back its own adapter's columns; the other products are thrown away.  They are
-// free: the pass is bound by reading X once (8192 rows of 4096: 67 MB, 10 us at
-// the copy rate) and the tensor cores idle beside it, while sorting the rows
-// first would read and write X once more.  128 rows x 512 elements is a unit
+// back its own adapter's columns; the other products are thrown away.  With rows in
+// runs, a few adapters to a tile, they are free: the pass is bound by reading X
+// once (8192 rows of 4096: 67 MB, 10 us at the copy rate) and the tensor cores idle
+// beside it, while sorting the rows first would read and write X once more.  They
+// are not where a tile's rows have many adapters: X passes through shared memory
+// once per four groups, ceil(adapters ceil(R / 16) / 4) times, and the wide product
+// takes as many masked MMAs (8192 rows of 4096 x 4096 in random order, the whole
+// forward: 64 adapters of rank 16 417 us, 128 of rank 256 3600, in runs 163 and 316).
+// 128 rows x 512 elements is a unit
 // small enough that a batch of 8192 rows gives 512 of them, and one of 64 rows
 // with an own adapter each 128.
 //

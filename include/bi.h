@@ -311,8 +311,8 @@ bi_status bi_grouped_forward_noalloc(void* y, const void* x, const void* w,
  * small ones, 2^-25 absolute.  With f16 a magnitude beyond 65504 enters as the f32
  * value itself (added in f32 FMAs after the others: correct, but slow where most
  * rows have such).  dA and dB take u and s_g h in four parts: f32's 24 bits, with f16 up
- * to 2^27, beyond which they are infinite.  A non-finite operand of a row, or of its
- * adapter, makes that row's results non-finite (an infinity or NaN).
+ * to 2^27, beyond which they are infinite.  A non-finite operand makes the results
+ * that it enters non-finite (an infinity, or NaN where parts of it meet a zero).
  *
  * Scratch, taken from the engine's pool for the call: on the tensor cores about
  * 4 ceil(L/512) M R bytes (L = K forward, N backward; R rounded up to 16) besides 37
