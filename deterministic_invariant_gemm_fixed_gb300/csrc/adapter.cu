@@ -556,7 +556,7 @@ cudaError_t grad_sum(const LaunchCtx& c, const AdapterGradJob* jobs, int count, 
     // about eight blocks per SM in all: most adapters have one chunk and nothing to add
     const int64_t y = lmax(1, lmin((most + 255) / 256, 8 * int64_t(c.sm_count) / (G * count)));
     const dim3 grid(static_cast<unsigned>(G), static_cast<unsigned>(y), static_cast<unsigned>(count));
-    const cudaError_t e = launch_pdl(grad_sum_kernel, grid, dim3(256), 0, c.stream, js, ch, R);
+    const cudaError_t e = launch_plain(grad_sum_kernel, grid, dim3(256), 0, c.stream, js, ch, R);
     if (e == cudaSuccess) c.count();
     return e;
 }
@@ -749,7 +749,7 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
         if (grads) {  // the rows sorted by adapter, for dA and dB
             e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
             if (e == cudaSuccess) {
-                e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, static_cast<uint32_t>(g), ch);
+                e = launch_plain(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, static_cast<uint32_t>(g), ch);
                 if (e == cudaSuccess) c.count();
             }
         }
@@ -820,7 +820,7 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     if (e == cudaSuccess && grads) {
         e = segment(c, row_adapters, m, g, seg, perm, p + o_hist);
         if (e == cudaSuccess) {
-            e = launch_pdl(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, G, ch);
+            e = launch_plain(adapter_chunks_kernel, dim3(1), dim3(1024), 0, s, seg, G, ch);
             if (e == cudaSuccess) c.count();
         }
     }

@@ -888,7 +888,6 @@ __global__ void __launch_bounds__(GT_THREADS, gt_ctas(RUN)) grad_tc_kernel(const
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    grid_dep_wait();
     const uint32_t chunk = p.chunk0 + blockIdx.x / p.strips;
     if (chunk >= p.ch.first[p.G]) return;
     int g = 0;  // the last adapter whose first chunk is <= chunk
@@ -920,7 +919,6 @@ __global__ void __launch_bounds__(GT_THREADS, gt_ctas(RUN)) grad_tc_kernel(const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
-    grid_dep_launch();  // after the CTA has its TMEM: a dependent kernel may ask for some
 
     if (warp < 4) {
         // thread t copies 16-byte piece t % 8 of each 128-byte atom row, rows t / 8 + 16 i
@@ -1037,7 +1035,7 @@ cudaError_t grad_run(const LaunchCtx& c, const GradParams& p, dim3 grid) {
         return cudaFuncSetAttribute(grad_tc_kernel<RUN>, cudaFuncAttributeMaxDynamicSharedMemorySize, gt_smem(RUN));
     });
     if (e != cudaSuccess) return e;
-    const cudaError_t r = launch_pdl(grad_tc_kernel<RUN>, grid, dim3(GT_THREADS), gt_smem(RUN), c.stream, p);
+    const cudaError_t r = launch_plain(grad_tc_kernel<RUN>, grid, dim3(GT_THREADS), gt_smem(RUN), c.stream, p);
     if (r == cudaSuccess) c.count();
     return r;
 }

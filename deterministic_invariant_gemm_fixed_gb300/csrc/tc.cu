@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // set-up above touches no global memory; everything below may read what
     // the previous kernel in the stream wrote
     grid_dep_wait();
-    grid_dep_launch();
+    // (behind the adapters' product nothing is let in early: see launch_plain)
+    if (MODE != ADAPTER) grid_dep_launch();
 
     if (MODE == ADAPTER && warp == 0) {
         // ------------------------------------------------------------ producer (both CTAs), adapter passes
