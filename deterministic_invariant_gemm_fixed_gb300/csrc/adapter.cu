@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "abi_util.h"
@@ -605,6 +606,58 @@ bi_status fail_too_long(bi_engine eng) {
                 "db's to 8388480");
 }
 
+// One adapter call on a device at a time: a call on another stream than the one before
+// waits for it on the device.  (With three streams' calls under way at once one of
+// them never ended, within some 250 turns, on a GPU that had nothing else left to do
+// and answered again once the process was gone.  No bounded wait had run out; which of
+// the hardware's own it was is not known.  Two streams ran 300 thousand turns.)  A
+// single stream pays a comparison.  The first call on a second stream waits for the
+// device on the host, as nothing marks where the first one's last call ends; from then
+// on an event does.  Calls that are being captured are left out: a graph's replays are
+// not seen here.
+struct TurnState {
+    std::mutex mu;
+    bool begun = false, many = false;
+    cudaStream_t stream = nullptr;  // of the last call; compared only, it may be gone
+    cudaEvent_t event = nullptr;    // behind that call, once there were two streams
+};
+struct AdapterTurn {
+    TurnState& state;
+    cudaStream_t stream;
+    std::lock_guard<std::mutex> lock;
+    cudaError_t err = cudaSuccess;
+    bool capturing = false;
+    static TurnState& of(int device) {
+        static TurnState states[MAX_DEVICES];
+        return states[device >= 0 && device < MAX_DEVICES ? device : 0];
+    }
+    AdapterTurn(bi_engine eng, cudaStream_t s) : state(of(eng->device)), stream(s), lock(state.mu) {
+        if (state.begun && !state.many && s == state.stream) return;
+        cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(s, &st) != cudaSuccess) cudaGetLastError();
+        capturing = st != cudaStreamCaptureStatusNone;
+        if (capturing) return;
+        if (state.begun && !state.many) {
+            if (state.event == nullptr) err = cudaEventCreateWithFlags(&state.event, cudaEventDisableTiming);
+            if (err != cudaSuccess) return;
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // another thread may be capturing
+            cudaThreadExchangeStreamCaptureMode(&mode);
+            err = cudaDeviceSynchronize();
+            cudaThreadExchangeStreamCaptureMode(&mode);
+            if (err != cudaSuccess) return;
+            state.many = true;
+        } else if (state.many && (s != state.stream || s == cudaStreamPerThread)) {
+            err = cudaStreamWaitEvent(s, state.event, 0);
+            if (err != cudaSuccess) return;
+        }
+        state.begun = true;
+        state.stream = s;
+    }
+    ~AdapterTurn() {
+        if (state.many && !capturing && err == cudaSuccess) cudaEventRecord(state.event, stream);
+    }
+};
+
 // Cuts of one scratch allocation.
 struct Cut {
     int64_t at = 0;
@@ -638,6 +691,8 @@ bi_status bi_adapter_forward(bi_engine eng, void* y, float* h, const void* x, co
     DeviceGuard guard(eng->device);
     if (!guard.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const AdapterTurn turn(eng, s);
+    if (turn.err != cudaSuccess) return cuda_fail(eng, turn.err, "adapter turn");
     const LaunchCtx c = ctx(eng, stream);
     const int R = static_cast<int>(r), pieces = pieces_of(k);
     if (tier) {
@@ -716,6 +771,8 @@ bi_status bi_adapter_backward(bi_engine eng, void* dx, float* da, float* db, con
     if (!dx && !da && !db) return BI_OK;
     if (!dy || !row_adapters || ((dx || da) && !b) || (dx && (!w || !a)) || (da && !x) || (db && !h))
         return fail(eng, BI_ERR_INVALID_ARG, "an operand that a requested gradient needs is NULL");
+    const AdapterTurn turn(eng, s);
+    if (turn.err != cudaSuccess) return cuda_fail(eng, turn.err, "adapter turn");
     const LaunchCtx c = ctx(eng, stream);
     const int R = static_cast<int>(r), pieces = pieces_of(n);
     const bool need_u = dx || da;

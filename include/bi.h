@@ -314,6 +314,10 @@ bi_status bi_grouped_forward_noalloc(void* y, const void* x, const void* w,
  * to 2^27, beyond which they are infinite.  A non-finite operand makes the results
  * that it enters non-finite (an infinity, or NaN where parts of it meet a zero).
  *
+ * Adapter calls on one device run one behind the other, whatever their streams: a
+ * call waits on the device for the one before on another stream, and the first call on
+ * a second stream waits for the device on the host (calls under capture do neither).
+ *
  * Scratch, taken from the engine's pool for the call: on the tensor cores about
  * 4 ceil(L/512) M R bytes (L = K forward, N backward; R rounded up to 16) besides 37
  * bytes a row and the parts (4 bytes per row and rank for the second product, 8 for

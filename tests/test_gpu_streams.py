@@ -36,18 +36,19 @@ def adapter_calls(eng, seed, m, k, n, r, g, dtype=torch.bfloat16):
 
 def test_scratch_makes_no_stream_wait_for_another(eng):
     """One stream's call takes scratch beside another stream's that pauses between two calls: it is done long before."""
-    (one, _), _ = adapter_calls(eng, 1, 4096, 1024, 512, 64, 4)
-    (other, _), (y, *_) = adapter_calls(eng, 2, 4096, 1024, 512, 64, 4)
+    a, b = ([torch.randn(300001, device="cuda") for _ in range(5)] for _ in range(2))
+    n, m, want = (torch.empty(1, device="cuda") for _ in range(3))
+    eng.grad_norm(want, b)
     torch.cuda.synchronize()
     s, t = torch.cuda.Stream(), torch.cuda.Stream()
     with torch.cuda.stream(s):
-        one()
+        eng.grad_norm(n, a)
         torch.cuda._sleep(1_000_000_000)  # about half a second
-        one()
+        eng.grad_norm(n, a)
         end = torch.cuda.Event()
         end.record()
     with torch.cuda.stream(t):
-        other()
+        eng.grad_norm(m, b)
         done = torch.cuda.Event()
         done.record()
     began = time.time()
@@ -55,9 +56,34 @@ def test_scratch_makes_no_stream_wait_for_another(eng):
         time.sleep(0.001)
     assert not end.query(), "the call waited for the other stream"
     torch.cuda.synchronize()
-    got = y.clone()
-    other()
-    assert torch.equal(got, y)
+    assert torch.equal(m, want)
+
+
+def test_adapter_calls_take_turns(eng):
+    """Adapter calls of one engine run one behind the other, whatever their streams: the second starts when the first has ended."""
+    (one, _), _ = adapter_calls(eng, 1, 4096, 1024, 512, 64, 4)
+    (other, _), (y, *_) = adapter_calls(eng, 2, 64, 1024, 512, 16, 4)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for stream, call in ((s, one), (t, other)):
+        with torch.cuda.stream(stream):
+            call()
+    torch.cuda.synchronize()
+    want = y.clone()
+    y.zero_()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+        one()
+        end = torch.cuda.Event()
+        end.record()
+    with torch.cuda.stream(t):
+        other()
+        done = torch.cuda.Event()
+        done.record()
+    while not done.query():
+        time.sleep(0.001)
+    assert end.query()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
 
 
 def test_two_streams_side_by_side(eng):
