@@ -1,5 +1,5 @@
 """Deterministic, batch-invariant training matmul for GB300 (sm_103a), with the
-adapters, router and gradient clipping that go beside it.
+adapters, router, few-token expert layer and gradient clipping that go beside it.
 
 Thin ctypes binding over the C ABI in ``include/bi.h`` (libbi.so, built in-tree
 by ``deterministic_invariant_gemm_fixed_gb300.build``).  The functions below
@@ -30,6 +30,7 @@ STATUS_NAMES = {0: "BI_OK", 1: "BI_ERR_INVALID_ARG", 2: "BI_ERR_MISALIGNED", 3: 
  BI_PASS_GROUPED_DWEIGHTS) = range(6)
 BI_DW_CHUNK = 256
 BI_STRATEGY_SCALAR, BI_STRATEGY_TENSOR_CORE, BI_STRATEGY_AUTO = 0, 1, 2
+BI_ACT_SILU, BI_ACT_GELU, BI_ACT_RELU = 0, 1, 2
 
 # Every entry point declared in include/bi.h, with its ctypes signature.
 _p, _i64, _i32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
@@ -59,6 +60,15 @@ SIGNATURES = {
     "bi_fp8_backward_dw": (_i32, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p]),
     "bi_adapter_forward": (_i32, [_p] * 10 + [_i64] * 5 + [_i32, _p, _i32]),
     "bi_adapter_backward": (_i32, [_p] * 12 + [_i64] * 5 + [_i32, _p, _i32]),
+    "bi_fp4_code_bytes": (_i64, [_i64, _i64]),
+    "bi_fp4_scale_bytes": (_i64, [_i64, _i64]),
+    "bi_fp4_quantize": (_i32, [_p] * 6 + [_i64] * 2 + [_i32, _p]),
+    "bi_fp4_dequantize": (_i32, [_p] * 4 + [_i64] * 2 + [_i32, _p]),
+    "bi_fp4_forward": (_i32, [_p] * 7 + [_i64] * 3 + [_i32, _p]),
+    "bi_fp4_backward_dx": (_i32, [_p] * 6 + [_i64] * 3 + [_i32, _p]),
+    "bi_fp4_backward_dw": (_i32, [_p] * 6 + [_i64] * 3 + [_i32, _p]),
+    "bi_moe_forward": (_i32, [_p] * 8 + [_i64] * 6 + [_i32, _i32, _p]),
+    "bi_moe_forward_fp4": (_i32, [_p] * 11 + [_i64] * 6 + [_i32, _i32, _p]),
     "bi_router_forward": (_i32, [_p] * 10 + [_i64] * 3 + [_i32, _i32, _p]),
     "bi_router_backward": (_i32, [_p] * 10 + [_i64] * 3 + [_i32, _i32, _p]),
     "bi_grad_norm": (_i32, [_p, _p, _p, _p, _p, _i64, _p]),
@@ -286,6 +296,85 @@ def bi_router_backward(engine, dlogits, logits, lse, ids, weights, counts, rows,
                                    dtype_code(dtype), _stream(stream))
 
 
+def bi_fp4_code_bytes(rows: int, cols: int) -> int:
+    return _lib.bi_fp4_code_bytes(rows, cols)
+
+
+def bi_fp4_scale_bytes(rows: int, cols: int) -> int:
+    return _lib.bi_fp4_scale_bytes(rows, cols)
+
+
+def fp4_buffers(rows: int, cols: int, device="cuda"):
+    """Buffers for an operand [rows][cols] in MXFP4: (codes, scales), uint8."""
+    import torch
+    sizes = bi_fp4_code_bytes(rows, cols), bi_fp4_scale_bytes(rows, cols)
+    if min(sizes) < 0:
+        raise ValueError(f"fp4_buffers: sizes out of range ({rows} x {cols})")
+    return tuple(torch.empty(n, dtype=torch.uint8, device=device) for n in sizes)
+
+
+def _fp4_ptr(t, need):
+    """A codes or scales buffer of at least `need` bytes; an empty one has no storage to point at."""
+    if t is not None and not isinstance(t, int) and t.numel() * t.element_size() < need:
+        raise ValueError(f"bi: an MXFP4 buffer of {t.numel() * t.element_size()} bytes where {need} are needed (fp4_buffers)")
+    return _ptr(t)
+
+
+def _fp4(q, s, rows, cols):
+    """Addresses of the codes and scales of an operand [rows][cols], sizes checked.
+    Sizes that the library refuses are left to it."""
+    cp = (cols + 255) // 256 * 256
+    return _fp4_ptr(q, rows * cp // 2), _fp4_ptr(s, (rows + 127) // 128 * cp * 4)
+
+
+def bi_fp4_quantize(engine, q, s, qt, st, src, rows, cols, dtype, stream=None) -> int:
+    return _lib.bi_fp4_quantize(engine, *_fp4(q, s, rows, cols), *_fp4(qt, st, cols, rows), _ptr(src), rows, cols,
+                                dtype_code(dtype), _stream(stream))
+
+
+def bi_fp4_dequantize(engine, dst, q, s, rows, cols, dtype, stream=None) -> int:
+    return _lib.bi_fp4_dequantize(engine, _ptr(dst), *_fp4(q, s, rows, cols), rows, cols, dtype_code(dtype), _stream(stream))
+
+
+def bi_fp4_forward(engine, y, xq, xs, wq, ws, bias, m, k, n, out_dtype, stream=None) -> int:
+    return _lib.bi_fp4_forward(engine, _ptr(y), *_fp4(xq, xs, m, k), *_fp4(wq, ws, n, k), _ptr(bias), m, k, n,
+                               dtype_code(out_dtype), _stream(stream))
+
+
+def bi_fp4_backward_dx(engine, dx, gq, gs, wq, ws, m, k, n, out_dtype, stream=None) -> int:
+    return _lib.bi_fp4_backward_dx(engine, _ptr(dx), *_fp4(gq, gs, m, n), *_fp4(wq, ws, k, n), m, k, n,
+                                   dtype_code(out_dtype), _stream(stream))
+
+
+def bi_fp4_backward_dw(engine, dw, xq, xs, gq, gs, m, k, n, out_dtype, stream=None) -> int:
+    return _lib.bi_fp4_backward_dw(engine, _ptr(dw), *_fp4(xq, xs, k, m), *_fp4(gq, gs, n, m), m, k, n,
+                                   dtype_code(out_dtype), _stream(stream))
+
+
+_ACTIVATIONS = {"silu": BI_ACT_SILU, "gelu": BI_ACT_GELU, "relu": BI_ACT_RELU}
+
+
+def activation_code(a) -> int:
+    """bi_activation from 'silu', 'gelu', 'relu' or an int."""
+    if isinstance(a, int):
+        return a
+    if a not in _ACTIVATIONS:
+        raise ValueError(f"unknown activation {a!r}")
+    return _ACTIVATIONS[a]
+
+
+def bi_moe_forward(engine, y, x, ids, weights, w_gate, w_up, w_down, t, c, k, f, n, e, activation, dtype, stream=None) -> int:
+    return _lib.bi_moe_forward(engine, _ptr(y), _ptr(x), _ptr(ids), _ptr(weights), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                               t, c, k, f, n, e, activation_code(activation), dtype_code(dtype), _stream(stream))
+
+
+def bi_moe_forward_fp4(engine, y, x, ids, weights, gate_q, gate_s, up_q, up_s, down_q, down_s, t, c, k, f, n, e, activation,
+                       dtype, stream=None) -> int:
+    return _lib.bi_moe_forward_fp4(engine, _ptr(y), _ptr(x), _ptr(ids), _ptr(weights), *_fp4(gate_q, gate_s, e * f, k),
+                                   *_fp4(up_q, up_s, e * f, k), *_fp4(down_q, down_s, e * n, f), t, c, k, f, n, e,
+                                   activation_code(activation), dtype_code(dtype), _stream(stream))
+
+
 class TensorSet:
     """A set of tensors as bi_grad_norm and bi_grad_clip take it: the host arrays
     of device pointers, element counts and dtypes.  A program whose gradient
@@ -440,6 +529,30 @@ class Engine:
 
     def fp8_backward_dw(self, dw, xq, gq, scale_x, scale_g, m, k, n, out_dtype, stream=None):
         self._ok(bi_fp8_backward_dw(self.handle, dw, xq, gq, scale_x, scale_g, m, k, n, out_dtype, stream))
+
+    def fp4_quantize(self, q, s, qt, st, src, rows, cols, dtype, stream=None):
+        self._ok(bi_fp4_quantize(self.handle, q, s, qt, st, src, rows, cols, dtype, stream))
+
+    def fp4_dequantize(self, dst, q, s, rows, cols, dtype, stream=None):
+        self._ok(bi_fp4_dequantize(self.handle, dst, q, s, rows, cols, dtype, stream))
+
+    def fp4_forward(self, y, xq, xs, wq, ws, bias, m, k, n, out_dtype, stream=None):
+        self._ok(bi_fp4_forward(self.handle, y, xq, xs, wq, ws, bias, m, k, n, out_dtype, stream))
+
+    def fp4_backward_dx(self, dx, gq, gs, wq, ws, m, k, n, out_dtype, stream=None):
+        self._ok(bi_fp4_backward_dx(self.handle, dx, gq, gs, wq, ws, m, k, n, out_dtype, stream))
+
+    def fp4_backward_dw(self, dw, xq, xs, gq, gs, m, k, n, out_dtype, stream=None):
+        self._ok(bi_fp4_backward_dw(self.handle, dw, xq, xs, gq, gs, m, k, n, out_dtype, stream))
+
+    def moe_forward(self, y, x, ids, weights, w_gate, w_up, w_down, t, c, k, f, n, e, activation, dtype, stream=None):
+        self._ok(bi_moe_forward(self.handle, y, x, ids, weights, w_gate, w_up, w_down, t, c, k, f, n, e, activation, dtype,
+                                stream))
+
+    def moe_forward_fp4(self, y, x, ids, weights, gate_q, gate_s, up_q, up_s, down_q, down_s, t, c, k, f, n, e, activation,
+                        dtype, stream=None):
+        self._ok(bi_moe_forward_fp4(self.handle, y, x, ids, weights, gate_q, gate_s, up_q, up_s, down_q, down_s, t, c, k, f,
+                                    n, e, activation, dtype, stream))
 
     def adapter_forward(self, y, h, x, w, bias, a, b, scales, ids, m, k, n, r, g, dtype, stream=None, tensor_cores=1):
         self._ok(bi_adapter_forward(self.handle, y, h, x, w, bias, a, b, scales, ids, m, k, n, r, g, dtype, stream,

@@ -40,7 +40,6 @@ constexpr int BN = 256;        // tile cols = MMA N (the 16-bit passes also have
 constexpr int BK = 64;         // contraction block = one 128-byte swizzle row of 16-bit data
 constexpr int THREADS = 192;
 constexpr int BAR_BYTES = 256;
-constexpr int GROUP_M = 16;    // raster: 16 row-tiles share the column sweep (L2 reuse)
 static_assert(GROUPED_TILE_ROWS == 256 && GROUPED_TAIL_ROWS == BK,
               "the grouping's tile and tail sizes are the pair kernel's");
 
@@ -138,21 +137,6 @@ static_assert(p_smem_bytes(0, 256, true) <= SMEM_LIMIT && p_smem_bytes(0, 128, t
 // accumulator b starts at column b * (allocation / 2).
 __host__ __device__ constexpr int p_tmem_cols(int bnt) { return 2 * bnt <= 256 ? 256 : 512; }
 
-__device__ __forceinline__ uint32_t mapa_rank(uint32_t saddr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                                 uint32_t bar_cluster) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar_cluster)
-        : "memory");
-}
-
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                                  uint32_t bar_cluster) {
     asm volatile(
@@ -162,39 +146,12 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// TMA store of a staged 32-row slice (2-D, or 3-D with the expert as z), in a
-// bulk async-group of the issuing thread; the group's smem reads finish before
-// cp.async.bulk.wait_group.read returns, its global writes before wait_group.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(x), "r"(y)
-                 : "memory");
-}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Raster of the dense tiles: GROUP_M row pairs share a sweep over the column
-// tiles (L2 reuse of the B columns).
-__host__ __device__ __forceinline__ void dense_raster(int t, int units_m, int num_n, int& mpair, int& nb) {
-    const int span = GROUP_M * num_n;
-    const int grp = t / span;
-    const int first = grp * GROUP_M;
-    const int gsize = min(units_m - first, GROUP_M);
-    const int r = t - grp * span;
-    mpair = first + r % gsize;
-    nb = r / gsize;
-}
-
 // One work unit of the pair kernel.
 struct PairTile {
     int g;        // expert (grouped modes)
@@ -378,25 +335,6 @@ __device__ __forceinline__ void mma_commit_pair_mc(uint32_t bar, uint16_t mask) 
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(bar), "h"(mask)
         : "memory");
-}
-
-// The same from warp-uniform code, issued by one lane.
-__device__ __forceinline__ void mma_commit_pair_lead(uint32_t bar, uint16_t mask, uint32_t lead) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
-        "h"(mask), "r"(lead)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-                 : "memory");
 }
 
 // kind::f16: format 0 = f16, 1 = bf16; kind::f8f6f4: 0 = e4m3; kind::tf32: 2 = tf32.

@@ -10,8 +10,9 @@
  *             dX[m,:] = dY[m,:] * W[e(m)]        dW[e] = sum over rows of expert e
  *                                                 of dY[m,:]^T X[m,:] (always f32)
  *
- * and beside them low-rank adapters of many requests, a router with its balance
- * loss, and gradient norm and clipping, each described at its declarations.
+ * and beside them the linear layer's products in FP8 and MXFP4, low-rank adapters of
+ * many requests, a router with its balance loss, an expert layer for few tokens, and
+ * gradient norm and clipping, each described at its declarations.
  *
  * Sources: sgemm-bi 0.1.1.post2 (PyPI page), sections "Use" (weight stored
  * [in, out]; the raw-pointer Engine.forward call with m, k, n, a dtype string,
@@ -213,6 +214,53 @@ bi_status bi_fp8_backward_dw(bi_engine engine, void* dw, const uint8_t* xq, cons
                              const float* scale_x, const float* scale_g, int64_t m, int64_t k, int64_t n,
                              bi_dtype out_dtype, void* stream);
 
+/* ---- MXFP4: 4-bit floating point with a scale per 32 values (tensor cores) ----
+ *
+ * An operand [R][C] in MXFP4 (OCP Microscaling Formats v1.0) stands for
+ * e2m1 code * 2^(scale - 127), one e2m1 code per value and one e8m0 scale byte per
+ * block of 32 consecutive values of a row (blocks counted from column 0; the last
+ * may be shorter).  The products below contract along C.  Codes: [R][Cp/2]
+ * bytes, Cp = C rounded up to 256, value 2i in the low half of byte i; scales: pieces
+ * [ceil(R/128)][Cp/128] of 512 bytes, the byte of row r and block b at
+ * 16 (r % 32) + 4 (r / 32 % 4) + b % 4 of its piece.  bi_fp4_code_bytes and
+ * bi_fp4_scale_bytes give the buffers' sizes (-1 for sizes out of range); both are
+ * 16-byte aligned.  Bytes past the values (columns C to Cp, scales of rows past R)
+ * have to be 0, as bi_fp4_quantize writes them.  A scale byte of 255 is NaN. */
+int64_t bi_fp4_code_bytes(int64_t rows, int64_t cols);
+int64_t bi_fp4_scale_bytes(int64_t rows, int64_t cols);
+
+/* src [rows][cols] to MXFP4: q, s along its columns (an operand [rows][cols]) and
+ * qt, st along its rows (the operand [cols][rows], src transposed), either pair
+ * NULL, from one read of src.  Per block 2^s with s = floor(log2 max|v|) - 2, at
+ * least -127; codes e2m1(v / 2^s), round to nearest even, larger ones to +-6 (v / 2^s
+ * is exact).  A block with an infinity or NaN gets the scale 255 and codes 0. */
+bi_status bi_fp4_quantize(bi_engine engine, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st, const void* src,
+                          int64_t rows, int64_t cols, bi_dtype dtype, void* stream);
+
+/* dst [rows][cols] = the values, rounded to dtype (exact for codes made from a
+ * matrix of that dtype). */
+bi_status bi_fp4_dequantize(bi_engine engine, void* dst, const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols,
+                            bi_dtype dtype, void* stream);
+
+/* The three products of a linear layer, each with both operands quantized along its
+ * own contraction; f32 accumulation, one rounding to out_dtype.
+ *   forward  y[M,N]  = x W + bias   xq of x [M][K], wq of W^T [N][K] (qt of W [K,N])
+ *   dX       dx[M,K] = dY W^T       gq of dY [M][N], wq of W [K][N]
+ *   dW       dw[K,N] = x^T dY       xq of x^T [K][M], gq of dY^T [N][M] (their qt)
+ * bias [N] (nullable) has out_dtype and is added in f32.  One chain of 64-wide blocks
+ * in ascending order per output element (a f32 result in pieces of 8192 of the
+ * contraction, added in order), no split, no atomics: run-to-run and batch invariant
+ * like the tensor-core tier.  Any sizes; outputs need the alignment of their type
+ * (rows of a multiple of 16 bytes on a 16-byte boundary are faster).  m = 0 writes +0
+ * to dw. */
+bi_status bi_fp4_forward(bi_engine engine, void* y, const uint8_t* xq, const uint8_t* xs, const uint8_t* wq,
+                         const uint8_t* ws, const void* bias, int64_t m, int64_t k, int64_t n, bi_dtype out_dtype,
+                         void* stream);
+bi_status bi_fp4_backward_dx(bi_engine engine, void* dx, const uint8_t* gq, const uint8_t* gs, const uint8_t* wq,
+                             const uint8_t* ws, int64_t m, int64_t k, int64_t n, bi_dtype out_dtype, void* stream);
+bi_status bi_fp4_backward_dw(bi_engine engine, void* dw, const uint8_t* xq, const uint8_t* xs, const uint8_t* gq,
+                             const uint8_t* gs, int64_t m, int64_t k, int64_t n, bi_dtype out_dtype, void* stream);
+
 /* Grouped forward: y[m,:] = round( X[m,:] * W[e(m)]^T ) with W [E,N,K] and
  * e(m) = row_experts[m]; rows with e(m) >= E are +0.  Rows need not be sorted.
  * Source: rublas 0.1.45 src/tensor_grouped/mod.rs, fn grouped_matmul_nt
@@ -369,6 +417,36 @@ bi_status bi_router_backward(bi_engine engine, void* dlogits, const void* logits
                              const uint32_t* ids, const float* weights, const uint32_t* counts, const uint32_t* rows,
                              const float* dweights, const float* dloss, int64_t t, int64_t e, int64_t k,
                              int normalize, bi_dtype dtype, void* stream);
+
+/* ---- Mixture-of-experts layer for the few tokens of a decoding step -------
+ *
+ *   h[t,j,:] = act(x[t,:] Wg[e]^T) * (x[t,:] Wu[e]^T)        e = ids[t,j], f32
+ *   y[t,:]   = round( sum over j of weights[t,j] * (h[t,j,:] Wd[e]^T) )
+ *
+ * x [T,K] and y [T,N] of dtype; ids [T,C] and weights [T,C] f32 as bi_router_forward
+ * gives them: an id >= E adds nothing (whatever its weight), a token without any
+ * choice gets a row of +0.  Wg and Wu [E,F,K], Wd [E,N,F] of dtype (the grouped
+ * calls' layout); w_gate NULL: h = act(x Wu^T).  act: v / (1 + e^-v) (SiLU),
+ * 0.5 v (1 + tanh(0.79788456 (v + 0.044715 v^3))) (GELU), max(v, 0).
+ *
+ * E <= 1024 and T * C <= 2048 (BI_ERR_UNSUPPORTED beyond: longer batches take the
+ * grouped calls).  Inner products are summed in f32 in an order fixed by K and F, a
+ * token's choices in the order of j: bit-identical run to run, and a row of y depends
+ * on its own x, ids and weights alone, whatever T.  Forward only.
+ * Scratch from the engine's pool: h, 4 T C F bytes. */
+typedef enum { BI_ACT_SILU = 0, BI_ACT_GELU = 1, BI_ACT_RELU = 2 } bi_activation;
+
+bi_status bi_moe_forward(bi_engine engine, void* y, const void* x, const uint32_t* ids, const float* weights,
+                         const void* w_gate, const void* w_up, const void* w_down, int64_t t, int64_t c, int64_t k,
+                         int64_t f, int64_t n, int64_t e, bi_activation activation, bi_dtype dtype, void* stream);
+
+/* The same with expert weights in MXFP4: gate and up as operands [E*F][K], down
+ * [E*N][F] (bi_fp4_quantize of the weights as [E*F, K] and [E*N, F]); their values
+ * enter exactly.  gate_q and gate_s NULL: no gate. */
+bi_status bi_moe_forward_fp4(bi_engine engine, void* y, const void* x, const uint32_t* ids, const float* weights,
+                             const uint8_t* gate_q, const uint8_t* gate_s, const uint8_t* up_q, const uint8_t* up_s,
+                             const uint8_t* down_q, const uint8_t* down_s, int64_t t, int64_t c, int64_t k, int64_t f,
+                             int64_t n, int64_t e, bi_activation activation, bi_dtype dtype, void* stream);
 
 /* ---- Gradient norm and clipping over a set of tensors --------------------
  *
