@@ -1,0 +1,801 @@
+// The few-token expert layer on tcgen05 (see moe.cu for the layer and its other form).
+//
+//   D [128 weight rows x tokens] = A [128 x K] B [tokens x K]^T
+//
+// The weights are the A operand: a decoding step is bound by reading them, and
+// this way each goes from memory to shared memory by TMA and on to the tensor cores without an
+// instruction of its own; the tokens, few, are the MMA's N.  A block takes 128 weight
+// rows of one expert at a time (hidden kernel: 64 of the gate's and 64 of up's, whose
+// products meet in the epilogue) and walks such units, one block per SM, the copies
+// running ahead from unit to unit.  An output element is one ascending chain over the
+// contraction in one f32 accumulator, whatever the number of tokens beside it.
+//
+// 16-bit weights: kind::f16, stages of 64.  The tokens of the hidden kernel are all tokens
+// of the batch, straight from x (up to 256 at a time): columns of tokens that chose
+// other experts are thrown away, which costs nothing next to gathering.  h enters the output
+// kernel as two 16-bit parts, high part and remainder, two MMAs into the same sum: to
+// 2^-17 of it in bf16.  f16 has not h's range: there h is kept in f32, and a kernel
+// between the two scales each choice's by a power of two, its largest to 2^14 (parts to
+// 2^-22 of a value, 2^-39 of the largest), which the sums are multiplied back by.
+//
+// MXFP4 weights: kind::mxf4 with block scales, stages of 256, the codes as they lie in
+// memory: no weight is ever expanded.  Its other operand has to be MXFP4 too, so a token's
+// x (and h) is written as a sum of PARTS rows in MXFP4: each part rounds what the parts
+// before left, per block of 32 with a scale that none of it exceeds, so a part leaves at
+// most a quarter of its scale's range and the twelfth less than 2^-23 of the block's largest
+// value.  The parts are N columns of their own (16 to a token, 12 used), added in the
+// epilogue from the smallest up.
+//
+// Sums of the output kernel's units go to memory once per choice; the block that
+// finishes the last unit of its 128 columns adds the choices of every token in order.
+#include "abi_util.h"
+#include "fp4.h"
+#include "moe.h"
+#include "tc_common.cuh"
+
+#include <cuda_fp4.h>
+
+namespace bi {
+namespace {
+
+constexpr int PARTS = 12, PART_ROWS = 16;  // MXFP4 rows of a token: used, and from one token to the next
+constexpr int T_LIMIT = 227 * 1024;
+constexpr int T_BARS = 512;
+constexpr int T_EX = 2 * 16 * 64 * 4;      // the epilogue's exchange between the gate's and up's warps
+constexpr int A_BYTES = 128 * 128;         // weights of a stage
+constexpr int MAX_STAGES = 12;
+constexpr int SF_COL = 256, SF_COLS = 24;  // tensor memory: accumulator, then two stages of scales (A 8, B 16)
+
+struct TcArgs {
+    MoeCall m;
+    uint16_t* h;        // 16-bit weights: planes [2][P][Fp]
+    float* hf;          // f16 weights, hidden kernel: h itself, [P][F]
+    const float* unscale;  // f16 weights, output kernel: [P] by which a place's sums are multiplied
+    uint8_t *hq, *hs;   // MXFP4: h's parts, an operand [16 places][F]
+    float* part;        // [P][Nq] the choices' sums
+    uint32_t* ticket;   // [tiles of N] units done
+    int64_t Fp, Nq;
+    int P, tiles, chunks;  // choices; row tiles of an expert; stages of the contraction
+    int cap;               // most tokens of a pass
+    int stage, depth;      // ring: bytes of a stage, stages
+    uint32_t fmt;          // 16-bit weights: 0 f16, 1 bf16
+    int out_fmt;           // y: 0 f16, 1 bf16, 2 f32
+    int out_tiles;         // tickets to clear
+    int* status;
+    unsigned long long wait_limit;
+};
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(lead)
+                 : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ void mma_16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc,
+                                         uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %7, 0;\n\tsetp.ne.b32 e, %8, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %4, [%5], [%6], p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr, uint32_t lead) {
+    constexpr uint32_t HI = (128u >> 4) | (1u << 14);
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b64 d;\n\tsetp.ne.b32 e, %3, 0;\n\tmov.b64 d, {%1, %2};\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}\n" ::"r"(taddr),
+        "r"(((saddr & 0x3FFFFu) >> 4) | (1u << 16)), "r"(HI), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+    return v;
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// A block's units, and within a unit its passes over the tokens.
+//   hidden: (expert, row tile), tiles of one expert next to one another
+//   output: (row tile, expert), so that whole tiles are finished one after the other
+// A pass: bf16 hidden, tokens [c0, c0 + 256) of the batch; else choices [c0, c0 + cap)
+// of the expert.
+template <bool FP4, bool OUT>
+struct Walk {
+    int u, e, tile, n, c0;
+    __device__ __forceinline__ bool more(const TcArgs& a, const Plan& p) const { return u < p.n * a.tiles; }
+    __device__ __forceinline__ void open(const TcArgs& a, const Plan& p) {
+        c0 = 0;
+        if (!more(a, p)) return;
+        const int slot = OUT ? u % p.n : u / a.tiles;
+        tile = OUT ? u / p.n : u % a.tiles;
+        e = p.active[slot];
+        n = FP4 || OUT ? static_cast<int>(p.cnt[e]) : a.m.T;
+    }
+    __device__ __forceinline__ void next(const TcArgs& a, const Plan& p) {
+        c0 += a.cap;
+        if (c0 < n) return;
+        u += gridDim.x;
+        open(a, p);
+    }
+    __device__ __forceinline__ int cols(const TcArgs& a) const { return min(a.cap, n - c0); }
+    __device__ __forceinline__ bool last_pass(const TcArgs& a) const { return c0 + a.cap >= n; }
+};
+
+// One part of a block of 32: the smallest scale that the largest magnitude does not
+// exceed six times of, as its byte.
+__device__ __forceinline__ uint32_t part_scale(uint32_t amax_bits) {
+    const uint32_t e = amax_bits >> 23, up = (amax_bits & 0x7fffffu) > 0x400000u ? 1u : 0u;
+    return e == 255u ? 255u : e + up < 2u ? 0u : e + up - 2u;
+}
+__device__ __forceinline__ float part_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+template <bool FP4, bool OUT>
+__global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
+    moe_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmSB, const TcArgs a) {
+    constexpr int ALIGN = FP4 ? 8 : 1;
+    constexpr int BPARTS = !FP4 && OUT ? 2 : 1;  // planes of B
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const MoeCall& m = a.m;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    uint8_t* after = smem_raw + plan_bytes(m.E, a.P, ALIGN);
+    float* ex = reinterpret_cast<float*>(after);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after + T_EX);
+    const uint32_t bar0 = smem_u32(bars), sbase = (bar0 + T_BARS + 1023u) & ~1023u;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
+    const uint32_t tfull = bar0 + 8u * (2 * MAX_STAGES), tempty = tfull + 8, drain = tfull + 16;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 3);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
+    uint32_t* last = slot + 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.depth; ++s) {
+            mbar_init(full_bar(s), FP4 ? 2 : 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 4);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(slot), 0);
+    if (!OUT) {
+        grid_dep_wait();
+        grid_dep_launch();
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < a.out_tiles; i += blockDim.x) a.ticket[i] = 0;
+    }
+    // (the output kernel: ids and weights were complete when the hidden kernel passed its
+    // own wait, and it let this kernel start only then)
+    const Plan p = build_plan<ALIGN>(smem_raw, m.ids, a.P, m.E);
+    const int64_t R = OUT ? m.N : m.F;       // rows of an expert
+    const bool gated = !OUT && m.gate != nullptr;
+    const int span = gated ? 64 : 128;       // rows of a tile, of each of the two matrices or of the one
+    Walk<FP4, OUT> w;
+    w.u = blockIdx.x;
+    w.open(a, p);
+    const int sfa_at = A_BYTES, b_at = A_BYTES + (FP4 ? 1024 : 0), b_bytes = a.cap * (FP4 ? PART_ROWS * 128 : 128);
+    const int sfb_at = b_at + b_bytes;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies, a lane each
+        // lanes 0, 1: 64 weight rows; then B's boxes of 16 rows; MXFP4: B's scales, 8 tokens a box
+        int s = 0, made = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        auto boxes = [&](const Walk<FP4, OUT>& x) { return FP4 ? x.cols(a) : (x.cols(a) + 15) / 16; };
+        auto weights = [&](const Walk<FP4, OUT>& x, int c) {
+            ok = __all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, a, DEV_TIMEOUT_PRODUCER));
+            if (!ok) return;
+            if (lane == 0) mbar_expect_tx(full_bar(s), A_BYTES + boxes(x) * BPARTS * 2048 + (FP4 ? (x.cols(a) + 7) / 8 * 1024 : 0));
+            __syncwarp();
+            const int64_t r = x.e * R + static_cast<int64_t>(x.tile) * span;
+            if (lane < 2)
+                tma_2d(sbase + s * a.stage + lane * (A_BYTES / 2), lane == 0 ? &tmA0 : &tmA1, c * (FP4 ? 128 : 64),
+                       static_cast<int>(gated ? r : r + lane * 64), full_bar(s));
+        };
+        auto tokens = [&](const Walk<FP4, OUT>& x, int c, int st) {
+            const int nb = boxes(x), first = FP4 || OUT ? static_cast<int>(p.first[x.e]) + x.c0 : x.c0;
+            if (lane < nb * BPARTS) {
+                const int part = lane / nb, b = lane - part * nb;
+                const int row = FP4 ? (first + b) * PART_ROWS : part * a.P + first + b * 16;
+                tma_2d(sbase + st * a.stage + b_at + part * b_bytes + b * 2048, &tmB, c * (FP4 ? 128 : 64), row, full_bar(st));
+            } else if (FP4 && lane < nb + (x.cols(a) + 7) / 8) {
+                tma_2d(sbase + st * a.stage + sfb_at + (lane - nb) * 1024, &tmSB, c * 256, first / 8 + lane - nb, full_bar(st));
+            }
+        };
+        auto advance = [&](Walk<FP4, OUT>& x, int& c) {
+            if (++c == a.chunks) { c = 0; x.next(a, p); }
+        };
+        Walk<FP4, OUT> x = w, x0 = w;
+        int c = 0, c0 = 0;
+        if (OUT) {  // the first stages' weights come in while the hidden kernel ends
+            for (; made < a.depth && x.more(a, p); ++made) {
+                weights(x, c);
+                if (++s == a.depth) { s = 0; ph ^= 1u; }
+                advance(x, c);
+            }
+            grid_dep_wait();
+            grid_dep_launch();
+            for (int i = 0; i < made; ++i) {
+                tokens(x0, c0, i);
+                advance(x0, c0);
+            }
+        }
+        while (x.more(a, p)) {
+            weights(x, c);
+            if (!ok) break;
+            tokens(x, c, s);
+            if (++s == a.depth) { s = 0; ph ^= 1u; }
+            ++made;
+            advance(x, c);
+        }
+        if (!ok) {  // a wait gave up: the copies in flight land first
+            __syncwarp();
+            const unsigned long long t0 = globaltimer();
+            while (globaltimer() - t0 < 1000000ull) {}
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        const uint32_t lead = elect_lane();
+        int s = 0, sf = 0;
+        uint32_t ph = 0, it = 0;
+        bool ok = true;
+        for (; ok && w.more(a, p); w.next(a, p), ++it) {
+            if (it) ok = __all_sync(0xffffffffu, mbar_wait_fast(tempty, (it - 1) & 1u, abort_flag, a, DEV_TIMEOUT_MMA));
+            if (!ok) break;
+            tc_fence_after();
+            const int cols = w.cols(a);
+            const uint32_t N = FP4 ? cols * PART_ROWS : (cols + 15) / 16 * 16;
+            for (int c = 0; c < a.chunks; ++c) {
+                ok = __all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, a, DEV_TIMEOUT_MMA));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t st = sbase + s * a.stage, da = desc_lo(st, false), db = desc_lo(st + b_at, false);
+                if constexpr (FP4) {
+                    const uint32_t ta = tmem + SF_COL + sf * SF_COLS, tb = ta + 8;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        scales_to_tmem(ta + k * 4, st + sfa_at + k * 512, lead);
+                        scales_to_tmem(tb + k * 8, st + sfb_at + k * 512, lead);
+                        if (cols > 8) scales_to_tmem(tb + k * 8 + 4, st + sfb_at + 1024 + k * 512, lead);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t id = (kk & 1) * 2;
+                        mma_mxf4(tmem, da + kk * K_STEP, db + kk * K_STEP,
+                                 (id << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 29), ta + (kk >> 1) * 4,
+                                 tb + (kk >> 1) * 8, (c | kk) != 0 ? 1u : 0u, lead);
+                    }
+                    sf ^= 1;
+                } else {
+                    const uint32_t idesc = (1u << 4) | (a.fmt << 7) | (a.fmt << 10) | ((N >> 3) << 17) | (8u << 24);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                        for (int part = 0; part < BPARTS; ++part)
+                            mma_16(tmem, da + kk * K_STEP, db + part * (b_bytes >> 4) + kk * K_STEP, idesc, (c | kk | part) != 0 ? 1u : 0u, lead);
+                }
+                commit(empty_bar(s), lead);
+                if (++s == a.depth) { s = 0; ph ^= 1u; }
+            }
+            if (!ok) break;
+            commit(tfull, lead);
+        }
+        __syncwarp();
+        if (lead) {
+            commit(drain, 1u);
+            mbar_drain(drain, 0);
+        }
+        __syncwarp();
+    } else if (FP4 && warp == 6) {
+        // ------------------------------------------------------------ the weights' scales
+        // A lane has rows lane and lane + 32 of either half of the tile, wherever their
+        // bytes lie, and puts them side by side in the order that the tensor cores take.
+        // Loaded a stage ahead.
+        const int64_t Lp = fp4_padded(OUT ? m.F : m.K), all = m.E * R;
+        const uint8_t* s0 = OUT ? m.down_s : gated ? m.gate_s : m.up_s;
+        const uint8_t* s1 = OUT ? m.down_s : m.up_s;
+        int s = 0, c = 0;
+        uint32_t ph = 0;
+        uint32_t v[8];
+        const uint8_t* at[4];
+        auto rows = [&] {
+            const int64_t r = w.e * R + static_cast<int64_t>(w.tile) * span;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t row = lmin(r + lane + (j & 1) * 32 + (j >= 2 && !gated ? 64 : 0), all - 1);
+                at[j] = (j < 2 ? s0 : s1) + fp4_scale_at(row, 0, Lp);
+            }
+        };
+        auto load = [&] {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int atom = 2 * c + (j >> 2);
+                v[j] = __ldg(reinterpret_cast<const uint32_t*>(at[j & 3] + static_cast<int64_t>(atom) * 512));
+            }
+        };
+        if (w.more(a, p)) {
+            rows();
+            load();
+        }
+        while (w.more(a, p)) {
+            if (!__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, a, DEV_TIMEOUT_PRODUCER))) break;
+            const uint32_t to = sbase + s * a.stage + sfa_at + lane * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 512), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(full_bar(s));
+            if (++s == a.depth) { s = 0; ph ^= 1u; }
+            if (++c == a.chunks) {
+                c = 0;
+                w.next(a, p);
+                if (w.more(a, p)) rows();
+            }
+            if (w.more(a, p)) load();
+        }
+    } else if (warp >= 2 && warp < 6) {
+        // ------------------------------------------------------------ epilogue
+        if (OUT) grid_dep_wait();
+        const int q = warp & 3;
+        uint32_t it = 0;
+        int k = 0;  // exchanges so far: the buffers take turns over all units
+        auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        auto all_warps = [](int ok) {
+            uint32_t r;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}\n"
+                         : "=r"(r) : "r"(ok) : "memory");
+            return r != 0;
+        };
+        for (; w.more(a, p); w.next(a, p), ++it) {
+            // the four warps go on or give up together: they meet below
+            if (!all_warps(__all_sync(0xffffffffu, mbar_wait(tfull, it & 1u, abort_flag, a, DEV_TIMEOUT_EPILOGUE)))) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
+            // the choices of this pass: places i0 .. i0 + items - 1 of the expert's
+            int i0 = w.c0, items = w.cols(a);
+            if (!FP4 && !OUT) {
+                const int n = static_cast<int>(p.cnt[w.e]);
+                i0 = items = 0;
+                for (int i = lane; i < n; i += 32) {
+                    const int tok = p.list[p.first[w.e] + i] / m.C;
+                    i0 += tok < w.c0;
+                    items += tok >= w.c0 && tok < w.c0 + a.cap;
+                }
+                i0 = __reduce_add_sync(0xffffffffu, i0);
+                items = __reduce_add_sync(0xffffffffu, items);
+            }
+            const uint16_t* mine = p.list + p.first[w.e] + i0;
+            const int place = static_cast<int>(p.first[w.e]) + i0;
+            const int half = gated ? q & 1 : q;
+            const int64_t row = static_cast<int64_t>(w.tile) * span + half * 32 + lane;  // of the hidden layer or the output
+            for (int b = 0; b < items; b += 16) {
+                const int cnt = min(16, items - b);
+                float v[16];
+                if constexpr (FP4) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[j] = 0.0f;
+                        if (j >= cnt) continue;
+                        uint32_t r[16];
+                        __syncwarp();
+                        tmem_ld16(tb + (b + j) * PART_ROWS, r);
+                        v[j] = __uint_as_float(r[PARTS - 1]);
+#pragma unroll
+                        for (int x = PARTS - 2; x >= 0; --x) v[j] = __fadd_rn(v[j], __uint_as_float(r[x]));
+                    }
+                } else {
+                    __syncwarp();
+                    uint32_t r[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int i = min(b + j, items - 1);
+                        r[j] = tmem_ld1(tb + (OUT ? i : mine[i] / m.C - w.c0));
+                    }
+                    tmem_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+                }
+                if (OUT) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < cnt && row < R)
+                            __stcg(a.part + mine[b + j] * a.Nq + row, a.unscale ? v[j] * __ldg(a.unscale + place + b + j) : v[j]);
+                    continue;
+                }
+                if (gated) {  // warps 2 and 3 have the rows of up that 0 and 1 have of the gate
+                    float* e = ex + (k++ & 1) * (16 * 64);
+                    if (q >= 2) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) e[j * 64 + (q & 1) * 32 + lane] = v[j];
+                    }
+                    meet();
+                    if (q >= 2) continue;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], m.act) * e[j * 64 + q * 32 + lane];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], m.act);
+                }
+                if constexpr (FP4) {
+                    if (row - lane >= a.Fp) continue;  // (whole blocks of 32)
+                    for (int j = 0; j < cnt; ++j) {
+                        float r = 0.0f;
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (x == j) r = v[x];
+                        if (row >= m.F) r = 0.0f;
+                        const int64_t at = static_cast<int64_t>(place + b + j) * PART_ROWS;
+                        for (int x = 0; x < PARTS; ++x) {
+                            const uint32_t byte = part_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(r) & 0x7fffffffu));
+                            uint32_t code = 0;
+                            if (byte != 255u) {
+                                code = __nv_cvt_float2_to_fp4x2(make_float2(r * part_inverse(byte), 0.0f), __NV_E2M1, cudaRoundNearest) & 15u;
+                                r = __fsub_rn(r, fp4_code_value(code) * fp4_scale_value(byte));
+                            } else {
+                                r = 0.0f;
+                            }
+                            uint32_t word = code << (4 * (lane & 7));
+                            word |= __shfl_xor_sync(0xffffffffu, word, 1);
+                            word |= __shfl_xor_sync(0xffffffffu, word, 2);
+                            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+                            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + (at + x) * (a.Fp / 2) + row / 2) = word;
+                            if (lane == 0) a.hs[fp4_scale_at(at + x, row >> 5, a.Fp)] = static_cast<uint8_t>(byte);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (j >= cnt || row >= m.F) continue;
+                        if (a.hf) {
+                            a.hf[static_cast<int64_t>(place + b + j) * m.F + row] = v[j];
+                            continue;
+                        }
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(v[j]), lo = __float2bfloat16_rn(v[j] - __bfloat162float(hi));
+                        uint16_t* o = a.h + static_cast<int64_t>(place + b + j) * a.Fp + row;
+                        o[0] = __bfloat16_as_ushort(hi);
+                        o[static_cast<int64_t>(a.P) * a.Fp] = __bfloat16_as_ushort(lo);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(tempty);
+            if (OUT && w.last_pass(a)) {
+                // the last of the tile's units adds up the choices
+                __threadfence();
+                meet();
+                if (threadIdx.x == 64) *last = atomicAdd(a.ticket + w.tile, 1u) == static_cast<uint32_t>(p.n - 1);
+                meet();
+                if (*reinterpret_cast<volatile uint32_t*>(last) != 0u) {
+                    __threadfence();
+                    const int64_t n0 = static_cast<int64_t>(w.tile) * 128 + lane * 4;
+                    for (int t0 = q; t0 < m.T; t0 += 16) {  // four tokens at a time: t0, t0 + 4, ..
+                        float4 sum[4] = {};
+#pragma unroll 4
+                        for (int j = 0; j < m.C; ++j) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int t = t0 + 4 * i, pr = t * m.C + j;
+                                if (t >= m.T || __ldg(m.ids + pr) >= static_cast<uint32_t>(m.E)) continue;
+                                const float4 d = __ldcg(reinterpret_cast<const float4*>(a.part + pr * a.Nq + n0));
+                                const float wt = __ldg(m.weights + pr);
+                                sum[i].x = fmaf(wt, d.x, sum[i].x);
+                                sum[i].y = fmaf(wt, d.y, sum[i].y);
+                                sum[i].z = fmaf(wt, d.z, sum[i].z);
+                                sum[i].w = fmaf(wt, d.w, sum[i].w);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int t = t0 + 4 * i;
+                            const float s[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                if (t >= m.T || n0 + x >= m.N) continue;
+                                const int64_t o = t * m.N + n0 + x;
+                                if (a.out_fmt == 2) static_cast<float*>(m.y)[o] = s[x];
+                                else if (a.out_fmt == 1) OutT<1>::store1(m.y, o, s[x]);
+                                else OutT<0>::store1(m.y, o, s[x]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        if (OUT && p.n == 0) {  // no choice at all
+            const int64_t es = a.out_fmt == 2 ? 4 : 2, bytes = m.T * m.N * es;
+            for (int64_t i = (blockIdx.x * 128ll + (threadIdx.x - 64)) * es; i < bytes; i += gridDim.x * 128ll * es) {
+                if (es == 4) *reinterpret_cast<float*>(static_cast<uint8_t*>(m.y) + i) = 0.0f;
+                else *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(m.y) + i) = 0;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// x as its parts, at the places of the tokens' choices; and zeros for the scales of h's
+// parts, whose last blocks no one writes.  16 lanes to 128 elements of a token.
+template <typename T>
+__global__ void __launch_bounds__(256) moe_parts_kernel(const T* x, const uint32_t* ids, uint8_t* xq, uint8_t* xs, uint8_t* hs, int64_t hs_bytes,
+                                                        int T_, int C, int E, int64_t K) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int P = T_ * C;
+    const Plan p = build_plan<8>(smem, ids, P, E);
+    uint16_t* place = reinterpret_cast<uint16_t*>(smem + plan_bytes(E, P, 8));  // of each choice
+    for (int s = threadIdx.x >> 5; s < p.n; s += 8) {
+        const int e = p.active[s];
+        for (int i = threadIdx.x & 31; i < static_cast<int>(p.cnt[e]); i += 32) place[p.list[p.first[e] + i]] = static_cast<uint16_t>(p.first[e] + i);
+    }
+    __syncthreads();
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < hs_bytes / 16; i += gridDim.x * 256ll) reinterpret_cast<uint4*>(hs)[i] = make_uint4(0, 0, 0, 0);
+    const int64_t Kp = fp4_padded(K), per = Kp / 128;
+    const int l16 = threadIdx.x & 15;
+    for (int64_t i = blockIdx.x * 16ll + (threadIdx.x >> 4); i < (T_ * per + 1) / 2 * 2; i += gridDim.x * 16ll) {  // (both halves of a warp)
+        const bool live = i < T_ * per;
+        const int64_t t = live ? i / per : 0, k = (live ? i - t * per : 0) * 128 + l16 * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = live && k + j < K ? static_cast<float>(x[t * K + k + j]) : 0.0f;
+        for (int part = 0; part < PARTS; ++part) {
+            uint32_t mx = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mx = max(mx, __float_as_uint(v[j]) & 0x7fffffffu);
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const uint32_t byte = part_scale(mx);
+            uint32_t word = 0;
+            if (byte != 255u) {
+                const float inv = part_inverse(byte), scale = fp4_scale_value(byte);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const uint32_t c = __nv_cvt_float2_to_fp4x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_E2M1, cudaRoundNearest);
+                    word |= c << (4 * j);
+                    v[j] = __fsub_rn(v[j], fp4_code_value(c & 15u) * scale);
+                    v[j + 1] = __fsub_rn(v[j + 1], fp4_code_value(c >> 4) * scale);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            }
+            if (!live) continue;
+            for (int j = 0; j < C; ++j) {
+                if (__ldg(ids + t * C + j) >= static_cast<uint32_t>(E)) continue;
+                const int64_t r = static_cast<int64_t>(place[t * C + j]) * PART_ROWS + part;
+                *reinterpret_cast<uint32_t*>(xq + r * (Kp / 2) + k / 2) = word;
+                if ((l16 & 3) == 0) xs[fp4_scale_at(r, k >> 5, Kp)] = static_cast<uint8_t>(byte);
+            }
+        }
+    }
+}
+
+// f16 weights: a choice's h, scaled by a power of two, in two f16 planes.  A block per place
+// (places that no choice has hold anything, and are not read).
+__global__ void __launch_bounds__(256) moe_planes_kernel(uint16_t* h, float* unscale, const float* hf, int64_t F, int64_t Fp, int P) {
+    __shared__ uint32_t top[8];
+    grid_dep_wait();
+    grid_dep_launch();
+    const float* v = hf + blockIdx.x * F;
+    uint32_t mx = 0;
+    for (int64_t f = threadIdx.x; f < F; f += 256) mx = max(mx, __float_as_uint(v[f]) & 0x7fffffffu);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, top[i]);
+    const uint32_t e = mx >> 23, field = e == 255u ? 127u : min(max(268u - e, 1u), 253u);
+    const float scale = __uint_as_float(field << 23);
+    uint16_t* o = h + blockIdx.x * Fp;
+    for (int64_t f = threadIdx.x; f < F; f += 256) {
+        const float x = v[f] * scale;
+        const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+        o[f] = __half_as_ushort(hi);
+        o[P * Fp + f] = __half_as_ushort(lo);
+    }
+    if (threadIdx.x == 0) unscale[blockIdx.x] = __uint_as_float((254u - field) << 23);
+}
+
+// rows of 16-bit x copied to rows of Kp (zeros past K)
+__global__ void __launch_bounds__(256) moe_copy_kernel(uint16_t* out, const uint16_t* x, int64_t T, int64_t K, int64_t Kp) {
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < T * Kp; i += gridDim.x * 256ll) {
+        const int64_t t = i / Kp, k = i - t * Kp;
+        out[i] = k < K ? x[t * K + k] : 0;
+    }
+}
+
+// [rows][inner] of 16-bit (box 64 x box_rows) or 8-bit (box 128 x box_rows) elements, pitch bytes apart.
+cudaError_t row_map(CUtensorMap* mp, bool bytes, const void* ptr, uint64_t inner, uint64_t rows, uint64_t pitch, uint32_t box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t dims[2] = {inner, rows}, strides[1] = {pitch};
+    cuuint32_t box[2] = {bytes ? 128u : 64u, box_rows}, es[2] = {1, 1};
+    return enc(mp, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess : cudaErrorInvalidValue;
+}
+cudaError_t word_map(CUtensorMap* mp, const void* ptr, uint64_t pieces, uint64_t words) {
+    auto enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t dims[2] = {words, pieces}, strides[1] = {words * 4};
+    cuuint32_t box[2] = {256, 1}, es[2] = {1, 1};
+    return enc(mp, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Scratch, part by part.
+struct Room {
+    int64_t x, xs, h, hs, hf, scale, part, ticket, bytes;  // offsets, and all
+    int64_t places, Kp, Fp, Nq;
+};
+Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
+    Room r{};
+    const int64_t P = static_cast<int64_t>(m.T) * m.C;
+    r.places = (plan_places(m.E, P, 8) + 7) / 8 * 8;
+    r.Kp = fp4 ? fp4_padded(m.K) : (m.K + 63) / 64 * 64;
+    r.Fp = fp4 ? fp4_padded(m.F) : (m.F + 7) / 8 * 8;
+    r.Nq = (m.N + 127) / 128 * 128;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t o = at;
+        at += round256(bytes);
+        return o;
+    };
+    const int64_t rows = r.places * PART_ROWS;
+    r.x = take(fp4 ? rows * (r.Kp / 2) : copy_x ? m.T * r.Kp * 2 : 0);
+    r.xs = take(fp4 ? rows / 128 * r.Kp * 4 : 0);
+    r.h = take(fp4 ? rows * (r.Fp / 2) : 2 * P * r.Fp * 2);
+    r.hs = take(fp4 ? rows / 128 * r.Fp * 4 : 0);
+    r.hf = take(!fp4 && f16 ? P * m.F * 4 : 0);
+    r.scale = take(!fp4 && f16 ? P * 4 : 0);
+    r.part = take(P * r.Nq * 4);
+    r.ticket = take(r.Nq / 128 * 4);
+    r.bytes = at;
+    return r;
+}
+
+template <bool FP4, bool OUT>
+cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b, const CUtensorMap& sb) {
+    auto kern = moe_tc_kernel<FP4, OUT>;
+    static PerDeviceOnce setup;
+    cudaError_t e = setup.run(c.eng->device, [&](int&) {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T_LIMIT);
+    });
+    if (e != cudaSuccess) return e;
+    constexpr int ALIGN = FP4 ? 8 : 1;
+    const int64_t rows = OUT ? a.m.N : a.m.F, len = OUT ? a.m.F : a.m.K;
+    const int span = !OUT && a.m.gate ? 64 : 128;
+    a.tiles = static_cast<int>((rows + span - 1) / span);
+    a.chunks = static_cast<int>(FP4 ? fp4_padded(len) / 256 : (len + 63) / 64);
+    const int tokens16 = (a.m.T + 15) / 16 * 16;
+    a.cap = FP4 ? (a.m.T <= 8 ? 8 : 16) : OUT ? (tokens16 < 128 ? tokens16 : 128) : (tokens16 < 256 ? tokens16 : 256);
+    a.stage = A_BYTES + (FP4 ? 1024 + a.cap * (PART_ROWS * 128) + a.cap / 8 * 1024 : a.cap * 128 * (OUT ? 2 : 1));
+    const int64_t fixed = plan_bytes(a.m.E, a.P, ALIGN) + T_EX + T_BARS + 1024;
+    a.depth = static_cast<int>(lmin(MAX_STAGES, (T_LIMIT - fixed) / a.stage));
+    if (a.depth < 2) return cudaErrorInvalidConfiguration;
+    const int64_t units = a.tiles * lmin(a.m.E, a.P);  // at most
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(lmin(units, c.sm_count))), dim3(FP4 ? 224 : 192), static_cast<size_t>(fixed + a.depth * a.stage),
+                   c.stream, a0, a1, b, sb, a);
+    if (e != cudaSuccess) return e;
+    c.count();
+    return cudaGetLastError();
+}
+
+template <bool FP4>
+cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype dt, uint8_t* scratch) {
+    const bool f16 = !FP4 && dt == BI_F16;
+    const Room r = room(m, FP4, copy_x, f16);
+    TcArgs a{};
+    a.m = m;
+    a.P = m.T * m.C;
+    a.h = reinterpret_cast<uint16_t*>(scratch + r.h);
+    a.hq = scratch + r.h;
+    a.hs = scratch + r.hs;
+    a.part = reinterpret_cast<float*>(scratch + r.part);
+    a.ticket = reinterpret_cast<uint32_t*>(scratch + r.ticket);
+    a.Fp = r.Fp;
+    a.Nq = r.Nq;
+    a.out_tiles = static_cast<int>(r.Nq / 128);
+    a.fmt = dt == BI_BF16;
+    if (f16) a.hf = reinterpret_cast<float*>(scratch + r.hf);
+    a.out_fmt = dt == BI_F32 ? 2 : dt == BI_BF16 ? 1 : 0;
+    a.status = c.status;
+    a.wait_limit = c.wait_limit_ns;
+    CUtensorMap gate, up, down, mx, mh, sx, sh;
+    cudaError_t e;
+    const int64_t rows = r.places * PART_ROWS, ef = m.E * m.F, en = m.E * m.N;
+    if (FP4) {
+        uint8_t *xq = scratch + r.x, *xs = scratch + r.xs;
+        const int smem = static_cast<int>(plan_bytes(m.E, a.P, 8) + (2 * a.P + 15) / 16 * 16);
+        const int64_t tasks = (m.T * (r.Kp / 128) + 15) / 16, zero = rows / 128 * r.Fp * 4;
+        const dim3 grid(static_cast<unsigned>(lmin(tasks > 16 ? tasks : 16, 4 * c.sm_count)));
+        auto go = [&](auto kern, auto* x) {
+            return launch_pdl(kern, grid, dim3(256), static_cast<size_t>(smem), c.stream, x, m.ids, xq, xs, a.hs, zero, m.T, m.C, m.E, m.K);
+        };
+        e = dt == BI_F32    ? go(moe_parts_kernel<float>, static_cast<const float*>(m.x))
+            : dt == BI_BF16 ? go(moe_parts_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16*>(m.x))
+                            : go(moe_parts_kernel<__half>, static_cast<const __half*>(m.x));
+        if (e != cudaSuccess) return e;
+        c.count();
+        if ((e = row_map(&up, true, m.up, r.Kp / 2, ef, r.Kp / 2, 64)) != cudaSuccess) return e;
+        if (m.gate && (e = row_map(&gate, true, m.gate, r.Kp / 2, ef, r.Kp / 2, 64)) != cudaSuccess) return e;
+        if ((e = row_map(&down, true, m.down, r.Fp / 2, en, r.Fp / 2, 64)) != cudaSuccess) return e;
+        if ((e = row_map(&mx, true, xq, r.Kp / 2, rows, r.Kp / 2, 16)) != cudaSuccess) return e;
+        if ((e = row_map(&mh, true, a.hq, r.Fp / 2, rows, r.Fp / 2, 16)) != cudaSuccess) return e;
+        if ((e = word_map(&sx, xs, rows / 128, r.Kp)) != cudaSuccess) return e;
+        if ((e = word_map(&sh, a.hs, rows / 128, r.Fp)) != cudaSuccess) return e;
+    } else {
+        const void* x = m.x;
+        int64_t pitch = m.K;
+        if (copy_x) {
+            uint16_t* xc = reinterpret_cast<uint16_t*>(scratch + r.x);
+            e = launch_pdl(moe_copy_kernel, dim3(static_cast<unsigned>(lmin((m.T * r.Kp + 255) / 256, 4 * c.sm_count))), dim3(256), 0, c.stream, xc,
+                           static_cast<const uint16_t*>(m.x), static_cast<int64_t>(m.T), m.K, r.Kp);
+            if (e != cudaSuccess) return e;
+            c.count();
+            x = xc;
+            pitch = r.Kp;
+        }
+        if ((e = row_map(&up, false, m.up, m.K, ef, m.K * 2, 64)) != cudaSuccess) return e;
+        if (m.gate && (e = row_map(&gate, false, m.gate, m.K, ef, m.K * 2, 64)) != cudaSuccess) return e;
+        if ((e = row_map(&down, false, m.down, m.F, en, m.F * 2, 64)) != cudaSuccess) return e;
+        if ((e = row_map(&mx, false, x, m.K, m.T, pitch * 2, 16)) != cudaSuccess) return e;
+        if ((e = row_map(&mh, false, a.h, m.F, 2ll * a.P, r.Fp * 2, 16)) != cudaSuccess) return e;
+        sx = sh = mx;
+    }
+    if (!m.gate) gate = up;
+    if ((e = launch<FP4, false>(c, a, gate, up, mx, sx)) != cudaSuccess) return e;
+    if (f16) {
+        float* unscale = reinterpret_cast<float*>(scratch + r.scale);
+        e = launch_pdl(moe_planes_kernel, dim3(static_cast<unsigned>(a.P)), dim3(256), 0, c.stream, a.h, unscale, a.hf, m.F, a.Fp, a.P);
+        if (e != cudaSuccess) return e;
+        c.count();
+        a.unscale = unscale;
+    }
+    return launch<FP4, true>(c, a, down, down, mh, sh);
+}
+
+}  // namespace
+
+int64_t moe_tc_scratch_bytes(const MoeCall& m, bool fp4, bool copy_x, bi_dtype dt) { return room(m, fp4, copy_x, dt == BI_F16).bytes; }
+
+cudaError_t moe_tc(const LaunchCtx& c, const MoeCall& m, bool fp4, bool copy_x, bi_dtype dt, void* scratch) {
+    return fp4 ? moe_form<true>(c, m, copy_x, dt, static_cast<uint8_t*>(scratch)) : moe_form<false>(c, m, copy_x, dt, static_cast<uint8_t*>(scratch));
+}
+
+}  // namespace bi
