@@ -26,14 +26,18 @@
 // value.  The parts are N columns of their own (16 to a token, 12 used), added in the
 // epilogue from the smallest up.
 //
-// Sums of the output kernel's units go to memory once per choice; the block that
-// finishes the last unit of its 128 columns adds the choices of every token in order.
+// Sums of the output kernel's units go to memory once per choice, and a third, small
+// kernel adds every token's choices in order.  (A block that adds up a tile once it has
+// finished the tile's last unit is late for its next unit, and so the last again: 182
+// against 95 us for 64 tokens, 64 experts of 2048 x 1408.)
 #include "abi_util.h"
 #include "fp4.h"
 #include "moe.h"
 #include "tc_common.cuh"
 
 #include <cuda_fp4.h>
+
+#include <type_traits>
 
 namespace bi {
 namespace {
@@ -53,14 +57,11 @@ struct TcArgs {
     const float* unscale;  // f16 weights, output kernel: [P] by which a place's sums are multiplied
     uint8_t *hq, *hs;   // MXFP4: h's parts, an operand [16 places][F]
     float* part;        // [P][Nq] the choices' sums
-    uint32_t* ticket;   // [tiles of N] units done
     int64_t Fp, Nq;
     int P, tiles, chunks;  // choices; row tiles of an expert; stages of the contraction
     int cap;               // most tokens of a pass
     int stage, depth;      // ring: bytes of a stage, stages
     uint32_t fmt;          // 16-bit weights: 0 f16, 1 bf16
-    int out_fmt;           // y: 0 f16, 1 bf16, 2 f32
-    int out_tiles;         // tickets to clear
     int* status;
     unsigned long long wait_limit;
 };
@@ -132,7 +133,6 @@ struct Walk {
         open(a, p);
     }
     __device__ __forceinline__ int cols(const TcArgs& a) const { return min(a.cap, n - c0); }
-    __device__ __forceinline__ bool last_pass(const TcArgs& a) const { return c0 + a.cap >= n; }
 };
 
 // One part of a block of 32: the smallest scale that the largest magnitude does not
@@ -142,6 +142,52 @@ __device__ __forceinline__ uint32_t part_scale(uint32_t amax_bits) {
     return e == 255u ? 255u : e + up < 2u ? 0u : e + up - 2u;
 }
 __device__ __forceinline__ float part_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// h of a lane's row for n tokens, places step apart: the next kernel's operand.
+template <bool FP4>
+__device__ __forceinline__ void hidden_out(const TcArgs& a, float (&r)[8], int64_t place, int step, int n, int64_t row) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (FP4) {
+        if (row - lane >= a.Fp) return;  // (whole blocks of 32)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (row >= a.m.F) r[j] = 0.0f;
+        for (int x = 0; x < PARTS; ++x) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // (independent of one another: they hide each other's latency)
+                if (j >= n) continue;
+                const uint32_t byte = part_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(r[j]) & 0x7fffffffu));
+                uint32_t code = 0;
+                if (byte != 255u) {
+                    code = __nv_cvt_float2_to_fp4x2(make_float2(r[j] * part_inverse(byte), 0.0f), __NV_E2M1, cudaRoundNearest) & 15u;
+                    r[j] = __fsub_rn(r[j], fp4_code_value(code) * fp4_scale_value(byte));
+                } else {
+                    r[j] = 0.0f;
+                }
+                uint32_t word = code << (4 * (lane & 7));
+                word |= __shfl_xor_sync(0xffffffffu, word, 1);
+                word |= __shfl_xor_sync(0xffffffffu, word, 2);
+                word |= __shfl_xor_sync(0xffffffffu, word, 4);
+                const int64_t at = (place + j * step) * PART_ROWS + x;
+                if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + at * (a.Fp / 2) + row / 2) = word;
+                if (lane == 0) a.hs[fp4_scale_at(at, row >> 5, a.Fp)] = static_cast<uint8_t>(byte);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= n || row >= a.m.F) continue;
+            if (a.hf) {
+                a.hf[(place + j * step) * a.m.F + row] = r[j];
+                continue;
+            }
+            const __nv_bfloat16 hi = __float2bfloat16_rn(r[j]), lo = __float2bfloat16_rn(r[j] - __bfloat162float(hi));
+            uint16_t* o = a.h + (place + j * step) * a.Fp + row;
+            o[0] = __bfloat16_as_ushort(hi);
+            o[static_cast<int64_t>(a.P) * a.Fp] = __bfloat16_as_ushort(lo);
+        }
+    }
+}
 
 template <bool FP4, bool OUT>
 __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
@@ -161,7 +207,6 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
     const uint32_t tfull = bar0 + 8u * (2 * MAX_STAGES), tempty = tfull + 8, drain = tfull + 16;
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
-    uint32_t* last = slot + 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.depth; ++s) {
@@ -185,8 +230,6 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
     if (!OUT) {
         grid_dep_wait();
         grid_dep_launch();
-        if (blockIdx.x == 0)
-            for (int i = threadIdx.x; i < a.out_tiles; i += blockDim.x) a.ticket[i] = 0;
     }
     // (the output kernel: ids and weights were complete when the hidden kernel passed its
     // own wait, and it let this kernel start only then)
@@ -376,6 +419,11 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
             if (!all_warps(__all_sync(0xffffffffu, mbar_wait(tfull, it & 1u, abort_flag, a, DEV_TIMEOUT_EPILOGUE)))) break;
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
+            auto drained = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(tempty);
+            };
             // the choices of this pass: places i0 .. i0 + items - 1 of the expert's
             int i0 = w.c0, items = w.cols(a);
             if (!FP4 && !OUT) {
@@ -420,6 +468,7 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
                 }
+                if (b + 16 >= items) drained();  // the last of the accumulator: the next pass's MMAs may start
                 if (OUT) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -427,112 +476,31 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
                             __stcg(a.part + mine[b + j] * a.Nq + row, a.unscale ? v[j] * __ldg(a.unscale + place + b + j) : v[j]);
                     continue;
                 }
-                if (gated) {  // warps 2 and 3 have the rows of up that 0 and 1 have of the gate
-                    float* e = ex + (k++ & 1) * (16 * 64);
-                    if (q >= 2) {
+                float r[8];
+                if (gated) {
+                    // warps 0 and 1 have the gate's rows, 2 and 3 up's: they swap half, the
+                    // first two finish the even tokens, the others the odd ones
+                    float* e = ex + (k++ & 1) * (16 * 64) + half * 32 + lane;
+                    const bool odd = q >= 2;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) e[j * 64 + (q & 1) * 32 + lane] = v[j];
-                    }
+                    for (int j = 0; j < 8; ++j) e[(2 * j + (odd ? 0 : 1)) * 64] = odd ? v[2 * j] : v[2 * j + 1];
                     meet();
-                    if (q >= 2) continue;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], m.act) * e[j * 64 + q * 32 + lane];
+                    for (int j = 0; j < 8; ++j) {
+                        const float other = e[(2 * j + (odd ? 1 : 0)) * 64];
+                        r[j] = odd ? activate(other, m.act) * v[2 * j + 1] : activate(v[2 * j], m.act) * other;
+                    }
+                    hidden_out<FP4>(a, r, place + b + (odd ? 1 : 0), 2, (cnt + (odd ? 0 : 1)) / 2, row);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], m.act);
-                }
-                if constexpr (FP4) {
-                    if (row - lane >= a.Fp) continue;  // (whole blocks of 32)
-                    for (int j = 0; j < cnt; ++j) {
-                        float r = 0.0f;
+                    for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            if (x == j) r = v[x];
-                        if (row >= m.F) r = 0.0f;
-                        const int64_t at = static_cast<int64_t>(place + b + j) * PART_ROWS;
-                        for (int x = 0; x < PARTS; ++x) {
-                            const uint32_t byte = part_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(r) & 0x7fffffffu));
-                            uint32_t code = 0;
-                            if (byte != 255u) {
-                                code = __nv_cvt_float2_to_fp4x2(make_float2(r * part_inverse(byte), 0.0f), __NV_E2M1, cudaRoundNearest) & 15u;
-                                r = __fsub_rn(r, fp4_code_value(code) * fp4_scale_value(byte));
-                            } else {
-                                r = 0.0f;
-                            }
-                            uint32_t word = code << (4 * (lane & 7));
-                            word |= __shfl_xor_sync(0xffffffffu, word, 1);
-                            word |= __shfl_xor_sync(0xffffffffu, word, 2);
-                            word |= __shfl_xor_sync(0xffffffffu, word, 4);
-                            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + (at + x) * (a.Fp / 2) + row / 2) = word;
-                            if (lane == 0) a.hs[fp4_scale_at(at + x, row >> 5, a.Fp)] = static_cast<uint8_t>(byte);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (j >= cnt || row >= m.F) continue;
-                        if (a.hf) {
-                            a.hf[static_cast<int64_t>(place + b + j) * m.F + row] = v[j];
-                            continue;
-                        }
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v[j]), lo = __float2bfloat16_rn(v[j] - __bfloat162float(hi));
-                        uint16_t* o = a.h + static_cast<int64_t>(place + b + j) * a.Fp + row;
-                        o[0] = __bfloat16_as_ushort(hi);
-                        o[static_cast<int64_t>(a.P) * a.Fp] = __bfloat16_as_ushort(lo);
+                        for (int j = 0; j < 8; ++j) r[j] = activate(v[8 * x + j], m.act);
+                        if (cnt > 8 * x) hidden_out<FP4>(a, r, place + b + 8 * x, 1, min(8, cnt - 8 * x), row);
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(tempty);
-            if (OUT && w.last_pass(a)) {
-                // the last of the tile's units adds up the choices
-                __threadfence();
-                meet();
-                if (threadIdx.x == 64) *last = atomicAdd(a.ticket + w.tile, 1u) == static_cast<uint32_t>(p.n - 1);
-                meet();
-                if (*reinterpret_cast<volatile uint32_t*>(last) != 0u) {
-                    __threadfence();
-                    const int64_t n0 = static_cast<int64_t>(w.tile) * 128 + lane * 4;
-                    for (int t0 = q; t0 < m.T; t0 += 16) {  // four tokens at a time: t0, t0 + 4, ..
-                        float4 sum[4] = {};
-#pragma unroll 4
-                        for (int j = 0; j < m.C; ++j) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int t = t0 + 4 * i, pr = t * m.C + j;
-                                if (t >= m.T || __ldg(m.ids + pr) >= static_cast<uint32_t>(m.E)) continue;
-                                const float4 d = __ldcg(reinterpret_cast<const float4*>(a.part + pr * a.Nq + n0));
-                                const float wt = __ldg(m.weights + pr);
-                                sum[i].x = fmaf(wt, d.x, sum[i].x);
-                                sum[i].y = fmaf(wt, d.y, sum[i].y);
-                                sum[i].z = fmaf(wt, d.z, sum[i].z);
-                                sum[i].w = fmaf(wt, d.w, sum[i].w);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int t = t0 + 4 * i;
-                            const float s[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                if (t >= m.T || n0 + x >= m.N) continue;
-                                const int64_t o = t * m.N + n0 + x;
-                                if (a.out_fmt == 2) static_cast<float*>(m.y)[o] = s[x];
-                                else if (a.out_fmt == 1) OutT<1>::store1(m.y, o, s[x]);
-                                else OutT<0>::store1(m.y, o, s[x]);
-                            }
-                        }
-                    }
-                }
-            }
-        }
-        if (OUT && p.n == 0) {  // no choice at all
-            const int64_t es = a.out_fmt == 2 ? 4 : 2, bytes = m.T * m.N * es;
-            for (int64_t i = (blockIdx.x * 128ll + (threadIdx.x - 64)) * es; i < bytes; i += gridDim.x * 128ll * es) {
-                if (es == 4) *reinterpret_cast<float*>(static_cast<uint8_t*>(m.y) + i) = 0.0f;
-                else *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(m.y) + i) = 0;
-            }
+            if (items == 0) drained();
         }
     }
     tc_fence_before();
@@ -555,6 +523,8 @@ __global__ void __launch_bounds__(256) moe_parts_kernel(const T* x, const uint32
     const int P = T_ * C;
     const Plan p = build_plan<8>(smem, ids, P, E);
     uint16_t* place = reinterpret_cast<uint16_t*>(smem + plan_bytes(E, P, 8));  // of each choice
+    for (int i = threadIdx.x; i < P; i += 256) place[i] = 0xffff;  // none
+    __syncthreads();
     for (int s = threadIdx.x >> 5; s < p.n; s += 8) {
         const int e = p.active[s];
         for (int i = threadIdx.x & 31; i < static_cast<int>(p.cnt[e]); i += 32) place[p.list[p.first[e] + i]] = static_cast<uint16_t>(p.first[e] + i);
@@ -592,13 +562,42 @@ __global__ void __launch_bounds__(256) moe_parts_kernel(const T* x, const uint32
             }
             if (!live) continue;
             for (int j = 0; j < C; ++j) {
-                if (__ldg(ids + t * C + j) >= static_cast<uint32_t>(E)) continue;
-                const int64_t r = static_cast<int64_t>(place[t * C + j]) * PART_ROWS + part;
+                const uint32_t at = place[t * C + j];
+                if (at == 0xffffu) continue;
+                const int64_t r = static_cast<int64_t>(at) * PART_ROWS + part;
                 *reinterpret_cast<uint32_t*>(xq + r * (Kp / 2) + k / 2) = word;
                 if ((l16 & 3) == 0) xs[fp4_scale_at(r, k >> 5, Kp)] = static_cast<uint8_t>(byte);
             }
         }
     }
+}
+
+// y[t] = sum over j of weights[t,j] * part[t,j], four columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(128) moe_sum_kernel(T* y, const float* part, const uint32_t* ids, const float* weights, int T_, int C, int E,
+                                                      int64_t N, int64_t Nq) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t per = (N + 3) / 4, i = blockIdx.x * 128ll + threadIdx.x;
+    if (i >= T_ * per) return;
+    const int64_t t = i / per, n0 = (i - t * per) * 4;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int j = 0; j < C; ++j) {
+        const int64_t pr = t * C + j;
+        const bool in = __ldg(ids + pr) < static_cast<uint32_t>(E);
+        const float w = __ldg(weights + pr);
+        const float4 d = in ? __ldg(reinterpret_cast<const float4*>(part + pr * Nq + n0)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in) {
+            s[0] = fmaf(w, d.x, s[0]);
+            s[1] = fmaf(w, d.y, s[1]);
+            s[2] = fmaf(w, d.z, s[2]);
+            s[3] = fmaf(w, d.w, s[3]);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        if (n0 + x < N) y[t * N + n0 + x] = static_cast<T>(s[x]);
 }
 
 // f16 weights: a choice's h, scaled by a power of two, in two f16 planes.  A block per place
@@ -660,7 +659,7 @@ cudaError_t word_map(CUtensorMap* mp, const void* ptr, uint64_t pieces, uint64_t
 
 // Scratch, part by part.
 struct Room {
-    int64_t x, xs, h, hs, hf, scale, part, ticket, bytes;  // offsets, and all
+    int64_t x, xs, h, hs, hf, scale, part, bytes;  // offsets, and all
     int64_t places, Kp, Fp, Nq;
 };
 Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
@@ -684,7 +683,6 @@ Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
     r.hf = take(!fp4 && f16 ? P * m.F * 4 : 0);
     r.scale = take(!fp4 && f16 ? P * 4 : 0);
     r.part = take(P * r.Nq * 4);
-    r.ticket = take(r.Nq / 128 * 4);
     r.bytes = at;
     return r;
 }
@@ -727,13 +725,10 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
     a.hq = scratch + r.h;
     a.hs = scratch + r.hs;
     a.part = reinterpret_cast<float*>(scratch + r.part);
-    a.ticket = reinterpret_cast<uint32_t*>(scratch + r.ticket);
     a.Fp = r.Fp;
     a.Nq = r.Nq;
-    a.out_tiles = static_cast<int>(r.Nq / 128);
     a.fmt = dt == BI_BF16;
     if (f16) a.hf = reinterpret_cast<float*>(scratch + r.hf);
-    a.out_fmt = dt == BI_F32 ? 2 : dt == BI_BF16 ? 1 : 0;
     a.status = c.status;
     a.wait_limit = c.wait_limit_ns;
     CUtensorMap gate, up, down, mx, mh, sx, sh;
@@ -787,7 +782,16 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
         c.count();
         a.unscale = unscale;
     }
-    return launch<FP4, true>(c, a, down, down, mh, sh);
+    if ((e = launch<FP4, true>(c, a, down, down, mh, sh)) != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>((m.T * ((m.N + 3) / 4) + 127) / 128));
+    auto sum = [&](auto* y) {
+        auto kern = moe_sum_kernel<std::remove_pointer_t<decltype(y)>>;
+        return launch_pdl(kern, grid, dim3(128), 0, c.stream, y, a.part, m.ids, m.weights, m.T, m.C, m.E, m.N, a.Nq);
+    };
+    e = dt == BI_F32 ? sum(static_cast<float*>(m.y)) : dt == BI_BF16 ? sum(static_cast<__nv_bfloat16*>(m.y)) : sum(static_cast<__half*>(m.y));
+    if (e != cudaSuccess) return e;
+    c.count();
+    return cudaGetLastError();
 }
 
 }  // namespace
