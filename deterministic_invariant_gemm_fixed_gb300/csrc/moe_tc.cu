@@ -48,6 +48,8 @@ constexpr int T_BARS = 512;
 constexpr int T_EX = 2 * 16 * 64 * 4;      // the epilogue's exchange between the gate's and up's warps
 constexpr int A_BYTES = 128 * 128;         // weights of a stage
 constexpr int MAX_STAGES = 12;
+constexpr int SF_WARPS = 4;                // MXFP4: warps that put the weights' scales in place
+constexpr int t_threads(bool fp4) { return 192 + (fp4 ? 32 * SF_WARPS : 0); }
 constexpr int SF_COL = 256, SF_COLS = 24;  // tensor memory: accumulator, then two stages of scales (A 8, B 16)
 
 struct TcArgs {
@@ -190,9 +192,9 @@ __device__ __forceinline__ void hidden_out(const TcArgs& a, float (&r)[8], int64
 }
 
 template <bool FP4, bool OUT>
-__global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
+__global__ void __launch_bounds__(t_threads(FP4), 1)
     moe_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmSB, const TcArgs a) {
+                  const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmB8, const TcArgs a) {
     constexpr int ALIGN = FP4 ? 8 : 1;
     constexpr int BPARTS = !FP4 && OUT ? 2 : 1;  // planes of B
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies, a lane each
-        // lanes 0, 1: 64 weight rows; then B's boxes of 16 rows; MXFP4: B's scales, 8 tokens a box
+        // lanes 0, 1: 64 weight rows; then B's boxes of 16 rows or 128; MXFP4: B's scales, 8 tokens a box
         int s = 0, made = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -261,13 +263,15 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
                        static_cast<int>(gated ? r : r + lane * 64), full_bar(s));
         };
         auto tokens = [&](const Walk<FP4, OUT>& x, int c, int st) {
-            const int nb = boxes(x), first = FP4 || OUT ? static_cast<int>(p.first[x.e]) + x.c0 : x.c0;
-            if (lane < nb * BPARTS) {
-                const int part = lane / nb, b = lane - part * nb;
+            // whole groups of eight boxes by one copy
+            const int nb = boxes(x), big = nb / 8, each = big + nb % 8;
+            const int first = FP4 || OUT ? static_cast<int>(p.first[x.e]) + x.c0 : x.c0;
+            if (lane < each * BPARTS) {
+                const int part = lane / each, i = lane - part * each, b = i < big ? i * 8 : big * 8 + i - big;
                 const int row = FP4 ? (first + b) * PART_ROWS : part * a.P + first + b * 16;
-                tma_2d(sbase + st * a.stage + b_at + part * b_bytes + b * 2048, &tmB, c * (FP4 ? 128 : 64), row, full_bar(st));
-            } else if (FP4 && lane < nb + (x.cols(a) + 7) / 8) {
-                tma_2d(sbase + st * a.stage + sfb_at + (lane - nb) * 1024, &tmSB, c * 256, first / 8 + lane - nb, full_bar(st));
+                tma_2d(sbase + st * a.stage + b_at + part * b_bytes + b * 2048, i < big ? &tmB8 : &tmB, c * (FP4 ? 128 : 64), row, full_bar(st));
+            } else if (FP4 && lane < each + (x.cols(a) + 7) / 8) {
+                tma_2d(sbase + st * a.stage + sfb_at + (lane - each) * 1024, &tmSB, c * 256, first / 8 + lane - each, full_bar(st));
             }
         };
         auto advance = [&](Walk<FP4, OUT>& x, int& c) {
@@ -354,17 +358,21 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
             mbar_drain(drain, 0);
         }
         __syncwarp();
-    } else if (FP4 && warp == 6) {
+    } else if (FP4 && warp >= 6) {
         // ------------------------------------------------------------ the weights' scales
         // A lane has rows lane and lane + 32 of either half of the tile, wherever their
         // bytes lie, and puts them side by side in the order that the tensor cores take.
-        // Loaded a stage ahead.
+        // Loaded for BATCH stages at once: the fence that hands a stage on waits for the
+        // loads in flight too (loads between the fences: 1.1 us a stage); and by SF_WARPS
+        // warps in turn, each taking as long over a stage as the tensor cores over several.
+        constexpr int BATCH = 4;
         const int64_t Lp = fp4_padded(OUT ? m.F : m.K), all = m.E * R;
         const uint8_t* s0 = OUT ? m.down_s : gated ? m.gate_s : m.up_s;
         const uint8_t* s1 = OUT ? m.down_s : m.up_s;
         int s = 0, c = 0;
         uint32_t ph = 0;
-        uint32_t v[8];
+        uint32_t v[BATCH][8];
+        bool have[BATCH];
         const uint8_t* at[4];
         auto rows = [&] {
             const int64_t r = w.e * R + static_cast<int64_t>(w.tile) * span;
@@ -374,32 +382,40 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
                 at[j] = (j < 2 ? s0 : s1) + fp4_scale_at(row, 0, Lp);
             }
         };
-        auto load = [&] {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int atom = 2 * c + (j >> 2);
-                v[j] = __ldg(reinterpret_cast<const uint32_t*>(at[j & 3] + static_cast<int64_t>(atom) * 512));
-            }
+        auto ahead = [&](int n) {  // the walk n stages on
+            for (; n > 0 && w.more(a, p); --n)
+                if (++c == a.chunks) { c = 0; w.next(a, p); }
         };
-        if (w.more(a, p)) {
+        auto load = [&](uint32_t (&x)[8], bool& got) {
+            got = w.more(a, p);
+            if (!got) return;
             rows();
-            load();
-        }
-        while (w.more(a, p)) {
-            if (!__all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, a, DEV_TIMEOUT_PRODUCER))) break;
-            const uint32_t to = sbase + s * a.stage + sfa_at + lane * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 512), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(full_bar(s));
-            if (++s == a.depth) { s = 0; ph ^= 1u; }
-            if (++c == a.chunks) {
-                c = 0;
-                w.next(a, p);
-                if (w.more(a, p)) rows();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = __ldg(reinterpret_cast<const uint32_t*>(at[j & 3] + static_cast<int64_t>(2 * c + (j >> 2)) * 512));
+            ahead(SF_WARPS);
+        };
+        ahead(warp - 6);
+        auto step = [&](int n) {  // the ring's stage n uses on
+            for (s += n; s >= a.depth; s -= a.depth) ph ^= 1u;
+        };
+        step(warp - 6);
+        bool go = true;
+        while (go) {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) load(v[i], have[i]);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                go = go && have[i] && __all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, a, DEV_TIMEOUT_PRODUCER));
+                if (!go) continue;
+                const uint32_t to = sbase + s * a.stage + sfa_at + lane * 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[i][0]), "r"(v[i][1]), "r"(v[i][2]), "r"(v[i][3]) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 512), "r"(v[i][4]), "r"(v[i][5]), "r"(v[i][6]), "r"(v[i][7]) : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(full_bar(s));
+                step(SF_WARPS);
             }
-            if (w.more(a, p)) load();
         }
     } else if (warp >= 2 && warp < 6) {
         // ------------------------------------------------------------ epilogue
@@ -513,60 +529,63 @@ __global__ void __launch_bounds__(FP4 ? 224 : 192, 1)
 }
 
 // x as its parts, at the places of the tokens' choices; and zeros for the scales of h's
-// parts, whose last blocks no one writes.  16 lanes to 128 elements of a token.
+// parts, whose last blocks no one writes.  A warp to 128 elements of a token.
+constexpr int X_THREADS = 128;
 template <typename T>
-__global__ void __launch_bounds__(256) moe_parts_kernel(const T* x, const uint32_t* ids, uint8_t* xq, uint8_t* xs, uint8_t* hs, int64_t hs_bytes,
-                                                        int T_, int C, int E, int64_t K) {
+__global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const uint32_t* ids, uint8_t* xq, uint8_t* xs, uint8_t* hs,
+                                                              int64_t hs_bytes, int T_, int C, int E, int64_t K) {
     extern __shared__ __align__(16) uint8_t smem[];
     grid_dep_wait();
     grid_dep_launch();
-    const int P = T_ * C;
+    const int P = T_ * C, lane = threadIdx.x & 31;
     const Plan p = build_plan<8>(smem, ids, P, E);
     uint16_t* place = reinterpret_cast<uint16_t*>(smem + plan_bytes(E, P, 8));  // of each choice
-    for (int i = threadIdx.x; i < P; i += 256) place[i] = 0xffff;  // none
+    for (int i = threadIdx.x; i < P; i += X_THREADS) place[i] = 0xffff;         // none
     __syncthreads();
-    for (int s = threadIdx.x >> 5; s < p.n; s += 8) {
+    for (int s = threadIdx.x >> 5; s < p.n; s += X_THREADS / 32) {
         const int e = p.active[s];
-        for (int i = threadIdx.x & 31; i < static_cast<int>(p.cnt[e]); i += 32) place[p.list[p.first[e] + i]] = static_cast<uint16_t>(p.first[e] + i);
+        for (int i = lane; i < static_cast<int>(p.cnt[e]); i += 32) place[p.list[p.first[e] + i]] = static_cast<uint16_t>(p.first[e] + i);
     }
     __syncthreads();
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < hs_bytes / 16; i += gridDim.x * 256ll) reinterpret_cast<uint4*>(hs)[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = blockIdx.x * int64_t(X_THREADS) + threadIdx.x; i < hs_bytes / 16; i += gridDim.x * int64_t(X_THREADS))
+        reinterpret_cast<uint4*>(hs)[i] = make_uint4(0, 0, 0, 0);
     const int64_t Kp = fp4_padded(K), per = Kp / 128;
-    const int l16 = threadIdx.x & 15;
-    for (int64_t i = blockIdx.x * 16ll + (threadIdx.x >> 4); i < (T_ * per + 1) / 2 * 2; i += gridDim.x * 16ll) {  // (both halves of a warp)
-        const bool live = i < T_ * per;
-        const int64_t t = live ? i / per : 0, k = (live ? i - t * per : 0) * 128 + l16 * 8;
-        float v[8];
+    for (int64_t i = blockIdx.x * int64_t(X_THREADS / 32) + (threadIdx.x >> 5); i < T_ * per; i += gridDim.x * int64_t(X_THREADS / 32)) {
+        const int64_t t = i / per, k = (i - t * per) * 128 + lane * 4;
+        float v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = live && k + j < K ? static_cast<float>(x[t * K + k + j]) : 0.0f;
+        for (int j = 0; j < 4; ++j) v[j] = k + j < K ? static_cast<float>(x[t * K + k + j]) : 0.0f;
+        uint32_t word[PARTS], bytes[PARTS / 4];
+#pragma unroll
         for (int part = 0; part < PARTS; ++part) {
             uint32_t mx = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mx = max(mx, __float_as_uint(v[j]) & 0x7fffffffu);
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            for (int j = 0; j < 4; ++j) mx = max(mx, __float_as_uint(v[j]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const uint32_t byte = part_scale(mx);
-            uint32_t word = 0;
-            if (byte != 255u) {
-                const float inv = part_inverse(byte), scale = fp4_scale_value(byte);
+            const float inv = byte == 255u ? 0.0f : part_inverse(byte), scale = fp4_scale_value(byte);
+            word[part] = 0;
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const uint32_t c = __nv_cvt_float2_to_fp4x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_E2M1, cudaRoundNearest);
-                    word |= c << (4 * j);
-                    v[j] = __fsub_rn(v[j], fp4_code_value(c & 15u) * scale);
-                    v[j + 1] = __fsub_rn(v[j + 1], fp4_code_value(c >> 4) * scale);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            for (int j = 0; j < 4; j += 2) {
+                const uint32_t c = byte == 255u ? 0u : __nv_cvt_float2_to_fp4x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_E2M1, cudaRoundNearest);
+                word[part] |= c << (4 * j);
+                v[j] = byte == 255u ? 0.0f : __fsub_rn(v[j], fp4_code_value(c & 15u) * scale);
+                v[j + 1] = byte == 255u ? 0.0f : __fsub_rn(v[j + 1], fp4_code_value(c >> 4) * scale);
             }
-            if (!live) continue;
-            for (int j = 0; j < C; ++j) {
-                const uint32_t at = place[t * C + j];
-                if (at == 0xffffu) continue;
-                const int64_t r = static_cast<int64_t>(at) * PART_ROWS + part;
-                *reinterpret_cast<uint32_t*>(xq + r * (Kp / 2) + k / 2) = word;
-                if ((l16 & 3) == 0) xs[fp4_scale_at(r, k >> 5, Kp)] = static_cast<uint8_t>(byte);
+            if (part % 4 == 0) bytes[part / 4] = 0;
+            bytes[part / 4] |= byte << (8 * (part % 4));
+        }
+        for (int j = 0; j < C; ++j) {
+            const uint32_t at = place[t * C + j];
+            if (at == 0xffffu) continue;
+            const int64_t r = static_cast<int64_t>(at) * PART_ROWS;
+            uint8_t* q = xq + r * (Kp / 2) + k / 2;
+            uint8_t* s = xs + fp4_scale_at(r, k >> 5, Kp);  // (16 rows of a place: 16 bytes apart)
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                *reinterpret_cast<uint16_t*>(q + part * (Kp / 2)) = static_cast<uint16_t>(word[part]);
+                if ((lane & 7) == 0) s[part * 16] = static_cast<uint8_t>(bytes[part / 4] >> (8 * (part % 4)));
             }
         }
     }
@@ -688,7 +707,8 @@ Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
 }
 
 template <bool FP4, bool OUT>
-cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b, const CUtensorMap& sb) {
+cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b, const CUtensorMap& sb,
+                   const CUtensorMap& b8) {
     auto kern = moe_tc_kernel<FP4, OUT>;
     static PerDeviceOnce setup;
     cudaError_t e = setup.run(c.eng->device, [&](int&) {
@@ -707,8 +727,8 @@ cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CU
     a.depth = static_cast<int>(lmin(MAX_STAGES, (T_LIMIT - fixed) / a.stage));
     if (a.depth < 2) return cudaErrorInvalidConfiguration;
     const int64_t units = a.tiles * lmin(a.m.E, a.P);  // at most
-    e = launch_pdl(kern, dim3(static_cast<unsigned>(lmin(units, c.sm_count))), dim3(FP4 ? 224 : 192), static_cast<size_t>(fixed + a.depth * a.stage),
-                   c.stream, a0, a1, b, sb, a);
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(lmin(units, c.sm_count))), dim3(t_threads(FP4)), static_cast<size_t>(fixed + a.depth * a.stage),
+                   c.stream, a0, a1, b, sb, b8, a);
     if (e != cudaSuccess) return e;
     c.count();
     return cudaGetLastError();
@@ -731,16 +751,16 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
     if (f16) a.hf = reinterpret_cast<float*>(scratch + r.hf);
     a.status = c.status;
     a.wait_limit = c.wait_limit_ns;
-    CUtensorMap gate, up, down, mx, mh, sx, sh;
+    CUtensorMap gate, up, down, mx, mh, mx8, mh8, sx, sh;
     cudaError_t e;
     const int64_t rows = r.places * PART_ROWS, ef = m.E * m.F, en = m.E * m.N;
     if (FP4) {
         uint8_t *xq = scratch + r.x, *xs = scratch + r.xs;
         const int smem = static_cast<int>(plan_bytes(m.E, a.P, 8) + (2 * a.P + 15) / 16 * 16);
-        const int64_t tasks = (m.T * (r.Kp / 128) + 15) / 16, zero = rows / 128 * r.Fp * 4;
-        const dim3 grid(static_cast<unsigned>(lmin(tasks > 16 ? tasks : 16, 4 * c.sm_count)));
+        const int64_t tasks = (m.T * (r.Kp / 128) + X_THREADS / 32 - 1) / (X_THREADS / 32), zero = rows / 128 * r.Fp * 4;
+        const dim3 grid(static_cast<unsigned>(lmin(tasks > 16 ? tasks : 16, 8 * c.sm_count)));
         auto go = [&](auto kern, auto* x) {
-            return launch_pdl(kern, grid, dim3(256), static_cast<size_t>(smem), c.stream, x, m.ids, xq, xs, a.hs, zero, m.T, m.C, m.E, m.K);
+            return launch_pdl(kern, grid, dim3(X_THREADS), static_cast<size_t>(smem), c.stream, x, m.ids, xq, xs, a.hs, zero, m.T, m.C, m.E, m.K);
         };
         e = dt == BI_F32    ? go(moe_parts_kernel<float>, static_cast<const float*>(m.x))
             : dt == BI_BF16 ? go(moe_parts_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16*>(m.x))
@@ -752,6 +772,8 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
         if ((e = row_map(&down, true, m.down, r.Fp / 2, en, r.Fp / 2, 64)) != cudaSuccess) return e;
         if ((e = row_map(&mx, true, xq, r.Kp / 2, rows, r.Kp / 2, 16)) != cudaSuccess) return e;
         if ((e = row_map(&mh, true, a.hq, r.Fp / 2, rows, r.Fp / 2, 16)) != cudaSuccess) return e;
+        if ((e = row_map(&mx8, true, xq, r.Kp / 2, rows, r.Kp / 2, 128)) != cudaSuccess) return e;
+        if ((e = row_map(&mh8, true, a.hq, r.Fp / 2, rows, r.Fp / 2, 128)) != cudaSuccess) return e;
         if ((e = word_map(&sx, xs, rows / 128, r.Kp)) != cudaSuccess) return e;
         if ((e = word_map(&sh, a.hs, rows / 128, r.Fp)) != cudaSuccess) return e;
     } else {
@@ -771,10 +793,12 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
         if ((e = row_map(&down, false, m.down, m.F, en, m.F * 2, 64)) != cudaSuccess) return e;
         if ((e = row_map(&mx, false, x, m.K, m.T, pitch * 2, 16)) != cudaSuccess) return e;
         if ((e = row_map(&mh, false, a.h, m.F, 2ll * a.P, r.Fp * 2, 16)) != cudaSuccess) return e;
+        if ((e = row_map(&mx8, false, x, m.K, m.T, pitch * 2, 128)) != cudaSuccess) return e;
+        if ((e = row_map(&mh8, false, a.h, m.F, 2ll * a.P, r.Fp * 2, 128)) != cudaSuccess) return e;
         sx = sh = mx;
     }
     if (!m.gate) gate = up;
-    if ((e = launch<FP4, false>(c, a, gate, up, mx, sx)) != cudaSuccess) return e;
+    if ((e = launch<FP4, false>(c, a, gate, up, mx, sx, mx8)) != cudaSuccess) return e;
     if (f16) {
         float* unscale = reinterpret_cast<float*>(scratch + r.scale);
         e = launch_pdl(moe_planes_kernel, dim3(static_cast<unsigned>(a.P)), dim3(256), 0, c.stream, a.h, unscale, a.hf, m.F, a.Fp, a.P);
@@ -782,7 +806,7 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
         c.count();
         a.unscale = unscale;
     }
-    if ((e = launch<FP4, true>(c, a, down, down, mh, sh)) != cudaSuccess) return e;
+    if ((e = launch<FP4, true>(c, a, down, down, mh, sh, mh8)) != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>((m.T * ((m.N + 3) / 4) + 127) / 128));
     auto sum = [&](auto* y) {
         auto kern = moe_sum_kernel<std::remove_pointer_t<decltype(y)>>;
