@@ -24,7 +24,9 @@
 // before left, per block of 32 with a scale that none of it exceeds, so a part leaves at
 // most a quarter of its scale's range and the twelfth less than 2^-23 of the block's largest
 // value.  The parts are N columns of their own (16 to a token, 12 used), added in the
-// epilogue from the smallest up.
+// epilogue from the smallest up.  A kernel of its own makes them, of x and of h: in the
+// hidden kernel's epilogue, which has 128 threads per SM, they took longer than all
+// else (f16, 96 tokens, 8 experts of 4096 x 4096: 200 us for that kernel, 97 without).
 //
 // Sums of the output kernel's units go to memory once per choice, and a third, small
 // kernel adds every token's choices in order.  (A block that adds up a tile once it has
@@ -55,9 +57,8 @@ constexpr int SF_COL = 256, SF_COLS = 24;  // tensor memory: accumulator, then t
 struct TcArgs {
     MoeCall m;
     uint16_t* h;        // 16-bit weights: planes [2][P][Fp]
-    float* hf;          // f16 weights, hidden kernel: h itself, [P][F]
+    float* hf;          // not bf16: h itself, [places][F], which a kernel of its own makes the next operand of
     const float* unscale;  // f16 weights, output kernel: [P] by which a place's sums are multiplied
-    uint8_t *hq, *hs;   // MXFP4: h's parts, an operand [16 places][F]
     float* part;        // [P][Nq] the choices' sums
     int64_t Fp, Nq;
     int P, tiles, chunks;  // choices; row tiles of an expert; stages of the contraction
@@ -145,49 +146,19 @@ __device__ __forceinline__ uint32_t part_scale(uint32_t amax_bits) {
 }
 __device__ __forceinline__ float part_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// h of a lane's row for n tokens, places step apart: the next kernel's operand.
-template <bool FP4>
-__device__ __forceinline__ void hidden_out(const TcArgs& a, float (&r)[8], int64_t place, int step, int n, int64_t row) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (FP4) {
-        if (row - lane >= a.Fp) return;  // (whole blocks of 32)
+// h of a lane's row for n tokens, places step apart.
+__device__ __forceinline__ void hidden_out(const TcArgs& a, const float (&r)[8], int64_t place, int step, int n, int64_t row) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (row >= a.m.F) r[j] = 0.0f;
-        for (int x = 0; x < PARTS; ++x) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {  // (independent of one another: they hide each other's latency)
-                if (j >= n) continue;
-                const uint32_t byte = part_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(r[j]) & 0x7fffffffu));
-                uint32_t code = 0;
-                if (byte != 255u) {
-                    code = __nv_cvt_float2_to_fp4x2(make_float2(r[j] * part_inverse(byte), 0.0f), __NV_E2M1, cudaRoundNearest) & 15u;
-                    r[j] = __fsub_rn(r[j], fp4_code_value(code) * fp4_scale_value(byte));
-                } else {
-                    r[j] = 0.0f;
-                }
-                uint32_t word = code << (4 * (lane & 7));
-                word |= __shfl_xor_sync(0xffffffffu, word, 1);
-                word |= __shfl_xor_sync(0xffffffffu, word, 2);
-                word |= __shfl_xor_sync(0xffffffffu, word, 4);
-                const int64_t at = (place + j * step) * PART_ROWS + x;
-                if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + at * (a.Fp / 2) + row / 2) = word;
-                if (lane == 0) a.hs[fp4_scale_at(at, row >> 5, a.Fp)] = static_cast<uint8_t>(byte);
-            }
+    for (int j = 0; j < 8; ++j) {
+        if (j >= n || row >= a.m.F) continue;
+        if (a.hf) {
+            a.hf[(place + j * step) * a.m.F + row] = r[j];
+            continue;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= n || row >= a.m.F) continue;
-            if (a.hf) {
-                a.hf[(place + j * step) * a.m.F + row] = r[j];
-                continue;
-            }
-            const __nv_bfloat16 hi = __float2bfloat16_rn(r[j]), lo = __float2bfloat16_rn(r[j] - __bfloat162float(hi));
-            uint16_t* o = a.h + (place + j * step) * a.Fp + row;
-            o[0] = __bfloat16_as_ushort(hi);
-            o[static_cast<int64_t>(a.P) * a.Fp] = __bfloat16_as_ushort(lo);
-        }
+        const __nv_bfloat16 hi = __float2bfloat16_rn(r[j]), lo = __float2bfloat16_rn(r[j] - __bfloat162float(hi));
+        uint16_t* o = a.h + (place + j * step) * a.Fp + row;
+        o[0] = __bfloat16_as_ushort(hi);
+        o[static_cast<int64_t>(a.P) * a.Fp] = __bfloat16_as_ushort(lo);
     }
 }
 
@@ -506,13 +477,13 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                         const float other = e[(2 * j + (odd ? 1 : 0)) * 64];
                         r[j] = odd ? activate(other, m.act) * v[2 * j + 1] : activate(v[2 * j], m.act) * other;
                     }
-                    hidden_out<FP4>(a, r, place + b + (odd ? 1 : 0), 2, (cnt + (odd ? 0 : 1)) / 2, row);
+                    hidden_out(a, r, place + b + (odd ? 1 : 0), 2, (cnt + (odd ? 0 : 1)) / 2, row);
                 } else {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) r[j] = activate(v[8 * x + j], m.act);
-                        if (cnt > 8 * x) hidden_out<FP4>(a, r, place + b + 8 * x, 1, min(8, cnt - 8 * x), row);
+                        if (cnt > 8 * x) hidden_out(a, r, place + b + 8 * x, 1, min(8, cnt - 8 * x), row);
                     }
                 }
             }
@@ -528,12 +499,13 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     }
 }
 
-// x as its parts, at the places of the tokens' choices; and zeros for the scales of h's
-// parts, whose last blocks no one writes.  A warp to 128 elements of a token.
+// Rows as their parts, at the places of the choices: x [T][K] (each token at those of its
+// C choices), or with BY_PLACE h [places][K] (C = 1, T choices).  A warp to 128 elements of a
+// row.
 constexpr int X_THREADS = 128;
-template <typename T>
-__global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const uint32_t* ids, uint8_t* xq, uint8_t* xs, uint8_t* hs,
-                                                              int64_t hs_bytes, int T_, int C, int E, int64_t K) {
+template <typename T, bool BY_PLACE>
+__global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const uint32_t* ids, uint8_t* xq, uint8_t* xs, int T_, int C, int E,
+                                                              int64_t K) {
     extern __shared__ __align__(16) uint8_t smem[];
     grid_dep_wait();
     grid_dep_launch();
@@ -547,14 +519,14 @@ __global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const 
         for (int i = lane; i < static_cast<int>(p.cnt[e]); i += 32) place[p.list[p.first[e] + i]] = static_cast<uint16_t>(p.first[e] + i);
     }
     __syncthreads();
-    for (int64_t i = blockIdx.x * int64_t(X_THREADS) + threadIdx.x; i < hs_bytes / 16; i += gridDim.x * int64_t(X_THREADS))
-        reinterpret_cast<uint4*>(hs)[i] = make_uint4(0, 0, 0, 0);
     const int64_t Kp = fp4_padded(K), per = Kp / 128;
     for (int64_t i = blockIdx.x * int64_t(X_THREADS / 32) + (threadIdx.x >> 5); i < T_ * per; i += gridDim.x * int64_t(X_THREADS / 32)) {
         const int64_t t = i / per, k = (i - t * per) * 128 + lane * 4;
+        if (BY_PLACE && place[t] == 0xffff) continue;
+        const T* row = x + (BY_PLACE ? static_cast<int64_t>(place[t]) : t) * K;
         float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = k + j < K ? static_cast<float>(x[t * K + k + j]) : 0.0f;
+        for (int j = 0; j < 4; ++j) v[j] = k + j < K ? static_cast<float>(row[k + j]) : 0.0f;
         uint32_t word[PARTS], bytes[PARTS / 4];
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
@@ -570,6 +542,7 @@ __global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const 
             for (int j = 0; j < 4; j += 2) {
                 const uint32_t c = byte == 255u ? 0u : __nv_cvt_float2_to_fp4x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_E2M1, cudaRoundNearest);
                 word[part] |= c << (4 * j);
+                // exact: the rest of a rounding to nearest
                 v[j] = byte == 255u ? 0.0f : __fsub_rn(v[j], fp4_code_value(c & 15u) * scale);
                 v[j + 1] = byte == 255u ? 0.0f : __fsub_rn(v[j + 1], fp4_code_value(c >> 4) * scale);
             }
@@ -581,7 +554,7 @@ __global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const 
             if (at == 0xffffu) continue;
             const int64_t r = static_cast<int64_t>(at) * PART_ROWS;
             uint8_t* q = xq + r * (Kp / 2) + k / 2;
-            uint8_t* s = xs + fp4_scale_at(r, k >> 5, Kp);  // (16 rows of a place: 16 bytes apart)
+            uint8_t* s = xs + fp4_scale_at(r, k >> 5, Kp);  // (the rows of a place: 16 bytes apart)
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
                 *reinterpret_cast<uint16_t*>(q + part * (Kp / 2)) = static_cast<uint16_t>(word[part]);
@@ -699,7 +672,7 @@ Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
     r.xs = take(fp4 ? rows / 128 * r.Kp * 4 : 0);
     r.h = take(fp4 ? rows * (r.Fp / 2) : 2 * P * r.Fp * 2);
     r.hs = take(fp4 ? rows / 128 * r.Fp * 4 : 0);
-    r.hf = take(!fp4 && f16 ? P * m.F * 4 : 0);
+    r.hf = take(fp4 ? r.places * m.F * 4 : f16 ? P * m.F * 4 : 0);
     r.scale = take(!fp4 && f16 ? P * 4 : 0);
     r.part = take(P * r.Nq * 4);
     r.bytes = at;
@@ -734,6 +707,16 @@ cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CU
     return cudaGetLastError();
 }
 
+template <typename T, bool BY_PLACE>
+cudaError_t parts(const LaunchCtx& c, const MoeCall& m, const T* x, uint8_t* xq, uint8_t* xs, int T_, int C, int64_t K) {
+    const int64_t P = static_cast<int64_t>(T_) * C, smem = plan_bytes(m.E, P, 8) + (2 * P + 15) / 16 * 16;
+    const int64_t blocks = (T_ * (fp4_padded(K) / 128) + X_THREADS / 32 - 1) / (X_THREADS / 32);
+    const cudaError_t e = launch_pdl(moe_parts_kernel<T, BY_PLACE>, dim3(static_cast<unsigned>(lmin(blocks, 8 * c.sm_count))), dim3(X_THREADS),
+                                     static_cast<size_t>(smem), c.stream, x, m.ids, xq, xs, T_, C, m.E, K);
+    if (e == cudaSuccess) c.count();
+    return e;
+}
+
 template <bool FP4>
 cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype dt, uint8_t* scratch) {
     const bool f16 = !FP4 && dt == BI_F16;
@@ -742,13 +725,11 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
     a.m = m;
     a.P = m.T * m.C;
     a.h = reinterpret_cast<uint16_t*>(scratch + r.h);
-    a.hq = scratch + r.h;
-    a.hs = scratch + r.hs;
     a.part = reinterpret_cast<float*>(scratch + r.part);
     a.Fp = r.Fp;
     a.Nq = r.Nq;
     a.fmt = dt == BI_BF16;
-    if (f16) a.hf = reinterpret_cast<float*>(scratch + r.hf);
+    if (FP4 || f16) a.hf = reinterpret_cast<float*>(scratch + r.hf);
     a.status = c.status;
     a.wait_limit = c.wait_limit_ns;
     CUtensorMap gate, up, down, mx, mh, mx8, mh8, sx, sh;
@@ -756,26 +737,19 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
     const int64_t rows = r.places * PART_ROWS, ef = m.E * m.F, en = m.E * m.N;
     if (FP4) {
         uint8_t *xq = scratch + r.x, *xs = scratch + r.xs;
-        const int smem = static_cast<int>(plan_bytes(m.E, a.P, 8) + (2 * a.P + 15) / 16 * 16);
-        const int64_t tasks = (m.T * (r.Kp / 128) + X_THREADS / 32 - 1) / (X_THREADS / 32), zero = rows / 128 * r.Fp * 4;
-        const dim3 grid(static_cast<unsigned>(lmin(tasks > 16 ? tasks : 16, 8 * c.sm_count)));
-        auto go = [&](auto kern, auto* x) {
-            return launch_pdl(kern, grid, dim3(X_THREADS), static_cast<size_t>(smem), c.stream, x, m.ids, xq, xs, a.hs, zero, m.T, m.C, m.E, m.K);
-        };
-        e = dt == BI_F32    ? go(moe_parts_kernel<float>, static_cast<const float*>(m.x))
-            : dt == BI_BF16 ? go(moe_parts_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16*>(m.x))
-                            : go(moe_parts_kernel<__half>, static_cast<const __half*>(m.x));
+        e = dt == BI_F32    ? parts<float, false>(c, m, static_cast<const float*>(m.x), xq, xs, m.T, m.C, m.K)
+            : dt == BI_BF16 ? parts<__nv_bfloat16, false>(c, m, static_cast<const __nv_bfloat16*>(m.x), xq, xs, m.T, m.C, m.K)
+                            : parts<__half, false>(c, m, static_cast<const __half*>(m.x), xq, xs, m.T, m.C, m.K);
         if (e != cudaSuccess) return e;
-        c.count();
         if ((e = row_map(&up, true, m.up, r.Kp / 2, ef, r.Kp / 2, 64)) != cudaSuccess) return e;
         if (m.gate && (e = row_map(&gate, true, m.gate, r.Kp / 2, ef, r.Kp / 2, 64)) != cudaSuccess) return e;
         if ((e = row_map(&down, true, m.down, r.Fp / 2, en, r.Fp / 2, 64)) != cudaSuccess) return e;
         if ((e = row_map(&mx, true, xq, r.Kp / 2, rows, r.Kp / 2, 16)) != cudaSuccess) return e;
-        if ((e = row_map(&mh, true, a.hq, r.Fp / 2, rows, r.Fp / 2, 16)) != cudaSuccess) return e;
+        if ((e = row_map(&mh, true, scratch + r.h, r.Fp / 2, rows, r.Fp / 2, 16)) != cudaSuccess) return e;
         if ((e = row_map(&mx8, true, xq, r.Kp / 2, rows, r.Kp / 2, 128)) != cudaSuccess) return e;
-        if ((e = row_map(&mh8, true, a.hq, r.Fp / 2, rows, r.Fp / 2, 128)) != cudaSuccess) return e;
+        if ((e = row_map(&mh8, true, scratch + r.h, r.Fp / 2, rows, r.Fp / 2, 128)) != cudaSuccess) return e;
         if ((e = word_map(&sx, xs, rows / 128, r.Kp)) != cudaSuccess) return e;
-        if ((e = word_map(&sh, a.hs, rows / 128, r.Fp)) != cudaSuccess) return e;
+        if ((e = word_map(&sh, scratch + r.hs, rows / 128, r.Fp)) != cudaSuccess) return e;
     } else {
         const void* x = m.x;
         int64_t pitch = m.K;
@@ -799,6 +773,7 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
     }
     if (!m.gate) gate = up;
     if ((e = launch<FP4, false>(c, a, gate, up, mx, sx, mx8)) != cudaSuccess) return e;
+    if (FP4 && (e = parts<float, true>(c, m, a.hf, scratch + r.h, scratch + r.hs, a.P, 1, m.F)) != cudaSuccess) return e;
     if (f16) {
         float* unscale = reinterpret_cast<float*>(scratch + r.scale);
         e = launch_pdl(moe_planes_kernel, dim3(static_cast<unsigned>(a.P)), dim3(256), 0, c.stream, a.h, unscale, a.hf, m.F, a.Fp, a.P);
