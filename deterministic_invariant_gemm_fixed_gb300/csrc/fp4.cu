@@ -61,168 +61,249 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t byte) {
 // Largest magnitude as bits: infinities and NaN compare above every number.
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// One 128 x 128 tile of src per block: its codes and scales along the columns (q, s)
-// and along the rows (qt, st: the operand's transpose), either of them absent.  The
-// tile is read once; the rows' direction works on the values as loaded, four
-// lanes to a block of 32, the columns' direction on the tile in shared memory, a
-// thread to a column's block.  Bound by memory: src read once, a quarter (bf16) of
-// it written per direction.
-constexpr int QT = 128;            // tile edge
+// One tile of src per block, TR rows (32 or 128) by 128 columns: its codes and scales
+// along the columns (q, s) and along the rows (qt, st: the operand's transpose), either of
+// them absent.  The tile is read once, all of a thread's loads in flight together; the
+// rows' direction works on the values as loaded, four lanes to a block of 32, the
+// columns' direction on the tile in shared memory, a thread to a block of one column (two
+// columns of 16-bit values, whose magnitudes are compared in pairs).
+//
+// Bound by memory where there are many tiles: src read once, a quarter (bf16) of it
+// written per direction.  A small matrix waits for one tile's chain of steps instead, and
+// takes the tiles of 32 rows, whose chain is a third as long; their column direction
+// writes 16 bytes at a time where the others write 64.
+constexpr int QT = 128;            // tile columns
 constexpr int Q_THREADS = 256;
-template <typename T> constexpr int q_pitch() { return QT + 8 / static_cast<int>(sizeof(T)); }  // elements
-template <typename T> constexpr int q_smem(bool cols) { return cols ? QT * q_pitch<T>() * static_cast<int>(sizeof(T)) + QT * 80 : 0; }
+template <typename T> constexpr int q_pitch() { return QT + 16 / static_cast<int>(sizeof(T)); }  // elements: rows stay on 16 bytes
+template <typename T, int TR> constexpr int q_smem(bool cols) { return cols ? TR * q_pitch<T>() * static_cast<int>(sizeof(T)) + QT * (TR / 2 + 16) : 0; }
 
-template <typename T>
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The f32 bits of a 16-bit magnitude.
+template <typename T> __device__ __forceinline__ uint32_t mag16(uint32_t h) {
+    if constexpr (sizeof(T) == 4) return h;
+    else return __float_as_uint(up<T>(*reinterpret_cast<const T*>(&h)));
+}
+
+template <typename T, int TR>
 __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const T* __restrict__ src, uint8_t* q, uint8_t* s, uint8_t* qt,
                                                                 uint8_t* st, int64_t R, int64_t C, int tiles_c, int vec) {
     grid_dep_wait();
     grid_dep_launch();
+    constexpr int WORDS = 2 * static_cast<int>(sizeof(T));  // 32-bit words of eight values
+    constexpr int ROUNDS = TR / 16, PITCH = q_pitch<T>(), CPITCH = TR / 2 + 16;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     T* tile = reinterpret_cast<T*>(smem_raw);
-    uint8_t* tcode = smem_raw + QT * q_pitch<T>() * sizeof(T);  // [128 columns][80]: 64 bytes of codes
-    __shared__ __align__(16) uint8_t sc[2][512];
+    uint8_t* tcode = smem_raw + TR * PITCH * sizeof(T);  // [128 columns][CPITCH]: TR / 2 bytes of codes
+    __shared__ __align__(16) uint8_t row_scale[TR][4];
+    __shared__ __align__(16) uint8_t col_scale[QT][4];
     const int tc = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles_c));
-    const int tr = static_cast<int>(blockIdx.x / static_cast<unsigned>(tiles_c));
-    const int64_t r0 = static_cast<int64_t>(tr) * QT, c0 = static_cast<int64_t>(tc) * QT;
+    const int64_t tr = blockIdx.x / static_cast<unsigned>(tiles_c);
+    const int64_t r0 = tr * TR, c0 = static_cast<int64_t>(tc) * QT;
     const int64_t Cp = fp4_padded(C), Rp = fp4_padded(R);
     const int tid = threadIdx.x;
 
     // 16 lanes to a row of the tile, 8 values each
     const int row_in = tid >> 4, part = tid & 15;
     const int64_t c = c0 + part * 8;
-#pragma unroll 4
-    for (int i = 0; i < QT / 16; ++i) {
-        const int lr = i * 16 + row_in;
-        const int64_t r = r0 + lr;
-        float v[8];
-        const bool in = r < R && c < C;
-        if (in && vec && c + 8 <= C) {
-            const uint4* p = reinterpret_cast<const uint4*>(src + r * C + c);
-            if constexpr (sizeof(T) == 4) {
-                const uint4 a = __ldcs(p), b = __ldcs(p + 1);
-                v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-                v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    constexpr int GROUP = sizeof(T) == 4 && ROUNDS > 4 ? 4 : ROUNDS;  // rows in flight
+#pragma unroll
+    for (int g = 0; g < ROUNDS; g += GROUP) {
+        uint32_t w[GROUP][WORDS];
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) {
+            const int64_t r = r0 + (g + i) * 16 + row_in;
+            const bool in = r < R && c < C;
+            if (in && vec && c + 8 <= C) {
+                const uint4* p = reinterpret_cast<const uint4*>(src + r * C + c);
+#pragma unroll
+                for (int x = 0; x < WORDS; x += 4) {
+                    const uint4 a = __ldcs(p + x / 4);
+                    w[i][x] = a.x; w[i][x + 1] = a.y; w[i][x + 2] = a.z; w[i][x + 3] = a.w;
+                }
             } else {
-                const uint4 a = __ldcs(p);
-                const T* e = reinterpret_cast<const T*>(&a);
+                T* e = reinterpret_cast<T*>(w[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = in && c + j < C ? src[r * C + c + j] : down<T>(0.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) {
+            const int lr = (g + i) * 16 + row_in;
+            if (q != nullptr) {
+                uint32_t m = 0;
+                if constexpr (WORDS == 4) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) m = max_u16x2(m, w[i][x] & 0x7fff7fffu);
+                    m = max(m >> 16, m & 0xffffu);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < WORDS; ++x) m = max(m, w[i][x] & 0x7fffffffu);
+                }
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const uint32_t byte = scale_byte(mag16<T>(m));
+                float v[8];
+                const T* e = reinterpret_cast<const T*>(w[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = up<T>(e[j]);
+                const uint32_t code = codes8(v, byte);
+                const int64_t r = r0 + lr;
+                if (r < R) *reinterpret_cast<uint32_t*>(q + r * (Cp / 2) + c / 2) = code;
+                if ((part & 3) == 0) row_scale[lr][part >> 2] = static_cast<uint8_t>(r < R ? byte : 0u);
             }
-        } else {
+            if (qt != nullptr) {
+                uint4* d = reinterpret_cast<uint4*>(tile + lr * PITCH + part * 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = in && c + j < C ? up<T>(src[r * C + c + j]) : 0.0f;
+                for (int x = 0; x < WORDS; x += 4) d[x / 4] = make_uint4(w[i][x], w[i][x + 1], w[i][x + 2], w[i][x + 3]);
+            }
         }
-        if (q != nullptr) {
+    }
+    __syncthreads();
+    if (q != nullptr && tid < TR && r0 + tid < (R + 127) / 128 * 128)
+        *reinterpret_cast<uint32_t*>(s + fp4_scale_at(r0 + tid, c0 / 32, Cp)) = *reinterpret_cast<const uint32_t*>(row_scale[tid]);
+    if (qt == nullptr || c0 >= C) return;
+    if constexpr (WORDS == 4) {  // two columns' blocks of 32 rows per thread
+        if (tid < 64 * (TR / 32)) {
+            const int lc = (tid & 63) * 2, b = tid >> 6;
+            const uint32_t* colp = reinterpret_cast<const uint32_t*>(tile + b * 32 * PITCH + lc);
+            uint32_t w[32], m = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                w[j] = colp[j * PITCH / 2];
+                m = max_u16x2(m, w[j] & 0x7fff7fffu);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t byte = scale_byte(mag16<T>(h ? m >> 16 : m & 0xffffu));
+                uint32_t o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = up<T>(reinterpret_cast<const T*>(&w[8 * x + j])[h]);
+                    o[x] = codes8(v, byte);
+                }
+                *reinterpret_cast<uint4*>(tcode + (lc + h) * CPITCH + b * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                col_scale[lc + h][b] = static_cast<uint8_t>(byte);  // columns past C are zeros: byte 0
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < (TR == 128 ? 2 : 1); ++i) {
+            const int lc = tid & 127, b = (tid >> 7) + 2 * i;
+            if (b >= TR / 32) break;
+            const T* colp = tile + b * 32 * PITCH + lc;
+            float v[4][8];
             uint32_t m = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, mag(v[j]));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            for (int j = 0; j < 32; ++j) {
+                v[j >> 3][j & 7] = up<T>(colp[j * PITCH]);
+                m = max(m, mag(v[j >> 3][j & 7]));
+            }
             const uint32_t byte = scale_byte(m);
-            const uint32_t code = codes8(v, byte);
-            if (r < R && c < Cp) *reinterpret_cast<uint32_t*>(q + r * (Cp / 2) + c / 2) = code;
-            if ((part & 3) == 0) sc[0][(lr & 31) * 16 + (lr >> 5) * 4 + (part >> 2)] = static_cast<uint8_t>(r < R ? byte : 0u);
-        }
-        if (qt != nullptr) {
-            T* d = tile + lr * q_pitch<T>() + part * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = down<T>(v[j]);  // exact: the value came from T
+            *reinterpret_cast<uint4*>(tcode + lc * CPITCH + b * 16) =
+                make_uint4(codes8(v[0], byte), codes8(v[1], byte), codes8(v[2], byte), codes8(v[3], byte));
+            col_scale[lc][b] = static_cast<uint8_t>(byte);
         }
     }
     __syncthreads();
-    if (q != nullptr && tr < (R + QT - 1) / QT && tid < 32)
-        reinterpret_cast<uint4*>(s + (static_cast<int64_t>(tr) * (Cp / QT) + tc) * 512)[tid] = reinterpret_cast<const uint4*>(sc[0])[tid];
-    if (qt == nullptr || c0 >= C) return;
-    // a column's block of 32 rows per thread, two of them
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int lc = tid & 127, b = (tid >> 7) + 2 * i;
-        const T* colp = tile + b * 32 * q_pitch<T>() + lc;
-        float v[4][8];
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            v[j >> 3][j & 7] = up<T>(colp[j * q_pitch<T>()]);
-            m = max(m, mag(v[j >> 3][j & 7]));
-        }
-        const uint32_t byte = scale_byte(m);
-        uint4 o;
-        o.x = codes8(v[0], byte);
-        o.y = codes8(v[1], byte);
-        o.z = codes8(v[2], byte);
-        o.w = codes8(v[3], byte);
-        *reinterpret_cast<uint4*>(tcode + lc * 80 + b * 16) = o;
-        sc[1][(lc & 31) * 16 + (lc >> 5) * 4 + b] = static_cast<uint8_t>(byte);  // columns past C are zeros: byte 0
+    constexpr int PIECES = TR / 32;  // of 16 bytes in a column's codes
+    for (int i = tid; i < QT * PIECES; i += Q_THREADS) {
+        const int lc = i / PIECES, piece = i % PIECES;
+        if (c0 + lc < C)
+            *reinterpret_cast<uint4*>(qt + (c0 + lc) * (Rp / 2) + r0 / 2 + piece * 16) =
+                *reinterpret_cast<const uint4*>(tcode + lc * CPITCH + piece * 16);
     }
-    __syncthreads();
-    if (r0 < Rp) {
-        for (int i = tid; i < QT * 4; i += Q_THREADS) {
-            const int lc = i >> 2, part4 = i & 3;
-            if (c0 + lc < C)
-                *reinterpret_cast<uint4*>(qt + (c0 + lc) * (Rp / 2) + r0 / 2 + part4 * 16) =
-                    *reinterpret_cast<const uint4*>(tcode + lc * 80 + part4 * 16);
-        }
-        if (tid < 32)
-            reinterpret_cast<uint4*>(st + (static_cast<int64_t>(tc) * (Rp / QT) + tr) * 512)[tid] =
-                reinterpret_cast<const uint4*>(sc[1])[tid];
+    if (tid < QT) {
+        uint8_t* to = st + fp4_scale_at(c0 + tid, r0 / 32, Rp);
+        if constexpr (TR == 128) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(col_scale[tid]);
+        else *to = col_scale[tid][0];
     }
 }
 
-// dst[r][c] = code * 2^s, rounded to T (exact where T's range holds it).  Eight
-// values per thread and step.
+// dst[r][c] = code * 2^s, rounded to T (exact where T's range holds it).  Eight values
+// per thread and row, threads along the columns, several rows in flight.
 template <typename T>
 __global__ void __launch_bounds__(256) fp4_dequantize_kernel(T* dst, const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                              int64_t R, int64_t C, int vec) {
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t per = (C + 7) / 8, n = R * per, Cp = fp4_padded(C);
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const int64_t r = i / per, c = (i - r * per) * 8;
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q + r * (Cp / 2) + c / 2));
-        const uint32_t byte = __ldg(s + fp4_scale_at(r, c / 32, Cp));
-        const float scale = fp4_scale_value(byte);
-        T o[8];
+    constexpr int ROWS = 4;
+    const int64_t c = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) * 8, Cp = fp4_padded(C);
+    if (c >= C) return;
+    const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.y;
+    for (int64_t ra = blockIdx.y * static_cast<int64_t>(blockDim.y) + threadIdx.y; ra < R; ra += ROWS * step) {
+        uint32_t w[ROWS], byte[ROWS];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = down<T>(fp4_code_value((w >> (4 * j)) & 15u) * scale);
-        T* d = dst + r * C + c;
-        if (vec && c + 8 <= C) {
+        for (int i = 0; i < ROWS; ++i) {
+            const int64_t r = lmin(ra + i * step, R - 1);
+            w[i] = __ldg(reinterpret_cast<const uint32_t*>(q + r * (Cp / 2) + c / 2));
+            byte[i] = __ldg(s + fp4_scale_at(r, c / 32, Cp));
+        }
 #pragma unroll
-            for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) reinterpret_cast<uint4*>(d)[j] = reinterpret_cast<const uint4*>(o)[j];
-        } else {
-            for (int j = 0; j < 8 && c + j < C; ++j) d[j] = o[j];
+        for (int i = 0; i < ROWS; ++i) {
+            const int64_t r = ra + i * step;
+            if (r >= R) break;
+            const float scale = fp4_scale_value(byte[i]);
+            __align__(16) T o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = down<T>(fp4_code_value((w[i] >> (4 * j)) & 15u) * scale);
+            T* d = dst + r * C + c;
+            if (vec) {
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) __stcs(reinterpret_cast<uint4*>(d) + j, reinterpret_cast<const uint4*>(o)[j]);
+            } else {
+                for (int j = 0; j < 8 && c + j < C; ++j) d[j] = o[j];
+            }
         }
     }
 }
 
-template <typename T>
-cudaError_t quantize_t(const LaunchCtx& c, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st, const void* src, int64_t R, int64_t C) {
+template <typename T, int TR>
+cudaError_t quantize_tiles(const LaunchCtx& c, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st, const void* src, int64_t R, int64_t C) {
     // tiles of the padded operands: along the columns to a multiple of 256, along the
-    // rows too where the transpose is asked for
+    // rows too where the transpose is asked for, to whole pieces of scales where not
     const int64_t tiles_c = q ? fp4_padded(C) / QT : (C + QT - 1) / QT;
-    const int64_t tiles_r = qt ? fp4_padded(R) / QT : (R + QT - 1) / QT;
-    if (tiles_c * tiles_r > 0x7fffffffll) return cudaErrorInvalidValue;
-    const int smem = q_smem<T>(qt != nullptr);
-    auto kern = fp4_quantize_kernel<T>;
+    const int64_t tiles_r = (qt ? fp4_padded(R) : (R + 127) / 128 * 128) / TR;
+    auto kern = fp4_quantize_kernel<T, TR>;
     static PerDeviceOnce setup;
     const cudaError_t e = setup.run(c.eng->device, [&](int&) {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, q_smem<T>(true));
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, q_smem<T, TR>(true));
     });
     if (e != cudaSuccess) return e;
     const int vec = C % (16 / static_cast<int64_t>(sizeof(T))) == 0 && aligned16(src);
-    const cudaError_t l = launch_pdl(kern, dim3(static_cast<unsigned>(tiles_c * tiles_r)), dim3(Q_THREADS), smem, c.stream,
-                                     static_cast<const T*>(src), q, s, qt, st, R, C, static_cast<int>(tiles_c), vec);
+    const cudaError_t l = launch_pdl(kern, dim3(static_cast<unsigned>(tiles_c * tiles_r)), dim3(Q_THREADS), q_smem<T, TR>(qt != nullptr),
+                                     c.stream, static_cast<const T*>(src), q, s, qt, st, R, C, static_cast<int>(tiles_c), vec);
     if (l != cudaSuccess) return l;
     c.count();
     return cudaGetLastError();
 }
 
 template <typename T>
+cudaError_t quantize_t(const LaunchCtx& c, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st, const void* src, int64_t R, int64_t C) {
+    // tiles of 32 rows until four of them per SM: then the SMs are busy with either
+    const int64_t small = fp4_padded(C) / QT * ((R + 31) / 32);
+    return small <= 4 * c.sm_count ? quantize_tiles<T, 32>(c, q, s, qt, st, src, R, C) : quantize_tiles<T, 128>(c, q, s, qt, st, src, R, C);
+}
+
+template <typename T>
 cudaError_t dequantize_t(const LaunchCtx& c, void* dst, const uint8_t* q, const uint8_t* s, int64_t R, int64_t C) {
-    const int64_t n = R * ((C + 7) / 8);
-    const int64_t blocks = lmin((n + 255) / 256, static_cast<int64_t>(c.sm_count) * 16);
+    const int64_t per = (C + 7) / 8;
+    unsigned bx = 8;
+    while (bx < 256 && bx < per) bx *= 2;
+    const unsigned by = 256 / bx;
+    const int64_t gx = (per + bx - 1) / bx;
+    int64_t gy = (R + by - 1) / by;
+    const int64_t most = lmax(1, c.sm_count * 32ll / gx);  // blocks enough for the whole GPU
+    if (gy > most) gy = most;
+    if (gy > 65535) gy = 65535;
     const int vec = C % 8 == 0 && aligned16(dst);
-    const cudaError_t l = launch_pdl(fp4_dequantize_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.stream,
-                                     static_cast<T*>(dst), q, s, R, C, vec);
+    const cudaError_t l = launch_pdl(fp4_dequantize_kernel<T>, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(bx, by), 0,
+                                     c.stream, static_cast<T*>(dst), q, s, R, C, vec);
     if (l != cudaSuccess) return l;
     c.count();
     return cudaGetLastError();
@@ -234,8 +315,8 @@ bi_status check_matrix(bi_engine eng, bi_dtype dt, int64_t rows, int64_t cols) {
     if (!eng) return fail(nullptr, BI_ERR_INVALID_ARG, "engine is NULL");
     if (dt != BI_F32 && dt != BI_BF16 && dt != BI_F16) return fail(eng, BI_ERR_INVALID_ARG, "dtype must be BI_F32, BI_BF16 or BI_F16");
     if (rows < 0 || cols <= 0) return fail(eng, BI_ERR_INVALID_ARG, "rows must be >= 0 and cols > 0");
-    if (rows > FP4_MAX_DIM || cols > FP4_MAX_DIM || fp4_padded(rows) / QT * (fp4_padded(cols) / QT) > 0x7fffffffll)
-        return fail(eng, BI_ERR_UNSUPPORTED, "rows and cols are limited to 2^31 - 256, and to 2^31 - 1 tiles of 128 x 128");
+    if (rows > FP4_MAX_DIM || cols > FP4_MAX_DIM || fp4_padded(rows) / QT * (fp4_padded(cols) / QT) > 0x1fffffffll)
+        return fail(eng, BI_ERR_UNSUPPORTED, "rows and cols are limited to 2^31 - 256, and to 2^29 - 1 tiles of 128 x 128");
     return BI_OK;
 }
 
