@@ -314,9 +314,11 @@ def fp4_buffers(rows: int, cols: int, device="cuda"):
 
 
 def _fp4_ptr(t, need):
-    """A codes or scales buffer of at least `need` bytes; an empty one has no storage to point at."""
-    if t is not None and not isinstance(t, int) and t.numel() * t.element_size() < need:
-        raise ValueError(f"bi: an MXFP4 buffer of {t.numel() * t.element_size()} bytes where {need} are needed (fp4_buffers)")
+    """A codes or scales buffer of at least `need` bytes."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.nbytes < need:
+        raise ValueError(f"bi: an MXFP4 buffer of {t.nbytes} bytes where {need} are needed (fp4_buffers)")
     return _ptr(t)
 
 

@@ -226,14 +226,15 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const T* __rest
 }
 
 // dst[r][c] = code * 2^s, rounded to T (exact where T's range holds it).  Eight values
-// per thread and row, threads along the columns, several rows in flight.
+// per thread and row, threads along the columns, several rows in flight (16 values of
+// 16 bits: 24 against 22 us for 8192 x 4096, half of each store's sector at a time).
 template <typename T>
 __global__ void __launch_bounds__(256) fp4_dequantize_kernel(T* dst, const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                              int64_t R, int64_t C, int vec) {
     grid_dep_wait();
     grid_dep_launch();
-    constexpr int ROWS = 4;
-    const int64_t c = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) * 8, Cp = fp4_padded(C);
+    constexpr int ROWS = 4, V = 8;
+    const int64_t c = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) * V, Cp = fp4_padded(C);
     if (c >= C) return;
     const int64_t step = static_cast<int64_t>(gridDim.y) * blockDim.y;
     for (int64_t ra = blockIdx.y * static_cast<int64_t>(blockDim.y) + threadIdx.y; ra < R; ra += ROWS * step) {
@@ -248,16 +249,26 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(T* dst, const uint8
         for (int i = 0; i < ROWS; ++i) {
             const int64_t r = ra + i * step;
             if (r >= R) break;
-            const float scale = fp4_scale_value(byte[i]);
-            __align__(16) T o[8];
+            // a code's bits as an f32's are the value * 2^-126; 2^126 2^s as one factor
+            // where it is in range
+            const bool one = byte[i] <= 128u;
+            const float scale = one ? __uint_as_float((byte[i] + 126u) << 23) : fp4_scale_value(byte[i]);
+            __align__(16) T o[V];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = down<T>(fp4_code_value((w[i] >> (4 * j)) & 15u) * scale);
+            for (int j = 0; j < V; ++j) {
+                const uint32_t code = w[i] >> (4 * j);
+                float v = __uint_as_float(((code & 8u) << 28) | ((code & 7u) << 22));
+                if (!one) v *= 8.507059173023462e37f;
+                o[j] = down<T>(v * scale);
+            }
             T* d = dst + r * C + c;
-            if (vec) {
+            if (vec && c + V <= C) {
 #pragma unroll
-                for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j) __stcs(reinterpret_cast<uint4*>(d) + j, reinterpret_cast<const uint4*>(o)[j]);
+                for (int j = 0; j < V * static_cast<int>(sizeof(T)) / 16; ++j) __stcs(reinterpret_cast<uint4*>(d) + j, reinterpret_cast<const uint4*>(o)[j]);
             } else {
-                for (int j = 0; j < 8 && c + j < C; ++j) d[j] = o[j];
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (c + j < C) d[j] = o[j];
             }
         }
     }
@@ -301,7 +312,7 @@ cudaError_t dequantize_t(const LaunchCtx& c, void* dst, const uint8_t* q, const 
     const int64_t most = lmax(1, c.sm_count * 32ll / gx);  // blocks enough for the whole GPU
     if (gy > most) gy = most;
     if (gy > 65535) gy = 65535;
-    const int vec = C % 8 == 0 && aligned16(dst);
+    const int vec = C % (16 / static_cast<int64_t>(sizeof(T))) == 0 && aligned16(dst);
     const cudaError_t l = launch_pdl(fp4_dequantize_kernel<T>, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(bx, by), 0,
                                      c.stream, static_cast<T*>(dst), q, s, R, C, vec);
     if (l != cudaSuccess) return l;

@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     const int cidx = static_cast<int>(blockIdx.x >> 1), ncl = static_cast<int>(gridDim.x >> 1);
     const int tiles = p.units_m * p.num_n;
 
+    if (warp == 2 && lane < 5) prefetch_map(lane == 0 ? &tmA : lane == 1 ? &tmB : lane == 2 ? &tmSA : lane == 3 ? &tmSB : &tmO);
     if (threadIdx.x == 0) {
         for (int s = 0; s < F_STAGES; ++s) {
             mbar_init(full_bar(s), 1);
@@ -255,27 +256,18 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) f[j] = __fadd_rn(f[j], __shfl_sync(0xffffffffu, bv[j & 7], ((cs + c16) >> 3) + (j >> 3)));
                     }
-                    if (p.tma_out) {
-                        const uint32_t at = buf + static_cast<uint32_t>(lane * 128);
-                        constexpr int CH = OES;  // 16-byte chunks of 16 columns
+                    const uint32_t at = buf + static_cast<uint32_t>(lane * 128);
+                    constexpr int CH = OES;  // 16-byte chunks of 16 columns
 #pragma unroll
-                        for (int j = 0; j < CH; ++j) {
-                            uint32_t w[4];
+                    for (int j = 0; j < CH; ++j) {
+                        uint32_t w[4];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                w[x] = OUT == 2 ? __float_as_uint(f[(4 * j + x) & 15]) : O::pack(f[(8 * j + 2 * x) & 15], f[(8 * j + 2 * x + 1) & 15]);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             at + static_cast<uint32_t>(((c16 * OES / 16 + j) ^ (lane & 7)) * 16)),
-                                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                         : "memory");
-                        }
-                    } else if (orow < p.rows) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (cb + j >= p.cols) break;
-                            if (OUT == 2) static_cast<float*>(p.out)[orow * p.ldo + cb + j] = f[j];
-                            else O::store1(p.out, orow * p.ldo + cb + j, f[j]);
-                        }
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = OUT == 2 ? __float_as_uint(f[(4 * j + x) & 15]) : O::pack(f[(8 * j + 2 * x) & 15], f[(8 * j + 2 * x + 1) & 15]);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         at + static_cast<uint32_t>(((c16 * OES / 16 + j) ^ (lane & 7)) * 16)),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
                     }
                 }
                 if (i == F_SHARED / CPS - 1) {
@@ -291,6 +283,21 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                         bulk_commit();
                     }
                     ++oslot;
+                } else if (any) {  // rows that TMA cannot store, one after the other, a lane to a column
+                    __syncwarp();
+                    const int rows = static_cast<int>(lmin(32, p.rows - row0));
+                    for (int r = 0; r < rows; ++r) {
+#pragma unroll
+                        for (int x = 0; x < CPS; x += 32) {
+                            const int cc = x + lane;
+                            if (col0 + cs + cc >= p.cols) continue;
+                            const uint8_t* from = smem + (buf - sbase) + r * 128 + (((cc * OES / 16) ^ (r & 7)) * 16) + cc * OES % 16;
+                            const int64_t o = (row0 + r) * p.ldo + col0 + cs + cc;
+                            if (OUT == 2) static_cast<uint32_t*>(p.out)[o] = *reinterpret_cast<const uint32_t*>(from);
+                            else static_cast<uint16_t*>(p.out)[o] = *reinterpret_cast<const uint16_t*>(from);
+                        }
+                    }
+                    __syncwarp();
                 }
             }
         }

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(slot + 1);
 
+    if (warp == 2 && lane < (FP4 ? 5 : 4)) prefetch_map(lane == 0 ? &tmA0 : lane == 1 ? &tmA1 : lane == 2 ? &tmB : lane == 3 ? &tmB8 : &tmSB);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.depth; ++s) {
             mbar_init(full_bar(s), FP4 ? 2 : 1);

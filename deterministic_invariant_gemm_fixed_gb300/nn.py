@@ -22,11 +22,17 @@ backward quantizes the output gradient with scale_g and computes dX and dW from
 the saved codes the same way.  The bias gradient is the fixed-order column sum
 of the unquantized output gradient.
 
+FP4 route: with `fp4=True` the three matmuls run on MXFP4 codes of x, the weight and
+the output gradient, each operand quantized along that product's contraction (blocks
+of 32 with a power-of-two scale taken from the block, so there are no scales to pass);
+the backward keeps codes of x and the weight in place of the tensors.
+
 Beside the layer: `adapter_linear` (a shared projection with the low-rank adapter
 of each row), `route` (a router's expert choice, weights, counts and balance
-loss, whose ids the grouped matmul takes) and `clip_grad_norm_` (global gradient
-norm and clipping of a parameter list), each over its own entry points of the
-library, so a training step made of them is bit-reproducible too.
+loss, whose ids the grouped matmul takes), `clip_grad_norm_` (global gradient
+norm and clipping of a parameter list) and `moe` (router and experts of a decoding
+step, with weights of x's type or in MXFP4), each over its own entry points of the
+library, so a program made of them is bit-reproducible too.
 """
 from __future__ import annotations
 
@@ -37,7 +43,7 @@ import threading
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import Engine, TensorSet
+from . import Engine, TensorSet, fp4_buffers
 
 _engines: dict[int, Engine] = {}
 _engines_lock = threading.Lock()
@@ -191,13 +197,67 @@ class _DeterministicLinearFp8(torch.autograd.Function):
         return gx, gw, gb, None
 
 
+class _DeterministicLinearFp4(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias):
+        _check(x, weight, bias)
+        k, n = weight.shape
+        x2 = x.reshape(-1, k).contiguous()
+        w = weight.contiguous()
+        b = bias.contiguous() if bias is not None else None
+        m, dt, dev = x2.shape[0], x.dtype, x.device
+        eng, stream = engine_for(dev), torch.cuda.current_stream(dev)
+        need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        xq, wq = fp4_buffers(m, k, dev), fp4_buffers(n, k, dev)
+        xt = fp4_buffers(k, m, dev) if need_w else (None, None)
+        wt = fp4_buffers(k, n, dev) if need_x else (None, None)
+        eng.fp4_quantize(*xq, *xt, x2, m, k, dt, stream)
+        eng.fp4_quantize(*wt, *wq, w, k, n, dt, stream)
+        y = torch.empty(m, n, dtype=dt, device=dev)
+        eng.fp4_forward(y, *xq, *wq, b, m, k, n, dt, stream)
+        ctx.save_for_backward(*xt, *wt)
+        ctx.sizes, ctx.dtype, ctx.has_bias, ctx.x_shape = (m, k, n), dt, bias is not None, x.shape
+        return y.reshape(*x.shape[:-1], n)
+
+    @staticmethod
+    @once_differentiable  # a second derivative is refused, not left out
+    def backward(ctx, gy):
+        xt, xts, wt, wts = ctx.saved_tensors
+        (m, k, n), dt = ctx.sizes, ctx.dtype
+        gy2 = gy.reshape(-1, n).to(dt).contiguous()
+        dev = gy2.device
+        eng, stream = engine_for(dev), torch.cuda.current_stream(dev)
+        gq = fp4_buffers(m, n, dev) if wt is not None else (None, None)
+        gt = fp4_buffers(n, m, dev) if xt is not None else (None, None)
+        if wt is not None or xt is not None:
+            eng.fp4_quantize(*gq, *gt, gy2, m, n, dt, stream)
+        gx = gw = gb = None
+        if wt is not None:
+            gx = torch.empty(m, k, dtype=dt, device=dev)
+            eng.fp4_backward_dx(gx, *gq, wt, wts, m, k, n, dt, stream)
+            gx = gx.reshape(ctx.x_shape)
+        if xt is not None:
+            gw = torch.empty(k, n, dtype=dt, device=dev)
+            eng.fp4_backward_dw(gw, xt, xts, *gt, m, k, n, dt, stream)
+        if ctx.has_bias and ctx.needs_input_grad[2]:
+            gb = torch.empty(n, dtype=dt, device=dev)
+            eng.bias_grad(gb, int(dt == torch.float32), gy2, m, n, dt, stream)
+        return gx, gw, gb
+
+
 def deterministic_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
-                         tensor_cores: bool = True, fp8: Fp8Scales | None = None) -> torch.Tensor:
+                         tensor_cores: bool = True, fp8: Fp8Scales | None = None, fp4: bool = False) -> torch.Tensor:
     """y = x @ weight (+ bias) with weight [in, out]; bit-reproducible forward and
     backward (scalar tier with tensor_cores=False, tcgen05 tier otherwise).
     With fp8 (Fp8Scales), the three matmuls run on e4m3 codes of x, the weight
     and the output gradient, quantized with the given per-tensor scales, on the
-    tensor cores (tensor_cores is then ignored)."""
+    tensor cores (tensor_cores is then ignored).  With fp4, on MXFP4 codes of them
+    (any sizes and types; likewise).  The gradients are those of the products, with
+    the rounding to codes passed through."""
+    if fp4:
+        if fp8 is not None:
+            raise ValueError("deterministic_linear: fp8 and fp4 exclude each other")
+        return _DeterministicLinearFp4.apply(x, weight, bias)
     if fp8 is not None:
         return _DeterministicLinearFp8.apply(x, weight, bias, fp8)
     return _DeterministicLinear.apply(x, weight, bias, tensor_cores)
@@ -354,6 +414,83 @@ def route(logits: torch.Tensor, k: int, normalize: bool = True, valid: torch.Ten
     E * sum_e (counts_e / kV) * mean_t p_te over the V rows that take part.
     Gradients of the weights and the loss reach the logits."""
     return _Route.apply(logits, k, normalize, valid)
+
+
+@dataclasses.dataclass
+class Fp4Weight:
+    """Expert weights [E, rows, length] kept in MXFP4 along their last dimension."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    shape: tuple[int, int, int]
+
+    @classmethod
+    def quantize(cls, w: torch.Tensor) -> "Fp4Weight":
+        if w.dim() != 3 or not w.is_cuda:
+            raise ValueError("Fp4Weight needs a CUDA tensor [experts, rows, length]")
+        e, r, n = w.shape
+        q, s = fp4_buffers(e * r, n, w.device)
+        engine_for(w.device).fp4_quantize(q, s, None, None, w.detach().contiguous(), e * r, n, w.dtype,
+                                          torch.cuda.current_stream(w.device))
+        return cls(q, s, (e, r, n))
+
+    def dequantize(self, dtype=torch.float32) -> torch.Tensor:
+        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        e, r, n = self.shape
+        engine_for(out.device).fp4_dequantize(out, self.codes, self.scales, e * r, n, dtype,
+                                              torch.cuda.current_stream(out.device))
+        return out
+
+
+def moe(x: torch.Tensor, logits: torch.Tensor, w_gate, w_up, w_down, k: int, normalize: bool = True,
+        valid: torch.Tensor | None = None, activation: str = "silu") -> torch.Tensor:
+    """A mixture-of-experts layer on the tokens x [..., in] of a decoding step, routed by
+    logits [..., E] (see `route`): y = sum over the k chosen experts of their weight times
+    (act(x w_gate[e].T) * (x w_up[e].T)) w_down[e].T, with w_gate and w_up [E, hidden, in]
+    (w_gate None: act(x w_up[e].T)) and w_down [E, out, hidden], all tensors of x's dtype
+    or all Fp4Weight.  activation: "silu", "gelu" (the tanh form) or "relu".  Rows with
+    valid = 0 get zeros.  A row's y does not depend on the rows beside it; more than
+    2048 / k tokens go in several calls, where `route` and the grouped matmul are
+    faster.  Forward only: tensors that require a gradient are refused."""
+    weights = [w for w in (w_gate, w_up, w_down) if w is not None]
+    fp4 = isinstance(w_up, Fp4Weight)
+    if any(isinstance(w, Fp4Weight) != fp4 for w in weights):
+        raise ValueError("moe: the expert weights must be all tensors or all Fp4Weight")
+    if not x.is_cuda or not logits.is_cuda or logits.device != x.device:
+        raise ValueError("moe needs CUDA tensors on one device")
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, logits, *weights)):
+        raise ValueError("moe has no backward: train with route and the grouped matmul, or call it under no_grad")
+    (e, f, n_in), (_, n_out, _) = w_up.shape, w_down.shape
+    if tuple(w_down.shape) != (e, n_out, f) or (w_gate is not None and tuple(w_gate.shape) != (e, f, n_in)):
+        raise ValueError("moe: w_gate and w_up must be [E, hidden, in] and w_down [E, out, hidden]")
+    if x.shape[-1] != n_in or logits.shape != (*x.shape[:-1], e):
+        raise ValueError("moe: x must be [..., in] and logits [..., E]")
+    if any((w.codes if fp4 else w).device != x.device for w in weights) or (not fp4 and any(w.dtype != x.dtype for w in weights)):
+        raise ValueError("moe: the expert weights must be on x's device and, unless quantized, of its dtype")
+    dev, dt = x.device, x.dtype
+    x2, l2 = x.reshape(-1, n_in).contiguous(), logits.reshape(-1, e).contiguous()
+    t = x2.shape[0]
+    if valid is not None:
+        if valid.shape != x.shape[:-1] or valid.dtype not in (torch.bool, torch.uint8) or valid.device != dev:
+            raise ValueError("valid must be bool or uint8, one per row of x")
+        valid = valid.reshape(-1).contiguous()
+    eng, stream = engine_for(dev), torch.cuda.current_stream(dev)
+    def new(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device=dev)
+    ids, p = new(t, k, dtype=torch.int32), new(t, k)
+    eng.router_forward(ids, p, new(e, dtype=torch.int32), new(1, dtype=torch.int32), new(e), new(1), new(t), l2, valid, t, e, k,
+                       normalize, l2.dtype, stream)
+    y = new(t, n_out, dtype=dt)
+    if fp4:
+        args = [v for w in (w_gate, w_up, w_down) for v in ((w.codes, w.scales) if w is not None else (None, None))]
+        call = eng.moe_forward_fp4
+    else:
+        args = [w.contiguous() if w is not None else None for w in (w_gate, w_up, w_down)]
+        call = eng.moe_forward
+    step = max(1, 2048 // k)
+    for i in range(0, t, step):
+        rows = slice(i, min(t, i + step))
+        call(y[rows], x2[rows], ids[rows], p[rows], *args, rows.stop - i, k, n_in, f, n_out, e, activation, dt, stream)
+    return y.reshape(*x.shape[:-1], n_out)
 
 
 def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
