@@ -156,11 +156,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             }
         }
         // CTA 0's MMA warp takes every copy of both CTAs before it finishes, unless a wait
-        // gave up: then the copies in flight, microseconds of work, get a millisecond
-        if (!ok) {
-            const unsigned long long t0 = globaltimer();
-            while (globaltimer() - t0 < 1000000ull) {}
-        }
+        // gave up (see the teardown)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (CTA 0)
         if (crank == 0) {
@@ -306,7 +302,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    __syncwarp();
+    if (threadIdx.x == 0 && *abort_flag) settle_copies();
+    __syncthreads();
     cluster_sync();
     if (warp == 1) {
         __syncwarp();

@@ -272,11 +272,6 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
             ++made;
             advance(x, c);
         }
-        if (!ok) {  // a wait gave up: the copies in flight land first
-            __syncwarp();
-            const unsigned long long t0 = globaltimer();
-            while (globaltimer() - t0 < 1000000ull) {}
-        }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         const uint32_t lead = elect_lane();
@@ -492,6 +487,8 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         }
     }
     tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) settle_copies();
     __syncthreads();
     if (warp == 1) {
         __syncwarp();

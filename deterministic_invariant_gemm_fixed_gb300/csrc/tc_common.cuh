@@ -82,6 +82,14 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// The same for copies, where what is in flight is not known (another role, or the other
+// CTA of a pair, may have given up first): a millisecond, in which microseconds of work
+// are done.  By one thread, before the CTA lets its shared memory go.
+static __device__ __noinline__ void settle_copies() {
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {}
+}
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
