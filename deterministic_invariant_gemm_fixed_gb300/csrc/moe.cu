@@ -11,8 +11,11 @@
 // added in the order j = 0, 1, ..: a row of y does not depend on the tokens beside it.
 //
 // Two forms.  16-bit weights that TMA can read (rows of a multiple of 16 bytes) and MXFP4
-// weights run on tcgen05 (moe_tc.cu).  This one, for f32 and for odd sizes, is a warp to
-// two weight rows in f32 FMAs, h in f32.
+// weights run on tcgen05 (moe_tc.cu).  This one, for f32 and for odd sizes, is in f32
+// FMAs, a warp to four weight rows and up to eight tokens at a time, h in f32: the lanes go
+// along the contraction, eight elements at a time, and are added by a tree.  A hidden warp's
+// rows are two of the gate's and the same two of up's; an output block has four rows, its
+// warps different experts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -23,8 +26,8 @@ namespace bi {
 namespace {
 
 constexpr int M_WARPS = 8, M_THREADS = 32 * M_WARPS;
-constexpr int M_ROWS = 2;                // weight rows of a warp
-constexpr int M_BLOCK = M_WARPS * M_ROWS;
+constexpr int M_ROWS = 4;                // weight rows of a warp
+constexpr int M_COLS = 8;                // most tokens of a pass
 
 template <typename T> __device__ __forceinline__ float up(T v);
 template <> __device__ __forceinline__ float up<float>(float v) { return v; }
@@ -55,189 +58,190 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int64_t k, int6
     }
 }
 
-// Weight rows [rows][L].
-template <typename T>
-struct Weights {
-    const T* w;
-    int64_t L;
-    int vec;
-    __device__ __forceinline__ void load(int64_t row, int64_t k, float (&v)[8]) const { load8<T>(w + row * L, k, L, vec != 0, v); }
-};
-
-// acc[r][c] += rows row0 + r of W times columns c of the operand (colp[c], of length L).
+// v[row * NC + column], one value for each lane: of the inner products of four weight rows
+// with NC columns, the one of index lane / (32 / (4 NC)).  The lanes' sums are added by the
+// tree of offsets 16, 8, .. 1, for a value the same whatever NC is.
 template <typename T, typename X, int NC>
-__device__ __forceinline__ void dot_rows(const Weights<T>& W, int64_t row0, int nrows, const X* const (&colp)[NC], bool xvec,
-                                         float (&acc)[M_ROWS][NC]) {
+__device__ __forceinline__ float dot_rows(const T* const (&row)[M_ROWS], bool vec, const X* const (&col)[NC], bool xvec, int64_t L) {
     const int lane = threadIdx.x & 31;
+    float v[M_ROWS * NC];
 #pragma unroll
-    for (int r = 0; r < M_ROWS; ++r)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) acc[r][c] = 0.0f;
+    for (int i = 0; i < M_ROWS * NC; ++i) v[i] = 0.0f;
 #pragma unroll 2
-    for (int64_t k = lane * 8; k < W.L; k += 256) {
+    for (int64_t k = lane * 8; k < L; k += 256) {
         float w[M_ROWS][8];
 #pragma unroll
-        for (int r = 0; r < M_ROWS; ++r) W.load(row0 + min(r, nrows - 1), k, w[r]);
+        for (int r = 0; r < M_ROWS; ++r) load8<T>(row[r], k, L, vec, w[r]);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float x[8];
-            load8<X>(colp[c], k, W.L, xvec, x);
+            load8<X>(col[c], k, L, xvec, x);
 #pragma unroll
             for (int r = 0; r < M_ROWS; ++r)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[r][c] = fmaf(w[r][i], x[i], acc[r][c]);
+                for (int i = 0; i < 8; ++i) v[r * NC + c] = fmaf(w[r][i], x[i], v[r * NC + c]);
         }
     }
+    int n = M_ROWS * NC;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1) {
+        if (n > 1) {  // the lanes with the offset's bit go on with the upper half of the values
+            n /= 2;
+            const bool upper = lane & o;
 #pragma unroll
-        for (int r = 0; r < M_ROWS; ++r)
-#pragma unroll
-            for (int c = 0; c < NC; ++c) acc[r][c] += __shfl_xor_sync(0xffffffffu, acc[r][c], o);
+            for (int i = 0; i < M_ROWS * NC / 2; ++i)
+                if (i < n) {
+                    const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+    return v[0];
 }
 
 template <typename T>
 struct MoeArgs {
-    Weights<T> gate, up, down;  // gate.w null: no gate
-    const void* x;
+    const T *gate, *up, *down;   // gate null: none
+    const T* x;
     const uint32_t* ids;
     const float* weights;
     float* h;                    // [P][F]
-    void* y;
-    int tokens, C, E, act, xvec, hvec;
+    T* y;
+    int tokens, C, E, act;
+    int wvec, dvec, xvec, hvec;  // whether load8 may read 16 bytes at a time: gate and up, down, x, h
     int64_t K, F, N;
 };
 
 template <typename T, int NC>
-__device__ __forceinline__ void hidden_tokens(const MoeArgs<T>& a, const Plan& p, int e, int c0, int cn, int64_t f0, int nrows) {
-    const T* colp[NC];
-    int pair[NC];
+__device__ __forceinline__ void hidden_tokens(const MoeArgs<T>& a, const uint16_t* list, int e, int n, int64_t f0) {
+    const int lane = threadIdx.x & 31;
+    const bool gated = a.gate != nullptr;
+    const T* row[M_ROWS];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        pair[c] = p.list[p.first[e] + c0 + min(c, cn - 1)];
-        colp[c] = static_cast<const T*>(a.x) + static_cast<int64_t>(pair[c] / a.C) * a.K;
+    for (int r = 0; r < M_ROWS; ++r) {
+        const int64_t f = e * a.F + lmin(f0 + (gated ? r % 2 : r), a.F - 1);
+        row[r] = (gated && r >= 2 ? a.gate : a.up) + f * a.K;
     }
-    float u[M_ROWS][NC], g[M_ROWS][NC];
-    dot_rows<T, T, NC>(a.up, e * a.F + f0, nrows, colp, a.xvec != 0, u);
-    if (a.gate.w != nullptr) dot_rows<T, T, NC>(a.gate, e * a.F + f0, nrows, colp, a.xvec != 0, g);
-    if ((threadIdx.x & 31) != 0) return;
-    for (int c = 0; c < NC && c < cn; ++c)
-        for (int r = 0; r < nrows; ++r)
-            a.h[pair[c] * a.F + f0 + r] = a.gate.w != nullptr ? activate(g[r][c], a.act) * u[r][c] : activate(u[r][c], a.act);
+    const T* col[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) col[c] = a.x + static_cast<int64_t>(list[min(c, n - 1)] / a.C) * a.K;
+    const float v = dot_rows<T, T, NC>(row, a.wvec != 0, col, a.xvec != 0, a.K);
+    constexpr int EACH = 32 / (M_ROWS * NC);  // lanes with the same value
+    const int r = lane / EACH / NC, c = lane / EACH % NC;
+    const float g = __shfl_down_sync(0xffffffffu, v, 16);  // the gate's rows are the upper half
+    if (lane % EACH == 0 && c < n && f0 + r < a.F && (!gated || r < 2))
+        a.h[list[c] * a.F + f0 + r] = gated ? activate(g, a.act) * v : activate(v, a.act);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(M_THREADS) moe_hidden_kernel(const MoeArgs<T> a) {
+__global__ void __launch_bounds__(M_THREADS, 2) moe_hidden_kernel(const MoeArgs<T> a) {
     extern __shared__ __align__(16) uint8_t smem[];
     grid_dep_wait();
     grid_dep_launch();
     const Plan p = build_plan<1>(smem, a.ids, a.tokens * a.C, a.E);
-    const int64_t f0 = static_cast<int64_t>(blockIdx.x) * M_BLOCK + (threadIdx.x >> 5) * M_ROWS;
+    const int64_t f0 = (static_cast<int64_t>(blockIdx.x) * M_WARPS + (threadIdx.x >> 5)) * (a.gate ? 2 : 4);
     if (static_cast<int>(blockIdx.y) >= p.n || f0 >= a.F) return;
     const int e = p.active[blockIdx.y], n = static_cast<int>(p.cnt[e]);
-    const int nrows = static_cast<int>(lmin(M_ROWS, a.F - f0));
-    for (int c0 = 0; c0 < n; c0 += 4) {
-        const int cn = min(4, n - c0);
-        if (cn == 1) hidden_tokens<T, 1>(a, p, e, c0, cn, f0, nrows);
-        else hidden_tokens<T, 4>(a, p, e, c0, cn, f0, nrows);
+    const uint16_t* list = p.list + p.first[e];
+    for (int c0 = 0; c0 < n; c0 += M_COLS) {
+        const int cn = min(M_COLS, n - c0);
+        if (cn == 1) hidden_tokens<T, 1>(a, list + c0, e, cn, f0);
+        else if (cn == 2) hidden_tokens<T, 2>(a, list + c0, e, cn, f0);
+        else if (cn <= 4) hidden_tokens<T, 4>(a, list + c0, e, cn, f0);
+        else hidden_tokens<T, 8>(a, list + c0, e, cn, f0);
     }
 }
 
 template <typename T, int NC>
-__device__ __forceinline__ void output_tokens(const MoeArgs<T>& a, const Plan& p, float* part, int e, int c0, int cn, int64_t n0,
-                                              int nrows) {
-    const float* colp[NC];
-    int pair[NC];
+__device__ __forceinline__ void output_tokens(const MoeArgs<T>& a, const uint16_t* list, float* part, int e, int n, int64_t n0) {
+    const int lane = threadIdx.x & 31;
+    const T* row[M_ROWS];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        pair[c] = p.list[p.first[e] + c0 + min(c, cn - 1)];
-        colp[c] = a.h + pair[c] * a.F;
-    }
-    float o[M_ROWS][NC];
-    dot_rows<T, float, NC>(a.down, e * a.N + n0, nrows, colp, a.hvec != 0, o);
-    if ((threadIdx.x & 31) == 0)
-        for (int c = 0; c < NC && c < cn; ++c)
-            for (int r = 0; r < M_ROWS; ++r) part[pair[c] * M_BLOCK + r] = o[r][c];
+    for (int r = 0; r < M_ROWS; ++r) row[r] = a.down + (e * a.N + lmin(n0 + r, a.N - 1)) * a.F;
+    const float* col[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) col[c] = a.h + list[min(c, n - 1)] * a.F;
+    const float v = dot_rows<T, float, NC>(row, a.dvec != 0, col, a.hvec != 0, a.F);
+    constexpr int EACH = 32 / (M_ROWS * NC);
+    const int r = lane / EACH / NC, c = lane / EACH % NC;
+    if (lane % EACH == 0 && c < n) part[list[c] * M_ROWS + r] = v;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(M_THREADS) moe_output_kernel(const MoeArgs<T> a) {
+__global__ void __launch_bounds__(M_THREADS, 2) moe_output_kernel(const MoeArgs<T> a) {
     extern __shared__ __align__(16) uint8_t smem[];
     grid_dep_wait();
     grid_dep_launch();
-    const int P = a.tokens * a.C;
+    const int P = a.tokens * a.C, warp = threadIdx.x >> 5;
     const Plan p = build_plan<1>(smem, a.ids, P, a.E);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * M_BLOCK + warp * M_ROWS;
-    if (n0 >= a.N) return;
-    const int nrows = static_cast<int>(lmin(M_ROWS, a.N - n0));
-    float* part = reinterpret_cast<float*>(smem + plan_bytes(a.E, P, 1)) + warp * M_ROWS;  // [P][M_BLOCK], this warp's rows
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * M_ROWS;
+    float* part = reinterpret_cast<float*>(smem + plan_bytes(a.E, P, 1));  // [P][M_ROWS]
+    int item = 0;  // (expert, up to eight of its tokens), dealt to the warps
     for (int i = 0; i < p.n; ++i) {
         const int e = p.active[i], n = static_cast<int>(p.cnt[e]);
-        for (int c0 = 0; c0 < n; c0 += 4) {
-            const int cn = min(4, n - c0);
-            if (cn == 1) output_tokens<T, 1>(a, p, part, e, c0, cn, n0, nrows);
-            else output_tokens<T, 4>(a, p, part, e, c0, cn, n0, nrows);
+        const uint16_t* list = p.list + p.first[e];
+        for (int c0 = 0; c0 < n; c0 += M_COLS, ++item) {
+            if (item % M_WARPS != warp) continue;
+            const int cn = min(M_COLS, n - c0);
+            if (cn == 1) output_tokens<T, 1>(a, list + c0, part, e, cn, n0);
+            else if (cn == 2) output_tokens<T, 2>(a, list + c0, part, e, cn, n0);
+            else if (cn <= 4) output_tokens<T, 4>(a, list + c0, part, e, cn, n0);
+            else output_tokens<T, 8>(a, list + c0, part, e, cn, n0);
         }
     }
-    __syncwarp();
-    for (int t = lane; t < a.tokens; t += 32)
-        for (int r = 0; r < nrows; ++r) {
-            float s = 0.0f;
-            for (int j = 0; j < a.C; ++j)
-                if (__ldg(a.ids + t * a.C + j) < static_cast<uint32_t>(a.E))
-                    s = fmaf(__ldg(a.weights + t * a.C + j), part[(t * a.C + j) * M_BLOCK + r], s);
-            static_cast<T*>(a.y)[t * a.N + n0 + r] = down<T>(s);
-        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.tokens * M_ROWS; i += M_THREADS) {
+        const int t = i / M_ROWS, r = i % M_ROWS;
+        if (n0 + r >= a.N) continue;
+        float s = 0.0f;
+        for (int j = 0; j < a.C; ++j)
+            if (__ldg(a.ids + t * a.C + j) < static_cast<uint32_t>(a.E))
+                s = fmaf(__ldg(a.weights + t * a.C + j), part[(t * a.C + j) * M_ROWS + r], s);
+        a.y[t * a.N + n0 + r] = down<T>(s);
+    }
 }
 
 template <typename T>
-cudaError_t moe_t(const LaunchCtx& c, const MoeArgs<T>& a) {
-    const int64_t P = static_cast<int64_t>(a.tokens) * a.C;
-    const int64_t plan = plan_bytes(a.E, P, 1), out_smem = plan + P * M_BLOCK * 4;
-    auto kh = moe_hidden_kernel<T>;
-    auto ko = moe_output_kernel<T>;
-    static PerDeviceOnce setup;
-    cudaError_t e = setup.run(c.eng->device, [&](int&) {
-        return cudaFuncSetAttribute(ko, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(plan_bytes(MOE_MAX_E, MOE_MAX_PAIRS, 1) + MOE_MAX_PAIRS * M_BLOCK * 4));
-    });
-    if (e != cudaSuccess) return e;
-    const dim3 gh(static_cast<unsigned>((a.F + M_BLOCK - 1) / M_BLOCK), static_cast<unsigned>(lmin(a.E, P)));
-    if ((e = launch_pdl(kh, gh, dim3(M_THREADS), plan, c.stream, a)) != cudaSuccess) return e;
-    c.count();
-    const dim3 go(static_cast<unsigned>((a.N + M_BLOCK - 1) / M_BLOCK));
-    if ((e = launch_pdl(ko, go, dim3(M_THREADS), out_smem, c.stream, a)) != cudaSuccess) return e;
-    c.count();
-    return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t moe_f32(const LaunchCtx& c, const MoeCall& m, float* h) {
+cudaError_t moe_fma(const LaunchCtx& c, const MoeCall& m, float* h) {
     MoeArgs<T> a{};
-    auto set = [](Weights<T>& w, const void* p, int64_t L) {
-        w.w = static_cast<const T*>(p);
-        w.L = L;
-        w.vec = L % 8 == 0 && aligned16(p);
-    };
-    set(a.gate, m.gate, m.K);
-    set(a.up, m.up, m.K);
-    set(a.down, m.down, m.F);
-    a.x = m.x;
+    a.gate = static_cast<const T*>(m.gate);
+    a.up = static_cast<const T*>(m.up);
+    a.down = static_cast<const T*>(m.down);
+    a.x = static_cast<const T*>(m.x);
     a.ids = m.ids;
     a.weights = m.weights;
     a.h = h;
-    a.y = m.y;
+    a.y = static_cast<T*>(m.y);
     a.tokens = m.T;
     a.C = m.C;
     a.E = m.E;
     a.act = m.act;
+    a.wvec = m.K % 8 == 0 && aligned16(m.gate) && aligned16(m.up);
+    a.dvec = m.F % 8 == 0 && aligned16(m.down);
     a.xvec = m.K % 8 == 0 && aligned16(m.x);
     a.hvec = m.F % 8 == 0;
     a.K = m.K;
     a.F = m.F;
     a.N = m.N;
-    return moe_t<T>(c, a);
+    const int64_t P = static_cast<int64_t>(a.tokens) * a.C, plan = plan_bytes(a.E, P, 1);
+    auto kh = moe_hidden_kernel<T>;
+    auto ko = moe_output_kernel<T>;
+    static PerDeviceOnce setup;
+    cudaError_t e = setup.run(c.eng->device, [&](int&) {
+        return cudaFuncSetAttribute(ko, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(plan_bytes(MOE_MAX_E, MOE_MAX_PAIRS, 1) + MOE_MAX_PAIRS * M_ROWS * 4));
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t span = M_WARPS * (a.gate ? 2 : 4);
+    const dim3 gh(static_cast<unsigned>((a.F + span - 1) / span), static_cast<unsigned>(lmin(a.E, P)));
+    if ((e = launch_pdl(kh, gh, dim3(M_THREADS), static_cast<size_t>(plan), c.stream, a)) != cudaSuccess) return e;
+    c.count();
+    const dim3 go(static_cast<unsigned>((a.N + M_ROWS - 1) / M_ROWS));
+    if ((e = launch_pdl(ko, go, dim3(M_THREADS), static_cast<size_t>(plan + P * M_ROWS * 4), c.stream, a)) != cudaSuccess) return e;
+    c.count();
+    return cudaGetLastError();
 }
 
 bi_status moe(bi_engine eng, const MoeCall& call, int64_t t, int64_t c, int64_t e, bool fp4, bi_dtype dt, void* stream, const char* name) {
@@ -276,9 +280,9 @@ bi_status moe(bi_engine eng, const MoeCall& call, int64_t t, int64_t c, int64_t 
     if (sc.err != cudaSuccess) return cuda_fail(eng, sc.err, "hidden scratch");
     cudaError_t err;
     if (tc) err = moe_tc(lc, m, fp4, copy_x, dt, sc.ptr);
-    else if (dt == BI_F32) err = moe_f32<float>(lc, m, static_cast<float*>(sc.ptr));
-    else if (dt == BI_BF16) err = moe_f32<__nv_bfloat16>(lc, m, static_cast<float*>(sc.ptr));
-    else err = moe_f32<__half>(lc, m, static_cast<float*>(sc.ptr));
+    else if (dt == BI_F32) err = moe_fma<float>(lc, m, static_cast<float*>(sc.ptr));
+    else if (dt == BI_BF16) err = moe_fma<__nv_bfloat16>(lc, m, static_cast<float*>(sc.ptr));
+    else err = moe_fma<__half>(lc, m, static_cast<float*>(sc.ptr));
     return err == cudaSuccess ? BI_OK : cuda_fail(eng, err, name);
 }
 
