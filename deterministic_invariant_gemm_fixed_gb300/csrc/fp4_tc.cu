@@ -36,10 +36,11 @@ constexpr int F_SFA = 1024, F_SFB = 2048;  // scales of 128 rows, of 256 columns
 constexpr int F_STAGE = 2 * F_TILE + F_SFA + F_SFB;
 static_assert(F_STAGE % 1024 == 0, "stages start on the swizzle's atom");
 constexpr int F_OUT = 4 * 2 * 32 * 128;    // output staging: two slices of 32 rows x 128 bytes per epilogue warp
+constexpr int F_BIAS = 4 * 256 * 4;        // the tile's bias in f32, a copy per epilogue warp
 constexpr int F_BARS = 256;
 constexpr int F_LIMIT = 227 * 1024;
-constexpr int F_STAGES = (F_LIMIT - 1024 - F_OUT - F_BARS) / F_STAGE;
-constexpr int F_SMEM = 1024 + F_STAGES * F_STAGE + F_OUT + F_BARS;
+constexpr int F_STAGES = (F_LIMIT - 1024 - F_OUT - F_BIAS - F_BARS) / F_STAGE;
+constexpr int F_SMEM = 1024 + F_STAGES * F_STAGE + F_OUT + F_BIAS + F_BARS;
 static_assert(F_STAGES == 5 && F_SMEM <= F_LIMIT, "ring depth");
 constexpr int F_ACC1 = 192, F_SHARED = 64;  // second accumulator's column; columns both have
 constexpr int F_SF = 448, F_SF_STAGE = 24;  // scales' first column; columns per stage (A 8, B 16)
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t ostage = sbase + F_STAGES * F_STAGE;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F_STAGES * F_STAGE + F_OUT);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F_STAGES * F_STAGE + F_OUT + F_BIAS);
     const uint32_t bar0 = smem_u32(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };                 // CTA 0: both CTAs' copies of a stage
     auto empty_bar = [&](int s) { return bar0 + 8u * (F_STAGES + s); };   // each CTA: CTA 0's commit
@@ -208,17 +209,20 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         const int qd = warp & 3;
         const uint32_t over = mapa_rank(tover_bar, 0);
         int it = 0, oslot = 0;
+        float* bias = reinterpret_cast<float*>(smem + F_STAGES * F_STAGE + F_OUT) + qd * 256;
         for (int t = cidx; t < tiles; t += ncl, ++it) {
             int mp, nb;
             dense_raster(t, p.units_m, p.num_n, mp, nb);
             const int64_t row0 = static_cast<int64_t>(mp) * 256 + crank * 128 + qd * 32, orow = row0 + lane;
             const int64_t col0 = static_cast<int64_t>(nb) * 256;
-            // the tile's bias: lane l holds columns col0 + 8l .. + 7
-            float bv[8];
+            if (p.bias != nullptr) {  // this warp's copy of the tile's
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t c = col0 + 8 * lane + i;
-                bv[i] = p.bias != nullptr && c < p.cols ? (OUT == 2 ? static_cast<const float*>(p.bias)[c] : O::load(p.bias, c)) : 0.0f;
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t c = col0 + i * 32 + lane;
+                    bias[i * 32 + lane] = c < p.cols ? (OUT == 2 ? static_cast<const float*>(p.bias)[c] : O::load(p.bias, c)) : 0.0f;
+                }
+                __syncwarp();
             }
             if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(it & 1), (it >> 1) & 1, abort_flag, p, DEV_TIMEOUT_EPILOGUE))) break;
             tc_fence_after();
@@ -226,50 +230,53 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             const int first = (it & 1) ? 0 : F_ACC1 / CPS;  // the slices of the shared columns come first
             for (int i = 0; i < SLICES; ++i) {
                 const int cs = (first + i) % SLICES * CPS;
-                const bool any = col0 + cs < p.cols;
+                const bool any = col0 + cs < p.cols && row0 < p.rows;
                 const uint32_t buf = ostage + static_cast<uint32_t>(qd * 8192 + (oslot & 1) * 4096);
-                if (any && p.tma_out) {
-                    if (lane == 0) bulk_wait_read<1>();  // the slice staged two slices ago has been read
+                uint32_t v[CPS];
+                if (any) {
                     __syncwarp();
-                }
 #pragma unroll
-                for (int c16 = 0; c16 < CPS; c16 += 16) {
-                    if (!any) break;
-                    __syncwarp();
-                    uint32_t v[16];
-                    tmem_ld16(tbase + cs + c16, v);
-                    const int64_t cb = col0 + cs + c16;
-                    float f[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
-                    if (OUT == 2 && p.accum && orow < p.rows) {  // the pieces before
-                        const float* prev = static_cast<const float*>(p.out) + orow * p.ldo + cb;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (cb + j < p.cols) f[j] = __fadd_rn(prev[j], f[j]);
-                    }
-                    if (p.bias != nullptr) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] = __fadd_rn(f[j], __shfl_sync(0xffffffffu, bv[j & 7], ((cs + c16) >> 3) + (j >> 3)));
-                    }
-                    const uint32_t at = buf + static_cast<uint32_t>(lane * 128);
-                    constexpr int CH = OES;  // 16-byte chunks of 16 columns
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            w[x] = OUT == 2 ? __float_as_uint(f[(4 * j + x) & 15]) : O::pack(f[(8 * j + 2 * x) & 15], f[(8 * j + 2 * x + 1) & 15]);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         at + static_cast<uint32_t>(((c16 * OES / 16 + j) ^ (lane & 7)) * 16)),
-                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                     : "memory");
-                    }
+                    for (int c16 = 0; c16 < CPS; c16 += 16) tmem_get16(tbase + cs + c16, v + c16);
+                    tmem_wait();
                 }
                 if (i == F_SHARED / CPS - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(over);
+                }
+                if (any) {
+                    if (p.tma_out) {
+                        if (lane == 0) bulk_wait_read<1>();  // the slice staged two slices ago has been read
+                        __syncwarp();
+                    }
+                    float* f = reinterpret_cast<float*>(v);
+                    if (OUT == 2 && p.accum && orow < p.rows) {  // the pieces before
+                        const float* prev = static_cast<const float*>(p.out) + orow * p.ldo + col0 + cs;
+#pragma unroll
+                        for (int j = 0; j < CPS; ++j)
+                            if (col0 + cs + j < p.cols) f[j] = __fadd_rn(prev[j], f[j]);
+                    }
+                    if (p.bias != nullptr) {
+#pragma unroll
+                        for (int j = 0; j < CPS; j += 4) {
+                            const float4 b = *reinterpret_cast<const float4*>(bias + cs + j);
+                            f[j] = __fadd_rn(f[j], b.x);
+                            f[j + 1] = __fadd_rn(f[j + 1], b.y);
+                            f[j + 2] = __fadd_rn(f[j + 2], b.z);
+                            f[j + 3] = __fadd_rn(f[j + 3], b.w);
+                        }
+                    }
+                    const uint32_t at = buf + static_cast<uint32_t>(lane * 128);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {  // 16-byte chunks of the row's 128 bytes
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = OUT == 2 ? v[(4 * j + x) % CPS] : O::pack(f[(8 * j + 2 * x) % CPS], f[(8 * j + 2 * x + 1) % CPS]);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + static_cast<uint32_t>((j ^ (lane & 7)) * 16)),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
                 }
                 if (any && p.tma_out) {
                     fence_proxy_async_smem();
@@ -282,6 +289,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                 } else if (any) {  // rows that TMA cannot store, one after the other, a lane to a column
                     __syncwarp();
                     const int rows = static_cast<int>(lmin(32, p.rows - row0));
+#pragma unroll 8
                     for (int r = 0; r < rows; ++r) {
 #pragma unroll
                         for (int x = 0; x < CPS; x += 32) {
