@@ -325,6 +325,8 @@ def _fp4_ptr(t, need):
 def _fp4(q, s, rows, cols):
     """Addresses of the codes and scales of an operand [rows][cols], sizes checked.
     Sizes that the library refuses are left to it."""
+    if q is None and s is None:
+        return None, None
     cp = (cols + 255) // 256 * 256
     return _fp4_ptr(q, rows * cp // 2), _fp4_ptr(s, (rows + 127) // 128 * cp * 4)
 

@@ -20,10 +20,12 @@
 //
 // MXFP4 weights: kind::mxf4 with block scales, stages of 256, the codes as they lie in
 // memory: no weight is ever expanded.  Its other operand has to be MXFP4 too, so a token's
-// x (and h) is written as a sum of PARTS rows in MXFP4: each part rounds what the parts
-// before left, per block of 32 with a scale that none of it exceeds, so a part leaves at
-// most a quarter of its scale's range and the twelfth less than 2^-23 of the block's largest
-// value.  The parts are N columns of their own (16 to a token, 12 used), added in the
+// x (and h) is written as a sum of PARTS rows in MXFP4.  Each part rounds what the parts
+// before left, per block of 32, by a scale 2^s at least a quarter of the largest of it:
+// up to 4 the codes are at most 1 apart, so at most 2^s / 2 is left where more than 2^(s+1)
+// was, and the next scale is 2^(s-3).  Three bits a part: eight leave at most 2^-23 of the
+// block's largest value.  (By scales that use codes up to 6, which are 2 apart there, a part
+// gains two bits: twelve parts.)  The parts are N columns of their own, added in the
 // epilogue from the smallest up.  A kernel of its own makes them, of x and of h: in the
 // hidden kernel's epilogue, which has 128 threads per SM, they took longer than all
 // else (f16, 96 tokens, 8 experts of 4096 x 4096: 200 us for that kernel, 97 without).
@@ -44,7 +46,8 @@
 namespace bi {
 namespace {
 
-constexpr int PARTS = 12, PART_ROWS = 16;  // MXFP4 rows of a token: used, and from one token to the next
+constexpr int PARTS = 8;                   // MXFP4 rows of a token
+constexpr int PLACES = 128 / PARTS;        // tokens whose rows are one piece of scales: an expert's places start on it
 constexpr int T_LIMIT = 227 * 1024;
 constexpr int T_BARS = 512;
 constexpr int T_EX = 2 * 16 * 64 * 4;      // the epilogue's exchange between the gate's and up's warps
@@ -137,11 +140,11 @@ struct Walk {
     __device__ __forceinline__ int cols(const TcArgs& a) const { return min(a.cap, n - c0); }
 };
 
-// One part of a block of 32: the smallest scale that the largest magnitude does not
-// exceed six times of, as its byte.
+// One part of a block of 32: the byte of the smallest scale of which the largest
+// magnitude is at most four times.
 __device__ __forceinline__ uint32_t part_scale(uint32_t amax_bits) {
-    const uint32_t e = amax_bits >> 23, up = (amax_bits & 0x7fffffu) > 0x400000u ? 1u : 0u;
-    return e == 255u ? 255u : e + up < 2u ? 0u : e + up - 2u;
+    const uint32_t e = amax_bits >> 23, exact = (amax_bits & 0x7fffffu) == 0 ? 1u : 0u;
+    return e == 255u ? 255u : e < 1u + exact ? 0u : e - 1u - exact;
 }
 __device__ __forceinline__ float part_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
@@ -165,7 +168,7 @@ template <bool FP4, bool OUT>
 __global__ void __launch_bounds__(t_threads(FP4), 1)
     moe_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmB8, const TcArgs a) {
-    constexpr int ALIGN = FP4 ? 8 : 1;
+    constexpr int ALIGN = FP4 ? PLACES : 1;
     constexpr int BPARTS = !FP4 && OUT ? 2 : 1;  // planes of B
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const MoeCall& m = a.m;
@@ -213,20 +216,20 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     Walk<FP4, OUT> w;
     w.u = blockIdx.x;
     w.open(a, p);
-    const int sfa_at = A_BYTES, b_at = A_BYTES + (FP4 ? 1024 : 0), b_bytes = a.cap * (FP4 ? PART_ROWS * 128 : 128);
+    const int sfa_at = A_BYTES, b_at = A_BYTES + (FP4 ? 1024 : 0), b_bytes = a.cap * (FP4 ? PARTS * 128 : 128);
     const int sfb_at = b_at + b_bytes;
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies, a lane each
-        // lanes 0, 1: 64 weight rows; then B's boxes of 16 rows or 128; MXFP4: B's scales, 8 tokens a box
+        // lanes 0, 1: 64 weight rows; then B's boxes of 16 rows or 128; MXFP4: B's scales, 16 tokens a box
         int s = 0, made = 0;
         uint32_t ph = 0;
         bool ok = true;
-        auto boxes = [&](const Walk<FP4, OUT>& x) { return FP4 ? x.cols(a) : (x.cols(a) + 15) / 16; };
+        auto boxes = [&](const Walk<FP4, OUT>& x) { return ((FP4 ? PARTS : 1) * x.cols(a) + 15) / 16; };
         auto weights = [&](const Walk<FP4, OUT>& x, int c) {
             ok = __all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, a, DEV_TIMEOUT_PRODUCER));
             if (!ok) return;
-            if (lane == 0) mbar_expect_tx(full_bar(s), A_BYTES + boxes(x) * BPARTS * 2048 + (FP4 ? (x.cols(a) + 7) / 8 * 1024 : 0));
+            if (lane == 0) mbar_expect_tx(full_bar(s), A_BYTES + boxes(x) * BPARTS * 2048 + (FP4 ? (x.cols(a) + PLACES - 1) / PLACES * 1024 : 0));
             __syncwarp();
             const int64_t r = x.e * R + static_cast<int64_t>(x.tile) * span;
             if (lane < 2)
@@ -239,10 +242,10 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
             const int first = FP4 || OUT ? static_cast<int>(p.first[x.e]) + x.c0 : x.c0;
             if (lane < each * BPARTS) {
                 const int part = lane / each, i = lane - part * each, b = i < big ? i * 8 : big * 8 + i - big;
-                const int row = FP4 ? (first + b) * PART_ROWS : part * a.P + first + b * 16;
+                const int row = FP4 ? first * PARTS + b * 16 : part * a.P + first + b * 16;
                 tma_2d(sbase + st * a.stage + b_at + part * b_bytes + b * 2048, i < big ? &tmB8 : &tmB, c * (FP4 ? 128 : 64), row, full_bar(st));
-            } else if (FP4 && lane < each + (x.cols(a) + 7) / 8) {
-                tma_2d(sbase + st * a.stage + sfb_at + (lane - each) * 1024, &tmSB, c * 256, first / 8 + lane - each, full_bar(st));
+            } else if (FP4 && lane < each + (x.cols(a) + PLACES - 1) / PLACES) {
+                tma_2d(sbase + st * a.stage + sfb_at + (lane - each) * 1024, &tmSB, c * 256, first / PLACES + lane - each, full_bar(st));
             }
         };
         auto advance = [&](Walk<FP4, OUT>& x, int& c) {
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
             if (!ok) break;
             tc_fence_after();
             const int cols = w.cols(a);
-            const uint32_t N = FP4 ? cols * PART_ROWS : (cols + 15) / 16 * 16;
+            const uint32_t N = ((FP4 ? PARTS : 1) * cols + 15) / 16 * 16;
             for (int c = 0; c < a.chunks; ++c) {
                 ok = __all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, a, DEV_TIMEOUT_MMA));
                 if (!ok) break;
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                     for (int k = 0; k < 2; ++k) {
                         scales_to_tmem(ta + k * 4, st + sfa_at + k * 512, lead);
                         scales_to_tmem(tb + k * 8, st + sfb_at + k * 512, lead);
-                        if (cols > 8) scales_to_tmem(tb + k * 8 + 4, st + sfb_at + 1024 + k * 512, lead);
+                        if (cols > PLACES) scales_to_tmem(tb + k * 8 + 4, st + sfb_at + 1024 + k * 512, lead);
                     }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
@@ -428,15 +431,18 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                 float v[16];
                 if constexpr (FP4) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v[j] = 0.0f;
+                    for (int j = 0; j < 16; j += 2) {
+                        v[j] = v[j + 1] = 0.0f;
                         if (j >= cnt) continue;
-                        uint32_t r[16];
+                        uint32_t r[16];  // two tokens' parts
+                        static_assert(PARTS == 8, "two tokens per load");
                         __syncwarp();
-                        tmem_ld16(tb + (b + j) * PART_ROWS, r);
-                        v[j] = __uint_as_float(r[PARTS - 1]);
+                        tmem_ld16(tb + (b + j) * PARTS, r);
 #pragma unroll
-                        for (int x = PARTS - 2; x >= 0; --x) v[j] = __fadd_rn(v[j], __uint_as_float(r[x]));
+                        for (int x = 7; x >= 0; --x) {
+                            v[j] = __fadd_rn(v[j], __uint_as_float(r[x]));
+                            v[j + 1] = __fadd_rn(v[j + 1], __uint_as_float(r[8 + x]));
+                        }
                     }
                 } else {
                     __syncwarp();
@@ -507,8 +513,8 @@ __global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const 
     grid_dep_wait();
     grid_dep_launch();
     const int P = T_ * C, lane = threadIdx.x & 31;
-    const Plan p = build_plan<8>(smem, ids, P, E);
-    uint16_t* place = reinterpret_cast<uint16_t*>(smem + plan_bytes(E, P, 8));  // of each choice
+    const Plan p = build_plan<PLACES>(smem, ids, P, E);
+    uint16_t* place = reinterpret_cast<uint16_t*>(smem + plan_bytes(E, P, PLACES));  // of each choice
     for (int i = threadIdx.x; i < P; i += X_THREADS) place[i] = 0xffff;         // none
     __syncthreads();
     for (int s = threadIdx.x >> 5; s < p.n; s += X_THREADS / 32) {
@@ -549,7 +555,7 @@ __global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const 
         for (int j = 0; j < C; ++j) {
             const uint32_t at = place[t * C + j];
             if (at == 0xffffu) continue;
-            const int64_t r = static_cast<int64_t>(at) * PART_ROWS;
+            const int64_t r = static_cast<int64_t>(at) * PARTS;
             uint8_t* q = xq + r * (Kp / 2) + k / 2;
             uint8_t* s = xs + fp4_scale_at(r, k >> 5, Kp);  // (the rows of a place: 16 bytes apart)
 #pragma unroll
@@ -654,7 +660,7 @@ struct Room {
 Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
     Room r{};
     const int64_t P = static_cast<int64_t>(m.T) * m.C;
-    r.places = (plan_places(m.E, P, 8) + 7) / 8 * 8;
+    r.places = (plan_places(m.E, P, PLACES) + PLACES - 1) / PLACES * PLACES;
     r.Kp = fp4 ? fp4_padded(m.K) : (m.K + 63) / 64 * 64;
     r.Fp = fp4 ? fp4_padded(m.F) : (m.F + 7) / 8 * 8;
     r.Nq = (m.N + 127) / 128 * 128;
@@ -664,7 +670,7 @@ Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
         at += round256(bytes);
         return o;
     };
-    const int64_t rows = r.places * PART_ROWS;
+    const int64_t rows = r.places * PARTS;
     r.x = take(fp4 ? rows * (r.Kp / 2) : copy_x ? m.T * r.Kp * 2 : 0);
     r.xs = take(fp4 ? rows / 128 * r.Kp * 4 : 0);
     r.h = take(fp4 ? rows * (r.Fp / 2) : 2 * P * r.Fp * 2);
@@ -685,14 +691,14 @@ cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CU
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T_LIMIT);
     });
     if (e != cudaSuccess) return e;
-    constexpr int ALIGN = FP4 ? 8 : 1;
+    constexpr int ALIGN = FP4 ? PLACES : 1;
     const int64_t rows = OUT ? a.m.N : a.m.F, len = OUT ? a.m.F : a.m.K;
     const int span = !OUT && a.m.gate ? 64 : 128;
     a.tiles = static_cast<int>((rows + span - 1) / span);
     a.chunks = static_cast<int>(FP4 ? fp4_padded(len) / 256 : (len + 63) / 64);
     const int tokens16 = (a.m.T + 15) / 16 * 16;
-    a.cap = FP4 ? (a.m.T <= 8 ? 8 : 16) : OUT ? (tokens16 < 128 ? tokens16 : 128) : (tokens16 < 256 ? tokens16 : 256);
-    a.stage = A_BYTES + (FP4 ? 1024 + a.cap * (PART_ROWS * 128) + a.cap / 8 * 1024 : a.cap * 128 * (OUT ? 2 : 1));
+    a.cap = FP4 ? (a.m.T <= PLACES ? PLACES : 2 * PLACES) : OUT ? (tokens16 < 128 ? tokens16 : 128) : (tokens16 < 256 ? tokens16 : 256);
+    a.stage = A_BYTES + (FP4 ? 1024 + a.cap * (PARTS * 128) + a.cap / PLACES * 1024 : a.cap * 128 * (OUT ? 2 : 1));
     const int64_t fixed = plan_bytes(a.m.E, a.P, ALIGN) + T_EX + T_BARS + 1024;
     a.depth = static_cast<int>(lmin(MAX_STAGES, (T_LIMIT - fixed) / a.stage));
     if (a.depth < 2) return cudaErrorInvalidConfiguration;
@@ -706,7 +712,13 @@ cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CU
 
 template <typename T, bool BY_PLACE>
 cudaError_t parts(const LaunchCtx& c, const MoeCall& m, const T* x, uint8_t* xq, uint8_t* xs, int T_, int C, int64_t K) {
-    const int64_t P = static_cast<int64_t>(T_) * C, smem = plan_bytes(m.E, P, 8) + (2 * P + 15) / 16 * 16;
+    const int64_t P = static_cast<int64_t>(T_) * C, smem = plan_bytes(m.E, P, PLACES) + (2 * P + 15) / 16 * 16;
+    static PerDeviceOnce setup;
+    const cudaError_t q = setup.run(c.eng->device, [&](int&) {
+        return cudaFuncSetAttribute(moe_parts_kernel<T, BY_PLACE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(plan_bytes(MOE_MAX_E, MOE_MAX_PAIRS, PLACES) + 2 * MOE_MAX_PAIRS));
+    });
+    if (q != cudaSuccess) return q;
     const int64_t blocks = (T_ * (fp4_padded(K) / 128) + X_THREADS / 32 - 1) / (X_THREADS / 32);
     const cudaError_t e = launch_pdl(moe_parts_kernel<T, BY_PLACE>, dim3(static_cast<unsigned>(lmin(blocks, 8 * c.sm_count))), dim3(X_THREADS),
                                      static_cast<size_t>(smem), c.stream, x, m.ids, xq, xs, T_, C, m.E, K);
@@ -731,7 +743,7 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
     a.wait_limit = c.wait_limit_ns;
     CUtensorMap gate, up, down, mx, mh, mx8, mh8, sx, sh;
     cudaError_t e;
-    const int64_t rows = r.places * PART_ROWS, ef = m.E * m.F, en = m.E * m.N;
+    const int64_t rows = r.places * PARTS, ef = m.E * m.F, en = m.E * m.N;
     if (FP4) {
         uint8_t *xq = scratch + r.x, *xs = scratch + r.xs;
         e = dt == BI_F32    ? parts<float, false>(c, m, static_cast<const float*>(m.x), xq, xs, m.T, m.C, m.K)
