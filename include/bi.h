@@ -429,11 +429,16 @@ bi_status bi_router_backward(bi_engine engine, void* dlogits, const void* logits
  * calls' layout); w_gate NULL: h = act(x Wu^T).  act: v / (1 + e^-v) (SiLU),
  * 0.5 v (1 + tanh(0.79788456 (v + 0.044715 v^3))) (GELU), max(v, 0).
  *
- * E <= 1024 and T * C <= 2048 (BI_ERR_UNSUPPORTED beyond: longer batches take the
- * grouped calls).  Inner products are summed in f32 in an order fixed by K and F, a
- * token's choices in the order of j: bit-identical run to run, and a row of y depends
- * on its own x, ids and weights alone, whatever T.  Forward only.
- * Scratch from the engine's pool: h, 4 T C F bytes. */
+ * E <= 1024 and T * C <= 2048, E * F and E * N <= 2^31 - 256 (BI_ERR_UNSUPPORTED
+ * beyond: longer batches take the grouped calls).  An inner product is one f32 sum in an
+ * order fixed by the types, K, F and the weights' alignment, a token's choices are
+ * added in the order of j: bit-identical run to run, and a row of y depends on its own
+ * x, ids and weights alone, whatever T.  16-bit weights on 16-byte boundaries with K and
+ * F multiples of 8 run on the tensor cores, where h enters the second product as two
+ * 16-bit parts (2^-17 of it; f16 by a power of two per choice, 2^-22 of it or 2^-39 of
+ * the choice's largest); others, and f32, in f32 FMAs.  A non-finite x, h or weight makes
+ * the rows it enters non-finite.  Tensors need the alignment of their type.  Forward
+ * only.  Scratch from the engine's pool: about T C (8 F + 4 N) bytes. */
 typedef enum { BI_ACT_SILU = 0, BI_ACT_GELU = 1, BI_ACT_RELU = 2 } bi_activation;
 
 bi_status bi_moe_forward(bi_engine engine, void* y, const void* x, const uint32_t* ids, const float* weights,
@@ -442,7 +447,10 @@ bi_status bi_moe_forward(bi_engine engine, void* y, const void* x, const uint32_
 
 /* The same with expert weights in MXFP4: gate and up as operands [E*F][K], down
  * [E*N][F] (bi_fp4_quantize of the weights as [E*F, K] and [E*N, F]); their values
- * enter exactly.  gate_q and gate_s NULL: no gate. */
+ * enter exactly, on the tensor cores for every dtype and size.  x and h enter as sums
+ * of eight MXFP4 rows, which leave at most 2^-23 of the largest value of their block of
+ * 32.  gate_q and gate_s NULL: no gate.  Scratch: with places = T C rounded up to 16 per
+ * expert, about places (4.25 (K + F) + 4 F) + 4 T C N bytes. */
 bi_status bi_moe_forward_fp4(bi_engine engine, void* y, const void* x, const uint32_t* ids, const float* weights,
                              const uint8_t* gate_q, const uint8_t* gate_s, const uint8_t* up_q, const uint8_t* up_s,
                              const uint8_t* down_q, const uint8_t* down_s, int64_t t, int64_t c, int64_t k, int64_t f,
