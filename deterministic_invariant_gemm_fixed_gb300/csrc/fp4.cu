@@ -20,6 +20,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 
+#include <type_traits>
+
 #include "abi_util.h"
 #include "fp4.h"
 
@@ -249,9 +251,25 @@ __global__ void __launch_bounds__(256) fp4_dequantize_kernel(T* dst, const uint8
         for (int i = 0; i < ROWS; ++i) {
             const int64_t r = ra + i * step;
             if (r >= R) break;
-            // a code's bits as an f32's are the value * 2^-126; 2^126 2^s as one factor
-            // where it is in range
+            // a code's bits as an f32's (or bf16's) are the value * 2^-126; 2^126 2^s as one
+            // factor where it is in range
             const bool one = byte[i] <= 128u;
+            if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+                // bf16: codes j and j + 4 in the halves of a register, one product for both
+                if (one && vec) {
+                    const uint32_t f = (byte[i] + 126u) * 0x00800080u;
+                    uint32_t p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t u = w[i] << (12 - 4 * j);
+                        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p[j]) : "r"((u & 0x80008000u) | ((u >> 6) & 0x01c001c0u)), "r"(f));
+                    }
+                    __stcs(reinterpret_cast<uint4*>(dst + r * C + c),
+                           make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410), __byte_perm(p[0], p[1], 0x7632),
+                                      __byte_perm(p[2], p[3], 0x7632)));
+                    continue;
+                }
+            }
             const float scale = one ? __uint_as_float((byte[i] + 126u) << 23) : fp4_scale_value(byte[i]);
             __align__(16) T o[V];
 #pragma unroll

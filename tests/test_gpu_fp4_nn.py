@@ -160,3 +160,14 @@ def test_step_with_fp4_layers_and_captured_backward():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(x.grad, grads[0]) and torch.equal(w.grad, grads[1])
+
+
+def test_empty_batches():
+    x, w, b = torch.empty(0, 64, device="cuda", requires_grad=True), torch.randn(64, 32, device="cuda", requires_grad=True), torch.randn(32, device="cuda", requires_grad=True)
+    y = nn.deterministic_linear(x, w, b, fp4=True)
+    assert y.shape == (0, 32)
+    y.sum().backward()
+    assert x.grad.shape == (0, 64) and not w.grad.any() and not b.grad.any()
+    up, down = torch.randn(4, 16, 64, device="cuda"), torch.randn(4, 8, 16, device="cuda")
+    with torch.no_grad():
+        assert nn.moe(x, torch.empty(0, 4, device="cuda"), None, up, down, 2).shape == (0, 8)

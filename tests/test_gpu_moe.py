@@ -262,3 +262,25 @@ def test_two_streams(eng):
                 got.append(layer.run(*d))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("fp4", [False, True], ids=["plain", "fp4"])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_most_choices_and_experts(eng, dtype, fp4):
+    """2048 choices over 1024 experts: the largest lists."""
+    layer = Layer(eng, dtype, 1024, 40, 24, 16, fp4)
+    data = layer.tokens(512, 4)
+    check(layer.run(*data), layer.ref(*data), dtype)
+
+
+def test_nan_scale_of_a_weight_block(eng):
+    """A weight block without a scale makes the rows NaN that chose its expert, and no other."""
+    layer = Layer(eng, "bf16", 4, 96, 64, 48, fp4=True)
+    x, ids, p = layer.tokens(20, 1)
+    clean = layer.run(x, ids, p)
+    scales = layer.w[5]  # of down: rows e * 48 + n, blocks along 64; row 2 * 48 is expert 2's first
+    r = 2 * 48
+    scales[(r // 128) * 2 * 512 + (r % 32) * 16 + (r // 32 % 4) * 4 + 1] = 255
+    y = layer.run(x, ids, p)
+    hit = (ids[:, 0] == 2)
+    assert torch.isnan(y[hit, 0]).all() and torch.equal(y[~hit], clean[~hit]) and torch.equal(y[:, 1:], clean[:, 1:])
