@@ -60,6 +60,22 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t byte) {
     for (int i = 0; i < 4; ++i) r |= codes2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
     return r;
 }
+// The same of two columns of bf16, in the halves of eight words, with a block each: the
+// products of a pair at once (exact, but for values far below the smallest code's border).
+__device__ __forceinline__ void codes8x2_bf16(const uint32_t* w, uint32_t byte0, uint32_t byte1, uint32_t& c0, uint32_t& c1) {
+    const uint32_t inv = (byte0 == 255u ? 0u : (254u - byte0) << 7) | (byte1 == 255u ? 0u : (254u - byte1) << 23);
+    c0 = c1 = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a, b;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[2 * i]), "r"(inv));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2 * i + 1]), "r"(inv));
+        c0 |= codes2(__uint_as_float(a << 16), __uint_as_float(b << 16)) << (8 * i);
+        c1 |= codes2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)) << (8 * i);
+    }
+    if (byte0 == 255u) c0 = 0;
+    if (byte1 == 255u) c1 = 0;
+}
 // Largest magnitude as bits: infinities and NaN compare above every number.
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
@@ -178,6 +194,16 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const T* __rest
                 w[j] = colp[j * PITCH / 2];
                 m = max_u16x2(m, w[j] & 0x7fff7fffu);
             }
+            if constexpr (!std::is_same<T, __half>::value) {
+                const uint32_t b0 = scale_byte(m << 16), b1 = scale_byte(m & 0xffff0000u);
+                uint32_t o[2][4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) codes8x2_bf16(w + 8 * x, b0, b1, o[0][x], o[1][x]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(tcode + (lc + h) * CPITCH + b * 16) = make_uint4(o[h][0], o[h][1], o[h][2], o[h][3]);
+                col_scale[lc][b] = static_cast<uint8_t>(b0);  // columns past C are zeros: byte 0
+                col_scale[lc + 1][b] = static_cast<uint8_t>(b1);
+            } else
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t byte = scale_byte(mag16<T>(h ? m >> 16 : m & 0xffffu));
@@ -190,7 +216,7 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const T* __rest
                     o[x] = codes8(v, byte);
                 }
                 *reinterpret_cast<uint4*>(tcode + (lc + h) * CPITCH + b * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-                col_scale[lc + h][b] = static_cast<uint8_t>(byte);  // columns past C are zeros: byte 0
+                col_scale[lc + h][b] = static_cast<uint8_t>(byte);
             }
         }
     } else {
