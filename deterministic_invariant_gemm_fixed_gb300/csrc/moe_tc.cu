@@ -221,59 +221,74 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies, a lane each
-        // lanes 0, 1: 64 weight rows; then B's boxes of 16 rows or 128; MXFP4: B's scales, 16 tokens a box
-        int s = 0, made = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        auto boxes = [&](const Walk<FP4, OUT>& x) { return ((FP4 ? PARTS : 1) * x.cols(a) + 15) / 16; };
-        auto weights = [&](const Walk<FP4, OUT>& x, int c) {
-            ok = __all_sync(0xffffffffu, mbar_wait_fast(empty_bar(s), ph ^ 1u, abort_flag, a, DEV_TIMEOUT_PRODUCER));
-            if (!ok) return;
-            if (lane == 0) mbar_expect_tx(full_bar(s), A_BYTES + boxes(x) * BPARTS * 2048 + (FP4 ? (x.cols(a) + PLACES - 1) / PLACES * 1024 : 0));
-            __syncwarp();
-            const int64_t r = x.e * R + static_cast<int64_t>(x.tile) * span;
-            if (lane < 2)
-                tma_2d(sbase + s * a.stage + lane * (A_BYTES / 2), lane == 0 ? &tmA0 : &tmA1, c * (FP4 ? 128 : 64),
-                       static_cast<int>(gated ? r : r + lane * 64), full_bar(s));
-        };
-        auto tokens = [&](const Walk<FP4, OUT>& x, int c, int st) {
-            // whole groups of eight boxes by one copy
-            const int nb = boxes(x), big = nb / 8, each = big + nb % 8;
+        // Lanes 30 and 31: 64 weight rows each.  From lane 0: B's boxes of 128 or 16 rows, then
+        // (MXFP4) B's scales, 16 tokens a box.  What a lane copies is found once per pass:
+        // a stage costs its wait and the copy (found anew for each stage: 0.37 us a stage).
+        const bool wlane = lane >= 30;
+        const CUtensorMap* map = nullptr;
+        uint32_t to = 0, bytes = 0;
+        int y = 0, xs = 0;
+        bool has = false;
+        auto aim = [&](const Walk<FP4, OUT>& x) {
+            const int cols = x.cols(a), nb = ((FP4 ? PARTS : 1) * cols + 15) / 16, big = nb / 8, each = big + nb % 8;
+            const int sf = FP4 ? (cols + PLACES - 1) / PLACES : 0;
             const int first = FP4 || OUT ? static_cast<int>(p.first[x.e]) + x.c0 : x.c0;
-            if (lane < each * BPARTS) {
-                const int part = lane / each, i = lane - part * each, b = i < big ? i * 8 : big * 8 + i - big;
-                const int row = FP4 ? first * PARTS + b * 16 : part * a.P + first + b * 16;
-                tma_2d(sbase + st * a.stage + b_at + part * b_bytes + b * 2048, i < big ? &tmB8 : &tmB, c * (FP4 ? 128 : 64), row, full_bar(st));
-            } else if (FP4 && lane < each + (x.cols(a) + PLACES - 1) / PLACES) {
-                tma_2d(sbase + st * a.stage + sfb_at + (lane - each) * 1024, &tmSB, c * 256, first / PLACES + lane - each, full_bar(st));
+            bytes = A_BYTES + nb * BPARTS * 2048 + sf * 1024;
+            xs = FP4 ? 128 : 64;
+            if (wlane) {
+                const int64_t r = x.e * R + static_cast<int64_t>(x.tile) * span;
+                map = lane == 30 ? &tmA0 : &tmA1;
+                to = sbase + (lane - 30) * (A_BYTES / 2);
+                y = static_cast<int>(gated ? r : r + (lane - 30) * 64);
+                has = true;
+            } else if (lane < each * BPARTS) {
+                const int part = lane >= each, i = lane - part * each, b = i < big ? i * 8 : big * 8 + i - big;
+                map = i < big ? &tmB8 : &tmB;
+                to = sbase + b_at + part * b_bytes + b * 2048;
+                y = FP4 ? first * PARTS + b * 16 : part * a.P + first + b * 16;
+                has = true;
+            } else {
+                map = &tmSB;
+                to = sbase + sfb_at + (lane - each) * 1024;
+                y = first / PLACES + lane - each;
+                xs = 256;
+                has = FP4 && lane < each + sf;
             }
         };
-        auto advance = [&](Walk<FP4, OUT>& x, int& c) {
-            if (++c == a.chunks) { c = 0; x.next(a, p); }
-        };
-        Walk<FP4, OUT> x = w, x0 = w;
-        int c = 0, c0 = 0;
-        if (OUT) {  // the first stages' weights come in while the hidden kernel ends
-            for (; made < a.depth && x.more(a, p); ++made) {
-                weights(x, c);
-                if (++s == a.depth) { s = 0; ph ^= 1u; }
-                advance(x, c);
+        struct At { Walk<FP4, OUT> x; int c, s; uint32_t ph; };
+        // up to `limit` stages from `at` on: the weights, with the expected bytes, or the rest, or both
+        auto stages = [&](At& at, int limit, bool weights, bool rest) {
+            int made = 0;
+            bool ok = true;
+            while (ok && made < limit && at.x.more(a, p)) {
+                aim(at.x);
+                const bool mine = has && (wlane ? weights : rest);
+                for (; at.c < a.chunks && made < limit; ++at.c, ++made) {
+                    if (weights) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_fast(empty_bar(at.s), at.ph ^ 1u, abort_flag, a, DEV_TIMEOUT_PRODUCER));
+                        if (!ok) break;
+                        if (lane == 31) mbar_expect_tx(full_bar(at.s), bytes);
+                        __syncwarp();
+                    }
+                    if (mine) tma_2d(to + at.s * a.stage, map, at.c * xs, y, full_bar(at.s));
+                    if (++at.s == a.depth) { at.s = 0; at.ph ^= 1u; }
+                }
+                if (at.c == a.chunks) {
+                    at.c = 0;
+                    at.x.next(a, p);
+                }
             }
+            return made;
+        };
+        At at{w, 0, 0, 0u};
+        if (OUT) {  // the first stages' weights come in while the kernel before ends
+            At again = at;
+            const int made = stages(at, a.depth, true, false);
             grid_dep_wait();
             grid_dep_launch();
-            for (int i = 0; i < made; ++i) {
-                tokens(x0, c0, i);
-                advance(x0, c0);
-            }
+            stages(again, made, false, true);
         }
-        while (x.more(a, p)) {
-            weights(x, c);
-            if (!ok) break;
-            tokens(x, c, s);
-            if (++s == a.depth) { s = 0; ph ^= 1u; }
-            ++made;
-            advance(x, c);
-        }
+        stages(at, 0x7fffffff, true, true);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         const uint32_t lead = elect_lane();
@@ -445,12 +460,14 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                         }
                     }
                 } else {
-                    __syncwarp();
+                    // a lane finds a token's column for all
+                    const int mycol = OUT ? b + lane : mine[min(b + lane, items - 1)] / m.C - w.c0;
                     uint32_t r[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const int i = min(b + j, items - 1);
-                        r[j] = tmem_ld1(tb + (OUT ? i : mine[i] / m.C - w.c0));
+                        r[j] = 0;
+                        const int col = __shfl_sync(0xffffffffu, mycol, j);
+                        if (j < cnt) r[j] = tmem_ld1(tb + col);
                     }
                     tmem_wait();
 #pragma unroll
@@ -464,17 +481,19 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                             __stcg(a.part + mine[b + j] * a.Nq + row, a.unscale ? v[j] * __ldg(a.unscale + place + b + j) : v[j]);
                     continue;
                 }
-                float r[8];
+                float r[8] = {};
                 if (gated) {
                     // warps 0 and 1 have the gate's rows, 2 and 3 up's: they swap half, the
                     // first two finish the even tokens, the others the odd ones
                     float* e = ex + (k++ & 1) * (16 * 64) + half * 32 + lane;
                     const bool odd = q >= 2;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) e[(2 * j + (odd ? 0 : 1)) * 64] = odd ? v[2 * j] : v[2 * j + 1];
+                    for (int j = 0; j < 8; ++j)
+                        if (2 * j < cnt) e[(2 * j + (odd ? 0 : 1)) * 64] = odd ? v[2 * j] : v[2 * j + 1];
                     meet();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
+                        if (2 * j >= cnt) break;
                         const float other = e[(2 * j + (odd ? 1 : 0)) * 64];
                         r[j] = odd ? activate(other, m.act) * v[2 * j + 1] : activate(v[2 * j], m.act) * other;
                     }
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) r[j] = activate(v[8 * x + j], m.act);
+                        for (int j = 0; j < 8; ++j) r[j] = 8 * x + j < cnt ? activate(v[8 * x + j], m.act) : 0.0f;
                         if (cnt > 8 * x) hidden_out(a, r, place + b + 8 * x, 1, min(8, cnt - 8 * x), row);
                     }
                 }
