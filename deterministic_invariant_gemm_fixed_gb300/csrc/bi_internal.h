@@ -54,11 +54,11 @@ struct PerDeviceOnce {
 // lets the kernel after it be scheduled early in turn, and is called after
 // grid_dep_wait() only: then no more than two kernels of a stream are ever under
 // way at once, and what a kernel finds complete is complete for the ones after it.
-// Both are no-ops for a kernel launched the ordinary way.  Two kernels read before
+// Both are no-ops for a kernel launched the ordinary way.  Some kernels read before
 // their wait: the adapters' small tiles (adapter_tc.cu) the shared operands, and the
-// expert layer's output kernel (moe.cu) the ids and weights.  These were complete
-// when the kernel before, always the adapters' narrow product or its finish, or the
-// expert layer's hidden kernel, passed its own wait.
+// expert layer's kernels behind its first one (moe_tc.cu) the ids and weights.  These
+// were complete when the kernel before, always the adapters' narrow product or its
+// finish, or another kernel of the expert layer's call, passed its own wait.
 #ifdef __CUDACC__
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -203,12 +203,14 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(slot), 0);
-    if (!OUT) {
+    // Behind another kernel of the layer, which waited for all before it and let this one
+    // start only then, ids and weights are complete already: the lists are made and the first
+    // weights fetched while that kernel ends.
+    constexpr bool EARLY = FP4 || OUT;
+    if (!EARLY) {
         grid_dep_wait();
         grid_dep_launch();
     }
-    // (the output kernel: ids and weights were complete when the hidden kernel passed its
-    // own wait, and it let this kernel start only then)
     const Plan p = build_plan<ALIGN>(smem_raw, m.ids, a.P, m.E);
     const int64_t R = OUT ? m.N : m.F;       // rows of an expert
     const bool gated = !OUT && m.gate != nullptr;
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
             return made;
         };
         At at{w, 0, 0, 0u};
-        if (OUT) {  // the first stages' weights come in while the kernel before ends
+        if (EARLY) {
             At again = at;
             const int made = stages(at, a.depth, true, false);
             grid_dep_wait();
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         }
     } else if (warp >= 2 && warp < 6) {
         // ------------------------------------------------------------ epilogue
-        if (OUT) grid_dep_wait();
+        if (EARLY) grid_dep_wait();
         const int q = warp & 3;
         uint32_t it = 0;
         int k = 0;  // exchanges so far: the buffers take turns over all units
@@ -529,18 +531,19 @@ template <typename T, bool BY_PLACE>
 __global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const uint32_t* ids, uint8_t* xq, uint8_t* xs, int T_, int C, int E,
                                                               int64_t K) {
     extern __shared__ __align__(16) uint8_t smem[];
-    grid_dep_wait();
-    grid_dep_launch();
+    if (!BY_PLACE) grid_dep_wait();  // (h's is behind the hidden kernel: the ids are complete)
     const int P = T_ * C, lane = threadIdx.x & 31;
     const Plan p = build_plan<PLACES>(smem, ids, P, E);
     uint16_t* place = reinterpret_cast<uint16_t*>(smem + plan_bytes(E, P, PLACES));  // of each choice
-    for (int i = threadIdx.x; i < P; i += X_THREADS) place[i] = 0xffff;         // none
+    for (int i = threadIdx.x; i < P; i += X_THREADS) place[i] = 0xffff;              // none
     __syncthreads();
     for (int s = threadIdx.x >> 5; s < p.n; s += X_THREADS / 32) {
         const int e = p.active[s];
         for (int i = lane; i < static_cast<int>(p.cnt[e]); i += 32) place[p.list[p.first[e] + i]] = static_cast<uint16_t>(p.first[e] + i);
     }
     __syncthreads();
+    if (BY_PLACE) grid_dep_wait();
+    grid_dep_launch();
     const int64_t Kp = fp4_padded(K), per = Kp / 128;
     for (int64_t i = blockIdx.x * int64_t(X_THREADS / 32) + (threadIdx.x >> 5); i < T_ * per; i += gridDim.x * int64_t(X_THREADS / 32)) {
         const int64_t t = i / per, k = (i - t * per) * 128 + lane * 4;
