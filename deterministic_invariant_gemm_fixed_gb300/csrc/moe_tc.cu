@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         At at{w, 0, 0, 0u};
         if (EARLY) {
             At again = at;
-            const int made = stages(at, a.depth, true, false);
+            const int made = stages(at, FP4 ? a.depth : min(a.depth, 4), true, false);  // (16-bit: four stages are fetched by the time the other ends)
             grid_dep_wait();
             grid_dep_launch();
             stages(again, made, false, true);
