@@ -319,7 +319,7 @@ def _fp4_ptr(t, need):
         return t
     if t.nbytes < need:
         raise ValueError(f"bi: an MXFP4 buffer of {t.nbytes} bytes where {need} are needed (fp4_buffers)")
-    return _ptr(t)
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _ptr(t)  # (which says what is wrong)
 
 
 def _fp4(q, s, rows, cols):
