@@ -18,7 +18,6 @@
 // copies them as they are.  Padding has code 0 and scale byte 0.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 
 #include <type_traits>
 
@@ -46,33 +45,33 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
 __device__ __forceinline__ float inverse_scale(uint32_t byte) {
     return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
-// Two codes, the first in the low half.
-__device__ __forceinline__ uint32_t codes2(float a, float b) {
-    return static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest));
+// Eight codes, the first in the lowest half byte.
+__device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d, float e, float f, float g, float h) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 w, x, y, z;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 w, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 y, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 z, %8, %7;\n\t"
+        "mov.b32 %0, {w, x, y, z};\n\t}" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h));
+    return r;
 }
 // The code of a value of a block without scale is 0: an infinity or NaN times the
 // zero inverse is NaN, which the conversion would make the largest code.
 __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t byte) {
     if (byte == 255u) return 0u;
     const float inv = inverse_scale(byte);
-    uint32_t r = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r |= codes2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
-    return r;
+    return codes_of(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv, v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
 }
 // The same of two columns of bf16, in the halves of eight words, with a block each: the
 // products of a pair at once (exact, but for values far below the smallest code's border).
 __device__ __forceinline__ void codes8x2_bf16(const uint32_t* w, uint32_t byte0, uint32_t byte1, uint32_t& c0, uint32_t& c1) {
     const uint32_t inv = (byte0 == 255u ? 0u : (254u - byte0) << 7) | (byte1 == 255u ? 0u : (254u - byte1) << 23);
-    c0 = c1 = 0;
+    uint32_t p[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t a, b;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[2 * i]), "r"(inv));
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2 * i + 1]), "r"(inv));
-        c0 |= codes2(__uint_as_float(a << 16), __uint_as_float(b << 16)) << (8 * i);
-        c1 |= codes2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)) << (8 * i);
-    }
+    for (int i = 0; i < 8; ++i) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(w[i]), "r"(inv));
+    auto lo = [&](int i) { return __uint_as_float(p[i] << 16); };
+    auto hi = [&](int i) { return __uint_as_float(p[i] & 0xffff0000u); };
+    c0 = codes_of(lo(0), lo(1), lo(2), lo(3), lo(4), lo(5), lo(6), lo(7));
+    c1 = codes_of(hi(0), hi(1), hi(2), hi(3), hi(4), hi(5), hi(6), hi(7));
     if (byte0 == 255u) c0 = 0;
     if (byte1 == 255u) c1 = 0;
 }
@@ -86,8 +85,8 @@ __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0
 // columns' direction on the tile in shared memory, a thread to a block of one column (two
 // columns of 16-bit values, whose magnitudes are compared in pairs).
 //
-// Bound by memory where there are many tiles: src read once, a quarter (bf16) of it
-// written per direction.  A small matrix waits for one tile's chain of steps instead, and
+// Bound by issue beside memory where there are many tiles (8192 x 4096 in bf16, both
+// directions: 103 MB in 25 us, issue 70 %).  A small matrix waits for one tile's chain of steps instead, and
 // takes the tiles of 32 rows, whose chain is a third as long; their column direction
 // writes 16 bytes at a time where the others write 64.
 constexpr int QT = 128;            // tile columns

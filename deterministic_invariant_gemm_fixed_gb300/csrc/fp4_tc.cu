@@ -21,7 +21,9 @@
 // columns) from 448 on.  The epilogue of a tile drains the 64 shared columns first;
 // then the next tile's MMAs start and the other 192 columns are stored beside them.
 //
-// Bound by the ring's feed from L2: 70 KB per pair and stage, for 33.6 MFLOP.
+// Bound by the ring's feed from L2, 70 KB per pair and stage for 33.6 MFLOP: 8192 x 4096 x
+// 12288 takes 131 us (6.3 PFLOP/s), 118 with a quarter of the MMAs; the tensor pipe is 60 %
+// busy.  One token's stage takes 0.39 us, a batch's 0.42.
 #include "abi_util.h"
 #include "fp4.h"
 #include "tc_common.cuh"

@@ -32,8 +32,14 @@
 //
 // Sums of the output kernel's units go to memory once per choice, and a third, small
 // kernel adds every token's choices in order.  (A block that adds up a tile once it has
-// finished the tile's last unit is late for its next unit, and so the last again: 182
-// against 95 us for 64 tokens, 64 experts of 2048 x 1408.)
+// finished the tile's last unit is late for its next unit, and so the last again: that
+// kernel took 182 against 55 us for 64 tokens, 64 experts of 2048 x 1408.)
+//
+// Bound by reading the weights where there are many: 64 tokens through 6 of 64 experts of
+// 2048 x 1408 in bf16 read 450 MB in 82 us (hidden) and 228 MB in 54 (output), caches cold,
+// set-up and ends included.  One token's 104 MB take 29 us over the three kernels, a third
+// of it set-up and ends.  MXFP4 with many tokens (96, 2 of 8 experts of 4096 x 4096: 88 us for
+// 220 MB) is bound by the tokens' rows, 1 KB a token and stage beside the weights' 16 KB.
 #include "abi_util.h"
 #include "fp4.h"
 #include "moe.h"
@@ -65,7 +71,7 @@ struct TcArgs {
     float* part;        // [P][Nq] the choices' sums
     int64_t Fp, Nq;
     int P, tiles, chunks;  // choices; row tiles of an expert; stages of the contraction
-    int cap;               // most tokens of a pass
+    int cap, passes;       // most columns of a pass; most passes
     int stage, depth;      // ring: bytes of a stage, stages
     uint32_t fmt;          // 16-bit weights: 0 f16, 1 bf16
     int* status;
@@ -114,30 +120,63 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     return v;
 }
 
-// A block's units, and within a unit its passes over the tokens.
-//   hidden: (expert, row tile), tiles of one expert next to one another
-//   output: (row tile, expert), so that whole tiles are finished one after the other
-// A pass: bf16 hidden, tokens [c0, c0 + 256) of the batch; else choices [c0, c0 + cap)
-// of the expert.
+// The passes of a call: an expert and up to cap columns, from column c0 of its own on.  A
+// column is a token of the batch (16-bit weights, hidden kernel) or one of the expert's
+// choices.  Experts with more of them have several passes, each as long as another
+// expert's: what the blocks share out is passes, so that an expert with many tokens does
+// not keep one block busy after the others.
+struct Passes {
+    uint16_t *e, *c0;  // c0 null: all 0
+    int n;
+};
+__host__ __device__ constexpr int64_t passes_bytes(int64_t most) { return (4 * most + 4 + 15) / 16 * 16; }
+template <bool CHOICES>
+__device__ __noinline__ void build_many_passes(const Passes q, uint32_t* n, const Plan p, int tokens, int cap) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        uint32_t run = 0;
+        for (int s0 = 0; s0 < p.n; s0 += 32) {
+            const int s = s0 + lane, e = s < p.n ? p.active[s] : 0;
+            const uint32_t all = s < p.n ? (CHOICES ? p.cnt[e] : static_cast<uint32_t>(tokens)) : 0u, mine = (all + cap - 1) / cap;
+            const uint32_t sum = lane_prefix(mine);
+            for (uint32_t i = 0; i < mine; ++i) {
+                q.e[run + sum - mine + i] = static_cast<uint16_t>(e);
+                q.c0[run + sum - mine + i] = static_cast<uint16_t>(i * cap);
+            }
+            run += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) *n = run;
+    }
+    __syncthreads();
+}
+template <bool CHOICES>
+__device__ __forceinline__ Passes build_passes(uint8_t* smem, int64_t most, const Plan& p, int tokens, int choices, int cap) {
+    if ((CHOICES ? choices : tokens) <= cap) return Passes{p.active, nullptr, p.n};  // a pass for each expert
+    Passes q{reinterpret_cast<uint16_t*>(smem), reinterpret_cast<uint16_t*>(smem) + most, 0};
+    uint32_t* n = reinterpret_cast<uint32_t*>(smem + passes_bytes(most)) - 1;
+    build_many_passes<CHOICES>(q, n, p, tokens, cap);
+    q.n = static_cast<int>(*n);
+    return q;
+}
+
+// A block's units: (pass, row tile), tiles of one pass next to one another, or in the
+// output kernel (row tile, pass).
 template <bool FP4, bool OUT>
 struct Walk {
-    int u, e, tile, n, c0;
-    __device__ __forceinline__ bool more(const TcArgs& a, const Plan& p) const { return u < p.n * a.tiles; }
-    __device__ __forceinline__ void open(const TcArgs& a, const Plan& p) {
-        c0 = 0;
-        if (!more(a, p)) return;
-        const int slot = OUT ? u % p.n : u / a.tiles;
-        tile = OUT ? u / p.n : u % a.tiles;
-        e = p.active[slot];
-        n = FP4 || OUT ? static_cast<int>(p.cnt[e]) : a.m.T;
+    int u, e, tile, n, c0;  // n: the pass's columns
+    __device__ __forceinline__ bool more(const TcArgs& a, const Passes& q) const { return u < q.n * a.tiles; }
+    __device__ __forceinline__ void open(const TcArgs& a, const Plan& p, const Passes& q) {
+        if (!more(a, q)) return;
+        const int pass = OUT ? u % q.n : u / a.tiles;
+        tile = OUT ? u / q.n : u % a.tiles;
+        e = q.e[pass];
+        c0 = q.c0 ? q.c0[pass] : 0;
+        n = min(a.cap, (FP4 || OUT ? static_cast<int>(p.cnt[e]) : a.m.T) - c0);
     }
-    __device__ __forceinline__ void next(const TcArgs& a, const Plan& p) {
-        c0 += a.cap;
-        if (c0 < n) return;
+    __device__ __forceinline__ void next(const TcArgs& a, const Plan& p, const Passes& q) {
         u += gridDim.x;
-        open(a, p);
+        open(a, p, q);
     }
-    __device__ __forceinline__ int cols(const TcArgs& a) const { return min(a.cap, n - c0); }
 };
 
 // One part of a block of 32: the byte of the smallest scale of which the largest
@@ -173,7 +212,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const MoeCall& m = a.m;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    uint8_t* after = smem_raw + plan_bytes(m.E, a.P, ALIGN);
+    uint8_t* after = smem_raw + plan_bytes(m.E, a.P, ALIGN) + passes_bytes(a.passes);
     float* ex = reinterpret_cast<float*>(after);
     uint64_t* bars = reinterpret_cast<uint64_t*>(after + T_EX);
     const uint32_t bar0 = smem_u32(bars), sbase = (bar0 + T_BARS + 1023u) & ~1023u;
@@ -212,12 +251,13 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         grid_dep_launch();
     }
     const Plan p = build_plan<ALIGN>(smem_raw, m.ids, a.P, m.E);
+    const Passes q = build_passes<FP4 || OUT>(smem_raw + plan_bytes(m.E, a.P, ALIGN), a.passes, p, m.T, a.P, a.cap);
     const int64_t R = OUT ? m.N : m.F;       // rows of an expert
     const bool gated = !OUT && m.gate != nullptr;
     const int span = gated ? 64 : 128;       // rows of a tile, of each of the two matrices or of the one
     Walk<FP4, OUT> w;
     w.u = blockIdx.x;
-    w.open(a, p);
+    w.open(a, p, q);
     const int sfa_at = A_BYTES, b_at = A_BYTES + (FP4 ? 1024 : 0), b_bytes = a.cap * (FP4 ? PARTS * 128 : 128);
     const int sfb_at = b_at + b_bytes;
 
@@ -232,7 +272,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         int y = 0, xs = 0;
         bool has = false;
         auto aim = [&](const Walk<FP4, OUT>& x) {
-            const int cols = x.cols(a), nb = ((FP4 ? PARTS : 1) * cols + 15) / 16, big = nb / 8, each = big + nb % 8;
+            const int cols = x.n, nb = ((FP4 ? PARTS : 1) * cols + 15) / 16, big = nb / 8, each = big + nb % 8;
             const int sf = FP4 ? (cols + PLACES - 1) / PLACES : 0;
             const int first = FP4 || OUT ? static_cast<int>(p.first[x.e]) + x.c0 : x.c0;
             bytes = A_BYTES + nb * BPARTS * 2048 + sf * 1024;
@@ -262,7 +302,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         auto stages = [&](At& at, int limit, bool weights, bool rest) {
             int made = 0;
             bool ok = true;
-            while (ok && made < limit && at.x.more(a, p)) {
+            while (ok && made < limit && at.x.more(a, q)) {
                 aim(at.x);
                 const bool mine = has && (wlane ? weights : rest);
                 for (; at.c < a.chunks && made < limit; ++at.c, ++made) {
@@ -277,7 +317,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                 }
                 if (at.c == a.chunks) {
                     at.c = 0;
-                    at.x.next(a, p);
+                    at.x.next(a, p, q);
                 }
             }
             return made;
@@ -297,11 +337,11 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         int s = 0, sf = 0;
         uint32_t ph = 0, it = 0;
         bool ok = true;
-        for (; ok && w.more(a, p); w.next(a, p), ++it) {
+        for (; ok && w.more(a, q); w.next(a, p, q), ++it) {
             if (it) ok = __all_sync(0xffffffffu, mbar_wait_fast(tempty, (it - 1) & 1u, abort_flag, a, DEV_TIMEOUT_MMA));
             if (!ok) break;
             tc_fence_after();
-            const int cols = w.cols(a);
+            const int cols = w.n;
             const uint32_t N = ((FP4 ? PARTS : 1) * cols + 15) / 16 * 16;
             for (int c = 0; c < a.chunks; ++c) {
                 ok = __all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, a, DEV_TIMEOUT_MMA));
@@ -369,11 +409,11 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
             }
         };
         auto ahead = [&](int n) {  // the walk n stages on
-            for (; n > 0 && w.more(a, p); --n)
-                if (++c == a.chunks) { c = 0; w.next(a, p); }
+            for (; n > 0 && w.more(a, q); --n)
+                if (++c == a.chunks) { c = 0; w.next(a, p, q); }
         };
         auto load = [&](uint32_t (&x)[8], bool& got) {
-            got = w.more(a, p);
+            got = w.more(a, q);
             if (!got) return;
             rows();
 #pragma unroll
@@ -406,7 +446,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     } else if (warp >= 2 && warp < 6) {
         // ------------------------------------------------------------ epilogue
         if (EARLY) grid_dep_wait();
-        const int q = warp & 3;
+        const int quad = warp & 3;
         uint32_t it = 0;
         int k = 0;  // exchanges so far: the buffers take turns over all units
         auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
@@ -416,18 +456,18 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                          : "=r"(r) : "r"(ok) : "memory");
             return r != 0;
         };
-        for (; w.more(a, p); w.next(a, p), ++it) {
+        for (; w.more(a, q); w.next(a, p, q), ++it) {
             // the four warps go on or give up together: they meet below
             if (!all_warps(__all_sync(0xffffffffu, mbar_wait(tfull, it & 1u, abort_flag, a, DEV_TIMEOUT_EPILOGUE)))) break;
             tc_fence_after();
-            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16);
             auto drained = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(tempty);
             };
             // the choices of this pass: places i0 .. i0 + items - 1 of the expert's
-            int i0 = w.c0, items = w.cols(a);
+            int i0 = w.c0, items = w.n;
             if (!FP4 && !OUT) {
                 const int n = static_cast<int>(p.cnt[w.e]);
                 i0 = items = 0;
@@ -441,7 +481,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
             }
             const uint16_t* mine = p.list + p.first[w.e] + i0;
             const int place = static_cast<int>(p.first[w.e]) + i0;
-            const int half = gated ? q & 1 : q;
+            const int half = gated ? quad & 1 : quad;
             const int64_t row = static_cast<int64_t>(w.tile) * span + half * 32 + lane;  // of the hidden layer or the output
             for (int b = 0; b < items; b += 16) {
                 const int cnt = min(16, items - b);
@@ -488,7 +528,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                     // warps 0 and 1 have the gate's rows, 2 and 3 up's: they swap half, the
                     // first two finish the even tokens, the others the odd ones
                     float* e = ex + (k++ & 1) * (16 * 64) + half * 32 + lane;
-                    const bool odd = q >= 2;
+                    const bool odd = quad >= 2;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (2 * j < cnt) e[(2 * j + (odd ? 0 : 1)) * 64] = odd ? v[2 * j] : v[2 * j + 1];
@@ -721,10 +761,12 @@ cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CU
     const int tokens16 = (a.m.T + 15) / 16 * 16;
     a.cap = FP4 ? (a.m.T <= PLACES ? PLACES : 2 * PLACES) : OUT ? (tokens16 < 128 ? tokens16 : 128) : (tokens16 < 256 ? tokens16 : 256);
     a.stage = A_BYTES + (FP4 ? 1024 + a.cap * (PARTS * 128) + a.cap / PLACES * 1024 : a.cap * 128 * (OUT ? 2 : 1));
-    const int64_t fixed = plan_bytes(a.m.E, a.P, ALIGN) + T_EX + T_BARS + 1024;
+    const int64_t active = lmin(a.m.E, a.P);  // experts, at most
+    a.passes = static_cast<int>(FP4 || OUT ? a.P : active * ((a.m.T + a.cap - 1) / a.cap));
+    const int64_t fixed = plan_bytes(a.m.E, a.P, ALIGN) + passes_bytes(a.passes) + T_EX + T_BARS + 1024;
     a.depth = static_cast<int>(lmin(MAX_STAGES, (T_LIMIT - fixed) / a.stage));
     if (a.depth < 2) return cudaErrorInvalidConfiguration;
-    const int64_t units = a.tiles * lmin(a.m.E, a.P);  // at most
+    const int64_t units = static_cast<int64_t>(a.tiles) * a.passes;  // at most
     e = launch_pdl(kern, dim3(static_cast<unsigned>(lmin(units, c.sm_count))), dim3(t_threads(FP4)), static_cast<size_t>(fixed + a.depth * a.stage),
                    c.stream, a0, a1, b, sb, b8, a);
     if (e != cudaSuccess) return e;
