@@ -284,3 +284,43 @@ def test_nan_scale_of_a_weight_block(eng):
     y = layer.run(x, ids, p)
     hit = (ids[:, 0] == 2)
     assert torch.isnan(y[hit, 0]).all() and torch.equal(y[~hit], clean[~hit]) and torch.equal(y[:, 1:], clean[:, 1:])
+
+
+@pytest.mark.parametrize("fp4", [False, True], ids=["plain", "fp4"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_x_and_y_off_alignment_keep_the_bits(eng, dtype, fp4):
+    """x and y one element off 16 bytes beside weights that are on it."""
+    layer = Layer(eng, dtype, 5, 136, 72, 56, fp4)
+    x, ids, p = layer.tokens(21, 2)
+    want = layer.run(x, ids, p)
+    off = torch.empty(x.numel() + 1, device="cuda", dtype=x.dtype)[1:].view(x.shape).copy_(x)
+    buf = torch.full((21 * 56 + 2,), 5.0, device="cuda").to(x.dtype)
+    layer.run(off, ids, p, y=buf[1:-1].view(21, 56))
+    assert torch.equal(buf[1:-1].view(21, 56), want) and buf[0] == 5 and buf[-1] == 5
+
+
+@pytest.mark.parametrize("fp4", [False, True], ids=["plain", "fp4"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_no_choice_at_all(eng, dtype, fp4):
+    layer = Layer(eng, dtype, 3, 64, 48, 40, fp4)
+    for t in (2, 40):
+        x, ids, p = layer.tokens(t, 2)
+        ids.fill_(3)
+        y = layer.run(x, ids, p)
+        assert not y.any() and not torch.signbit(y).any()
+    eng.check()
+
+
+@pytest.mark.parametrize("fp4", [False, True], ids=["plain", "fp4"])
+def test_popular_expert_and_long_batch(eng, fp4):
+    """Experts with several passes beside ones with a single token, and more tokens than one pass of the batch."""
+    layer = Layer(eng, "bf16", 6, 320, 80, 136, fp4)
+    x, ids, p = layer.tokens(600, 1)
+    ids[:] = 2
+    ids[::50] = 4
+    ids[7], ids[599] = 0, 5
+    y = layer.run(x, ids, p)
+    rows = torch.tensor([0, 1, 7, 50, 255, 256, 300, 511, 512, 599], device="cuda")
+    check(y[rows], layer.ref(x[rows], ids[rows], p[rows]), "bf16")
+    for r in (7, 300, 599):
+        assert torch.equal(layer.run(x[r:r + 1].contiguous(), ids[r:r + 1].contiguous(), p[r:r + 1].contiguous()), y[r:r + 1])

@@ -140,3 +140,31 @@ def test_tensors_of_another_stream_and_two_graphs(eng):
         graphs[i].replay()
     torch.cuda.synchronize()
     assert all(torch.equal(y, w) for y, w in zip(outs, want))
+
+
+def test_offsets_beyond_32_bits(eng):
+    """A matrix of more than 2^31 elements, and expert weights of more than 2^32 bytes: the last rows and the last expert."""
+    import numpy as np
+    import fp4_ref
+    rows, cols = 270016, 8192
+    x = torch.zeros(rows, cols, device="cuda", dtype=torch.bfloat16)
+    x[-3:] = torch.randn(3, cols, device="cuda")
+    q, s = bi.fp4_buffers(rows, cols)
+    eng.fp4_quantize(q, s, None, None, x, rows, cols, "bf16")
+    back = torch.empty_like(x)
+    eng.fp4_dequantize(back, q, s, rows, cols, "bf16")
+    assert np.array_equal(back[-3:].double().cpu().numpy(), fp4_ref.rounded(x[-3:].double().cpu().numpy()))
+    assert not back[:-3].any()
+    del x, back, q, s
+    e, f, k, n = 600, 1024, 4096, 64
+    up, down = torch.zeros(e, f, k, device="cuda", dtype=torch.bfloat16), torch.zeros(e, n, f, device="cuda", dtype=torch.bfloat16)
+    up[-1] = torch.randn(f, k, device="cuda") / 64
+    down[-1] = torch.randn(n, f, device="cuda") / 32
+    xt = torch.randn(2, k, device="cuda").bfloat16()
+    ids = torch.tensor([[e - 1], [0]], device="cuda", dtype=torch.int32)
+    y = torch.empty(2, n, device="cuda", dtype=torch.bfloat16)
+    eng.moe_forward(y, xt, ids, torch.ones(2, 1, device="cuda"), None, up, down, 2, 1, k, f, n, e, "relu", "bf16")
+    want = torch.relu(xt[0].double() @ up[-1].double().T) @ down[-1].double().T
+    # sums of 4096 and 1024 products in f32 (2^-15 of their magnitudes at most, which are below 64 times the result's rms)
+    assert (y[0].double() - want).abs().max() <= 2.0 ** -8 * want.abs().max() + 2.0 ** -9 * want.square().mean().sqrt()
+    assert not y[1].any()
