@@ -405,6 +405,7 @@ bi_status bi_fp4_quantize(bi_engine eng, uint8_t* q, uint8_t* s, uint8_t* qt, ui
     if (!src || (!q && !qt)) return fail(eng, BI_ERR_INVALID_ARG, "src, and q with s or qt with st, must not be NULL");
     if (!aligned16(q) || !aligned16(s) || !aligned16(qt) || !aligned16(st))
         return fail(eng, BI_ERR_MISALIGNED, "codes and scales need 16-byte alignment");
+    if (reinterpret_cast<uintptr_t>(src) % bi::dsize(dtype) != 0) return fail(eng, BI_ERR_MISALIGNED, "src needs the alignment of its type");
     DeviceGuard g(eng->device);
     if (!g.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
     const bi::LaunchCtx c = ctx(eng, stream);
@@ -421,6 +422,7 @@ bi_status bi_fp4_dequantize(bi_engine eng, void* dst, const uint8_t* q, const ui
     if (rows == 0) return BI_OK;
     if (!dst || !q || !s) return fail(eng, BI_ERR_INVALID_ARG, "dst, q and s must not be NULL");
     if (!aligned16(q) || !aligned16(s)) return fail(eng, BI_ERR_MISALIGNED, "codes and scales need 16-byte alignment");
+    if (reinterpret_cast<uintptr_t>(dst) % bi::dsize(dtype) != 0) return fail(eng, BI_ERR_MISALIGNED, "dst needs the alignment of its type");
     DeviceGuard g(eng->device);
     if (!g.ok) return fail(eng, BI_ERR_CUDA, "cudaSetDevice failed");
     const bi::LaunchCtx c = ctx(eng, stream);

@@ -233,7 +233,8 @@ int64_t bi_fp4_scale_bytes(int64_t rows, int64_t cols);
  * qt, st along its rows (the operand [cols][rows], src transposed), either pair
  * NULL, from one read of src.  Per block 2^s with s = floor(log2 max|v|) - 2, at
  * least -127; codes e2m1(v / 2^s), round to nearest even, larger ones to +-6 (v / 2^s
- * is exact).  A block with an infinity or NaN gets the scale 255 and codes 0. */
+ * is exact).  A block with an infinity or NaN gets the scale 255 and codes 0.  src (and
+ * dst below) needs the alignment of its type. */
 bi_status bi_fp4_quantize(bi_engine engine, uint8_t* q, uint8_t* s, uint8_t* qt, uint8_t* st, const void* src,
                           int64_t rows, int64_t cols, bi_dtype dtype, void* stream);
 
@@ -437,7 +438,7 @@ bi_status bi_router_backward(bi_engine engine, void* dlogits, const void* logits
  * F multiples of 8 run on the tensor cores, where h enters the second product as two
  * 16-bit parts (2^-17 of it; f16 by a power of two per choice, 2^-22 of it or 2^-39 of
  * the choice's largest); others, and f32, in f32 FMAs.  A non-finite x, h or weight makes
- * the rows it enters non-finite.  Tensors need the alignment of their type.  Forward
+ * the rows it enters non-finite (but for a -inf that ReLU takes to 0).  Tensors need the alignment of their type.  Forward
  * only.  Scratch from the engine's pool: about T C (8 F + 4 N) bytes. */
 typedef enum { BI_ACT_SILU = 0, BI_ACT_GELU = 1, BI_ACT_RELU = 2 } bi_activation;
 

@@ -168,3 +168,17 @@ def test_offsets_beyond_32_bits(eng):
     # sums of 4096 and 1024 products in f32 (2^-15 of their magnitudes at most, which are below 64 times the result's rms)
     assert (y[0].double() - want).abs().max() <= 2.0 ** -8 * want.abs().max() + 2.0 ** -9 * want.square().mean().sqrt()
     assert not y[1].any()
+
+
+@pytest.mark.parametrize("dtype,off", [("bf16", 1), ("f16", 1), ("f32", 1), ("f32", 2)])
+def test_matrix_off_its_types_alignment(eng, dtype, off):
+    """The unquantized matrix is read and written an element at a time at least: addresses
+    between elements are refused on the host."""
+    x = torch.zeros(5, 64, device="cuda")
+    buf = bi.fp4_buffers(4, 64)
+    for call in (lambda: eng.fp4_quantize(*buf, None, None, x.data_ptr() + off, 4, 64, dtype),
+                 lambda: eng.fp4_dequantize(x.data_ptr() + off, *buf, 4, 64, dtype)):
+        with pytest.raises(bi.BiError) as err:
+            call()
+        assert err.value.status == bi.BI_ERR_MISALIGNED
+    assert not x.any()
