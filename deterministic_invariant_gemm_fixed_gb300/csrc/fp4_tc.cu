@@ -22,8 +22,8 @@
 // then the next tile's MMAs start and the other 192 columns are stored beside them.
 //
 // Bound by the ring's feed from L2, 70 KB per pair and stage for 33.6 MFLOP: 8192 x 4096 x
-// 12288 takes 131 us (6.3 PFLOP/s), 118 with a quarter of the MMAs; the tensor pipe is 60 %
-// busy.  One token's stage takes 0.39 us, a batch's 0.42.
+// 12288 takes 128 us (6.4 PFLOP/s), the tensor pipe 60 % busy.  One token's stage takes
+// 0.39 us, a batch's 0.4.
 #include "abi_util.h"
 #include "fp4.h"
 #include "tc_common.cuh"
@@ -53,6 +53,7 @@ struct Fp4Params {
     int64_t ldo, rows, cols;
     const void* bias;
     int units_m, num_n;
+    int wide;       // a sweep over the columns is shared by 32 row tiles, not 16
     int kb0, nkb;   // the stages of this launch
     int accum;      // f32: add to what the output holds
     int tma_out;    // the output's rows are multiples of 16 bytes: stored by TMA
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         bool ok = true;
         for (int t = cidx; ok && t < tiles; t += ncl) {
             int mp, nb;
-            dense_raster(t, p.units_m, p.num_n, mp, nb);
+            dense_raster(t, p.units_m, p.num_n, mp, nb, p.wide ? 32 : 16);
             const int y = lane == 0 ? mp * 256 + static_cast<int>(crank) * 128
                         : lane == 1 ? nb * 256 + static_cast<int>(crank) * 128
                         : lane == 2 ? mp * 2 + static_cast<int>(crank) : nb * 2;
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         float* bias = reinterpret_cast<float*>(smem + F_STAGES * F_STAGE + F_OUT) + qd * 256;
         for (int t = cidx; t < tiles; t += ncl, ++it) {
             int mp, nb;
-            dense_raster(t, p.units_m, p.num_n, mp, nb);
+            dense_raster(t, p.units_m, p.num_n, mp, nb, p.wide ? 32 : 16);
             const int64_t row0 = static_cast<int64_t>(mp) * 256 + crank * 128 + qd * 32, orow = row0 + lane;
             const int64_t col0 = static_cast<int64_t>(nb) * 256;
             if (p.bias != nullptr) {  // this warp's copy of the tile's
@@ -380,6 +381,11 @@ cudaError_t product_t(const LaunchCtx& c, void* out, const uint8_t* a, const uin
     p.cols = cols;
     p.units_m = static_cast<int>((rows + 255) / 256);
     p.num_n = static_cast<int>((cols + 255) / 256);
+    // 32 row tiles to a sweep over the columns, which reads b from memory once per group, while
+    // a's codes of them stay in L2 (up to 32 MB: depth 8192), else 16: 8192 x 4096 x 12288 128
+    // against 134 us, 65536 x 2048 x 8192 432 against 456; 8192 x 12288 x 12288 332 against 319.
+    // (The number itself as a parameter: one token 13.7 against 13.3 us.)
+    p.wide = 32 * 256 * (depth_p / 2) <= (32 << 20);
     p.tma_out = cols * esize % 16 == 0 && aligned16(out);
     if (!p.tma_out) mo = ma;
     else if ((e = make_out_map(&mo, OUT, out, cols, rows, cols)) != cudaSuccess) return e;

@@ -196,13 +196,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
 }
 
 constexpr int RASTER_ROWS = 16;  // 16 row-tiles share the column sweep (L2 reuse)
-// Raster of the dense tiles: RASTER_ROWS row pairs share a sweep over the column
+// Raster of the dense tiles: `group` row pairs share a sweep over the column
 // tiles (L2 reuse of the B columns).
-__host__ __device__ __forceinline__ void dense_raster(int t, int units_m, int num_n, int& mpair, int& nb) {
-    const int span = RASTER_ROWS * num_n;
+__host__ __device__ __forceinline__ void dense_raster(int t, int units_m, int num_n, int& mpair, int& nb, int group = RASTER_ROWS) {
+    const int span = group * num_n;
     const int grp = t / span;
-    const int first = grp * RASTER_ROWS;
-    const int gsize = min(units_m - first, RASTER_ROWS);
+    const int first = grp * group;
+    const int gsize = min(units_m - first, group);
     const int r = t - grp * span;
     mpair = first + r % gsize;
     nb = r / gsize;

@@ -255,3 +255,19 @@ def test_captured_and_replayed(eng):
     got = y.clone()
     step()
     assert torch.equal(got, y)
+
+
+@pytest.mark.parametrize("m,k,n", [(8500, 96, 530), (4400, 8500, 530)])
+def test_many_row_tiles(eng, m, k, n):
+    """More row tiles than share a sweep over the columns, the last group a short one: the
+    rows are those of calls with few."""
+    a, _ = quantized(eng, torch.randn(m, k, device="cuda", dtype=torch.bfloat16), both=False)
+    b, _ = quantized(eng, torch.randn(n, k, device="cuda", dtype=torch.bfloat16), both=False)
+    y = torch.full((m, n), 7.0, device="cuda", dtype=torch.bfloat16)
+    eng.fp4_forward(y, *a, *b, None, m, k, n, "bf16")
+    cp = -(-k // 256) * 256
+    z = torch.empty_like(y)
+    for r in range(0, m, 1024):  # whole pieces of scales
+        c = min(1024, m - r)
+        eng.fp4_forward(z[r:r + c], a[0][r * cp // 2:], a[1][r // 128 * cp * 4:], *b, None, c, k, n, "bf16")
+    assert torch.equal(y, z)
