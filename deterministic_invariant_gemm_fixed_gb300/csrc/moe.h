@@ -3,11 +3,9 @@
 #pragma once
 
 #include "bi_internal.h"
+#include "moe_ring.h"
 
 namespace bi {
-
-constexpr int64_t MOE_MAX_PAIRS = 2048;  // token choices of a call
-constexpr int64_t MOE_MAX_E = 1024;
 
 struct MoeCall {
     void* y;                     // [T][N]
@@ -50,11 +48,6 @@ struct Plan {
     uint16_t* active;  // [E] experts with choices
     int n;             // how many
 };
-__host__ __device__ constexpr int64_t plan_places(int64_t E, int64_t P, int64_t align) { return P + (align - 1) * (E < P ? E : P); }
-// (a multiple of 16, the last four bytes n)
-__host__ __device__ constexpr int64_t plan_bytes(int64_t E, int64_t P, int64_t align) {
-    return (14 * E + 2 * plan_places(E, P, align) + 4 + 15) / 16 * 16;
-}
 
 __device__ __forceinline__ uint32_t lane_prefix(uint32_t v) {  // inclusive sum over the lanes
     const int lane = threadIdx.x & 31;

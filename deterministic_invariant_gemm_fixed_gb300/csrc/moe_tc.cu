@@ -52,14 +52,6 @@
 namespace bi {
 namespace {
 
-constexpr int PARTS = 8;                   // MXFP4 rows of a token
-constexpr int PLACES = 128 / PARTS;        // tokens whose rows are one piece of scales: an expert's places start on it
-constexpr int T_LIMIT = 227 * 1024;
-constexpr int T_BARS = 512;
-constexpr int T_EX = 2 * 16 * 64 * 4;      // the epilogue's exchange between the gate's and up's warps
-constexpr int A_BYTES = 128 * 128;         // weights of a stage
-constexpr int MAX_STAGES = 12;
-constexpr int SF_WARPS = 4;                // MXFP4: warps that put the weights' scales in place
 constexpr int t_threads(bool fp4) { return 192 + (fp4 ? 32 * SF_WARPS : 0); }
 constexpr int SF_COL = 256, SF_COLS = 24;  // tensor memory: accumulator, then two stages of scales (A 8, B 16)
 
@@ -129,7 +121,6 @@ struct Passes {
     uint16_t *e, *c0;  // c0 null: all 0
     int n;
 };
-__host__ __device__ constexpr int64_t passes_bytes(int64_t most) { return (4 * most + 4 + 15) / 16 * 16; }
 template <bool CHOICES>
 __device__ __noinline__ void build_many_passes(const Passes q, uint32_t* n, const Plan p, int tokens, int cap) {
     if (threadIdx.x < 32) {
@@ -389,9 +380,11 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
         // A lane has rows lane and lane + 32 of either half of the tile, wherever their
         // bytes lie, and puts them side by side in the order that the tensor cores take.
         // Loaded for BATCH stages at once: the fence that hands a stage on waits for the
-        // loads in flight too (loads between the fences: 1.1 us a stage); and by SF_WARPS
-        // warps in turn, each taking as long over a stage as the tensor cores over several.
+        // loads in flight too (loads between the fences: 1.1 us a stage); and by up to SF_WARPS
+        // warps in turn, each taking as long over a stage as the tensor cores over several
+        // (never more warps than stages: moe_scale_warps).
         constexpr int BATCH = 4;
+        const int turn = moe_scale_warps(a.depth), first = warp - 6;
         const int64_t Lp = fp4_padded(OUT ? m.F : m.K), all = m.E * R;
         const uint8_t* s0 = OUT ? m.down_s : gated ? m.gate_s : m.up_s;
         const uint8_t* s1 = OUT ? m.down_s : m.up_s;
@@ -419,14 +412,14 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 x[j] = __ldg(reinterpret_cast<const uint32_t*>(at[j & 3] + static_cast<int64_t>(2 * c + (j >> 2)) * 512));
-            ahead(SF_WARPS);
+            ahead(turn);
         };
-        ahead(warp - 6);
+        ahead(first);
         auto step = [&](int n) {  // the ring's stage n uses on
             for (s += n; s >= a.depth; s -= a.depth) ph ^= 1u;
         };
-        step(warp - 6);
-        bool go = true;
+        step(first);
+        bool go = first < turn;
         while (go) {
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) load(v[i], have[i]);
@@ -440,7 +433,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive(full_bar(s));
-                step(SF_WARPS);
+                step(turn);
             }
         }
     } else if (warp >= 2 && warp < 6) {
@@ -753,21 +746,18 @@ cudaError_t launch(const LaunchCtx& c, TcArgs a, const CUtensorMap& a0, const CU
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T_LIMIT);
     });
     if (e != cudaSuccess) return e;
-    constexpr int ALIGN = FP4 ? PLACES : 1;
     const int64_t rows = OUT ? a.m.N : a.m.F, len = OUT ? a.m.F : a.m.K;
     const int span = !OUT && a.m.gate ? 64 : 128;
     a.tiles = static_cast<int>((rows + span - 1) / span);
     a.chunks = static_cast<int>(FP4 ? fp4_padded(len) / 256 : (len + 63) / 64);
-    const int tokens16 = (a.m.T + 15) / 16 * 16;
-    a.cap = FP4 ? (a.m.T <= PLACES ? PLACES : 2 * PLACES) : OUT ? (tokens16 < 128 ? tokens16 : 128) : (tokens16 < 256 ? tokens16 : 256);
-    a.stage = A_BYTES + (FP4 ? 1024 + a.cap * (PARTS * 128) + a.cap / PLACES * 1024 : a.cap * 128 * (OUT ? 2 : 1));
-    const int64_t active = lmin(a.m.E, a.P);  // experts, at most
-    a.passes = static_cast<int>(FP4 || OUT ? a.P : active * ((a.m.T + a.cap - 1) / a.cap));
-    const int64_t fixed = plan_bytes(a.m.E, a.P, ALIGN) + passes_bytes(a.passes) + T_EX + T_BARS + 1024;
-    a.depth = static_cast<int>(lmin(MAX_STAGES, (T_LIMIT - fixed) / a.stage));
+    const MoeRing ring = moe_ring(FP4, OUT, a.m.T, a.P, a.m.E);
+    a.cap = ring.cap;
+    a.passes = ring.passes;
+    a.stage = ring.stage;
+    a.depth = ring.depth;
     if (a.depth < 2) return cudaErrorInvalidConfiguration;
     const int64_t units = static_cast<int64_t>(a.tiles) * a.passes;  // at most
-    e = launch_pdl(kern, dim3(static_cast<unsigned>(lmin(units, c.sm_count))), dim3(t_threads(FP4)), static_cast<size_t>(fixed + a.depth * a.stage),
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(lmin(units, c.sm_count))), dim3(t_threads(FP4)), static_cast<size_t>(ring.fixed + a.depth * a.stage),
                    c.stream, a0, a1, b, sb, b8, a);
     if (e != cudaSuccess) return e;
     c.count();
