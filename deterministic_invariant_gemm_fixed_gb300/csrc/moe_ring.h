@@ -37,7 +37,8 @@ constexpr MoeRing moe_ring(bool fp4, bool out, int T, int64_t P, int64_t E) {
     r.cap = fp4 ? (T <= PLACES ? PLACES : 2 * PLACES) : out ? (tokens16 < 128 ? tokens16 : 128) : (tokens16 < 256 ? tokens16 : 256);
     r.stage = A_BYTES + (fp4 ? 1024 + r.cap * (PARTS * 128) + r.cap / PLACES * 1024 : r.cap * 128 * (out ? 2 : 1));
     const int64_t active = E < P ? E : P;  // experts, at most
-    r.passes = static_cast<int>(fp4 || out ? P : active * ((T + r.cap - 1) / r.cap));
+    // (choices shared out among the active experts make at most one pass each that is not full)
+    r.passes = static_cast<int>(fp4 || out ? active + P / r.cap : active * ((T + r.cap - 1) / r.cap));
     r.fixed = plan_bytes(E, P, fp4 ? PLACES : 1) + passes_bytes(r.passes) + T_EX + T_BARS + 1024;
     const int64_t depth = (T_LIMIT - r.fixed) / r.stage;
     r.depth = static_cast<int>(depth < MAX_STAGES ? depth : MAX_STAGES);

@@ -112,6 +112,29 @@ def test_every_ring_fits_and_no_more_warps_than_stages(host):
                     assert 1 <= host.scale_warps(d) <= d
 
 
+def test_pass_lists_take_the_room_they_need(host):
+    """Room for every expert's choices in passes of `cap`, however they fall, and hardly more: a place per
+    choice cost calls of a few dozen experts a stage of the ring."""
+    o = (ctypes.c_int64 * 5)()
+    rng = random.Random(5)
+    for fp4, out in ((1, 0), (1, 1), (0, 1)):
+        for _ in range(400):
+            c = rng.randint(1, 16)
+            t, e = rng.randint(1, 2048 // c), rng.randint(1, 1024)
+            host.ring(fp4, out, t, c, e, o)
+            cap, room, choices = o[0], o[1], t * c
+            worst = min(e, choices) + (choices - min(e, choices)) // cap
+            assert worst <= room <= worst + 1 + min(e, choices) // cap
+            counts = [0] * e  # and some choice of them
+            some = rng.randint(1, e)
+            for _ in range(choices):
+                counts[rng.randrange(some)] += 1
+            assert sum(-(-n // cap) for n in counts) <= room
+    for out in (0, 1):
+        host.ring(1, out, 256, 8, 64, o)
+        assert o[3] == 4
+
+
 @pytest.mark.parametrize("depth", range(1, 13))
 def test_scale_warps_keep_to_the_phases(host, depth):
     rng = random.Random(depth)
