@@ -16,6 +16,7 @@ constexpr int64_t passes_bytes(int64_t most) { return (4 * most + 4 + 15) / 16 *
 
 constexpr int PARTS = 8;                   // MXFP4 rows of a token
 constexpr int PLACES = 128 / PARTS;        // tokens whose rows are one piece of scales: an expert's places start on it
+constexpr int H_PLANES = 3;                // 16-bit parts of a hidden value
 constexpr int T_LIMIT = 227 * 1024;
 constexpr int T_BARS = 512;
 constexpr int T_EX = 2 * 16 * 64 * 4;      // the epilogue's exchange between the gate's and up's warps
@@ -34,8 +35,10 @@ struct MoeRing {
 constexpr MoeRing moe_ring(bool fp4, bool out, int T, int64_t P, int64_t E) {
     MoeRing r{};
     const int tokens16 = (T + 15) / 16 * 16;
-    r.cap = fp4 ? (T <= PLACES ? PLACES : 2 * PLACES) : out ? (tokens16 < 128 ? tokens16 : 128) : (tokens16 < 256 ? tokens16 : 256);
-    r.stage = A_BYTES + (fp4 ? 1024 + r.cap * (PARTS * 128) + r.cap / PLACES * 1024 : r.cap * 128 * (out ? 2 : 1));
+    // (output kernel: three parts of 64 choices are 192 columns of the MMA; with 32 or 48 choices a pass 64
+    // tokens over 64 experts take 138 us for 141, but 96 over 8 179 and 181 for 171)
+    r.cap = fp4 ? (T <= PLACES ? PLACES : 2 * PLACES) : out ? (tokens16 < 64 ? tokens16 : 64) : (tokens16 < 256 ? tokens16 : 256);
+    r.stage = A_BYTES + (fp4 ? 1024 + r.cap * (PARTS * 128) + r.cap / PLACES * 1024 : r.cap * 128 * (out ? H_PLANES : 1));
     const int64_t active = E < P ? E : P;  // experts, at most
     // (choices shared out among the active experts make at most one pass each that is not full)
     r.passes = static_cast<int>(fp4 || out ? active + P / r.cap : active * ((T + r.cap - 1) / r.cap));

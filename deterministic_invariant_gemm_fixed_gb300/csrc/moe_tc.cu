@@ -13,10 +13,14 @@
 // 16-bit weights: kind::f16, stages of 64.  The tokens of the hidden kernel are all tokens
 // of the batch, straight from x (up to 256 at a time): columns of tokens that chose
 // other experts are thrown away, which costs nothing next to gathering.  h enters the output
-// kernel as two 16-bit parts, high part and remainder, two MMAs into the same sum: to
-// 2^-17 of it in bf16.  f16 has not h's range: there h is kept in f32, and a kernel
-// between the two scales each choice's by a power of two, its largest to 2^14 (parts to
-// 2^-22 of a value, 2^-39 of the largest), which the sums are multiplied back by.
+// kernel as three 16-bit parts, each what the ones before left: all 24 bits of its f32
+// value.  They are N columns of their own, added in the epilogue from the smallest up: a sum of the
+// tensor cores cuts off what it shifts out, once for every MMA into it.  (Two parts into
+// one sum leave 2^-17 of h in bf16: 64 tokens, 64 experts of 2048 x 1408, 3.7 results of
+// 1000 are not the 64-bit value's rounding, here 2.4; 138 and 141 us.)  f16 has not h's range:
+// there h is kept in f32, and a kernel between the two scales each choice's by a power of
+// two, its largest to 2^14 (its parts stop at 2^-39 of the largest), which the sums are
+// multiplied back by.
 //
 // MXFP4 weights: kind::mxf4 with block scales, stages of 256, the codes as they lie in
 // memory: no weight is ever expanded.  Its other operand has to be MXFP4 too, so a token's
@@ -57,7 +61,7 @@ constexpr int SF_COL = 256, SF_COLS = 24;  // tensor memory: accumulator, then t
 
 struct TcArgs {
     MoeCall m;
-    uint16_t* h;        // 16-bit weights: planes [2][P][Fp]
+    uint16_t* h;        // 16-bit weights: planes [H_PLANES][P][Fp]
     float* hf;          // not bf16: h itself, [places][F], which a kernel of its own makes the next operand of
     const float* unscale;  // f16 weights, output kernel: [P] by which a place's sums are multiplied
     float* part;        // [P][Nq] the choices' sums
@@ -187,10 +191,15 @@ __device__ __forceinline__ void hidden_out(const TcArgs& a, const float (&r)[8],
             a.hf[(place + j * step) * a.m.F + row] = r[j];
             continue;
         }
-        const __nv_bfloat16 hi = __float2bfloat16_rn(r[j]), lo = __float2bfloat16_rn(r[j] - __bfloat162float(hi));
+        // eight bits of the 24 a plane, cut off so that no plane leaves bf16's range
+        float v = r[j];
         uint16_t* o = a.h + (place + j * step) * a.Fp + row;
-        o[0] = __bfloat16_as_ushort(hi);
-        o[static_cast<int64_t>(a.P) * a.Fp] = __bfloat16_as_ushort(lo);
+#pragma unroll
+        for (int x = 0; x < H_PLANES; ++x) {
+            const __nv_bfloat16 b = __float2bfloat16_rz(v);
+            o[x * static_cast<int64_t>(a.P) * a.Fp] = __bfloat16_as_ushort(b);
+            v -= __bfloat162float(b);
+        }
     }
 }
 
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     moe_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmB8, const TcArgs a) {
     constexpr int ALIGN = FP4 ? PLACES : 1;
-    constexpr int BPARTS = !FP4 && OUT ? 2 : 1;  // planes of B
+    constexpr int BPARTS = !FP4 && OUT ? H_PLANES : 1;  // planes of B
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const MoeCall& m = a.m;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
     Walk<FP4, OUT> w;
     w.u = blockIdx.x;
     w.open(a, p, q);
-    const int sfa_at = A_BYTES, b_at = A_BYTES + (FP4 ? 1024 : 0), b_bytes = a.cap * (FP4 ? PARTS * 128 : 128);
+    const int sfa_at = A_BYTES, b_at = A_BYTES + (FP4 ? 1024 : 0), b_bytes = a.cap * (FP4 ? PARTS : BPARTS) * 128;
     const int sfb_at = b_at + b_bytes;
 
     if (warp == 0) {
@@ -275,9 +284,9 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                 y = static_cast<int>(gated ? r : r + (lane - 30) * 64);
                 has = true;
             } else if (lane < each * BPARTS) {
-                const int part = lane >= each, i = lane - part * each, b = i < big ? i * 8 : big * 8 + i - big;
+                const int part = BPARTS == 1 ? 0 : lane / each, i = lane - part * each, b = i < big ? i * 8 : big * 8 + i - big;
                 map = i < big ? &tmB8 : &tmB;
-                to = sbase + b_at + part * b_bytes + b * 2048;
+                to = sbase + b_at + (part * nb + b) * 2048;
                 y = FP4 ? first * PARTS + b * 16 : part * a.P + first + b * 16;
                 has = true;
             } else {
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
             if (!ok) break;
             tc_fence_after();
             const int cols = w.n;
-            const uint32_t N = ((FP4 ? PARTS : 1) * cols + 15) / 16 * 16;
+            const uint32_t N = ((FP4 ? PARTS : 1) * cols + 15) / 16 * 16 * BPARTS;
             for (int c = 0; c < a.chunks; ++c) {
                 ok = __all_sync(0xffffffffu, mbar_wait_fast(full_bar(s), ph, abort_flag, a, DEV_TIMEOUT_MMA));
                 if (!ok) break;
@@ -359,9 +368,7 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                     const uint32_t idesc = (1u << 4) | (a.fmt << 7) | (a.fmt << 10) | ((N >> 3) << 17) | (8u << 24);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                        for (int part = 0; part < BPARTS; ++part)
-                            mma_16(tmem, da + kk * K_STEP, db + part * (b_bytes >> 4) + kk * K_STEP, idesc, (c | kk | part) != 0 ? 1u : 0u, lead);
+                        mma_16(tmem, da + kk * K_STEP, db + kk * K_STEP, idesc, (c | kk) != 0 ? 1u : 0u, lead);
                 }
                 commit(empty_bar(s), lead);
                 if (++s == a.depth) { s = 0; ph ^= 1u; }
@@ -494,9 +501,22 @@ __global__ void __launch_bounds__(t_threads(FP4), 1)
                             v[j + 1] = __fadd_rn(v[j + 1], __uint_as_float(r[8 + x]));
                         }
                     }
+                } else if constexpr (OUT) {
+                    const int plane = (items + 15) / 16 * 16;  // columns of a part
+                    uint32_t r[H_PLANES][16];
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < H_PLANES; ++x) tmem_get16(tb + x * plane + b, r[x]);
+                    tmem_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {  // the smallest first
+                        v[j] = __uint_as_float(r[H_PLANES - 1][j]);
+#pragma unroll
+                        for (int x = H_PLANES - 2; x >= 0; --x) v[j] = __fadd_rn(__uint_as_float(r[x][j]), v[j]);
+                    }
                 } else {
                     // a lane finds a token's column for all
-                    const int mycol = OUT ? b + lane : mine[min(b + lane, items - 1)] / m.C - w.c0;
+                    const int mycol = mine[min(b + lane, items - 1)] / m.C - w.c0;
                     uint32_t r[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -650,7 +670,7 @@ __global__ void __launch_bounds__(128) moe_sum_kernel(T* y, const float* part, c
         if (n0 + x < N) y[t * N + n0 + x] = static_cast<T>(s[x]);
 }
 
-// f16 weights: a choice's h, scaled by a power of two, in two f16 planes.  A block per place
+// f16 weights: a choice's h, scaled by a power of two, in f16 planes.  A block per place
 // (places that no choice has hold anything, and are not read).
 __global__ void __launch_bounds__(256) moe_planes_kernel(uint16_t* h, float* unscale, const float* hf, int64_t F, int64_t Fp, int P) {
     __shared__ uint32_t top[8];
@@ -668,10 +688,13 @@ __global__ void __launch_bounds__(256) moe_planes_kernel(uint16_t* h, float* uns
     const float scale = __uint_as_float(field << 23);
     uint16_t* o = h + blockIdx.x * Fp;
     for (int64_t f = threadIdx.x; f < F; f += 256) {
-        const float x = v[f] * scale;
-        const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
-        o[f] = __half_as_ushort(hi);
-        o[P * Fp + f] = __half_as_ushort(lo);
+        float x = v[f] * scale;
+#pragma unroll
+        for (int i = 0; i < H_PLANES; ++i) {
+            const __half b = __float2half_rn(x);
+            o[i * P * Fp + f] = __half_as_ushort(b);
+            x -= __half2float(b);
+        }
     }
     if (threadIdx.x == 0) unscale[blockIdx.x] = __uint_as_float((254u - field) << 23);
 }
@@ -728,7 +751,7 @@ Room room(const MoeCall& m, bool fp4, bool copy_x, bool f16) {
     const int64_t rows = r.places * PARTS;
     r.x = take(fp4 ? rows * (r.Kp / 2) : copy_x ? m.T * r.Kp * 2 : 0);
     r.xs = take(fp4 ? rows / 128 * r.Kp * 4 : 0);
-    r.h = take(fp4 ? rows * (r.Fp / 2) : 2 * P * r.Fp * 2);
+    r.h = take(fp4 ? rows * (r.Fp / 2) : H_PLANES * P * r.Fp * 2);
     r.hs = take(fp4 ? rows / 128 * r.Fp * 4 : 0);
     r.hf = take(fp4 ? r.places * m.F * 4 : f16 ? P * m.F * 4 : 0);
     r.scale = take(!fp4 && f16 ? P * 4 : 0);
@@ -829,9 +852,9 @@ cudaError_t moe_form(const LaunchCtx& c, const MoeCall& m, bool copy_x, bi_dtype
         if (m.gate && (e = row_map(&gate, false, m.gate, m.K, ef, m.K * 2, 64)) != cudaSuccess) return e;
         if ((e = row_map(&down, false, m.down, m.F, en, m.F * 2, 64)) != cudaSuccess) return e;
         if ((e = row_map(&mx, false, x, m.K, m.T, pitch * 2, 16)) != cudaSuccess) return e;
-        if ((e = row_map(&mh, false, a.h, m.F, 2ll * a.P, r.Fp * 2, 16)) != cudaSuccess) return e;
+        if ((e = row_map(&mh, false, a.h, m.F, static_cast<int64_t>(H_PLANES) * a.P, r.Fp * 2, 16)) != cudaSuccess) return e;
         if ((e = row_map(&mx8, false, x, m.K, m.T, pitch * 2, 128)) != cudaSuccess) return e;
-        if ((e = row_map(&mh8, false, a.h, m.F, 2ll * a.P, r.Fp * 2, 128)) != cudaSuccess) return e;
+        if ((e = row_map(&mh8, false, a.h, m.F, static_cast<int64_t>(H_PLANES) * a.P, r.Fp * 2, 128)) != cudaSuccess) return e;
         sx = sh = mx;
     }
     if (!m.gate) gate = up;

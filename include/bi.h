@@ -435,11 +435,11 @@ bi_status bi_router_backward(bi_engine engine, void* dlogits, const void* logits
  * order fixed by the types, K, F and the weights' alignment, a token's choices are
  * added in the order of j: bit-identical run to run, and a row of y depends on its own
  * x, ids and weights alone, whatever T.  16-bit weights on 16-byte boundaries with K and
- * F multiples of 8 run on the tensor cores, where h enters the second product as two
- * 16-bit parts (2^-17 of it; f16 by a power of two per choice, 2^-22 of it or 2^-39 of
+ * F multiples of 8 run on the tensor cores, where h enters the second product as three
+ * 16-bit parts that hold its f32 value (f16 by a power of two per choice, down to 2^-39 of
  * the choice's largest); others, and f32, in f32 FMAs.  A non-finite x, h or weight makes
  * the rows it enters non-finite (but for a -inf that ReLU takes to 0).  Tensors need the alignment of their type.  Forward
- * only.  Scratch from the engine's pool: about T C (8 F + 4 N) bytes. */
+ * only.  Scratch from the engine's pool: about T C (10 F + 4 N) bytes. */
 typedef enum { BI_ACT_SILU = 0, BI_ACT_GELU = 1, BI_ACT_RELU = 2 } bi_activation;
 
 bi_status bi_moe_forward(bi_engine engine, void* y, const void* x, const uint32_t* ids, const float* weights,
