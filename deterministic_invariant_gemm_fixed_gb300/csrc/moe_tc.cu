@@ -618,11 +618,13 @@ __global__ void __launch_bounds__(X_THREADS) moe_parts_kernel(const T* x, const 
             word[part] = 0;
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
-                const uint32_t c = byte == 255u ? 0u : __nv_cvt_float2_to_fp4x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_E2M1, cudaRoundNearest);
+                const float a = __fmul_rn(v[j], inv), b = __fmul_rn(v[j + 1], inv);
+                const uint32_t c = byte == 255u ? 0u : __nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest);
                 word[part] |= c << (4 * j);
-                // exact: the rest of a rounding to nearest
-                v[j] = byte == 255u ? 0.0f : __fsub_rn(v[j], fp4_code_value(c & 15u) * scale);
-                v[j + 1] = byte == 255u ? 0.0f : __fsub_rn(v[j + 1], fp4_code_value(c >> 4) * scale);
+                // exact: the rest of a rounding to nearest (taken before the scale: the code of a
+                // value near 2^128 may stand for 2^128)
+                v[j] = byte == 255u ? 0.0f : __fmul_rn(__fsub_rn(a, fp4_code_value(c & 15u)), scale);
+                v[j + 1] = byte == 255u ? 0.0f : __fmul_rn(__fsub_rn(b, fp4_code_value(c >> 4)), scale);
             }
             if (part % 4 == 0) bytes[part / 4] = 0;
             bytes[part / 4] |= byte << (8 * (part % 4));
