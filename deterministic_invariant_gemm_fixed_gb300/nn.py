@@ -33,6 +33,10 @@ loss, whose ids the grouped matmul takes), `clip_grad_norm_` (global gradient
 norm and clipping of a parameter list) and `moe` (router and experts of a decoding
 step, with weights of x's type or in MXFP4), each over its own entry points of the
 library, so a program made of them is bit-reproducible too.
+
+Calls are asynchronous.  A kernel whose wait for its own copies ran out stops with its
+results unfinished; no function here asks for that, which would synchronize:
+`engine_for(device).check()` does, and raises BiError.
 """
 from __future__ import annotations
 
@@ -450,7 +454,8 @@ def moe(x: torch.Tensor, logits: torch.Tensor, w_gate, w_up, w_down, k: int, nor
     or all Fp4Weight.  activation: "silu", "gelu" (the tanh form) or "relu".  Rows with
     valid = 0 get zeros.  A row's y does not depend on the rows beside it; more than
     2048 / k tokens go in several calls, where `route` and the grouped matmul are
-    faster.  Forward only: tensors that require a gradient are refused."""
+    faster.  Forward only: tensors that require a gradient are refused.  A device-side
+    error is raised by engine_for(x.device).check(), after one call or many."""
     weights = [w for w in (w_gate, w_up, w_down) if w is not None]
     fp4 = isinstance(w_up, Fp4Weight)
     if any(isinstance(w, Fp4Weight) != fp4 for w in weights):
