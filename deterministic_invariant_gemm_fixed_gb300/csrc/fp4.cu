@@ -85,8 +85,9 @@ __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0
 // columns' direction on the tile in shared memory, a thread to a block of one column (two
 // columns of 16-bit values, whose magnitudes are compared in pairs).
 //
-// Bound by issue beside memory where there are many tiles (8192 x 4096 in bf16, both
-// directions: 103 MB in 25 us, issue 70 %).  A small matrix waits for one tile's chain of steps instead, and
+// Issue, beside memory, is what is busiest where there are many tiles (8192 x 4096 in bf16, both
+// directions: 103 MB in 25 us, issue 70 %); the rows' direction scales bf16 a value at a time,
+// where the columns' scales pairs.  A small matrix waits for one tile's chain of steps instead, and
 // takes the tiles of 32 rows, whose chain is a third as long; their column direction
 // writes 16 bytes at a time where the others write 64.
 constexpr int QT = 128;            // tile columns

@@ -7,12 +7,13 @@
 // instruction of its own; the tokens, few, are the MMA's N.  A block takes 128 weight
 // rows of one expert at a time (hidden kernel: 64 of the gate's and 64 of up's, whose
 // products meet in the epilogue) and walks such units, one block per SM, the copies
-// running ahead from unit to unit.  An output element is one ascending chain over the
+// running ahead from unit to unit.  A column's element is one ascending chain over the
 // contraction in one f32 accumulator, whatever the number of tokens beside it.
 //
 // 16-bit weights: kind::f16, stages of 64.  The tokens of the hidden kernel are all tokens
 // of the batch, straight from x (up to 256 at a time): columns of tokens that chose
-// other experts are thrown away, which costs nothing next to gathering.  h enters the output
+// other experts are thrown away.  For a few tokens that costs nothing next to gathering; with 256
+// a stage brings twice as much of x as of the weights, and the ring is shorter.  h enters the output
 // kernel as three 16-bit parts, each what the ones before left: all 24 bits of its f32
 // value.  They are N columns of their own, added in the epilogue from the smallest up: a sum of the
 // tensor cores cuts off what it shifts out, once for every MMA into it.  (Two parts into
@@ -40,9 +41,9 @@
 // kernel took 182 against 55 us for 64 tokens, 64 experts of 2048 x 1408.)
 //
 // Bound by reading the weights where there are many: 64 tokens through 6 of 64 experts of
-// 2048 x 1408 in bf16 read 450 MB in 82 us (hidden) and 228 MB in 54 (output), caches cold,
+// 2048 x 1408 in bf16 read 450 MB in 85 us (hidden) and 228 MB in 56 (output), caches cold,
 // set-up and ends included.  One token's 104 MB take 29 us over the three kernels, a third
-// of it set-up and ends.  MXFP4 with many tokens (96, 2 of 8 experts of 4096 x 4096: 88 us for
+// of it set-up and ends.  MXFP4 with many tokens (96, 2 of 8 experts of 4096 x 4096: 86 us for
 // 220 MB) is bound by the tokens' rows, 1 KB a token and stage beside the weights' 16 KB.
 #include "abi_util.h"
 #include "fp4.h"
