@@ -450,8 +450,9 @@ bi_status bi_moe_forward(bi_engine engine, void* y, const void* x, const uint32_
  * [E*N][F] (bi_fp4_quantize of the weights as [E*F, K] and [E*N, F]); their values
  * enter exactly, on the tensor cores for every dtype and size.  x and h enter as sums
  * of eight MXFP4 rows, which leave at most 2^-23 of the largest value of their block of
- * 32: a value far below it keeps fewer bits than f32 has, also where dtype is f32.  gate_q and gate_s NULL: no gate.  Scratch: with places = T C rounded up to 16 per
- * expert, about places (4.25 (K + F) + 4 F) + 4 T C N bytes. */
+ * 32 (2^-129 where that is more): a value far below it keeps fewer bits than f32 has,
+ * also where dtype is f32.  gate_q and gate_s NULL: no gate.  Scratch: with places = T C
+ * rounded up to 16 per expert, about places (4.25 (K + F) + 4 F) + 4 T C N bytes. */
 bi_status bi_moe_forward_fp4(bi_engine engine, void* y, const void* x, const uint32_t* ids, const float* weights,
                              const uint8_t* gate_q, const uint8_t* gate_s, const uint8_t* up_q, const uint8_t* up_s,
                              const uint8_t* down_q, const uint8_t* down_s, int64_t t, int64_t c, int64_t k, int64_t f,
